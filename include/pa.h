@@ -157,6 +157,81 @@ pa_status pa_attention_varlen_q8(const void* q, const void* k_cache, const void*
                                  pa_stream_t stream);
 
 /*
+ * q4 KV pages: 4-bit codes with a bf16 scale and offset for every 32 values
+ * (20 bytes instead of 64).  The pages' grouping of q8_0 ("Inference
+ * optimisation", AI-infra book ch. 8, §8.4.2 and Fig. 8-23) carried to four
+ * bits, with an offset, since sixteen levels around zero waste half of them on
+ * a channel that lies to one side.  A q4 pool is
+ * [num_blocks, num_kv_heads, PA_Q4_SLAB_BYTES] bytes; one (block, kv head)
+ * slab holds
+ *   codes   1024 bytes: token t's dims 32 g .. 32 g + 31 (group g) are the 16
+ *           bytes at 64 t + 16 (g ^ ((t >> 1) & 3)); of their little-endian
+ *           32-bit word w, dim 32 g + 8 w + 2 i is bits 4 i .. 4 i + 3 and dim
+ *           32 g + 8 w + 2 i + 1 bits 16 + 4 i .. 16 + 4 i + 3 (i = 0 .. 3);
+ *   scales  256 bytes: at 1024 + 16 t + 4 g the bf16 D, then the bf16 Z of
+ *           token t's group g.
+ * A code c stands for the bf16 nearest (ties to even) to Z + D (1 + c / 16);
+ * every call below computes with these bf16 values.  Quantising a group, in
+ * binary32 operations rounded to nearest even: lo, hi = its least and greatest
+ * value, D = bf16(16 ((hi - lo) / 15)), Z = bf16(lo - D), code = 16 ((x - Z) /
+ * D) - 16 rounded to the nearest integer (ties to even) and clamped to
+ * [0, 15]; all codes 0 when D is 0 (a group of equal values is kept exactly).
+ * Inputs must be finite and at most 2^126 in magnitude; a group with others
+ * gets unspecified bytes (no other group is touched).
+ */
+#define PA_Q4_SLAB_BYTES (PA_BLOCK_SIZE * PA_HEAD_DIM / 2 + PA_BLOCK_SIZE * (PA_HEAD_DIM / 32) * 4) /* 1280 */
+
+/*
+ * pa_kv_append_q4 -- pa_kv_append into q4 pools: each (token, kv head) row of
+ * k_new / v_new is quantized in groups of 32 as described above and stored
+ * with its scales in the slot's page.  Same arguments, validation and error
+ * word as pa_kv_append; k_cache and v_cache are q4 pools (16-byte aligned).
+ * With duplicate slots the stored row may mix the rows written to it.
+ */
+pa_status pa_kv_append_q4(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
+                          void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                          int32_t head_dim, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_kv_read_q4 -- read cached rows of q4 pools back as bf16, by slot: the
+ * values that pa_attention_varlen_q4 computes with, bit for bit (to move a
+ * prefix to another worker, or into a bf16 pool through pa_kv_append).
+ *   For row i with slot = slot_mapping[i], block = slot / 16 and offset =
+ *   slot % 16, and every kv head h:
+ *     k_out[i, h, :] = the values of k_cache[block, h], token offset  (v
+ *     likewise).
+ *   slot < 0 (padding) gives a row of zeros; so does a slot >= num_blocks *
+ *   16, which is also recorded as PA_ERR_DEVICE_INDEX.  A slot may be named
+ *   any number of times.
+ * slot_mapping   [n_tokens] int64, device.
+ * k_cache, v_cache  q4 pools, 16-byte aligned, read only.
+ * k_out, v_out   [n_tokens, num_kv_heads, head_dim] bf16, 16-byte aligned;
+ *                must not overlap each other or the pools.
+ * workspace      device, >= PA_ERROR_WORD_BYTES bytes; only the error word is
+ *                used.
+ * n_tokens = 0 is valid and launches nothing.
+ * Errors: PA_ERR_INVALID_ARG (n_tokens < 0, null or misaligned pointers),
+ *   PA_ERR_UNSUPPORTED (shape), PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA.
+ */
+pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const void* k_cache, const void* v_cache,
+                        int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void* k_out,
+                        void* v_out, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_attention_varlen_q4 -- pa_attention_varlen over q4 pools, for decode,
+ * chunked-prefill and verify rows alike: every K and V element is the bf16
+ * value its code stands for, the rest of the definition, the arguments, the
+ * workspace (pa_attention_workspace_size) and the errors are unchanged.
+ */
+pa_status pa_attention_varlen_q4(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                                 const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                                 const int32_t* qo_indptr, const int32_t* seq_lens_host,
+                                 const int32_t* qo_indptr_host, int32_t num_reqs, int32_t total_q,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 pa_stream_t stream);
+
+/*
  * pa_copy_blocks -- copy-on-write block copy ("Inference optimisation",
  * AI-infra book ch. 8, §8.3.2 and Fig. 8-15: before a branch writes into a
  * block it shares with another request, it gets its own copy of that block,
@@ -469,7 +544,8 @@ typedef enum {
   PA_KERNEL_PREFIX = 6,      /* shared-prefix pass of pa_attention_varlen_shared_prefix */
   PA_KERNEL_PREFIX_MERGE = 7, /* merge of that pass's key-chunk partials */
   PA_KERNEL_COPY_BLOCKS = 8,  /* pa_copy_blocks */
-  PA_KERNEL_DECODE_STEP = 9   /* pa_decode_step */
+  PA_KERNEL_DECODE_STEP = 9,  /* pa_decode_step */
+  PA_KERNEL_KV_READ = 10      /* pa_kv_read_q4 */
 } pa_kernel_kind;
 
 pa_status pa_set_decode_ctas(int32_t n);

@@ -28,7 +28,7 @@ PA_ERR_DEVICE_INDEX = 5
 PA_ERR_DEVICE_TIMEOUT = 6
 PA_ERROR_WORD_BYTES = 256
 KERNEL_KINDS = {1: "kv_append", 2: "decode", 3: "combine", 4: "prefill", 5: "merge", 6: "prefix", 7: "prefix_merge", 8: "copy_blocks",
-                9: "decode_step"}
+                9: "decode_step", 10: "kv_read"}
 
 
 class PAError(RuntimeError):
@@ -52,6 +52,10 @@ _SIGS = {
     "pa_copy_blocks": (_i32, [_P, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _sz, _P]),
     "pa_kv_append_q8": (_i32, [_P, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _sz, _P]),
     "pa_attention_varlen_q8": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32,
+                                      _i32, _f32, _P, _P, _P, _sz, _P]),
+    "pa_kv_append_q4": (_i32, [_P, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _sz, _P]),
+    "pa_kv_read_q4": (_i32, [_P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _P, _P, _sz, _P]),
+    "pa_attention_varlen_q4": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32,
                                       _i32, _f32, _P, _P, _P, _sz, _P]),
     "pa_attention_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "pa_attention_varlen": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -201,6 +205,104 @@ def pa_attention_varlen_q8(q, k_cache, v_cache, block_tables, seq_lens, qo_indpt
         max_len = int(slh.max()) if R else 1
         workspace = new_workspace(pa_attention_workspace_size(R, total_q, Hq, D, max_len), q.device)
     _check(_lib.pa_attention_varlen_q8(_ptr(q), _ptr(k_cache), _ptr(v_cache), nb, _ptr(block_tables),
+                                       block_tables.shape[1], _ptr(seq_lens), _ptr(qo_indptr),
+                                       ctypes.c_void_p(slh.data_ptr()), ctypes.c_void_p(qih.data_ptr()), R, total_q,
+                                       Hq, Hkv, D, 16, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                       workspace.numel(), _stream(stream)))
+    return (out, lse) if (return_lse or lse is not None) else out
+
+
+PA_Q4_SLAB_BYTES = 16 * 128 // 2 + 16 * (128 // 32) * 4
+
+
+def new_q4_pool(num_blocks, num_kv_heads, device):
+    """An empty q4 pool [num_blocks, Hkv, PA_Q4_SLAB_BYTES] (uint8): every
+    code stands for 0."""
+    return torch.zeros((num_blocks, num_kv_heads, PA_Q4_SLAB_BYTES), dtype=torch.uint8, device=device)
+
+
+def pa_kv_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, workspace=None, stream=None):
+    """Quantize k_new / v_new [N, Hkv, D] bf16 into q4 pools (uint8
+    [num_blocks, Hkv, PA_Q4_SLAB_BYTES]) at slot_mapping (int64 [N], negative
+    = skip)."""
+    _need(k_new, torch.bfloat16, "k_new")
+    _need(v_new, torch.bfloat16, "v_new")
+    _need(k_cache, torch.uint8, "k_cache")
+    _need(v_cache, torch.uint8, "v_cache")
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    N, Hkv, D = k_new.shape
+    nb = k_cache.shape[0]
+    if v_new.shape != k_new.shape or v_cache.shape != k_cache.shape or k_cache.shape[1:] != (Hkv, PA_Q4_SLAB_BYTES) \
+            or slot_mapping.shape != (N,):
+        raise ValueError("inconsistent shapes")
+    if workspace is None:
+        workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
+    _check(_lib.pa_kv_append_q4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_cache), _ptr(v_cache), nb,
+                                16, Hkv, D, _ptr(workspace), workspace.numel(), _stream(stream)))
+    return workspace
+
+
+def pa_kv_read_q4(slot_mapping, k_cache, v_cache, k_out=None, v_out=None, workspace=None, stream=None):
+    """Rows of q4 pools (uint8 [num_blocks, Hkv, PA_Q4_SLAB_BYTES]) at
+    slot_mapping (int64 [N]; negative = a row of zeros) as bf16 [N, Hkv, D]:
+    the values pa_attention_varlen_q4 computes with.  Returns (k_out, v_out)."""
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    _need(k_cache, torch.uint8, "k_cache")
+    _need(v_cache, torch.uint8, "v_cache")
+    nb, Hkv, slab = k_cache.shape
+    if v_cache.shape != k_cache.shape or slab != PA_Q4_SLAB_BYTES or slot_mapping.dim() != 1:
+        raise ValueError("inconsistent shapes")
+    shape = (slot_mapping.shape[0], Hkv, 128)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+    _need(k_out, torch.bfloat16, "k_out")
+    _need(v_out, torch.bfloat16, "v_out")
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("k_out and v_out must be [N, Hkv, 128]")
+    if workspace is None:
+        workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
+    _check(_lib.pa_kv_read_q4(_ptr(slot_mapping), shape[0], _ptr(k_cache), _ptr(v_cache), nb, 16, Hkv, 128,
+                              _ptr(k_out), _ptr(v_out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return k_out, v_out
+
+
+def pa_attention_varlen_q4(q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, sm_scale, *, seq_lens_host=None,
+                           qo_indptr_host=None, out=None, lse=None, workspace=None, stream=None, return_lse=False):
+    """pa_attention_varlen over q4 pools (decode, chunked-prefill and verify
+    rows)."""
+    _need(q, torch.bfloat16, "q")
+    _need(k_cache, torch.uint8, "k_cache")
+    _need(v_cache, torch.uint8, "v_cache")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(seq_lens, torch.int32, "seq_lens")
+    _need(qo_indptr, torch.int32, "qo_indptr")
+    total_q, Hq, D = q.shape
+    nb, Hkv, slab = k_cache.shape
+    R = seq_lens.shape[0]
+    if v_cache.shape != k_cache.shape or slab != PA_Q4_SLAB_BYTES or qo_indptr.shape != (R + 1,) \
+            or block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("inconsistent shapes")
+    slh = _host_i32(seq_lens if seq_lens_host is None else seq_lens_host)
+    qih = _host_i32(qo_indptr if qo_indptr_host is None else qo_indptr_host)
+    if slh.shape != (R,) or qih.shape != (R + 1,):
+        raise ValueError("host copies must have the shapes of seq_lens and qo_indptr")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None and return_lse:
+        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.shape != (total_q, Hq):
+            raise ValueError("lse must be [total_q, Hq]")
+    if workspace is None:
+        max_len = int(slh.max()) if R else 1
+        workspace = new_workspace(pa_attention_workspace_size(R, total_q, Hq, D, max_len), q.device)
+    _check(_lib.pa_attention_varlen_q4(_ptr(q), _ptr(k_cache), _ptr(v_cache), nb, _ptr(block_tables),
                                        block_tables.shape[1], _ptr(seq_lens), _ptr(qo_indptr),
                                        ctypes.c_void_p(slh.data_ptr()), ctypes.c_void_p(qih.data_ptr()), R, total_q,
                                        Hq, Hkv, D, 16, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),

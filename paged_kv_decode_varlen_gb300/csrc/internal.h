@@ -23,6 +23,37 @@ struct AppendParams {
   int* err;
 };
 
+// Read-back of q4 rows by slot (zero rows for slots outside the pool).
+struct ReadParams {
+  const int64_t* slot_mapping;
+  int64_t n_tokens;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  int64_t num_blocks;
+  int32_t num_kv_heads;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int* err;
+};
+
+struct AttnQ4Params {
+  const uint16_t* q;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  int64_t num_blocks;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_req;
+  const int32_t* seq_lens;
+  const int32_t* qo_indptr;
+  int32_t num_reqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  int* err;
+};
+
 struct CopyParams {
   uint16_t* k_cache;
   uint16_t* v_cache;
@@ -241,6 +272,9 @@ pa_status set_error(pa_status s, const char* fmt, ...);
 // Each launcher enqueues one kernel on `stream` and returns its launch error.
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append_q8(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_append_q4(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read_q4(const ReadParams& p, cudaStream_t stream);
+cudaError_t launch_attn_q4(const AttnQ4Params& p, int total_q, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 // overlap: programmatic launch after the stream's previous kernel; diag:
 // the timeout-path diagnostic instantiation (bf16 pages, warp-granular);

@@ -502,14 +502,16 @@ namespace {
 
 // The attention entry points.  prefix_pages > 0: the first prefix_pages
 // pages of every request are one shared prefix, attended once for all
-// queries by the prefix pass and folded into each row's own part.  q8: the
-// pools hold q8_0 pages (decode rows only).
+// queries by the prefix pass and folded into each row's own part.  pages:
+// what the pools hold (q8_0 pages: decode rows only).
+enum class Pages { kBf16, kQ8, kQ4 };
 pa_status attention(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
                     const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
                     const int32_t* qo_indptr, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
                     int32_t num_reqs, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                     int32_t block_size, int32_t prefix_pages, float sm_scale, void* out, float* lse, void* workspace,
-                    size_t workspace_bytes, cudaStream_t stream, bool q8 = false) {
+                    size_t workspace_bytes, cudaStream_t stream, Pages pages = Pages::kBf16) {
+  const bool q8 = pages == Pages::kQ8;
   pa_status s = check_shape(num_q_heads, num_kv_heads, head_dim, block_size);
   if (s != PA_OK) return s;
   if (num_reqs < 0 || num_reqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_reqs %d outside [0, 65535]", num_reqs);
@@ -574,6 +576,26 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   if (workspace_bytes < need)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
   if (total_q == 0) return ok();
+  if (pages == Pages::kQ4) {
+    pa::AttnQ4Params ap;
+    ap.q = static_cast<const uint16_t*>(q);
+    ap.k_cache = static_cast<const uint8_t*>(k_cache);
+    ap.v_cache = static_cast<const uint8_t*>(v_cache);
+    ap.num_blocks = num_blocks;
+    ap.block_tables = block_tables;
+    ap.max_blocks_per_req = max_blocks_per_req;
+    ap.seq_lens = seq_lens;
+    ap.qo_indptr = qo_indptr;
+    ap.num_reqs = num_reqs;
+    ap.num_q_heads = num_q_heads;
+    ap.num_kv_heads = num_kv_heads;
+    ap.scale_log2 = sm_scale * pa::kLog2e;
+    ap.out = static_cast<uint16_t*>(out);
+    ap.lse = lse;
+    ap.err = static_cast<int*>(workspace);
+    s = run_launch(PA_KERNEL_DECODE, "attention_q4", stream, [&] { return pa::launch_attn_q4(ap, total_q, stream); });
+    return s == PA_OK ? ok() : s;
+  }
   // a prefix read by one request only is not worth a separate pass
   const int32_t P = active >= 2 ? prefix_pages : 0;
   if (P > 0 && prefix_qtiles(total_q) > 65535)
@@ -797,7 +819,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
 
 pa_status append(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens, void* k_cache,
                  void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
-                 void* workspace, size_t workspace_bytes, pa_stream_t stream, bool q8);
+                 void* workspace, size_t workspace_bytes, pa_stream_t stream, Pages pages);
 
 }  // namespace
 
@@ -824,14 +846,50 @@ pa_status pa_kv_append(const void* k_new, const void* v_new, const int64_t* slot
                        void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
                        int32_t head_dim, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
   return append(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_blocks, block_size, num_kv_heads,
-                head_dim, workspace, workspace_bytes, stream, false);
+                head_dim, workspace, workspace_bytes, stream, Pages::kBf16);
 }
 
 pa_status pa_kv_append_q8(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
                           void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
                           int32_t head_dim, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
   return append(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_blocks, block_size, num_kv_heads,
-                head_dim, workspace, workspace_bytes, stream, true);
+                head_dim, workspace, workspace_bytes, stream, Pages::kQ8);
+}
+
+pa_status pa_kv_append_q4(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
+                          void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                          int32_t head_dim, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  return append(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_blocks, block_size, num_kv_heads,
+                head_dim, workspace, workspace_bytes, stream, Pages::kQ4);
+}
+
+pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const void* k_cache, const void* v_cache,
+                        int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void* k_out,
+                        void* v_out, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (n_tokens < 0) return fail(PA_ERR_INVALID_ARG, "n_tokens %lld < 0", (long long)n_tokens);
+  if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks must be positive");
+  pa_status s = check_shape(PA_GQA_GROUP * num_kv_heads, num_kv_heads, head_dim, block_size);
+  if (s != PA_OK) return s;
+  if (!k_cache || !v_cache || !workspace) return fail(PA_ERR_INVALID_ARG, "null cache or workspace pointer");
+  if (n_tokens > 0 && (!slot_mapping || !k_out || !v_out)) return fail(PA_ERR_INVALID_ARG, "null slot or output pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(workspace, 4))
+    return fail(PA_ERR_INVALID_ARG, "tensors must be 16-byte aligned (slot_mapping 8, workspace 4)");
+  if (workspace_bytes < PA_ERROR_WORD_BYTES)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %d bytes", workspace_bytes, PA_ERROR_WORD_BYTES);
+  if (n_tokens == 0) return ok();
+  pa::ReadParams p;
+  p.slot_mapping = slot_mapping;
+  p.n_tokens = n_tokens;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.num_kv_heads = num_kv_heads;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.err = static_cast<int*>(workspace);
+  s = run_launch(PA_KERNEL_KV_READ, "kv_read_q4", stream, [&] { return pa::launch_kv_read_q4(p, stream); });
+  return s == PA_OK ? ok() : s;
 }
 
 pa_status pa_attention_varlen_q8(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
@@ -843,7 +901,19 @@ pa_status pa_attention_varlen_q8(const void* q, const void* k_cache, const void*
                                  pa_stream_t stream) {
   return attention(q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_req, seq_lens, qo_indptr,
                    seq_lens_host, qo_indptr_host, num_reqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size,
-                   0, sm_scale, out, lse, workspace, workspace_bytes, stream, true);
+                   0, sm_scale, out, lse, workspace, workspace_bytes, stream, Pages::kQ8);
+}
+
+pa_status pa_attention_varlen_q4(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                                 const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                                 const int32_t* qo_indptr, const int32_t* seq_lens_host,
+                                 const int32_t* qo_indptr_host, int32_t num_reqs, int32_t total_q,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 pa_stream_t stream) {
+  return attention(q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_req, seq_lens, qo_indptr,
+                   seq_lens_host, qo_indptr_host, num_reqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size,
+                   0, sm_scale, out, lse, workspace, workspace_bytes, stream, Pages::kQ4);
 }
 
 }  // extern "C"
@@ -852,7 +922,7 @@ namespace {
 
 pa_status append(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens, void* k_cache,
                  void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
-                 void* workspace, size_t workspace_bytes, pa_stream_t stream, bool q8) {
+                 void* workspace, size_t workspace_bytes, pa_stream_t stream, Pages pages) {
   if (n_tokens < 0) return fail(PA_ERR_INVALID_ARG, "n_tokens %lld < 0", (long long)n_tokens);
   if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks must be positive");
   pa_status s = check_shape(PA_GQA_GROUP * num_kv_heads, num_kv_heads, head_dim, block_size);
@@ -875,8 +945,17 @@ pa_status append(const void* k_new, const void* v_new, const int64_t* slot_mappi
   p.num_blocks = num_blocks;
   p.num_kv_heads = num_kv_heads;
   p.err = static_cast<int*>(workspace);
-  s = run_launch(PA_KERNEL_KV_APPEND, q8 ? "kv_append_q8" : "kv_append", stream,
-                 [&] { return q8 ? pa::launch_kv_append_q8(p, stream) : pa::launch_kv_append(p, stream); });
+  switch (pages) {
+    case Pages::kBf16:
+      s = run_launch(PA_KERNEL_KV_APPEND, "kv_append", stream, [&] { return pa::launch_kv_append(p, stream); });
+      break;
+    case Pages::kQ8:
+      s = run_launch(PA_KERNEL_KV_APPEND, "kv_append_q8", stream, [&] { return pa::launch_kv_append_q8(p, stream); });
+      break;
+    case Pages::kQ4:
+      s = run_launch(PA_KERNEL_KV_APPEND, "kv_append_q4", stream, [&] { return pa::launch_kv_append_q4(p, stream); });
+      break;
+  }
   return s == PA_OK ? ok() : s;
 }
 
