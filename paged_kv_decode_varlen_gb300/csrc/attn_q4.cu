@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(128) attn_q4_kernel(const AttnQ4Params p) {
     if (p.qo_indptr[mid] <= tok) lo = mid; else hi = mid - 1;
   }
   const int r = lo;
+  if (p.qo_indptr[r + 1] - p.qo_indptr[r] == 1) return;  // a decode row
   const int n_keys = p.seq_lens[r] - (p.qo_indptr[r + 1] - tok) + 1;
   const uint16_t* q = p.q + ((size_t)tok * p.num_q_heads + head) * kHeadDim;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};

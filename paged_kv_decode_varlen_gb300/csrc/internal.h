@@ -92,6 +92,12 @@ constexpr int kMinWarpSegPages = 8;
 constexpr int kWgWarps = 12;
 constexpr int kWgMaxPagesPerCta = 3072;
 constexpr int kWgMaxItemsPerCta = 192;
+// The decode kernel over q4 pages: one CTA of kQ4Warps warps per SM, a warp
+// segment each; pages and rows a segment may hold.
+constexpr int kQ4Warps = 16;
+constexpr int kQ4MaxPagesPerCta = 2048;
+constexpr int kQ4MaxItemsPerCta = 192;
+static_assert(kQ4MaxPagesPerCta % kQ4Warps == 0 && kQ4MaxItemsPerCta % 32 == 0, "whole warp segments and table rounds");
 // Bytes of one (page, kv head) slab of K or V in bf16 (16 tokens x 128 dims).
 constexpr int kSlabBytesHost = 16 * 128 * 2;
 struct DecodePlan {
@@ -283,6 +289,9 @@ cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 // the warp-granular kernel (plan in whole warp segments of kWgWarps warps)
 cudaError_t launch_decode(const DecodeParams& p, const DecodePlan& plan, int grid, bool q8, bool overlap,
                           bool diag, bool cta_granular, cudaStream_t stream);
+// q4 pages, a plan in whole warp segments of kQ4Warps warps
+cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, int grid, bool overlap,
+                             cudaStream_t stream);
 // warp_granular: the warp-granular kernel (grid: one CTA per SM at most; no
 // segment may hold more than kWgMaxItemsPerCta rows or kWgMaxPagesPerCta
 // pages), else the CTA-granular one (windows of rows)

@@ -511,7 +511,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
                     int32_t num_reqs, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                     int32_t block_size, int32_t prefix_pages, float sm_scale, void* out, float* lse, void* workspace,
                     size_t workspace_bytes, cudaStream_t stream, Pages pages = Pages::kBf16) {
-  const bool q8 = pages == Pages::kQ8;
+  const bool q8 = pages == Pages::kQ8, q4 = pages == Pages::kQ4;
   pa_status s = check_shape(num_q_heads, num_kv_heads, head_dim, block_size);
   if (s != PA_OK) return s;
   if (num_reqs < 0 || num_reqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_reqs %d outside [0, 65535]", num_reqs);
@@ -576,7 +576,15 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   if (workspace_bytes < need)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
   if (total_q == 0) return ok();
-  if (pages == Pages::kQ4) {
+  // a prefix read by one request only is not worth a separate pass
+  const int32_t P = active >= 2 ? prefix_pages : 0;
+  if (P > 0 && prefix_qtiles(total_q) > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "total_q %d too large for the shared-prefix pass", total_q);
+
+  char* ws = static_cast<char*>(workspace);
+  int* err = reinterpret_cast<int*>(ws);
+  const float scale_log2 = sm_scale * pa::kLog2e;
+  if (q4 && !tiles.empty()) {
     pa::AttnQ4Params ap;
     ap.q = static_cast<const uint16_t*>(q);
     ap.k_cache = static_cast<const uint8_t*>(k_cache);
@@ -592,18 +600,11 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     ap.scale_log2 = sm_scale * pa::kLog2e;
     ap.out = static_cast<uint16_t*>(out);
     ap.lse = lse;
-    ap.err = static_cast<int*>(workspace);
-    s = run_launch(PA_KERNEL_DECODE, "attention_q4", stream, [&] { return pa::launch_attn_q4(ap, total_q, stream); });
-    return s == PA_OK ? ok() : s;
+    ap.err = err;
+    s = run_launch(PA_KERNEL_PREFILL, "attention_q4", stream, [&] { return pa::launch_attn_q4(ap, total_q, stream); });
+    if (s != PA_OK) return s;
+    tiles.clear();
   }
-  // a prefix read by one request only is not worth a separate pass
-  const int32_t P = active >= 2 ? prefix_pages : 0;
-  if (P > 0 && prefix_qtiles(total_q) > 65535)
-    return fail(PA_ERR_UNSUPPORTED, "total_q %d too large for the shared-prefix pass", total_q);
-
-  char* ws = static_cast<char*>(workspace);
-  int* err = reinterpret_cast<int*>(ws);
-  const float scale_log2 = sm_scale * pa::kLog2e;
   float* prefix_o = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_o) : nullptr;
   float* prefix_lse = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_lse) : nullptr;
   static thread_local pa::TcMaps maps;
@@ -803,6 +804,16 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       // the tile kernel's tail, they made the step 1-2 us longer, not shorter.
       // Beside a concurrent prefix pass they start as soon as it has.
       const bool overlap = d0 > 0 || (P == 0 && tiles.empty()) || concurrent;
+      if (q4) {
+        const int grid = plan_decode(decode_rows.data() + d0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, gcap,
+                                     sm_count(), pa::kQ4Warps, pa::kQ4MaxPagesPerCta, pa::kQ4MaxItemsPerCta, plan);
+        if (grid < 0) return fail(PA_ERR_UNSUPPORTED, "no decode plan within the kernel limits");
+        if (grid == 0) continue;
+        s = run_launch(PA_KERNEL_DECODE, "decode_q4", stream,
+                       [&] { return pa::launch_decode_q4(dp, plan, grid, overlap, stream); });
+        if (s != PA_OK) return s;
+        continue;
+      }
       const bool diag = !q8 && g_decode_fault.load() != 0;
       bool cta_granular = false;
       const int grid = choose_decode_plan(decode_rows.data() + d0, n, seq_lens_host, qo_indptr_host, P, num_kv_heads,
