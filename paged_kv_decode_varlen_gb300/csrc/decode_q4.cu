@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = kQ4Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;  // pages in flight per warp
+constexpr int kStages = 2;  // page pairs in flight per warp (a power of two)
 constexpr float kRescaleSlack = 8.f;  // the running max is re-based when it grows by more than 2^8
 
 struct Item {        // one row's pages within this CTA's segment
@@ -52,19 +52,24 @@ struct Item {        // one row's pages within this CTA's segment
 };
 
 struct __align__(128) Smem {
-  uint8_t ring[kWarps][kStages][2][kQ4Slab];  // K slab, V slab
-  float4 part_o[kWarps][2][4][32];            // a warp's part of its first / last item: 16 values per lane
+  uint8_t ring[kWarps][kStages][2][2][kQ4Slab];  // two pages per stage, K slab and V slab
+  // a warp's part of its first item, 16 values per lane; the part of its last
+  // one goes where its ring was
+  float4 part_o[kWarps][4][32];
   float part_m[kWarps][2][kGroup], part_l[kWarps][2][kGroup];
   uint64_t full[kWarps][kStages];
   int32_t ids[kQ4MaxPagesPerCta];
   Item items[kQ4MaxItemsPerCta];
   int arrived[kQ4MaxItemsPerCta];  // warps done with their part of the item
-  int stage_page[kWarps][kStages];
   int n_items;
-  int abort_flag;
 };
+static_assert(sizeof(float4) * 4 * 32 <= sizeof(Smem::ring[0]), "a part fits a warp's ring");
 static_assert(sizeof(Smem) <= 227 * 1024, "one CTA per SM");
 static_assert(kQ4Slab % 128 == 0, "matrix-load rows of a slab meet the banks as laid out in q4.cuh");
+
+__device__ __forceinline__ float4* part_of(Smem& sm, int warp, int slot) {
+  return slot == 0 ? &sm.part_o[warp][0][0] : reinterpret_cast<float4*>(sm.ring[warp]);
+}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -157,11 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (npg <= 0) return;
   if (tid == 0) {
     for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) {
-        mbar_init(&sm.full[w][s], 1);
-        sm.stage_page[w][s] = -1;
-      }
-    sm.abort_flag = 0;
+      for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[w][s], 1);
     fence_mbar_init();
   }
   for (int i = tid; i < kQ4MaxItemsPerCta; i += kThreads) sm.arrived[i] = 0;
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- block ids of the segment's pages; a page with an id outside the pool
   // (or past the table) is recorded and skipped
   const int n_cov = sm.items[n_items - 1].q_start + sm.items[n_items - 1].n;
+  int ok = 1;
   for (int q = tid; q < n_cov; q += kThreads) {
     int lo = 0, hi = n_items - 1;
     while (lo < hi) {  // last item with q_start <= q
@@ -230,10 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blk < 0 || blk >= p.num_blocks) {
       record_error(p.err, PA_ERR_DEVICE_INDEX);
       blk = -1;
+      ok = 0;
     }
     sm.ids[q] = blk;
   }
-  __syncthreads();
+  const bool ids_ok = __syncthreads_and(ok) != 0;
 
   // ---- this warp's pages [a, e) of the segment
   const int sw = plan.seg / kWarps;
@@ -250,23 +253,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(p.k_cache);
   const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v_cache);
-  // segment page q -> warp page j = q - a -> stage j % kStages (lane 0 only)
-  auto issue = [&](int q) {
-    const int j = q - a, s = j % kStages;
-    const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab;
-    mbar_arrive_expect_tx(&sm.full[warp][s], 2 * kQ4Slab);
-    bulk_g2s(sm.ring[warp][s][0], kbase + off, kQ4Slab, &sm.full[warp][s]);
-    bulk_g2s(sm.ring[warp][s][1], vbase + off, kQ4Slab, &sm.full[warp][s]);
-    sm.stage_page[warp][s] = j;
+  // Pages a + 2 i and a + 2 i + 1 -> stage i % kStages.  Lanes 0 .. 3 issue the
+  // K and V slab of the two pages; a page with a bad id is fetched from block 0
+  // and does not count.
+  const int n_pairs = (e - a + 1) >> 1;
+  auto issue = [&](int i) {
+    if (lane < 4) {
+      const int s = i & (kStages - 1), q = a + 2 * i + (lane >> 1);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (q + 1 < e ? 4 : 2) * kQ4Slab);
+      if (q < e) {
+        const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab;
+        bulk_g2s(sm.ring[warp][s][lane >> 1][lane & 1], ((lane & 1) ? vbase : kbase) + off, kQ4Slab, &sm.full[warp][s]);
+      }
+    }
   };
-  if (lane == 0)
-    for (int q = a; q < min(e, a + kStages); ++q) issue(q);
+  for (int i = 0; i < min(n_pairs, kStages); ++i) issue(i);
 
   const int r = lane >> 2;   // token slot (r, r + 8) in the scores; dim row in the output
   const int cq = lane & 3;   // the lane's head in scores and output
   // matrix-load address of lane l: matrix (group) l / 8, row (token) l % 8
   const uint32_t ld_at = (uint32_t)q4_code_at(lane & 7, lane >> 3);
-  bool aborted = false;
+  int issued = min(n_pairs, kStages);
+  bool gave_up = false;
 
   for (; k < n_items; ++k) {
     const Item it = sm.items[k];
@@ -296,99 +304,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the first key), and the sum of this lane's own weights
     float m = -INFINITY, nm = 0.f, l = 0.f;
 
-    for (int q = i0; q < i1; ++q) {
-      const int j = q - a, s = j % kStages;
-      if (!mbar_wait_bounded(&sm.full[warp][s], (uint32_t)(j / kStages) & 1u)) {
+    for (int q = i0; q < i1;) {
+      const int j = q - a, i = j >> 1, s = i & (kStages - 1);
+      if (!mbar_wait_bounded(&sm.full[warp][s], (uint32_t)(i / kStages) & 1u)) {
         record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-        *reinterpret_cast<volatile int*>(&sm.abort_flag) = 1;
-        aborted = true;
+        gave_up = true;
         break;
       }
-      if (sm.ids[q] >= 0) {
-        const uint32_t ks = smem_addr(sm.ring[warp][s][0]), vs = smem_addr(sm.ring[warp][s][1]);
-        const int live = q == q_last ? tail : kPage;  // tokens of the page that count
-        // ---- scores: tokens r and r + 8 of head cq
+      // two pages at once where the pair lies in the row, else one: page 0 is
+      // q, page 1 its neighbour in the stage, of which no token counts then
+      const int half = j & 1, n = (half == 0 && q + 1 < i1) ? 2 : 1;
+      int live[2];  // tokens of each page that count
+      live[0] = q == q_last ? tail : kPage;
+      live[1] = n == 1 ? 0 : q + 1 == q_last ? tail : kPage;
+      if (!ids_ok) {
+        if (sm.ids[q] < 0) live[0] = 0;
+        if (n == 2 && sm.ids[q + 1] < 0) live[1] = 0;
+      }
+      const uint32_t st = smem_addr(sm.ring[warp][s][half]), step = half ? 0u - 2 * kQ4Slab : 2u * kQ4Slab;
+      // ---- scores: tokens r and r + 8 of head cq, of both pages
+      float sc[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t ks = st + u * step;
         float c[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-          uint32_t ka[4], kb[4];
-          ldmatrix4(ka, ks + ld_at);
-          ldmatrix4(kb, ks + ld_at + 8 * kQ4Row);
-          const uint4 za = lds128(ks + kQ4Codes + 16 * r), zb = lds128(ks + kQ4Codes + 16 * (r + 8));
+        uint32_t ka[4], kb[4];
+        ldmatrix4(ka, ks + ld_at);
+        ldmatrix4(kb, ks + ld_at + 8 * kQ4Row);
+        const uint4 za = lds128(ks + kQ4Codes + 16 * r), zb = lds128(ks + kQ4Codes + 16 * (r + 8));
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t da = q4_dup_d(at(za, g)), oa = q4_dup_z(at(za, g));
-            const uint32_t db = q4_dup_d(at(zb, g)), ob = q4_dup_z(at(zb, g));
-            mma16816(c, bf16x2_fma(q4_unit_pair<0>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<0>(kb[g]), db, ob),
-                     bf16x2_fma(q4_unit_pair<1>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<1>(kb[g]), db, ob), qb[g].x,
-                     qb[g].y);
-            mma16816(c, bf16x2_fma(q4_unit_pair<2>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<2>(kb[g]), db, ob),
-                     bf16x2_fma(q4_unit_pair<3>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<3>(kb[g]), db, ob), qb[g].z,
-                     qb[g].w);
-          }
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t da = q4_dup_d(at(za, g)), oa = q4_dup_z(at(za, g));
+          const uint32_t db = q4_dup_d(at(zb, g)), ob = q4_dup_z(at(zb, g));
+          mma16816(c, bf16x2_fma(q4_unit_pair<0>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<0>(kb[g]), db, ob),
+                   bf16x2_fma(q4_unit_pair<1>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<1>(kb[g]), db, ob), qb[g].x,
+                   qb[g].y);
+          mma16816(c, bf16x2_fma(q4_unit_pair<2>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<2>(kb[g]), db, ob),
+                   bf16x2_fma(q4_unit_pair<3>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<3>(kb[g]), db, ob), qb[g].z,
+                   qb[g].w);
         }
-        float s0 = r < live ? c[0] * p.scale_log2 : -INFINITY;
-        float s1 = r + 8 < live ? c[2] * p.scale_log2 : -INFINITY;
-        float mx = fmaxf(s0, s1);
-        if (__any_sync(0xffffffffu, mx > m + kRescaleSlack)) {  // rare after the first page
+        sc[2 * u] = c[0] * p.scale_log2;
+        sc[2 * u + 1] = c[2] * p.scale_log2;
+      }
+      const bool whole = live[0] == kPage && live[1] == kPage;
+      if (!whole) {
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          if (mx > m + kRescaleSlack) {
-            const float corr = fast_exp2(m - mx);  // m = -inf -> 0
-            m = mx;
-            nm = -mx;
-            l *= corr;
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[g][x][i] *= corr;
-          }
+        for (int u = 0; u < 2; ++u) {
+          if (r >= live[u]) sc[2 * u] = -INFINITY;
+          if (r + 8 >= live[u]) sc[2 * u + 1] = -INFINITY;
         }
-        const float p0 = fast_exp2(s0 + nm), p1 = fast_exp2(s1 + nm);
-        l += p0 + p1;
-        // weights as two bf16 each (leading bits, rest), transposed into the
-        // second product's B operand
-        const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffff0000u);
-        const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffff0000u);
-        const uint32_t pb0 = movmatrix_trans(pack_bf16x2(h0, p0 - h0));
-        const uint32_t pb1 = movmatrix_trans(pack_bf16x2(h1, p1 - h1));
-        // ---- output: dims of row r of each group's words, tokens 2 cq, 2 cq
-        // + 1 and the same + 8
+      }
+      float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+      if (__any_sync(0xffffffffu, mx > m + kRescaleSlack)) {  // rare after the first pages
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx > m + kRescaleSlack) {
+          const float corr = fast_exp2(m - mx);  // m = -inf -> 0
+          m = mx;
+          nm = -mx;
+          l *= corr;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) acc[g][x][y] *= corr;
+        }
+      }
+      // weights as two bf16 each (leading bits, rest), transposed into the
+      // second product's B operand
+      uint32_t pb[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = fast_exp2(sc[u] + nm);
+        l += w;
+        const float h = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+        pb[u] = movmatrix_trans(pack_bf16x2(h, w - h));
+      }
+      // ---- output: dims of row r of each group's words, tokens 2 cq, 2 cq +
+      // 1 and the same + 8
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t vs = st + u * step + kQ4Slab;
         uint32_t va[4], vb[4];
         ldmatrix4_trans(va, vs + ld_at);
         ldmatrix4_trans(vb, vs + ld_at + 8 * kQ4Row);
-        const uint32_t sc = vs + kQ4Codes + 32 * cq;
-        uint4 z0 = lds128(sc), z1 = lds128(sc + 16), z2 = lds128(sc + 128), z3 = lds128(sc + 144);
-        if (live < kPage) {  // a token that does not count has weight 0: its values must be finite
+        const uint32_t sp = vs + kQ4Codes + 32 * cq;
+        uint4 z0 = lds128(sp), z1 = lds128(sp + 16), z2 = lds128(sp + 128), z3 = lds128(sp + 144);
+        if (!whole) {  // a token that does not count has weight 0: its values must be finite
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          if (2 * cq >= live) z0 = zero;
-          if (2 * cq + 1 >= live) z1 = zero;
-          if (2 * cq + 8 >= live) z2 = zero;
-          if (2 * cq + 9 >= live) z3 = zero;
+          if (2 * cq >= live[u]) z0 = zero;
+          if (2 * cq + 1 >= live[u]) z1 = zero;
+          if (2 * cq + 8 >= live[u]) z2 = zero;
+          if (2 * cq + 9 >= live[u]) z3 = zero;
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const uint32_t da = __byte_perm(at(z0, g), at(z1, g), 0x5410), oa = __byte_perm(at(z0, g), at(z1, g), 0x7632);
           const uint32_t db = __byte_perm(at(z2, g), at(z3, g), 0x5410), ob = __byte_perm(at(z2, g), at(z3, g), 0x7632);
           mma16816(acc[g][0], bf16x2_fma(q4_unit_pair<0>(va[g]), da, oa), bf16x2_fma(q4_unit_pair<1>(va[g]), da, oa),
-                   bf16x2_fma(q4_unit_pair<0>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<1>(vb[g]), db, ob), pb0, pb1);
+                   bf16x2_fma(q4_unit_pair<0>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<1>(vb[g]), db, ob), pb[2 * u],
+                   pb[2 * u + 1]);
           mma16816(acc[g][1], bf16x2_fma(q4_unit_pair<2>(va[g]), da, oa), bf16x2_fma(q4_unit_pair<3>(va[g]), da, oa),
-                   bf16x2_fma(q4_unit_pair<2>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<3>(vb[g]), db, ob), pb0, pb1);
+                   bf16x2_fma(q4_unit_pair<2>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<3>(vb[g]), db, ob), pb[2 * u],
+                   pb[2 * u + 1]);
         }
       }
-      // the warp is done with the page: refill its stage
-      __syncwarp();
-      if (lane == 0 && q + kStages < e) {
-        fence_proxy_async_smem();
-        issue(q + kStages);
-      }
-      if ((j & 15) == 15 && *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
-        aborted = true;
-        break;
+      q += n;
+      // the pair is done with: refill its stage
+      if (((q - a) & 1) == 0) {
+        __syncwarp();
+        if (issued < n_pairs) {
+          fence_proxy_async_smem();
+          issue(issued);
+          ++issued;
+        }
       }
     }
-    if (aborted) break;
+    if (gave_up) break;
 
     // ---- this warp's part of the item: head cq, value 4 g + i is dim 32 g +
     // 8 (r / 2) + r % 2 + 2 i, unnormalised
@@ -405,8 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mg.add(m, l, x);
     } else {
       const int slot = it.q_start <= a ? 0 : 1;  // the warp's first item, or its last
+      float4* mine = part_of(sm, warp, slot);
+      __syncwarp();  // every lane has read the ring
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sm.part_o[warp][slot][i][lane] = x[i];
+      for (int i = 0; i < 4; ++i) mine[32 * i + lane] = x[i];
       if (r == 0) {
         sm.part_m[warp][slot][cq] = m;
         sm.part_l[warp][slot][cq] = l;
@@ -423,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sl = it.q_start <= w * sw ? 0 : 1;
         float4 y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = sm.part_o[w][sl][i][lane];
+        for (int i = 0; i < 4; ++i) y[i] = part_of(sm, w, sl)[32 * i + lane];
         mg.add(sm.part_m[w][sl][cq], sm.part_l[w][sl][cq], y);
       }
     }
@@ -476,12 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.lse && r == 0) p.lse[orow] = mg.l > 0.f ? (mg.m + log2f(mg.l)) * kLn2 : -INFINITY;
   }
 
-  if (aborted && lane == 0) {
-    // a wait gave up: let the copies in flight land (bounded), then leave
-    for (int s = 0; s < kStages; ++s) {
-      const int j = sm.stage_page[warp][s];
-      if (j >= 0) mbar_wait_bounded(&sm.full[warp][s], (uint32_t)(j / kStages) & 1u);
-    }
+  if (gave_up && lane == 0) {
+    // a wait ran out: let the last copies issued into each stage land
+    // (bounded), then leave
+    for (int i = max(0, issued - kStages); i < issued; ++i)
+      mbar_wait_bounded(&sm.full[warp][i & (kStages - 1)], (uint32_t)(i / kStages) & 1u);
   }
 }
 

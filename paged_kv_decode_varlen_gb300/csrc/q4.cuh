@@ -35,7 +35,9 @@ __device__ __forceinline__ int q4_scale_at(int t, int g) { return kQ4Codes + (t 
 template <int i>
 __device__ __forceinline__ uint32_t q4_unit_pair(uint32_t w) {
   const uint32_t s = i == 0 ? w << 3 : w >> (i == 0 ? 0 : 4 * i - 3);
-  return (s & 0x00780078u) | 0x3f803f80u;
+  uint32_t u;  // (s & mask) | one in one instruction
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(s), "r"(0x00780078u), "r"(0x3f803f80u));
+  return u;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
