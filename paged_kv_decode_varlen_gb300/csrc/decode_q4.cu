@@ -38,7 +38,14 @@ namespace {
 
 constexpr int kWarps = kQ4Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 2;  // page pairs in flight per warp (a power of two)
+#ifndef Q4_PAIR
+#define Q4_PAIR 2
+#endif
+#ifndef Q4_STAGES
+#define Q4_STAGES 2
+#endif
+constexpr int kPair = Q4_PAIR;  // pages per stage
+constexpr int kStages = Q4_STAGES;  // stages in flight per warp
 constexpr float kRescaleSlack = 8.f;  // the running max is re-based when it grows by more than 2^8
 
 struct Item {        // one row's pages within this CTA's segment
@@ -52,7 +59,7 @@ struct Item {        // one row's pages within this CTA's segment
 };
 
 struct __align__(128) Smem {
-  uint8_t ring[kWarps][kStages][2][2][kQ4Slab];  // two pages per stage, K slab and V slab
+  uint8_t ring[kWarps][kStages][kPair][2][kQ4Slab];  // two pages per stage, K slab and V slab
   // a warp's part of its first item, 16 values per lane; the part of its last
   // one goes where its ring was
   float4 part_o[kWarps][4][32];
@@ -256,11 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Pages a + 2 i and a + 2 i + 1 -> stage i % kStages.  Lanes 0 .. 3 issue the
   // K and V slab of the two pages; a page with a bad id is fetched from block 0
   // and does not count.
-  const int n_pairs = (e - a + 1) >> 1;
+  const int n_pairs = (e - a + kPair - 1) / kPair;
   auto issue = [&](int i) {
-    if (lane < 4) {
-      const int s = i & (kStages - 1), q = a + 2 * i + (lane >> 1);
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (q + 1 < e ? 4 : 2) * kQ4Slab);
+    if (lane < 2 * kPair) {
+      const int s = i % kStages, q = a + kPair * i + (lane >> 1);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (kPair == 2 && q + 1 < e ? 4 : 2) * kQ4Slab);
       if (q < e) {
         const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab;
         bulk_g2s(sm.ring[warp][s][lane >> 1][lane & 1], ((lane & 1) ? vbase : kbase) + off, kQ4Slab, &sm.full[warp][s]);
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, nm = 0.f, l = 0.f;
 
     for (int q = i0; q < i1;) {
-      const int j = q - a, i = j >> 1, s = i & (kStages - 1);
+      const int j = q - a, i = j / kPair, s = i % kStages;
       if (!mbar_wait_bounded(&sm.full[warp][s], (uint32_t)(i / kStages) & 1u)) {
         record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
         gave_up = true;
@@ -313,19 +320,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // two pages at once where the pair lies in the row, else one: page 0 is
       // q, page 1 its neighbour in the stage, of which no token counts then
-      const int half = j & 1, n = (half == 0 && q + 1 < i1) ? 2 : 1;
-      int live[2];  // tokens of each page that count
+      const int half = kPair == 2 ? j & 1 : 0, n = (kPair == 2 && half == 0 && q + 1 < i1) ? 2 : 1;
+      int live[kPair];  // tokens of each page that count
       live[0] = q == q_last ? tail : kPage;
-      live[1] = n == 1 ? 0 : q + 1 == q_last ? tail : kPage;
+      if (kPair == 2) live[kPair - 1] = n == 1 ? 0 : q + 1 == q_last ? tail : kPage;
       if (!ids_ok) {
         if (sm.ids[q] < 0) live[0] = 0;
-        if (n == 2 && sm.ids[q + 1] < 0) live[1] = 0;
+        if (n == 2 && sm.ids[q + 1] < 0) live[kPair - 1] = 0;
       }
       const uint32_t st = smem_addr(sm.ring[warp][s][half]), step = half ? 0u - 2 * kQ4Slab : 2u * kQ4Slab;
       // ---- scores: tokens r and r + 8 of head cq, of both pages
-      float sc[4];
+      float sc[2 * kPair];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kPair; ++u) {
         const uint32_t ks = st + u * step;
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t ka[4], kb[4];
@@ -346,15 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         sc[2 * u] = c[0] * p.scale_log2;
         sc[2 * u + 1] = c[2] * p.scale_log2;
       }
-      const bool whole = live[0] == kPage && live[1] == kPage;
+      const bool whole = live[0] == kPage && live[kPair - 1] == kPage;
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kPair; ++u) {
           if (r >= live[u]) sc[2 * u] = -INFINITY;
           if (r + 8 >= live[u]) sc[2 * u + 1] = -INFINITY;
         }
       }
-      float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+      float mx = fmaxf(sc[0], sc[1]);
+      if (kPair == 2) mx = fmaxf(mx, fmaxf(sc[2 * kPair - 2], sc[2 * kPair - 1]));
       if (__any_sync(0xffffffffu, mx > m + kRescaleSlack)) {  // rare after the first pages
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -373,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // weights as two bf16 each (leading bits, rest), transposed into the
       // second product's B operand
-      uint32_t pb[4];
+      uint32_t pb[2 * kPair];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2 * kPair; ++u) {
         const float w = fast_exp2(sc[u] + nm);
         l += w;
         const float h = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
@@ -384,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- output: dims of row r of each group's words, tokens 2 cq, 2 cq +
       // 1 and the same + 8
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kPair; ++u) {
         const uint32_t vs = st + u * step + kQ4Slab;
         uint32_t va[4], vb[4];
         ldmatrix4_trans(va, vs + ld_at);
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       q += n;
       // the pair is done with: refill its stage
-      if (((q - a) & 1) == 0) {
+      if ((q - a) % kPair == 0) {
         __syncwarp();
         if (issued < n_pairs) {
           fence_proxy_async_smem();
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a wait ran out: let the last copies issued into each stage land
     // (bounded), then leave
     for (int i = max(0, issued - kStages); i < issued; ++i)
-      mbar_wait_bounded(&sm.full[warp][i & (kStages - 1)], (uint32_t)(i / kStages) & 1u);
+      mbar_wait_bounded(&sm.full[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
   }
 }
 

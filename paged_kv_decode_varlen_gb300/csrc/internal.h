@@ -36,24 +36,6 @@ struct ReadParams {
   int* err;
 };
 
-struct AttnQ4Params {
-  const uint16_t* q;
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
-  int64_t num_blocks;
-  const int32_t* block_tables;
-  int32_t max_blocks_per_req;
-  const int32_t* seq_lens;
-  const int32_t* qo_indptr;
-  int32_t num_reqs;
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
-  float scale_log2;
-  uint16_t* out;
-  float* lse;
-  int* err;
-};
-
 struct CopyParams {
   uint16_t* k_cache;
   uint16_t* v_cache;
@@ -94,8 +76,11 @@ constexpr int kWgMaxPagesPerCta = 3072;
 constexpr int kWgMaxItemsPerCta = 192;
 // The decode kernel over q4 pages: one CTA of kQ4Warps warps per SM, a warp
 // segment each; pages and rows a segment may hold.
-constexpr int kQ4Warps = 16;
-constexpr int kQ4MaxPagesPerCta = 2048;
+#ifndef Q4_WARPS
+#define Q4_WARPS 16
+#endif
+constexpr int kQ4Warps = Q4_WARPS;
+constexpr int kQ4MaxPagesPerCta = 2040 / kQ4Warps * kQ4Warps;
 constexpr int kQ4MaxItemsPerCta = 192;
 static_assert(kQ4MaxPagesPerCta % kQ4Warps == 0 && kQ4MaxItemsPerCta % 32 == 0, "whole warp segments and table rounds");
 // Bytes of one (page, kv head) slab of K or V in bf16 (16 tokens x 128 dims).
@@ -280,7 +265,6 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append_q8(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append_q4(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read_q4(const ReadParams& p, cudaStream_t stream);
-cudaError_t launch_attn_q4(const AttnQ4Params& p, int total_q, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 // overlap: programmatic launch after the stream's previous kernel; diag:
 // the timeout-path diagnostic instantiation (bf16 pages, warp-granular);
@@ -297,6 +281,9 @@ cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, int 
 // pages), else the CTA-granular one (windows of rows)
 cudaError_t launch_decode_step(const DecodeParams& p, const StepPlan& plan, int grid, bool warp_granular,
                                cudaStream_t stream);
+// q4 pages: one CTA per (item of kQ4TileTokens queries, kv head)
+cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const CUtensorMap& q_map,
+                              cudaStream_t stream);
 // ctas: CTAs of the launch (0: one per (item, kv head) job; fewer run
 // several jobs each)
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, const TcMaps& maps, int ctas,
@@ -309,6 +296,8 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.
 constexpr int kPrefillQTile = 32;
 constexpr int kTcKeyTile = 128;
+// Query tokens per CTA of the tile kernel over q4 pages (two MMA tiles).
+constexpr int kQ4TileTokens = 2 * kPrefillQTile;
 // Decode kernel: pages a CTA may hold block ids for (bounds the segment).
 constexpr int kDecodeMaxPagesPerCta = 1024;
 

@@ -443,30 +443,39 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tiled maps of q ([total_q][Hq][128] bf16, boxes 64 x 4 heads x 32 tokens)
-// and of the K / V pools (rows of 128 bf16, one per (block, kv head, token),
-// boxes 64 x 16 rows), 128-byte swizzled; out-of-range q tokens read as 0.
-pa_status make_tc_maps(const void* q, int32_t total_q, int32_t num_q_heads, const void* k_cache, const void* v_cache,
-                       int64_t num_blocks, int32_t num_kv_heads, pa::TcMaps& m) {
+// Tiled map of q ([total_q][Hq][128] bf16, boxes 64 x 4 heads x 32 tokens),
+// 128-byte swizzled; out-of-range q tokens read as 0.
+pa_status make_q_map(const void* q, int32_t total_q, int32_t num_q_heads, CUtensorMap& m) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const int64_t rows = num_blocks * num_kv_heads * pa::kPage;
-  if (rows >= (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "pool of %lld rows: too many for the tile kernels",
-                                               (long long)rows);
   const cuuint32_t estr[3] = {1, 1, 1};
   const cuuint64_t qdims[3] = {(cuuint64_t)pa::kHeadDim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
   const cuuint64_t qstrides[2] = {(cuuint64_t)pa::kHeadDim * 2, (cuuint64_t)num_q_heads * pa::kHeadDim * 2};
   const cuuint32_t qbox[3] = {64, (cuuint32_t)pa::kGroup, (cuuint32_t)pa::kPrefillQTile};
-  CUresult r = enc(&m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), qdims, qstrides, qbox, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), qdims, qstrides, qbox, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "encoding the q tensor map: CUresult %d", (int)r);
+  return PA_OK;
+}
+
+// The q map and those of the K / V pools (rows of 128 bf16, one per (block, kv
+// head, token), boxes 64 x 16 rows), 128-byte swizzled.
+pa_status make_tc_maps(const void* q, int32_t total_q, int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                       int64_t num_blocks, int32_t num_kv_heads, pa::TcMaps& m) {
+  const int64_t rows = num_blocks * num_kv_heads * pa::kPage;
+  if (rows >= (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "pool of %lld rows: too many for the tile kernels",
+                                               (long long)rows);
+  const pa_status s = make_q_map(q, total_q, num_q_heads, m.q);
+  if (s != PA_OK) return s;
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  const cuuint32_t estr[2] = {1, 1};
   const cuuint64_t kdims[2] = {(cuuint64_t)pa::kHeadDim, (cuuint64_t)rows};
   const cuuint64_t kstrides[1] = {(cuuint64_t)pa::kHeadDim * 2};
   const cuuint32_t kbox[2] = {64, (cuuint32_t)pa::kPage};
-  r = enc(&m.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(k_cache), kdims, kstrides, kbox, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(&m.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(k_cache), kdims, kstrides, kbox, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "encoding the K tensor map: CUresult %d", (int)r);
   r = enc(&m.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(v_cache), kdims, kstrides, kbox, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -563,8 +572,9 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     if (qo_len == 1) {
       decode_rows.push_back(r);
     } else if (qo_len > 1) {
-      for (int32_t j0 = 0; j0 < qo_len; j0 += pa::kPrefillQTile) {
-        tiles.push_back({L - qo_len + std::min(qo_len, j0 + pa::kPrefillQTile), (int32_t)item_req.size()});
+      const int32_t q_tile = q4 ? pa::kQ4TileTokens : pa::kPrefillQTile;
+      for (int32_t j0 = 0; j0 < qo_len; j0 += q_tile) {
+        tiles.push_back({L - qo_len + std::min(qo_len, j0 + q_tile), (int32_t)item_req.size()});
         item_req.push_back(r);
         item_q0.push_back(j0);
       }
@@ -584,32 +594,12 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   char* ws = static_cast<char*>(workspace);
   int* err = reinterpret_cast<int*>(ws);
   const float scale_log2 = sm_scale * pa::kLog2e;
-  if (q4 && !tiles.empty()) {
-    pa::AttnQ4Params ap;
-    ap.q = static_cast<const uint16_t*>(q);
-    ap.k_cache = static_cast<const uint8_t*>(k_cache);
-    ap.v_cache = static_cast<const uint8_t*>(v_cache);
-    ap.num_blocks = num_blocks;
-    ap.block_tables = block_tables;
-    ap.max_blocks_per_req = max_blocks_per_req;
-    ap.seq_lens = seq_lens;
-    ap.qo_indptr = qo_indptr;
-    ap.num_reqs = num_reqs;
-    ap.num_q_heads = num_q_heads;
-    ap.num_kv_heads = num_kv_heads;
-    ap.scale_log2 = sm_scale * pa::kLog2e;
-    ap.out = static_cast<uint16_t*>(out);
-    ap.lse = lse;
-    ap.err = err;
-    s = run_launch(PA_KERNEL_PREFILL, "attention_q4", stream, [&] { return pa::launch_attn_q4(ap, total_q, stream); });
-    if (s != PA_OK) return s;
-    tiles.clear();
-  }
   float* prefix_o = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_o) : nullptr;
   float* prefix_lse = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_lse) : nullptr;
   static thread_local pa::TcMaps maps;
   if (P > 0 || !tiles.empty()) {
-    s = make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
+    s = q4 ? make_q_map(q, total_q, num_q_heads, maps.q)
+           : make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
     if (s != PA_OK) return s;
   }
 
@@ -686,7 +676,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     // prefix, one launch of each): the tiles on a few SMs, the decode stream
     // on the others.
     const int forced_p = g_prefill_ctas.load();
-    if (P == 0 && !q8 && !decode_rows.empty() && decode_rows.size() <= (size_t)pa::kPlanMaxRows &&
+    if (P == 0 && pages == Pages::kBf16 && !decode_rows.empty() && decode_rows.size() <= (size_t)pa::kPlanMaxRows &&
         tiles.size() <= (size_t)pa::kMaxPrefillItems && g_forced_ctas.load() <= 0 && g_decode_fault.load() == 0 &&
         forced_p >= 0) {
       const int jobs = (int)tiles.size() * num_kv_heads;
@@ -705,7 +695,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         concurrent = true;
         decode_slots = std::max(1, sm_count() - prefill_ctas) * kDecodeCtasPerSm;
       }
-    } else if (P == 0 && decode_rows.empty() && forced_p >= 0 && !q8 &&
+    } else if (P == 0 && decode_rows.empty() && forced_p >= 0 && pages == Pages::kBf16 &&
                tiles.size() <= (size_t)pa::kMaxPrefillItems && g_forced_ctas.load() <= 0 &&
                g_decode_fault.load() == 0) {
       // a batch of tile jobs alone: persistent CTAs, each running its jobs
@@ -757,7 +747,10 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         items.q_start[i] = item_q0[idx];
       }
       s = run_launch(PA_KERNEL_PREFILL, "prefill", stream,
-                     [&] { return pa::launch_prefill(pp, items, maps, prefill_ctas, stream); });
+                     [&] {
+                       return q4 ? pa::launch_prefill_q4(pp, items, maps.q, stream)
+                                 : pa::launch_prefill(pp, items, maps, prefill_ctas, stream);
+                     });
       if (s != PA_OK) return s;
     }
   }

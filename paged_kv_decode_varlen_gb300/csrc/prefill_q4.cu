@@ -1,0 +1,461 @@
+// Tensor-core tiles of attention over 4-bit pages: rows with several query
+// tokens (prompt chunks, verify rows).
+//
+// What is computed: query j of a row with h cached tokens sits at position
+// h + j and attends to keys 0 .. h + j; scores, softmax and output as in
+// decode_q4.cu, keys and values the bf16 numbers that the codes stand for.
+//
+// Work.  One CTA per (64 query tokens, kv head): two query tiles A and B of 32
+// tokens x 4 heads = 128 rows, the M of one tcgen05.mma each, against key
+// tiles of 128 (8 pages).  The two tiles share every dequantised K and V tile,
+// and their softmaxes alternate on the tensor cores: while tile A's warps turn
+// scores into weights, B's products run.
+//   Bound.  Per key tile the four products of 128 x 128 x 128 take 2048 cycles
+// of the tensor cores, the exponentials of both tiles and the instructions of
+// all warps some 1900 of the schedulers', so neither waits long for the other.
+//
+// Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory
+// lane = row).  8: copies Q (TMA).  9: owns the tensor memory, one thread
+// issues the products.  10, 11 and 12, 13: K and V producers.  Each of a
+// producer pair's 64 threads owns one (token, group) place of a page: it reads
+// 16 bytes of codes and their (D, Z) from each of the tile's 8 pages, a tile
+// ahead, and writes 32 bf16 values into the 128-byte-swizzled operand tile.
+// (Dequantised once per CTA in registers: a second copy of the cache in bf16
+// is never made.)
+//
+// Tensor memory: scores of A and B (128 columns each), outputs of A and B (128
+// each).  A tile's weights (bf16 pairs, the A operand of the PV product)
+// overwrite its scores, so its next score product is issued only after its PV
+// product has completed.  The softmax therefore reads its scores twice, 64
+// columns at a time: for the maximum, then for the weights.  Weights are
+// rounded to bf16, as the tensor cores take them; their sum is kept in
+// binary32 from the unrounded ones, as are scores, maxima and outputs.
+//
+// Every wait is bounded; on a timeout the CTA records the error, lets its
+// copies and products finish (bounded), frees its tensor memory and returns.
+#include <math.h>
+#include <stddef.h>
+
+#include "internal.h"
+#include "q4.cuh"
+#include "tc.cuh"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kTok = kPrefillQTile;          // query tokens of a tile
+constexpr int kRows = kTok * kGroup;         // 128
+constexpr int kKeys = kTcKeyTile;            // 128 keys per tile
+constexpr int kPagesPerTile = kKeys / kPage;
+constexpr int kHalf = 128 * 128;             // 128 rows x 64 bf16
+constexpr int kTileBytes = 2 * kHalf;
+constexpr int kKStages = 2, kVStages = 2;
+constexpr int kQWarp = 8, kMmaWarp = 9, kKWarp = 10, kVWarp = 12;
+constexpr int kThreads = 14 * 32;
+constexpr int kProducers = 64;               // threads of a producer pair
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
+constexpr float kRescaleSlack = 8.f;
+constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys, false);
+constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
+static_assert(kRows == 128 && kKeys == 128 && kQ4TileTokens == 2 * kTok, "tile shape");
+static_assert(kProducers * 16 == kQ4Codes, "a producer thread per 16 bytes of a page's codes");
+
+struct __align__(1024) Smem {
+  uint8_t q[2][kTileBytes];  // then each tile's output rows on their way out
+  uint8_t k[kKStages][kTileBytes];
+  uint8_t v[kVStages][kTileBytes];
+  uint64_t bar_q;
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2], pv_done[2];  // per query tile, phase j for key tile j
+  uint32_t bad[8];   // pages of key tile j whose block id is outside the pool (entry j % 8)
+  uint32_t tmem;
+  int abort;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        record_error(err, PA_ERR_DEVICE_TIMEOUT);
+        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// 64 columns of this thread's lane
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  tmem_ld32_async(taddr, a);
+  tmem_ld32_async(taddr + 32, b);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tmem_bind32(a);
+  tmem_bind32(b);
+}
+
+struct Job {
+  int32_t tok0;  // first query token of the job
+  int32_t nq;    // its query tokens (1 .. 64)
+  int32_t kvh;
+  int32_t pos0;  // position of the first
+  int32_t keys;  // keys its last query sees
+  const int32_t* table;
+};
+
+// K or V producer thread i (0 .. 63) of a pair: dequantises its place of every
+// page of every key tile.
+__device__ __forceinline__ void produce(Smem& sm, const Job& job, bool is_k, int i, const uint8_t* cache,
+                                        int num_kv_heads, int64_t num_blocks, int n_tiles, int* err) {
+  const int lane = threadIdx.x & 31;
+  const int t = i >> 2, g = (i & 3) ^ ((t >> 1) & 3);
+  const int last_page = (job.keys - 1) / kPage;
+  // block ids four tiles at a time, one group ahead: lane l holds page l % 8
+  // of tile 4 G + l / 8; -1: past the row's keys, -2: outside the pool
+  auto load_group = [&](int G) -> int {
+    const int page = (4 * G + (lane >> 3)) * kPagesPerTile + (lane & 7);
+    if (page > last_page) return -1;
+    const int32_t b = job.table[page];
+    if (b < 0 || b >= num_blocks) {
+      if (is_k) record_error(err, PA_ERR_DEVICE_INDEX);
+      return -2;
+    }
+    return b;
+  };
+  int grp = load_group(0), grp_next = load_group(1);
+  uint4 code[kPagesPerTile];
+  uint32_t dz[kPagesPerTile];
+  // page u of tile j of the current (or next) group into code[u], dz[u]; a
+  // key past the end, or of a page outside the pool, becomes 0
+  auto fetch = [&](int u, int j, int ids) {
+    const int id = __shfl_sync(0xffffffffu, ids, ((j & 3) << 3) + u);
+    code[u] = make_uint4(0u, 0u, 0u, 0u);
+    dz[u] = 0u;
+    if (id >= 0 && (j * kPagesPerTile + u) * kPage + t < job.keys) {
+      const uint8_t* slab = cache + ((size_t)id * num_kv_heads + job.kvh) * kQ4Slab;
+      code[u] = __ldg(reinterpret_cast<const uint4*>(slab) + i);
+      dz[u] = __ldg(reinterpret_cast<const uint32_t*>(slab + q4_scale_at(t, g)));
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kPagesPerTile; ++u) fetch(u, 0, grp);
+  uint64_t* full = is_k ? sm.k_full : sm.v_full;
+  uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+  constexpr int n_st = kKStages;
+  static_assert(kKStages == kVStages, "one ring depth");
+  // Row t of a page, 16-byte chunk c of its 64-dim half at c ^ (t & 7).  The
+  // words of groups 2 and 3 are stored in the order 2, 3, 0, 1, so that the
+  // eight lanes of a store phase (2 tokens x 4 groups) meet eight chunks.
+  const int swap = g & 2;
+  const uint32_t row = (g >> 1) * kHalf + t * 128;
+  for (int j = 0; j < n_tiles; ++j) {
+    const int s = j % n_st;
+    if (is_k) {
+      const unsigned bad = __ballot_sync(0xffffffffu, grp == -2);
+      if (i == 0) sm.bad[j & 7] = (bad >> ((j & 3) << 3)) & 0xffu;
+    }
+    if (j >= n_st && !__all_sync(0xffffffffu, wait(sm, &empty[s], ((j / n_st) - 1) & 1, err))) return;
+    int ids = grp;
+    if (((j + 1) & 3) == 0) {  // the next tile starts a group
+      ids = grp_next;
+      grp_next = load_group(((j + 1) >> 2) + 1);
+    }
+    const uint32_t dst = smem_addr(is_k ? sm.k[s] : sm.v[s]) + row;
+#pragma unroll
+    for (int u = 0; u < kPagesPerTile; ++u) {
+      const uint4 c = code[u];
+      const uint32_t z = dz[u];
+      if (j + 1 < n_tiles) fetch(u, j + 1, ids);
+      const uint32_t w[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint4 val = q4_word_values(w[x], z);
+        const uint32_t at = dst + u * (kPage * 128) + (((((g & 1) << 2) + (x ^ swap)) ^ (t & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(val.x), "r"(val.y), "r"(val.z), "r"(val.w)
+                     : "memory");
+      }
+    }
+    grp = ids;
+    fence_proxy_async_smem();  // the products read the tile through the async proxy
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[s]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_q4_kernel(const PrefillParams p, const __grid_constant__ PrefillItems items,
+                      const __grid_constant__ CUtensorMap q_map) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Job job;
+  {
+    const int it = blockIdx.x / p.num_kv_heads;
+    const int r = items.req[it], j0 = items.q_start[it];
+    const int qo0 = p.qo_indptr[r], c = p.qo_indptr[r + 1] - qo0;
+    job.tok0 = qo0 + j0;
+    job.nq = min(kQ4TileTokens, c - j0);
+    job.kvh = blockIdx.x % p.num_kv_heads;
+    job.pos0 = p.seq_lens[r] - c + j0;
+    job.keys = job.pos0 + job.nq;
+    job.table = p.block_tables + (size_t)r * p.max_blocks_per_req;
+  }
+  // metadata that differ from the host plan: record and skip the job
+  if (job.nq <= 0 || job.pos0 < 0 || (job.keys - 1) / kPage >= p.max_blocks_per_req) {
+    if (threadIdx.x == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
+    return;
+  }
+  const int n_tiles = (job.keys + kKeys - 1) / kKeys;
+  const int n_x = job.nq > kTok ? 2 : 1;  // query tiles
+  if (warp == kQWarp && lane == 0) {
+    mbar_init(&sm.bar_q, 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&sm.k_full[s], kProducers / 32);
+      mbar_init(&sm.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&sm.v_full[s], kProducers / 32);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_full[x], kRows);
+      mbar_init(&sm.pv_done[x], 1);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&sm.bar_q, n_x * kTileBytes);
+    for (int x = 0; x < n_x; ++x) {
+      tma_load_3d(sm.q[x], &q_map, 0, job.kvh * kGroup, job.tok0 + x * kTok, &sm.bar_q);
+      tma_load_3d(sm.q[x] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + x * kTok, &sm.bar_q);
+    }
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp >= kKWarp) {
+    const bool is_k = warp < kVWarp;
+    produce(sm, job, is_k, (warp - (is_k ? kKWarp : kVWarp)) * 32 + lane,
+            reinterpret_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles,
+            p.err);
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int last_s[2] = {-1, -1}, last_pv[2] = {-1, -1};
+      auto issue_s = [&](int x, int j) {
+        const uint32_t qb = smem_addr(sm.q[x]), kb = smem_addr(sm.k[j % kKStages]);
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;  // 64-dim half, 16-dim step in it
+          mma_bf16(tmem + kColS + x * kKeys, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), kIdescS,
+                   ks > 0);
+        }
+        commit(&sm.s_full[x]);
+        if (x == n_x - 1) commit(&sm.k_empty[j % kKStages]);
+        last_s[x] = j;
+      };
+      auto issue_pv = [&](int x, int j) {
+        const uint32_t pt = tmem + kColS + x * kKeys, vb = smem_addr(sm.v[j % kVStages]);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_bf16_ts(tmem + kColO + x * kHeadDim, pt + 8 * ks, desc_sw128(vb + ks * 2 * 1024, kHalf, 1024), kIdescO,
+                      (j > 0 || ks > 0) ? 1u : 0u);
+        commit(&sm.pv_done[x]);
+        if (x == n_x - 1) commit(&sm.v_empty[j % kVStages]);
+        last_pv[x] = j;
+      };
+      bool ok = wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err);
+      if (ok) {
+        fence_after_sync();
+        for (int x = 0; x < n_x; ++x) issue_s(x, 0);
+      }
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        ok = wait(sm, &sm.v_full[j % kVStages], (j / kVStages) & 1, p.err);
+        for (int x = 0; ok && x < n_x; ++x) {
+          if (!(ok = wait(sm, &sm.p_full[x], j & 1, p.err))) break;
+          fence_after_sync();
+          issue_pv(x, j);
+          if (j + 1 < n_tiles) {
+            const int j1 = j + 1;
+            ok = (x > 0 || wait(sm, &sm.k_full[j1 % kKStages], (j1 / kKStages) & 1, p.err)) &&
+                 wait(sm, &sm.pv_done[x], j & 1, p.err);  // the weights lie where the scores go
+            if (!ok) break;
+            fence_after_sync();
+            issue_s(x, j1);
+          }
+        }
+      }
+      // every product issued has completed before the tensor memory is freed
+      for (int x = 0; x < n_x; ++x) {
+        if (last_s[x] >= 0) mbar_wait_bounded(&sm.s_full[x], last_s[x] & 1);
+        if (last_pv[x] >= 0) mbar_wait_bounded(&sm.pv_done[x], last_pv[x] & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kQWarp) {
+    if (lane == 0) mbar_wait_bounded(&sm.bar_q, 0);  // Q has landed before the CTA may leave
+  } else if ((warp >> 2) < n_x) {
+    // -------------------------------------------------------------- softmax
+    const int x = warp >> 2;
+    const int row = threadIdx.x & 127;  // 4 * token + head in group
+    const int pos = job.pos0 + x * kTok + (row >> 2);
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = lane_base + kColS + x * kKeys, t_o = lane_base + kColO + x * kHeadDim;
+    const float scale = p.scale_log2;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x], j & 1, p.err));
+      if (!ok) break;
+      fence_after_sync();
+      const int kbase = j * kKeys;
+      const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm.bad[j & 7]);
+      // keys this row may see: the first `seen` of the tile, less bad pages
+      const int seen = min(pos, job.keys - 1) - kbase + 1;
+      const bool masked = kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u;
+      auto hidden = [&](int key) { return key >= seen || ((bad >> (key >> 4)) & 1u); };
+      // ---- maximum of the scaled scores
+      float mt = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[32], b[32];
+        load64(t_s + 64 * h, a, b);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            mt = fmaxf(mt, hidden(64 * h + i) ? -INFINITY : __uint_as_float(a[i]) * scale);
+            mt = fmaxf(mt, hidden(64 * h + 32 + i) ? -INFINITY : __uint_as_float(b[i]) * scale);
+          }
+        } else {
+          float mx[4];  // independent chains over scores of the sign of the scale
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = scale >= 0.f ? -INFINITY : INFINITY;
+          if (scale >= 0.f) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+            mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              mx[i & 3] = fminf(mx[i & 3], fminf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+            mt = fmaxf(mt, fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale);
+          }
+        }
+      }
+      const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
+      float corr = 1.f;
+      if (grow) {
+        corr = fast_exp2(m_run - mt);  // m_run = -inf -> 0
+        l_run *= corr;
+        m_run = mt;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, grow)) {
+        // O is stable: this tile's scores were issued after PV of tile j - 1
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(t_o + 32 * c, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= corr;
+          tmem_st32(t_o + 32 * c, o);
+        }
+      }
+      // ---- weights, over the scores they come from
+      const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+      const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[32], b[32], w[32];
+        load64(t_s + 64 * h, a, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t lo = i < 16 ? a[2 * (i & 15)] : b[2 * (i & 15)];
+          const uint32_t hi = i < 16 ? a[2 * (i & 15) + 1] : b[2 * (i & 15) + 1];
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), sc2, nm2);
+          float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+          if (masked) {
+            if (hidden(64 * h + 2 * i)) e.x = 0.f;
+            if (hidden(64 * h + 2 * i + 1)) e.y = 0.f;
+          }
+          ls[i & 1] = __fadd2_rn(ls[i & 1], e);
+          w[i] = pack_bf16x2(e.x, e.y);
+        }
+        tmem_st32u(t_s + 32 * h, w);
+      }
+      l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+      fence_before_sync();  // the tensor-memory accesses above precede the arrive
+      mbar_arrive(&sm.p_full[x]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x], (n_tiles - 1) & 1, p.err));
+    if (ok) {
+      fence_after_sync();
+      // bf16 rows through the tile's Q buffer (its last score product is
+      // done): 256 B per row, 16-byte chunk c at c ^ (row & 15)
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      uint8_t* stg = sm.q[x];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(t_o + 32 * c, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(stg + row * 256 + (((4 * c + i) ^ (row & 15)) << 4)) =
+              make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+      }
+      const int tok = x * kTok + (row >> 2);
+      if (p.lse && tok < job.nq)
+        p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
+            l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + x), "n"(kRows) : "memory");
+    if (!*reinterpret_cast<volatile int*>(&sm.abort)) {
+#pragma unroll 4
+      for (int i = 0; i < kRows * 16 / kRows; ++i) {  // 16 threads write one 256-byte row
+        const int L = i * kRows + row;
+        const int rr = L >> 4, c = L & 15;
+        const int tok = x * kTok + (rr >> 2);
+        if (tok >= job.nq) continue;
+        const size_t orow = (size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (rr & 3);
+        *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 8 * c) =
+            *reinterpret_cast<const uint4*>(sm.q[x] + rr * 256 + ((c ^ (rr & 15)) << 4));
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+std::atomic<bool> g_attr_set[kMaxDevices];
+
+}  // namespace
+
+cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const CUtensorMap& q_map,
+                              cudaStream_t stream) {
+  if (items.count <= 0) return cudaSuccess;
+  const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel, (int)kSmemBytes, g_attr_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_q4_kernel, dim3((unsigned)(items.count * p.num_kv_heads)), dim3(kThreads), kSmemBytes,
+                    stream, p, items, q_map);
+}
+
+}  // namespace pa
