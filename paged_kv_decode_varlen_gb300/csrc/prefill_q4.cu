@@ -15,13 +15,13 @@
 // all warps some 1900 of the schedulers', so neither waits long for the other.
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory
-// lane = row).  8: copies Q (TMA).  9: owns the tensor memory, one thread
-// issues the products.  10, 11 and 12, 13: K and V producers.  Each of a
-// producer pair's 64 threads owns one (token, group) place of a page: it reads
-// 16 bytes of codes and their (D, Z) from each of the tile's 8 pages, a tile
-// ahead, and writes 32 bf16 values into the 128-byte-swizzled operand tile.
-// (Dequantised once per CTA in registers: a second copy of the cache in bf16
-// is never made.)
+// lane = row).  8: copies Q (TMA), owns the tensor memory, one thread issues
+// the products as their inputs become ready.  9-15: producers.  A unit of
+// their work is one page's K or V slab: each lane reads two 16-byte pieces of
+// codes (tokens t and t + 8 of one group) and their (D, Z), three units ahead,
+// and writes 64 bf16 values into the 128-byte-swizzled operand tile.  A key
+// tile is 16 units, dealt out to the seven warps in turn.  (Dequantised once
+// per CTA in registers: a second copy of the cache in bf16 is never made.)
 //
 // Tensor memory: scores of A and B (128 columns each), outputs of A and B (128
 // each).  A tile's weights (bf16 pairs, the A operand of the PV product)
@@ -33,6 +33,7 @@
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its
 // copies and products finish (bounded), frees its tensor memory and returns.
+#include <limits.h>
 #include <math.h>
 #include <stddef.h>
 
@@ -52,16 +53,18 @@ constexpr int kPagesPerTile = kKeys / kPage;
 constexpr int kHalf = 128 * 128;             // 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kKStages = 2, kVStages = 2;
-constexpr int kQWarp = 8, kMmaWarp = 9, kKWarp = 10, kVWarp = 12;
-constexpr int kThreads = 14 * 32;
-constexpr int kProducers = 64;               // threads of a producer pair
+constexpr int kMmaWarp = 8, kProducer0 = 9, kProducers = 7;
+constexpr int kThreads = (kProducer0 + kProducers) * 32;
+constexpr int kUnits = 2 * kPagesPerTile;    // slabs of a key tile
+constexpr int kAhead = 3;                    // units a producer warp reads ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
 constexpr float kRescaleSlack = 8.f;
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
 static_assert(kRows == 128 && kKeys == 128 && kQ4TileTokens == 2 * kTok, "tile shape");
-static_assert(kProducers * 16 == kQ4Codes, "a producer thread per 16 bytes of a page's codes");
+static_assert(2 * 32 * 16 == kQ4Codes, "two pieces of codes per lane");
+static_assert(kKStages == kVStages, "one ring depth");
 
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];  // then each tile's output rows on their way out
@@ -71,7 +74,8 @@ struct __align__(1024) Smem {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], pv_done[2];  // per query tile, phase j for key tile j
-  uint32_t bad[8];   // pages of key tile j whose block id is outside the pool (entry j % 8)
+  uint64_t drained;  // every product issued has completed
+  uint64_t bad[8];   // byte u of entry j % 8: page u of key tile j has a block id outside the pool
   uint32_t tmem;
   int abort;
 };
@@ -94,6 +98,19 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, i
   }
 }
 
+// Whether phase `parity` of `bar` has completed (never waits).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // 64 columns of this thread's lane
 __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
   tmem_ld32_async(taddr, a);
@@ -112,82 +129,97 @@ struct Job {
   const int32_t* table;
 };
 
-// K or V producer thread i (0 .. 63) of a pair: dequantises its place of every
-// page of every key tile.
-__device__ __forceinline__ void produce(Smem& sm, const Job& job, bool is_k, int i, const uint8_t* cache,
-                                        int num_kv_heads, int64_t num_blocks, int n_tiles, int* err) {
+// Producer warp w: units w, w + 7, ... of the job (unit u: key tile u / 16, K
+// pages 0 .. 7, then V pages 0 .. 7).
+__device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const uint8_t* k_cache,
+                                        const uint8_t* v_cache, int num_kv_heads, int64_t num_blocks, int n_tiles,
+                                        int* err) {
   const int lane = threadIdx.x & 31;
-  const int t = i >> 2, g = (i & 3) ^ ((t >> 1) & 3);
+  const int t = lane >> 2, g = (lane & 3) ^ ((t >> 1) & 3);  // tokens t and t + 8 of group g
   const int last_page = (job.keys - 1) / kPage;
-  // block ids four tiles at a time, one group ahead: lane l holds page l % 8
-  // of tile 4 G + l / 8; -1: past the row's keys, -2: outside the pool
-  auto load_group = [&](int G) -> int {
-    const int page = (4 * G + (lane >> 3)) * kPagesPerTile + (lane & 7);
-    if (page > last_page) return -1;
+  const int n_units = n_tiles * kUnits;
+  // block id of the warp's unit n (lane l of a batch: unit 32 B + l), a batch
+  // ahead; -1: past the row's keys, -2: outside the pool
+  auto load_ids = [&](int n0) -> int {
+    const int u = w + kProducers * (n0 + lane);
+    const int page = (u / kUnits) * kPagesPerTile + (u & (kPagesPerTile - 1));
+    if (u >= n_units || page > last_page) return -1;
     const int32_t b = job.table[page];
     if (b < 0 || b >= num_blocks) {
-      if (is_k) record_error(err, PA_ERR_DEVICE_INDEX);
+      record_error(err, PA_ERR_DEVICE_INDEX);
       return -2;
     }
     return b;
   };
-  int grp = load_group(0), grp_next = load_group(1);
-  uint4 code[kPagesPerTile];
-  uint32_t dz[kPagesPerTile];
-  // page u of tile j of the current (or next) group into code[u], dz[u]; a
-  // key past the end, or of a page outside the pool, becomes 0
-  auto fetch = [&](int u, int j, int ids) {
-    const int id = __shfl_sync(0xffffffffu, ids, ((j & 3) << 3) + u);
-    code[u] = make_uint4(0u, 0u, 0u, 0u);
-    dz[u] = 0u;
-    if (id >= 0 && (j * kPagesPerTile + u) * kPage + t < job.keys) {
-      const uint8_t* slab = cache + ((size_t)id * num_kv_heads + job.kvh) * kQ4Slab;
-      code[u] = __ldg(reinterpret_cast<const uint4*>(slab) + i);
-      dz[u] = __ldg(reinterpret_cast<const uint32_t*>(slab + q4_scale_at(t, g)));
+  int ids = load_ids(0), ids_next = load_ids(32);
+  uint4 code[kAhead][2];
+  uint32_t dz[kAhead][2];
+  int id_of[kAhead];
+  // unit n into slot d; a key past the end, or of a page outside the pool, becomes 0
+  auto fetch = [&](int n, int d) {
+    if (n > 0 && (n & 31) == 0) {
+      ids = ids_next;
+      ids_next = load_ids(n + 32);
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, n & 31);
+    id_of[d] = id;
+    code[d][0] = code[d][1] = make_uint4(0u, 0u, 0u, 0u);
+    dz[d][0] = dz[d][1] = 0u;
+    if (id < 0) return;
+    const int u = w + kProducers * n;
+    const int left = job.keys - ((u / kUnits) * kPagesPerTile + (u & (kPagesPerTile - 1))) * kPage;
+    const uint8_t* slab = ((u & kPagesPerTile) ? v_cache : k_cache) + ((size_t)id * num_kv_heads + job.kvh) * kQ4Slab;
+    const uint4* c = reinterpret_cast<const uint4*>(slab) + lane;
+    const uint32_t* z = reinterpret_cast<const uint32_t*>(slab + q4_scale_at(t, g));
+    if (t < left) {
+      code[d][0] = __ldg(c);
+      dz[d][0] = __ldg(z);
+    }
+    if (t + 8 < left) {
+      code[d][1] = __ldg(c + 32);
+      dz[d][1] = __ldg(z + 8 * kQ4Groups);
     }
   };
-#pragma unroll
-  for (int u = 0; u < kPagesPerTile; ++u) fetch(u, 0, grp);
-  uint64_t* full = is_k ? sm.k_full : sm.v_full;
-  uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-  constexpr int n_st = kKStages;
-  static_assert(kKStages == kVStages, "one ring depth");
   // Row t of a page, 16-byte chunk c of its 64-dim half at c ^ (t & 7).  The
   // words of groups 2 and 3 are stored in the order 2, 3, 0, 1, so that the
   // eight lanes of a store phase (2 tokens x 4 groups) meet eight chunks.
   const int swap = g & 2;
-  const uint32_t row = (g >> 1) * kHalf + t * 128;
-  for (int j = 0; j < n_tiles; ++j) {
-    const int s = j % n_st;
-    if (is_k) {
-      const unsigned bad = __ballot_sync(0xffffffffu, grp == -2);
-      if (i == 0) sm.bad[j & 7] = (bad >> ((j & 3) << 3)) & 0xffu;
-    }
-    if (j >= n_st && !__all_sync(0xffffffffu, wait(sm, &empty[s], ((j / n_st) - 1) & 1, err))) return;
-    int ids = grp;
-    if (((j + 1) & 3) == 0) {  // the next tile starts a group
-      ids = grp_next;
-      grp_next = load_group(((j + 1) >> 2) + 1);
-    }
-    const uint32_t dst = smem_addr(is_k ? sm.k[s] : sm.v[s]) + row;
+  uint32_t at[4];
 #pragma unroll
-    for (int u = 0; u < kPagesPerTile; ++u) {
-      const uint4 c = code[u];
-      const uint32_t z = dz[u];
-      if (j + 1 < n_tiles) fetch(u, j + 1, ids);
-      const uint32_t w[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+  for (int x = 0; x < 4; ++x)
+    at[x] = (g >> 1) * kHalf + t * 128 + (((((g & 1) << 2) + (x ^ swap)) ^ (t & 7)) << 4);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint4 val = q4_word_values(w[x], z);
-        const uint32_t at = dst + u * (kPage * 128) + (((((g & 1) << 2) + (x ^ swap)) ^ (t & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(val.x), "r"(val.y), "r"(val.z), "r"(val.w)
-                     : "memory");
+  for (int d = 0; d < kAhead; ++d) fetch(d, d);
+  for (int n0 = 0; w + kProducers * n0 < n_units; n0 += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int n = n0 + d, u = w + kProducers * n;
+      if (u >= n_units) return;
+      const int j = u / kUnits, pg = u & (kPagesPerTile - 1), s = j % kKStages;
+      const bool is_v = u & kPagesPerTile;
+      if (!is_v && lane == 0) reinterpret_cast<volatile uint8_t*>(&sm.bad[j & 7])[pg] = id_of[d] == -2;
+      if (j >= kKStages &&
+          !__all_sync(0xffffffffu, wait(sm, is_v ? &sm.v_empty[s] : &sm.k_empty[s], ((j / kKStages) - 1) & 1, err)))
+        return;
+      const uint32_t dst = smem_addr(is_v ? sm.v[s] : sm.k[s]) + pg * (kPage * 128);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint4 c = code[d][y];
+        const uint32_t z = dz[d][y];
+        const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 val = q4_word_values(word[x], z);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + y * (8 * 128) + at[x]), "r"(val.x),
+                       "r"(val.y), "r"(val.z), "r"(val.w)
+                       : "memory");
+        }
       }
+      fetch(n + kAhead, d);
+      fence_proxy_async_smem();  // the products read the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(is_v ? &sm.v_full[s] : &sm.k_full[s]);
     }
-    grp = ids;
-    fence_proxy_async_smem();  // the products read the tile through the async proxy
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[s]);
   }
 }
 
@@ -218,14 +250,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_tiles = (job.keys + kKeys - 1) / kKeys;
   const int n_x = job.nq > kTok ? 2 : 1;  // query tiles
-  if (warp == kQWarp && lane == 0) {
+  if (warp == kMmaWarp && lane == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int s = 0; s < kKStages; ++s) {
-      mbar_init(&sm.k_full[s], kProducers / 32);
+      mbar_init(&sm.k_full[s], kPagesPerTile);
       mbar_init(&sm.k_empty[s], 1);
     }
     for (int s = 0; s < kVStages; ++s) {
-      mbar_init(&sm.v_full[s], kProducers / 32);
+      mbar_init(&sm.v_full[s], kPagesPerTile);
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -233,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.p_full[x], kRows);
       mbar_init(&sm.pv_done[x], 1);
     }
+    mbar_init(&sm.drained, 1);
     sm.abort = 0;
     fence_mbar_init();
     mbar_arrive_expect_tx(&sm.bar_q, n_x * kTileBytes);
@@ -241,21 +274,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_3d(sm.q[x] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + x * kTok, &sm.bar_q);
     }
   }
-  if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_alloc(&sm.tmem, kTmemCols);
+  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sm.tmem;
 
-  if (warp >= kKWarp) {
-    const bool is_k = warp < kVWarp;
-    produce(sm, job, is_k, (warp - (is_k ? kKWarp : kVWarp)) * 32 + lane,
-            reinterpret_cast<const uint8_t*>(is_k ? p.k_cache : p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles,
-            p.err);
+  if (warp >= kProducer0) {
+    produce(sm, job, warp - kProducer0, reinterpret_cast<const uint8_t*>(p.k_cache),
+            reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles, p.err);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      int last_s[2] = {-1, -1}, last_pv[2] = {-1, -1};
+      // per query tile: its next PV product's key tile, and whether that was
+      // issued (and the next score product waits for it to complete, since the
+      // weights lie where the scores go)
+      int next[2] = {0, 0};
+      bool pv_out[2] = {false, false};
       auto issue_s = [&](int x, int j) {
         const uint32_t qb = smem_addr(sm.q[x]), kb = smem_addr(sm.k[j % kKStages]);
 #pragma unroll
@@ -265,8 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                    ks > 0);
         }
         commit(&sm.s_full[x]);
-        if (x == n_x - 1) commit(&sm.k_empty[j % kKStages]);
-        last_s[x] = j;
       };
       auto issue_pv = [&](int x, int j) {
         const uint32_t pt = tmem + kColS + x * kKeys, vb = smem_addr(sm.v[j % kVStages]);
@@ -275,39 +311,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16_ts(tmem + kColO + x * kHeadDim, pt + 8 * ks, desc_sw128(vb + ks * 2 * 1024, kHalf, 1024), kIdescO,
                       (j > 0 || ks > 0) ? 1u : 0u);
         commit(&sm.pv_done[x]);
-        if (x == n_x - 1) commit(&sm.v_empty[j % kVStages]);
-        last_pv[x] = j;
       };
       bool ok = wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err);
       if (ok) {
         fence_after_sync();
         for (int x = 0; x < n_x; ++x) issue_s(x, 0);
+        commit(&sm.k_empty[0]);
       }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        ok = wait(sm, &sm.v_full[j % kVStages], (j / kVStages) & 1, p.err);
-        for (int x = 0; ok && x < n_x; ++x) {
-          if (!(ok = wait(sm, &sm.p_full[x], j & 1, p.err))) break;
-          fence_after_sync();
-          issue_pv(x, j);
-          if (j + 1 < n_tiles) {
+      // whichever product can go next; a K or V stage is free once the slower
+      // query tile has used it
+      unsigned long long t0 = 0;
+      for (uint32_t idle = 0; ok && (next[0] < n_tiles || (n_x == 2 && next[1] < n_tiles));) {
+        bool did = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int j = next[x], other = n_x == 2 ? next[x ^ 1] : INT_MAX;
+          if (x >= n_x || j >= n_tiles) continue;
+          if (!pv_out[x]) {
+            if (!mbar_test(&sm.v_full[j % kVStages], (j / kVStages) & 1) || !mbar_test(&sm.p_full[x], j & 1)) continue;
+            fence_after_sync();
+            issue_pv(x, j);
+            if (other > j || (other == j && pv_out[x ^ 1])) commit(&sm.v_empty[j % kVStages]);
+            pv_out[x] = true;
+            if (j == n_tiles - 1) next[x] = n_tiles;
+          } else {
             const int j1 = j + 1;
-            ok = (x > 0 || wait(sm, &sm.k_full[j1 % kKStages], (j1 / kKStages) & 1, p.err)) &&
-                 wait(sm, &sm.pv_done[x], j & 1, p.err);  // the weights lie where the scores go
-            if (!ok) break;
+            if (!mbar_test(&sm.pv_done[x], j & 1) || !mbar_test(&sm.k_full[j1 % kKStages], (j1 / kKStages) & 1)) continue;
             fence_after_sync();
             issue_s(x, j1);
+            if (other >= j1) commit(&sm.k_empty[j1 % kKStages]);
+            pv_out[x] = false;
+            next[x] = j1;
+          }
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 63u) == 0) {
+          if (*reinterpret_cast<volatile int*>(&sm.abort)) ok = false;
+          const unsigned long long now = globaltimer();
+          if (idle == 64u) t0 = now;
+          if (now - t0 > kWaitLimitNs) {
+            record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+            *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+            ok = false;
           }
         }
       }
-      // every product issued has completed before the tensor memory is freed
-      for (int x = 0; x < n_x; ++x) {
-        if (last_s[x] >= 0) mbar_wait_bounded(&sm.s_full[x], last_s[x] & 1);
-        if (last_pv[x] >= 0) mbar_wait_bounded(&sm.pv_done[x], last_pv[x] & 1);
-      }
+      // every product issued has completed before the tensor memory is freed,
+      // and Q has landed before the CTA leaves: a commit tracks all of them
+      commit(&sm.drained);
+      mbar_wait_bounded(&sm.drained, 0);
+      mbar_wait_bounded(&sm.bar_q, 0);
     }
     __syncwarp();
-  } else if (warp == kQWarp) {
-    if (lane == 0) mbar_wait_bounded(&sm.bar_q, 0);  // Q has landed before the CTA may leave
   } else if ((warp >> 2) < n_x) {
     // -------------------------------------------------------------- softmax
     const int x = warp >> 2;
@@ -315,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = job.pos0 + x * kTok + (row >> 2);
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lane_base + kColS + x * kKeys, t_o = lane_base + kColO + x * kHeadDim;
-    const float scale = p.scale_log2;
+    const float scale = p.scale_log2;  // not 0 (see the launch)
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
@@ -323,38 +380,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       fence_after_sync();
       const int kbase = j * kKeys;
-      const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm.bad[j & 7]);
-      // keys this row may see: the first `seen` of the tile, less bad pages
-      const int seen = min(pos, job.keys - 1) - kbase + 1;
-      const bool masked = kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u;
-      auto hidden = [&](int key) { return key >= seen || ((bad >> (key >> 4)) & 1u); };
-      // ---- maximum of the scaled scores
+      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&sm.bad[j & 7]);
+      // ---- maximum of the scaled scores.  A tile with hidden keys (after the
+      // row's position, past the end, of a bad page) first gets their scores
+      // replaced by the infinity that scales to -inf, so the weights below need
+      // no mask.
+      if (kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u) {
+        const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the tile before the first hidden one
+        const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          uint32_t a[32];
+          tmem_ld32_async(t_s + 32 * h, a);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          tmem_bind32(a);
+          const uint32_t pages = (uint32_t)(bad >> (16 * h));  // bytes of pages 2 h and 2 h + 1
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * h + i >= seen || (pages & (i < 16 ? 0xffu : 0xff00u))) a[i] = hide;
+          tmem_st32u(t_s + 32 * h, a);
+        }
+      }
       float mt = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t a[32], b[32];
         load64(t_s + 64 * h, a, b);
-        if (masked) {
+        float mx[4];  // independent chains over scores of the sign of the scale
+        if (scale >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            mt = fmaxf(mt, hidden(64 * h + i) ? -INFINITY : __uint_as_float(a[i]) * scale);
-            mt = fmaxf(mt, hidden(64 * h + 32 + i) ? -INFINITY : __uint_as_float(b[i]) * scale);
-          }
+          for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+          mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
         } else {
-          float mx[4];  // independent chains over scores of the sign of the scale
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = scale >= 0.f ? -INFINITY : INFINITY;
-          if (scale >= 0.f) {
+          for (int i = 0; i < 4; ++i) mx[i] = INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
-            mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              mx[i & 3] = fminf(mx[i & 3], fminf(__uint_as_float(a[i]), __uint_as_float(b[i])));
-            mt = fmaxf(mt, fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale);
-          }
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fminf(mx[i & 3], fminf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+          mt = fmaxf(mt, fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale);
         }
       }
       const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
@@ -388,11 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t lo = i < 16 ? a[2 * (i & 15)] : b[2 * (i & 15)];
           const uint32_t hi = i < 16 ? a[2 * (i & 15) + 1] : b[2 * (i & 15) + 1];
           const float2 d = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), sc2, nm2);
-          float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-          if (masked) {
-            if (hidden(64 * h + 2 * i)) e.x = 0.f;
-            if (hidden(64 * h + 2 * i + 1)) e.y = 0.f;
-          }
+          const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
           ls[i & 1] = __fadd2_rn(ls[i & 1], e);
           w[i] = pack_bf16x2(e.x, e.y);
         }
@@ -425,7 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
             l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + x), "n"(kRows) : "memory");
+    if (x == 0)
+      asm volatile("bar.sync 1, %0;" ::"n"(kRows) : "memory");
+    else
+      asm volatile("bar.sync 2, %0;" ::"n"(kRows) : "memory");
     if (!*reinterpret_cast<volatile int*>(&sm.abort)) {
 #pragma unroll 4
       for (int i = 0; i < kRows * 16 / kRows; ++i) {  // 16 threads write one 256-byte row
@@ -454,8 +517,12 @@ cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items,
   if (items.count <= 0) return cudaSuccess;
   const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel, (int)kSmemBytes, g_attr_set);
   if (e != cudaSuccess) return e;
+  // a zero scale (every score 0) as 2^-100, so that a hidden score scales to
+  // -inf: scores of finite inputs stay below 2^-60 and weigh 1 as before
+  PrefillParams pp = p;
+  if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
   return launch_pdl(prefill_q4_kernel, dim3((unsigned)(items.count * p.num_kv_heads)), dim3(kThreads), kSmemBytes,
-                    stream, p, items, q_map);
+                    stream, pp, items, q_map);
 }
 
 }  // namespace pa
