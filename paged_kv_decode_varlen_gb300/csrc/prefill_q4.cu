@@ -111,6 +111,17 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // 64 columns of this thread's lane
 __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
   tmem_ld32_async(taddr, a);
@@ -288,82 +299,93 @@ __global__ void __launch_bounds__(kThreads, 1)
             reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles, p.err);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      // per query tile: its next PV product's key tile, and whether that was
-      // issued (and the next score product waits for it to complete, since the
-      // weights lie where the scores go)
-      int next[2] = {0, 0};
-      bool pv_out[2] = {false, false};
-      auto issue_s = [&](int x, int j) {
-        const uint32_t qb = smem_addr(sm.q[x]), kb = smem_addr(sm.k[j % kKStages]);
+    // The whole warp runs this loop (so that descriptors and addresses are
+    // warp-uniform values) and one elected lane issues.  Per query tile: its
+    // next PV product's key tile, and whether that was issued (and the next
+    // score product waits for it to complete, since the weights lie where the
+    // scores go).
+    int next[2] = {0, 0};
+    bool pv_out[2] = {false, false};
+    const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024);
+    const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)phase & 1u)); };
+    auto issue_s = [&](int x, int j, bool frees) {
+      const uint64_t qd = q_desc + (uint32_t)x * (kTileBytes >> 4), kd = k_desc + (uint32_t)(j % kKStages) * (kTileBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;  // 64-dim half, 16-dim step in it
-          mma_bf16(tmem + kColS + x * kKeys, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), kIdescS,
-                   ks > 0);
+          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
+          mma_bf16(tm + kColS + x * kKeys, qd + off, kd + off, kIdescS, ks > 0);
         }
         commit(&sm.s_full[x]);
-      };
-      auto issue_pv = [&](int x, int j) {
-        const uint32_t pt = tmem + kColS + x * kKeys, vb = smem_addr(sm.v[j % kVStages]);
+        if (frees) commit(&sm.k_empty[j % kKStages]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int x, int j, bool frees) {
+      const uint64_t vd = v_desc + (uint32_t)(j % kVStages) * (kTileBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_bf16_ts(tmem + kColO + x * kHeadDim, pt + 8 * ks, desc_sw128(vb + ks * 2 * 1024, kHalf, 1024), kIdescO,
+        for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
+          mma_bf16_ts(tm + kColO + x * kHeadDim, tm + kColS + x * kKeys + 8 * ks, vd + ks * (2 * 1024 >> 4), kIdescO,
                       (j > 0 || ks > 0) ? 1u : 0u);
         commit(&sm.pv_done[x]);
-      };
-      bool ok = wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err);
-      if (ok) {
-        fence_after_sync();
-        for (int x = 0; x < n_x; ++x) issue_s(x, 0);
-        commit(&sm.k_empty[0]);
+        if (frees) commit(&sm.v_empty[j % kVStages]);
       }
-      // whichever product can go next; a K or V stage is free once the slower
-      // query tile has used it
-      unsigned long long t0 = 0;
-      for (uint32_t idle = 0; ok && (next[0] < n_tiles || (n_x == 2 && next[1] < n_tiles));) {
-        bool did = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = next[x], other = n_x == 2 ? next[x ^ 1] : INT_MAX;
-          if (x >= n_x || j >= n_tiles) continue;
-          if (!pv_out[x]) {
-            if (!mbar_test(&sm.v_full[j % kVStages], (j / kVStages) & 1) || !mbar_test(&sm.p_full[x], j & 1)) continue;
-            fence_after_sync();
-            issue_pv(x, j);
-            if (other > j || (other == j && pv_out[x ^ 1])) commit(&sm.v_empty[j % kVStages]);
-            pv_out[x] = true;
-            if (j == n_tiles - 1) next[x] = n_tiles;
-          } else {
-            const int j1 = j + 1;
-            if (!mbar_test(&sm.pv_done[x], j & 1) || !mbar_test(&sm.k_full[j1 % kKStages], (j1 / kKStages) & 1)) continue;
-            fence_after_sync();
-            issue_s(x, j1);
-            if (other >= j1) commit(&sm.k_empty[j1 % kKStages]);
-            pv_out[x] = false;
-            next[x] = j1;
-          }
-          did = true;
-        }
-        if (did) {
-          idle = 0;
-        } else if ((++idle & 63u) == 0) {
-          if (*reinterpret_cast<volatile int*>(&sm.abort)) ok = false;
-          const unsigned long long now = globaltimer();
-          if (idle == 64u) t0 = now;
-          if (now - t0 > kWaitLimitNs) {
-            record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-            *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-            ok = false;
-          }
-        }
-      }
-      // every product issued has completed before the tensor memory is freed,
-      // and Q has landed before the CTA leaves: a commit tracks all of them
-      commit(&sm.drained);
-      mbar_wait_bounded(&sm.drained, 0);
-      mbar_wait_bounded(&sm.bar_q, 0);
+      __syncwarp();
+    };
+    bool ok = __all_sync(0xffffffffu, wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err));
+    if (ok) {
+      fence_after_sync();
+      for (int x = 0; x < n_x; ++x) issue_s(x, 0, x == n_x - 1);
     }
+    // whichever product can go next; a K or V stage is free once the slower
+    // query tile has used it
+    unsigned long long t0 = 0;
+    for (uint32_t idle = 0; ok && (next[0] < n_tiles || (n_x == 2 && next[1] < n_tiles));) {
+      bool did = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = next[x], other = n_x == 2 ? next[x ^ 1] : INT_MAX;
+        if (x >= n_x || j >= n_tiles) continue;
+        if (!pv_out[x]) {
+          if (!ready(&sm.p_full[x], j) || !ready(&sm.v_full[j % kVStages], j / kVStages)) continue;
+          fence_after_sync();
+          issue_pv(x, j, other > j || (other == j && pv_out[x ^ 1]));
+          pv_out[x] = true;
+          if (j == n_tiles - 1) next[x] = n_tiles;
+        } else {
+          const int j1 = j + 1;
+          if (!ready(&sm.pv_done[x], j) || !ready(&sm.k_full[j1 % kKStages], j1 / kKStages)) continue;
+          fence_after_sync();
+          issue_s(x, j1, other >= j1);
+          pv_out[x] = false;
+          next[x] = j1;
+        }
+        did = true;
+      }
+      if (did) {
+        idle = 0;
+      } else if ((++idle & 63u) == 0) {
+        const unsigned long long now = globaltimer();
+        if (idle == 64u) t0 = now;
+        int stop = *reinterpret_cast<volatile int*>(&sm.abort);
+        if (now - t0 > kWaitLimitNs) {
+          record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+          *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+          stop = 1;
+        }
+        ok = __all_sync(0xffffffffu, !stop);
+      }
+    }
+    // every product issued has completed before the tensor memory is freed,
+    // and Q has landed before the CTA leaves: a commit tracks all of them
+    if (elect_one()) commit(&sm.drained);
+    __syncwarp();
+    mbar_wait_bounded(&sm.drained, 0);
+    mbar_wait_bounded(&sm.bar_q, 0);
     __syncwarp();
   } else if ((warp >> 2) < n_x) {
     // -------------------------------------------------------------- softmax
