@@ -111,15 +111,49 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// True in one lane of the (converged) warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
+// 1 in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t one;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(one));
-  return one != 0;
+  return one;
+}
+
+// tc::mma_bf16, tc::mma_bf16_ts and tc::commit by the lanes with `on` set,
+// without a branch: run by a whole warp whose control flow is warp-uniform, the
+// descriptors stay uniform registers and a product is one instruction (in a
+// branch of one lane they cost six, and with the schedulers busy a group of
+// eight took 890 cycles to issue against 514 to run).
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(on)
+      : "memory");
 }
 
 // 64 columns of this thread's lane
@@ -241,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Job job;
   {
     const int it = blockIdx.x / p.num_kv_heads;
@@ -313,28 +347,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)phase & 1u)); };
     auto issue_s = [&](int x, int j, bool frees) {
       const uint64_t qd = q_desc + (uint32_t)x * (kTileBytes >> 4), kd = k_desc + (uint32_t)(j % kKStages) * (kTileBytes >> 4);
-      if (elect_one()) {
+      const uint32_t on = elect_one();
 #pragma unroll
-        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
-          mma_bf16(tm + kColS + x * kKeys, qd + off, kd + off, kIdescS, ks > 0);
-        }
-        commit(&sm.s_full[x]);
-        if (frees) commit(&sm.k_empty[j % kKStages]);
+      for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
+        mma_ss_if(on, tm + kColS + x * kKeys, qd + off, kd + off, kIdescS, ks > 0);
       }
-      __syncwarp();
+      commit_if(on, &sm.s_full[x]);
+      if (frees) commit_if(on, &sm.k_empty[j % kKStages]);
     };
     auto issue_pv = [&](int x, int j, bool frees) {
       const uint64_t vd = v_desc + (uint32_t)(j % kVStages) * (kTileBytes >> 4);
-      if (elect_one()) {
+      const uint32_t on = elect_one();
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
-          mma_bf16_ts(tm + kColO + x * kHeadDim, tm + kColS + x * kKeys + 8 * ks, vd + ks * (2 * 1024 >> 4), kIdescO,
-                      (j > 0 || ks > 0) ? 1u : 0u);
-        commit(&sm.pv_done[x]);
-        if (frees) commit(&sm.v_empty[j % kVStages]);
-      }
-      __syncwarp();
+      for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
+        mma_ts_if(on, tm + kColO + x * kHeadDim, tm + kColS + x * kKeys + 8 * ks, vd + ks * (2 * 1024 >> 4), kIdescO,
+                  (j > 0 || ks > 0) ? 1u : 0u);
+      commit_if(on, &sm.pv_done[x]);
+      if (frees) commit_if(on, &sm.v_empty[j % kVStages]);
     };
     bool ok = __all_sync(0xffffffffu, wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err));
     if (ok) {
@@ -382,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every product issued has completed before the tensor memory is freed,
     // and Q has landed before the CTA leaves: a commit tracks all of them
-    if (elect_one()) commit(&sm.drained);
-    __syncwarp();
+    commit_if(elect_one(), &sm.drained);
     mbar_wait_bounded(&sm.drained, 0);
     mbar_wait_bounded(&sm.bar_q, 0);
     __syncwarp();
