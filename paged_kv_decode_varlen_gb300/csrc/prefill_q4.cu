@@ -26,8 +26,9 @@
 // Tensor memory: scores of A and B (128 columns each), outputs of A and B (128
 // each).  A tile's weights (bf16 pairs, the A operand of the PV product)
 // overwrite its scores, so its next score product is issued only after its PV
-// product has completed.  The softmax therefore reads its scores twice, 64
-// columns at a time: for the maximum, then for the weights.  Weights are
+// product has completed.  The softmax takes the scores once, 32 columns at a
+// time, against a running maximum that is re-based only when it grows by more
+// than 2^8.  Weights are
 // rounded to bf16, as the tensor cores take them; their sum is kept in
 // binary32 from the unrounded ones, as are scores, maxima and outputs.
 //
@@ -98,19 +99,6 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, i
   }
 }
 
-// Whether phase `parity` of `bar` has completed (never waits).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // 1 in one lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t one;
@@ -156,13 +144,54 @@ __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
       : "memory");
 }
 
-// 64 columns of this thread's lane
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
-  tmem_ld32_async(taddr, a);
-  tmem_ld32_async(taddr + 32, b);
+// Waits for this thread's tensor-memory loads; `r` is bound to the wait.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  tmem_bind32(a);
-  tmem_bind32(b);
+  tmem_bind32(r);
+}
+// 16 columns of this thread's lane, without a wait (wait_st) / with its wait
+__device__ __forceinline__ void store16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A row's maximum grew (rare): scales its output columns, and the weights of
+// the tile's first `quarters` quarters already stored, by corr.  Whole warp;
+// out of line to keep its registers off the softmax loop.
+__device__ __noinline__ void rescale(uint32_t t_o, uint32_t t_p, int quarters, bool has_o, float corr) {
+  wait_st();
+  if (has_o) {
+#pragma unroll 1
+    for (int c = 0; c < kHeadDim; c += 16) {
+      uint32_t o[16];
+      load16(t_o + c, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+      store16(t_o + c, o);
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < 16 * quarters; c += 16) {
+    uint32_t w[16];
+    load16(t_p + c, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(bf16lo(w[i]) * corr, bf16hi(w[i]) * corr);
+    store16(t_p + c, w);
+  }
+  wait_st();
 }
 
 struct Job {
@@ -334,17 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     // The whole warp runs this loop (so that descriptors and addresses are
-    // warp-uniform values) and one elected lane issues.  Per query tile: its
-    // next PV product's key tile, and whether that was issued (and the next
-    // score product waits for it to complete, since the weights lie where the
-    // scores go).
-    int next[2] = {0, 0};
-    bool pv_out[2] = {false, false};
+    // warp-uniform values) and one elected lane issues.
     const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024);
     const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
     const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)phase & 1u)); };
     auto issue_s = [&](int x, int j, bool frees) {
       const uint64_t qd = q_desc + (uint32_t)x * (kTileBytes >> 4), kd = k_desc + (uint32_t)(j % kKStages) * (kTileBytes >> 4);
       const uint32_t on = elect_one();
@@ -371,43 +394,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       for (int x = 0; x < n_x; ++x) issue_s(x, 0, x == n_x - 1);
     }
-    // whichever product can go next; a K or V stage is free once the slower
-    // query tile has used it
-    unsigned long long t0 = 0;
-    for (uint32_t idle = 0; ok && (next[0] < n_tiles || (n_x == 2 && next[1] < n_tiles));) {
-      bool did = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = next[x], other = n_x == 2 ? next[x ^ 1] : INT_MAX;
-        if (x >= n_x || j >= n_tiles) continue;
-        if (!pv_out[x]) {
-          if (!ready(&sm.p_full[x], j) || !ready(&sm.v_full[j % kVStages], j / kVStages)) continue;
-          fence_after_sync();
-          issue_pv(x, j, other > j || (other == j && pv_out[x ^ 1]));
-          pv_out[x] = true;
-          if (j == n_tiles - 1) next[x] = n_tiles;
-        } else {
-          const int j1 = j + 1;
-          if (!ready(&sm.pv_done[x], j) || !ready(&sm.k_full[j1 % kKStages], j1 / kKStages)) continue;
-          fence_after_sync();
-          issue_s(x, j1, other >= j1);
-          pv_out[x] = false;
-          next[x] = j1;
-        }
-        did = true;
-      }
-      if (did) {
-        idle = 0;
-      } else if ((++idle & 63u) == 0) {
-        const unsigned long long now = globaltimer();
-        if (idle == 64u) t0 = now;
-        int stop = *reinterpret_cast<volatile int*>(&sm.abort);
-        if (now - t0 > kWaitLimitNs) {
-          record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-          *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-          stop = 1;
-        }
-        ok = __all_sync(0xffffffffu, !stop);
+    // PV of tile A, then its next scores, then the same for B: A's softmax
+    // runs while B's products do.  (Taking whichever product was ready let the
+    // two tiles fall into step: both softmaxes, then all four products.)
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      for (int x = 0; ok && x < n_x; ++x) {
+        const bool last = x == n_x - 1;
+        ok = __all_sync(0xffffffffu, wait(sm, &sm.p_full[x], j & 1, p.err) &&
+                                         (x > 0 || wait(sm, &sm.v_full[j % kVStages], (j / kVStages) & 1, p.err)));
+        if (!ok) break;
+        fence_after_sync();
+        issue_pv(x, j, last);
+        if (j + 1 == n_tiles) continue;
+        const int j1 = j + 1;
+        // the weights lie where the scores go: PV first
+        ok = __all_sync(0xffffffffu, (x > 0 || wait(sm, &sm.k_full[j1 % kKStages], (j1 / kKStages) & 1, p.err)) &&
+                                         wait(sm, &sm.pv_done[x], j & 1, p.err));
+        if (!ok) break;
+        fence_after_sync();
+        issue_s(x, j1, last);
       }
     }
     // every product issued has completed before the tensor memory is freed,
@@ -432,84 +437,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       const int kbase = j * kKeys;
       const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&sm.bad[j & 7]);
-      // ---- maximum of the scaled scores.  A tile with hidden keys (after the
-      // row's position, past the end, of a bad page) first gets their scores
-      // replaced by the infinity that scales to -inf, so the weights below need
-      // no mask.
-      if (kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u) {
-        const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the tile before the first hidden one
-        const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          uint32_t a[32];
-          tmem_ld32_async(t_s + 32 * h, a);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          tmem_bind32(a);
+      // hidden keys: after the row's position, past the end, of a bad page
+      const bool masked = kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u;
+      const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the tile before the first hidden one
+      const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
+      // One pass over the scores in quarters of 32 keys, the next quarter's
+      // load in flight: its maximum, then its weights, against the running
+      // maximum; when that has to be re-based (rare after the first tile) the
+      // output and the weights stored so far are rescaled.
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t buf[2][32];
+      tmem_ld32_async(t_s, buf[0]);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t(&c)[32] = buf[h & 1];
+        wait_ld(c);
+        if (h < 3) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
+        if (masked) {
           const uint32_t pages = (uint32_t)(bad >> (16 * h));  // bytes of pages 2 h and 2 h + 1
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * h + i >= seen || (pages & (i < 16 ? 0xffu : 0xff00u))) a[i] = hide;
-          tmem_st32u(t_s + 32 * h, a);
+            if (32 * h + i >= seen || (pages & (i < 16 ? 0xffu : 0xff00u))) c[i] = hide;
         }
-      }
-      float mt = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[32], b[32];
-        load64(t_s + 64 * h, a, b);
-        float mx[4];  // independent chains over scores of the sign of the scale
+        float mx[4];  // independent chains, over scores of the sign of the scale
+        float mt;
         if (scale >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(c[i]), __uint_as_float(c[i + 4]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
-          mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
+          for (int i = 8; i < 32; i += 2)
+            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(c[i]), __uint_as_float(c[i + 1])));
+          mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = INFINITY;
+          for (int i = 0; i < 4; ++i) mx[i] = fminf(__uint_as_float(c[i]), __uint_as_float(c[i + 4]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fminf(mx[i & 3], fminf(__uint_as_float(a[i]), __uint_as_float(b[i])));
-          mt = fmaxf(mt, fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale);
+          for (int i = 8; i < 32; i += 2)
+            mx[(i >> 1) & 3] = fminf(mx[(i >> 1) & 3], fminf(__uint_as_float(c[i]), __uint_as_float(c[i + 1])));
+          mt = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale;
         }
-      }
-      const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
-      float corr = 1.f;
-      if (grow) {
-        corr = fast_exp2(m_run - mt);  // m_run = -inf -> 0
-        l_run *= corr;
-        m_run = mt;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, grow)) {
-        // O is stable: this tile's scores were issued after PV of tile j - 1
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tmem_ld32(t_o + 32 * c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= corr;
-          tmem_st32(t_o + 32 * c, o);
+        const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
+        if (__any_sync(0xffffffffu, grow)) {
+          if (h < 3) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
+          const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
+          if (grow) m_run = mt;
+          l_run *= corr;
+          const float2 c2 = make_float2(corr, corr);
+          ls[0] = __fmul2_rn(ls[0], c2);
+          ls[1] = __fmul2_rn(ls[1], c2);
+          // O is stable: this tile's scores were issued after PV of tile j - 1
+          rescale(t_o, t_s, h, j > 0, corr);
         }
-      }
-      // ---- weights, over the scores they come from
-      const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
-      const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+        uint32_t w[16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[32], b[32], w[32];
-        load64(t_s + 64 * h, a, b);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t lo = i < 16 ? a[2 * (i & 15)] : b[2 * (i & 15)];
-          const uint32_t hi = i < 16 ? a[2 * (i & 15) + 1] : b[2 * (i & 15) + 1];
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), sc2, nm2);
+        for (int i = 0; i < 16; ++i) {
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1])), sc2, nm2);
           const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
           ls[i & 1] = __fadd2_rn(ls[i & 1], e);
           w[i] = pack_bf16x2(e.x, e.y);
         }
-        tmem_st32u(t_s + 32 * h, w);
+        store16(t_s + 16 * h, w);  // weights over scores already read
       }
       l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+      wait_st();
       fence_before_sync();  // the tensor-memory accesses above precede the arrive
       mbar_arrive(&sm.p_full[x]);
     }
