@@ -221,24 +221,57 @@ def new_q4_pool(num_blocks, num_kv_heads, device):
     return torch.zeros((num_blocks, num_kv_heads, PA_Q4_SLAB_BYTES), dtype=torch.uint8, device=device)
 
 
+# The q4 calls are short (a few microseconds on the device for a small batch),
+# so their marshalling is kept lean: plain integers for pointers and one check
+# per tensor.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch.cuda.current_device
+
+
+def _stream_handle(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _data(t, dtype, name, device):
+    """Address of a contiguous tensor of dtype on CUDA device `device`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    return t.data_ptr()
+
+
+def _host_data(t, n, name):
+    """(int32 host tensor of n elements, its address) from a tensor or a
+    sequence; no copy when t is one already."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and not t.is_cuda and t.is_contiguous()):
+        t = _host_i32(t)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have {n} elements")
+    return t, t.data_ptr()
+
+
 def pa_kv_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, workspace=None, stream=None):
     """Quantize k_new / v_new [N, Hkv, D] bf16 into q4 pools (uint8
     [num_blocks, Hkv, PA_Q4_SLAB_BYTES]) at slot_mapping (int64 [N], negative
     = skip)."""
-    _need(k_new, torch.bfloat16, "k_new")
-    _need(v_new, torch.bfloat16, "v_new")
-    _need(k_cache, torch.uint8, "k_cache")
-    _need(v_cache, torch.uint8, "v_cache")
-    _need(slot_mapping, torch.int64, "slot_mapping")
     N, Hkv, D = k_new.shape
-    nb = k_cache.shape[0]
-    if v_new.shape != k_new.shape or v_cache.shape != k_cache.shape or k_cache.shape[1:] != (Hkv, PA_Q4_SLAB_BYTES) \
+    nb, Hkv2, slab = k_cache.shape
+    if v_new.shape != k_new.shape or v_cache.shape != k_cache.shape or Hkv2 != Hkv or slab != PA_Q4_SLAB_BYTES \
             or slot_mapping.shape != (N,):
         raise ValueError("inconsistent shapes")
+    dev = _current_device()
     if workspace is None:
         workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
-    _check(_lib.pa_kv_append_q4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_cache), _ptr(v_cache), nb,
-                                16, Hkv, D, _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check(_lib.pa_kv_append_q4(_data(k_new, torch.bfloat16, "k_new", dev), _data(v_new, torch.bfloat16, "v_new", dev),
+                                _data(slot_mapping, torch.int64, "slot_mapping", dev), N,
+                                _data(k_cache, torch.uint8, "k_cache", dev), _data(v_cache, torch.uint8, "v_cache", dev),
+                                nb, 16, Hkv, D, _data(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                                _stream_handle(stream, dev)))
     return workspace
 
 
@@ -246,25 +279,25 @@ def pa_kv_read_q4(slot_mapping, k_cache, v_cache, k_out=None, v_out=None, worksp
     """Rows of q4 pools (uint8 [num_blocks, Hkv, PA_Q4_SLAB_BYTES]) at
     slot_mapping (int64 [N]; negative = a row of zeros) as bf16 [N, Hkv, D]:
     the values pa_attention_varlen_q4 computes with.  Returns (k_out, v_out)."""
-    _need(slot_mapping, torch.int64, "slot_mapping")
-    _need(k_cache, torch.uint8, "k_cache")
-    _need(v_cache, torch.uint8, "v_cache")
     nb, Hkv, slab = k_cache.shape
     if v_cache.shape != k_cache.shape or slab != PA_Q4_SLAB_BYTES or slot_mapping.dim() != 1:
         raise ValueError("inconsistent shapes")
-    shape = (slot_mapping.shape[0], Hkv, 128)
+    N = slot_mapping.shape[0]
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        k_out = torch.empty((N, Hkv, 128), dtype=torch.bfloat16, device=k_cache.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
-    _need(k_out, torch.bfloat16, "k_out")
-    _need(v_out, torch.bfloat16, "v_out")
-    if k_out.shape != shape or v_out.shape != shape:
+        v_out = torch.empty((N, Hkv, 128), dtype=torch.bfloat16, device=k_cache.device)
+    if k_out.shape != (N, Hkv, 128) or v_out.shape != (N, Hkv, 128):
         raise ValueError("k_out and v_out must be [N, Hkv, 128]")
+    dev = _current_device()
     if workspace is None:
         workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
-    _check(_lib.pa_kv_read_q4(_ptr(slot_mapping), shape[0], _ptr(k_cache), _ptr(v_cache), nb, 16, Hkv, 128,
-                              _ptr(k_out), _ptr(v_out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check(_lib.pa_kv_read_q4(_data(slot_mapping, torch.int64, "slot_mapping", dev), N,
+                              _data(k_cache, torch.uint8, "k_cache", dev), _data(v_cache, torch.uint8, "v_cache", dev),
+                              nb, 16, Hkv, 128, _data(k_out, torch.bfloat16, "k_out", dev),
+                              _data(v_out, torch.bfloat16, "v_out", dev),
+                              _data(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                              _stream_handle(stream, dev)))
     return k_out, v_out
 
 
@@ -272,42 +305,36 @@ def pa_attention_varlen_q4(q, k_cache, v_cache, block_tables, seq_lens, qo_indpt
                            qo_indptr_host=None, out=None, lse=None, workspace=None, stream=None, return_lse=False):
     """pa_attention_varlen over q4 pools (decode, chunked-prefill and verify
     rows)."""
-    _need(q, torch.bfloat16, "q")
-    _need(k_cache, torch.uint8, "k_cache")
-    _need(v_cache, torch.uint8, "v_cache")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(seq_lens, torch.int32, "seq_lens")
-    _need(qo_indptr, torch.int32, "qo_indptr")
     total_q, Hq, D = q.shape
     nb, Hkv, slab = k_cache.shape
     R = seq_lens.shape[0]
     if v_cache.shape != k_cache.shape or slab != PA_Q4_SLAB_BYTES or qo_indptr.shape != (R + 1,) \
             or block_tables.dim() != 2 or block_tables.shape[0] != R:
         raise ValueError("inconsistent shapes")
-    slh = _host_i32(seq_lens if seq_lens_host is None else seq_lens_host)
-    qih = _host_i32(qo_indptr if qo_indptr_host is None else qo_indptr_host)
-    if slh.shape != (R,) or qih.shape != (R + 1,):
-        raise ValueError("host copies must have the shapes of seq_lens and qo_indptr")
+    slh, slh_at = _host_data(seq_lens if seq_lens_host is None else seq_lens_host, R, "seq_lens_host")
+    qih, qih_at = _host_data(qo_indptr if qo_indptr_host is None else qo_indptr_host, R + 1, "qo_indptr_host")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out")
-    if out.shape != q.shape:
+    elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if lse is None and return_lse:
         lse = torch.empty((total_q, Hq), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if lse.shape != (total_q, Hq):
-            raise ValueError("lse must be [total_q, Hq]")
+    elif lse is not None and lse.shape != (total_q, Hq):
+        raise ValueError("lse must be [total_q, Hq]")
+    dev = _current_device()
     if workspace is None:
         max_len = int(slh.max()) if R else 1
         workspace = new_workspace(pa_attention_workspace_size(R, total_q, Hq, D, max_len), q.device)
-    _check(_lib.pa_attention_varlen_q4(_ptr(q), _ptr(k_cache), _ptr(v_cache), nb, _ptr(block_tables),
-                                       block_tables.shape[1], _ptr(seq_lens), _ptr(qo_indptr),
-                                       ctypes.c_void_p(slh.data_ptr()), ctypes.c_void_p(qih.data_ptr()), R, total_q,
-                                       Hq, Hkv, D, 16, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)))
-    return (out, lse) if (return_lse or lse is not None) else out
+    _check(_lib.pa_attention_varlen_q4(_data(q, torch.bfloat16, "q", dev), _data(k_cache, torch.uint8, "k_cache", dev),
+                                       _data(v_cache, torch.uint8, "v_cache", dev), nb,
+                                       _data(block_tables, torch.int32, "block_tables", dev), block_tables.shape[1],
+                                       _data(seq_lens, torch.int32, "seq_lens", dev),
+                                       _data(qo_indptr, torch.int32, "qo_indptr", dev), slh_at, qih_at, R, total_q, Hq,
+                                       Hkv, D, 16, float(sm_scale), _data(out, torch.bfloat16, "out", dev),
+                                       None if lse is None else _data(lse, torch.float32, "lse", dev),
+                                       _data(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                                       _stream_handle(stream, dev)))
+    return (out, lse) if lse is not None else out
 
 
 def pa_copy_blocks(src_blocks, dst_blocks, k_cache, v_cache, workspace=None, stream=None):

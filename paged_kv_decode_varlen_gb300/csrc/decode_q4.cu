@@ -1,32 +1,33 @@
-// Flash-decode over 4-bit pages (rows with one query token).
+// Flash-decode over 4-bit pages: rows with one query token, and rows with a
+// few (verify rows).
 //
-// What is computed: for a decode row and each of the 4 query heads of a kv
-// head, s_t = sm_scale <q, K_t> over the row's keys, out = sum_t p_t V_t /
-// sum_t p_t with p_t = 2^(s_t log2 e - m), K_t and V_t the bf16 values of the
-// page's codes (q4.cuh).
+// What is computed: query j of a row with n queries and L keys attends to keys
+// 0 .. L - n + j; for each of the 4 query heads of a kv head, s_t = sm_scale
+// <q, K_t>, out = sum_t p_t V_t / sum_t p_t with p_t = 2^(s_t log2 e - m), K_t
+// and V_t the bf16 values of the page's codes (q4.cuh).
 //
 // Work.  As in the bf16 decode kernel the rows' pages are laid end to end for
-// each kv head and cut into equal segments, one CTA of 16 warps per SM and
-// segment; each warp streams its sixteenth of the segment through a ring of
-// its own (two 1280-byte bulk copies per page), so warps never wait for one
-// another.  A row cut between warps is put together in shared memory by the
-// last of them to finish, a row cut between CTAs in the workspace by the last
-// CTA.
+// each kv head and cut into equal segments, one CTA per SM and segment; each
+// warp streams its share of the segment through a ring of its own (1280-byte
+// bulk copies, two pages at a time), so warps never wait for one another.  A
+// row cut between warps is put together in shared memory by the last of them
+// to finish, a row cut between CTAs in the workspace by the last CTA; parts are
+// always added in page order, so results do not depend on who came last.
 //
-// Arithmetic.  A page is 16 tokens, the M of one mma.m16n8k16, and the four
-// heads fill half of its N: 8 products give the page's scores, 8 the page's
-// part of the output, and the 4 KiB of values exist only as the products' A
-// operands, in registers.  (The 5th-generation tensor cores take their
-// operands from shared or tensor memory, so the values would have to be
-// written out and read again, and M = 128 keys would need 8 pages per product;
-// the products here are 7 % of the issue slots.)  Codes arrive in operand
-// order through 8 x 8 matrix loads: K straight (a lane gets 8 dims of a
-// token), V transposed (a lane gets 4 dims of two tokens), so that one shift,
-// one insert and one packed FMA turn each pair of codes into an operand half.
-//   Columns 2 h and 2 h + 1 of the second product carry the weight of head h
-// as two bf16, its leading 8 bits and the rest, which the idle half of N takes
-// for nothing: the weights keep 16 bits, scores, sums and output stay in
-// binary32.
+// Arithmetic.  A page is 16 tokens, the M of one mma.m16n8k16, and four heads
+// of two queries are its N: 8 products give a page's scores for 8 (query, head)
+// columns, 8 its part of the output, and the 4 KiB of values exist only as the
+// products' A operands, in registers, whatever the number of queries.  (The
+// 5th-generation tensor cores take their operands from shared or tensor memory,
+// so the values would have to be written out and read again, and M = 128 keys
+// would need 8 pages per product.)  Codes arrive in operand order through 8 x 8
+// matrix loads: K straight (a lane gets 8 dims of a token), V transposed (a
+// lane gets 4 dims of two tokens), so that one shift, one insert and one packed
+// FMA turn each pair of codes into an operand half.
+//   With one query the columns of the second product come in pairs: the weight
+// of a head as two bf16, its leading 8 bits and the rest, so that the idle half
+// of N keeps 16 bits of every weight.  With several queries the weights are
+// rounded to bf16.  Scores, sums and outputs stay in binary32.
 #include <math.h>
 #include <stddef.h>
 
@@ -36,16 +37,8 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = kQ4Warps;
-constexpr int kThreads = kWarps * 32;
-#ifndef Q4_PAIR
-#define Q4_PAIR 2
-#endif
-#ifndef Q4_STAGES
-#define Q4_STAGES 2
-#endif
-constexpr int kPair = Q4_PAIR;  // pages per stage
-constexpr int kStages = Q4_STAGES;  // stages in flight per warp
+constexpr int kPair = 2;     // pages per stage
+constexpr int kStages = 2;   // stages in flight per warp
 constexpr float kRescaleSlack = 8.f;  // the running max is re-based when it grows by more than 2^8
 
 struct Item {        // one row's pages within this CTA's segment
@@ -54,28 +47,49 @@ struct Item {        // one row's pages within this CTA's segment
   int32_t p0;       // row page index of the item's first page
   int32_t r;        // request
   int32_t L;        // its seq_len
-  int32_t tok;      // its query token
+  int32_t tok;      // its first query token
+  int32_t nq;       // its query tokens
   int32_t A;        // stream position of the row's page 0
 };
 
+// kTiles: 8-column tiles (two queries of 4 heads each); 0: one query, weights
+// as two bf16.
+template <int kTiles>
+struct Shape {
+  static constexpr bool kOne = kTiles == 0;
+  static constexpr int kT = kOne ? 1 : kTiles;
+  static constexpr int kCols = kOne ? 1 : 2;       // (query, head) columns per lane and tile
+  static constexpr int kVec = kCols * 4;           // float4 of output values per lane and tile
+  static constexpr int kTileCols = kOne ? 4 : 8;   // columns of a tile
+  static constexpr int kWarps = q4_decode_warps(kTiles);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kPartBytes = kT * kVec * 32 * 16;
+  static constexpr int kRingBytes = kStages * kPair * 2 * kQ4Slab;
+};
+
+template <int kTiles>
 struct __align__(128) Smem {
-  uint8_t ring[kWarps][kStages][kPair][2][kQ4Slab];  // two pages per stage, K slab and V slab
-  // a warp's part of its first item, 16 values per lane; the part of its last
-  // one goes where its ring was
-  float4 part_o[kWarps][4][32];
-  float part_m[kWarps][2][kGroup], part_l[kWarps][2][kGroup];
-  uint64_t full[kWarps][kStages];
+  using S = Shape<kTiles>;
+  // per warp: two pages per stage, K slab and V slab; its last item's part
+  // takes the ring's place at the end
+  uint8_t ring[S::kWarps][S::kRingBytes > S::kPartBytes ? S::kRingBytes : S::kPartBytes];
+  uint8_t part[S::kWarps][S::kPartBytes];  // a warp's part of its first item
+  float part_m[S::kWarps][2][S::kT * S::kTileCols], part_l[S::kWarps][2][S::kT * S::kTileCols];
+  uint64_t full[S::kWarps][kStages];
   int32_t ids[kQ4MaxPagesPerCta];
   Item items[kQ4MaxItemsPerCta];
   int arrived[kQ4MaxItemsPerCta];  // warps done with their part of the item
   int n_items;
 };
-static_assert(sizeof(float4) * 4 * 32 <= sizeof(Smem::ring[0]), "a part fits a warp's ring");
-static_assert(sizeof(Smem) <= 227 * 1024, "one CTA per SM");
-static_assert(kQ4Slab % 128 == 0, "matrix-load rows of a slab meet the banks as laid out in q4.cuh");
+static_assert(sizeof(Smem<0>) <= 227 * 1024 && sizeof(Smem<2>) <= 227 * 1024 && sizeof(Smem<3>) <= 227 * 1024,
+              "one CTA per SM");
+static_assert(kQ4Slab % 128 == 0 && Shape<3>::kPartBytes % 128 == 0,
+              "matrix-load rows of a slab meet the banks as laid out in q4.cuh");
 
-__device__ __forceinline__ float4* part_of(Smem& sm, int warp, int slot) {
-  return slot == 0 ? &sm.part_o[warp][0][0] : reinterpret_cast<float4*>(sm.ring[warp]);
+// A warp's part (slot 0: of its first item, 1: of its last), [tile][vector][lane].
+template <int kTiles>
+__device__ __forceinline__ float4* part_of(Smem<kTiles>& sm, int warp, int slot) {
+  return reinterpret_cast<float4*>(slot == 0 ? sm.part[warp] : sm.ring[warp]);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -115,7 +129,7 @@ __device__ __forceinline__ uint32_t at(const uint4& v, int g) { return g == 0 ? 
 // kernel's epilogue) as bf16: lanes r and r ^ 1 hold the even and the odd dims
 // of the same words and exchange halves, so each stores 8 neighbouring dims of
 // two groups.
-__device__ __forceinline__ void store_row(uint16_t* row, const float (&o)[16], int r) {
+__device__ __forceinline__ void store_row(uint16_t* row, const float (&o)[16], int r, bool used) {
   const bool odd = r & 1;
   float mine[8], other[8];
 #pragma unroll
@@ -131,35 +145,74 @@ __device__ __forceinline__ void store_row(uint16_t* row, const float (&o)[16], i
       const float a = mine[4 * g + i], b = other[4 * g + i];
       w[i] = odd ? pack_bf16x2(b, a) : pack_bf16x2(a, b);
     }
-    *reinterpret_cast<uint4*>(row + 32 * (g + (odd ? 2 : 0)) + 8 * (r >> 1)) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (used)
+      *reinterpret_cast<uint4*>(row + 32 * (g + (odd ? 2 : 0)) + 8 * (r >> 1)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// Running log-sum-exp merge of parts of one head (16 values per lane).
-struct Merge {
-  float m = -INFINITY, l = 0.f;
-  float o[16] = {};
-  // a part with maximum (or lse) m2, weight sum l2 and values x
-  __device__ __forceinline__ void add(float m2, float l2, const float4 (&x)[4]) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
-    const float f = fast_exp2(m - mn), f2 = fast_exp2(m2 - mn);
-    l = l * f + l2 * f2;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[4 * i] = fmaf(f2, x[i].x, o[4 * i] * f);
-      o[4 * i + 1] = fmaf(f2, x[i].y, o[4 * i + 1] * f);
-      o[4 * i + 2] = fmaf(f2, x[i].z, o[4 * i + 2] * f);
-      o[4 * i + 3] = fmaf(f2, x[i].w, o[4 * i + 3] * f);
-    }
-  }
+// One tile's columns of this lane: maximum, weight sum and 16 unnormalised
+// values per column (vector v = 4 col + group: 4 dims).
+template <int kCols>
+struct Part {
+  float m[kCols], l[kCols];
+  float4 o[4 * kCols];
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
-    decode_q4_kernel(const DecodeParams p, const __grid_constant__ DecodePlan plan) {
+// Log-sum-exp merge of n parts, in order.  m_at(i, c), l_at(i, c): maximum and
+// weight sum of column c of this lane in part i; row(i): the part's vectors of
+// this lane at stride 32.  The eight lanes of a column read the maxima of eight
+// parts at a time; then the values of four parts are in flight at once.
+template <int kCols, class M, class L, class Row>
+__device__ __forceinline__ void merge_parts(Part<kCols>& out, int n, int lane, M&& m_at, L&& l_at, Row&& row) {
+  const int r = lane >> 2;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    float mx = -INFINITY;
+    for (int i = r; i < n; i += 8) mx = fmaxf(mx, m_at(i, c));
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    out.m[c] = mx;
+    out.l[c] = 0.f;
+  }
+#pragma unroll
+  for (int v = 0; v < 4 * kCols; ++v) out.o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = kCols == 1 ? 4 : 2;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float4 x[kBatch][4 * kCols];
+    float w[kBatch][kCols];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = min(i0 + u, n - 1);
+      const float4* src = row(i);
+#pragma unroll
+      for (int v = 0; v < 4 * kCols; ++v) x[u][v] = src[32 * v + lane];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float f = (i0 + u >= n || out.m[c] == -INFINITY) ? 0.f : fast_exp2(m_at(i, c) - out.m[c]);
+        w[u][c] = f;
+        out.l[c] = fmaf(f, l_at(i, c), out.l[c]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int v = 0; v < 4 * kCols; ++v) {
+        const float f = w[u][v >> 2];
+        out.o[v].x = fmaf(f, x[u][v].x, out.o[v].x);
+        out.o[v].y = fmaf(f, x[u][v].y, out.o[v].y);
+        out.o[v].z = fmaf(f, x[u][v].z, out.o[v].z);
+        out.o[v].w = fmaf(f, x[u][v].w, out.o[v].w);
+      }
+  }
+}
+
+template <int kTiles, class Plan>
+__global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
+    decode_q4_kernel(const DecodeParams p, const __grid_constant__ Plan plan) {
+  using S = Shape<kTiles>;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kT = S::kT, kCols = S::kCols;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  Smem<kTiles>& sm = *reinterpret_cast<Smem<kTiles>*>(smem_raw);
   const int b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hkv = p.num_kv_heads;
@@ -177,17 +230,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // from the kernel parameters alone, so it is built before the wait for the
   // previous kernel
   if (warp == 1) {
+    const int2 at = plan.start[sidx];  // first row and its first page
     int base_q = 0, n_it = 0;
     for (int k0 = 0; k0 < kQ4MaxItemsPerCta; k0 += 32) {
-      const int item = plan.first_row[sidx] + k0 + lane;
-      const bool exists = item < plan.n_rows;
-      int r = 0, L = 0, size = 0, tok = 0;
-      const int p0 = (k0 + lane == 0) ? plan.first_page[sidx] : 0;
-      if (exists) {
-        r = plan.rows[item];
-        L = plan.seq[item];
-        tok = plan.tok[item];
-        size = max((L + kPage - 1) / kPage - p0, 0);
+      const int item = at.x + k0 + lane;
+      const int p0 = (k0 + lane == 0) ? at.y : 0;
+      int4 row = make_int4(0, 0, 0, 0);  // request, seq_len, first query token, queries
+      int size = 0;
+      if (item < plan.n_rows) {
+        row = plan.row[item];
+        size = max((row.y + kPage - 1) / kPage - p0, 0);
       }
       int incl = size;
 #pragma unroll
@@ -202,9 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.q_start = start;
         it.n = min(size, npg - start);
         it.p0 = p0;
-        it.r = r;
-        it.L = L;
-        it.tok = tok;
+        it.r = row.x;
+        it.L = row.y;
+        it.tok = row.z;
+        it.nq = row.w;
         it.A = S0 + start - p0;
       }
       const unsigned covered = __ballot_sync(0xffffffffu, in_seg);
@@ -214,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead < 32 || base_q >= npg) break;
     }
     if (lane == 0) {
-      if (base_q < npg) record_error(p.err, PA_ERR_DEVICE_INDEX);  // metadata differ from the plan
+      if (base_q < npg) record_error(p.err, PA_ERR_DEVICE_INDEX);  // not planned on the host
       sm.n_items = n_it;
     }
   }
@@ -260,6 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(p.k_cache);
   const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v_cache);
+  // slab of the page `half` of stage s: K, then V one slab further
+  auto slab_at = [&](int s, int half) { return sm.ring[warp] + (s * kPair + half) * (2 * kQ4Slab); };
   // Pages a + 2 i and a + 2 i + 1 -> stage i % kStages.  Lanes 0 .. 3 issue the
   // K and V slab of the two pages; a page with a bad id is fetched from block 0
   // and does not count.
@@ -267,49 +322,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto issue = [&](int i) {
     if (lane < 2 * kPair) {
       const int s = i % kStages, q = a + kPair * i + (lane >> 1);
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (kPair == 2 && q + 1 < e ? 4 : 2) * kQ4Slab);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (q + 1 < e ? 4 : 2) * kQ4Slab);
       if (q < e) {
         const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab;
-        bulk_g2s(sm.ring[warp][s][lane >> 1][lane & 1], ((lane & 1) ? vbase : kbase) + off, kQ4Slab, &sm.full[warp][s]);
+        bulk_g2s(slab_at(s, lane >> 1) + (lane & 1) * kQ4Slab, ((lane & 1) ? vbase : kbase) + off, kQ4Slab,
+                 &sm.full[warp][s]);
       }
     }
   };
   for (int i = 0; i < min(n_pairs, kStages); ++i) issue(i);
 
   const int r = lane >> 2;   // token slot (r, r + 8) in the scores; dim row in the output
-  const int cq = lane & 3;   // the lane's head in scores and output
+  const int cq = lane & 3;   // the lane's columns in scores and output: head cq, or 2 cq and 2 cq + 1
   // matrix-load address of lane l: matrix (group) l / 8, row (token) l % 8
   const uint32_t ld_at = (uint32_t)q4_code_at(lane & 7, lane >> 3);
   int issued = min(n_pairs, kStages);
   bool gave_up = false;
 
   for (; k < n_items; ++k) {
-    const Item it = sm.items[k];
+    const Item& it = sm.items[k];
     const int i0 = max(it.q_start, a), i1 = min(it.q_start + it.n, e);
     if (i0 >= i1) break;  // past this warp's pages
-    const int pages_r = (it.L + kPage - 1) / kPage;
-    const int tail = it.L - (pages_r - 1) * kPage;  // tokens of the row's last page
-    const int q_last = it.q_start + (pages_r - 1 - it.p0);
-    // q as the first product's B operand: column 2 h holds head h (column
-    // 2 h + 1 zeros); k step (g, e) takes dims 32 g + 8 cq + 4 e .. + 3
-    uint4 qb[4];
-    {
+    const int L = it.L, nq = it.nq;
+    const int page0 = it.p0 - it.q_start;  // row page of segment page q: page0 + q
+    // keys the lane's columns of tile y see (columns past the last query: all)
+    auto sees = [&](int y) { return S::kOne ? L : min(L - nq + 2 * y + (cq >> 1) + 1, L); };
+    // q as the first product's B operand: column n of tile y is query 2 y + n
+    // / 4, head n % 4 (one query: column 2 h is head h, column 2 h + 1 zeros);
+    // k step (g, e) takes dims 32 g + 8 cq + 4 e .. + 3
+    uint4 qb[kT][4];
+#pragma unroll
+    for (int y = 0; y < kT; ++y) {
+      const int query = S::kOne ? 0 : 2 * y + (r >> 2), head = S::kOne ? r >> 1 : r & 3;
+      const bool used = S::kOne ? (r & 1) == 0 : query < nq;
       const uint16_t* qrow =
-          p.q + ((size_t)it.tok * p.num_q_heads + (size_t)kvh * kGroup + (lane >> 3)) * kHeadDim + 8 * cq;
+          p.q + ((size_t)(it.tok + (used ? query : 0)) * p.num_q_heads + (size_t)kvh * kGroup + head) * kHeadDim + 8 * cq;
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        qb[g] = (r & 1) ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(qrow + 32 * g);
+        qb[y][g] = used ? *reinterpret_cast<const uint4*>(qrow + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
     }
-    float acc[4][2][4];
+    float acc[kT][4][2][4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int y = 0; y < kT; ++y)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][x][i] = 0.f;
-    // running max of head cq (the same in its 8 lanes), minus it (0 before
-    // the first key), and the sum of this lane's own weights
-    float m = -INFINITY, nm = 0.f, l = 0.f;
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[y][g][x][i] = 0.f;
+    // per column: running max (the same in the column's 8 lanes), minus it (0
+    // before the first key), and the sum of this lane's own weights
+    float m[kT][kCols], nm[kT][kCols], l[kT][kCols];
+#pragma unroll
+    for (int y = 0; y < kT; ++y)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        m[y][c] = -INFINITY;
+        nm[y][c] = l[y][c] = 0.f;
+      }
 
     for (int q = i0; q < i1;) {
       const int j = q - a, i = j / kPair, s = i % kStages;
@@ -320,21 +390,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // two pages at once where the pair lies in the row, else one: page 0 is
       // q, page 1 its neighbour in the stage, of which no token counts then
-      const int half = kPair == 2 ? j & 1 : 0, n = (kPair == 2 && half == 0 && q + 1 < i1) ? 2 : 1;
-      int live[kPair];  // tokens of each page that count
-      live[0] = q == q_last ? tail : kPage;
-      if (kPair == 2) live[kPair - 1] = n == 1 ? 0 : q + 1 == q_last ? tail : kPage;
+      const int half = j & 1, n = (half == 0 && q + 1 < i1) ? 2 : 1;
+      int pos[kPair];  // row position of each page's first token (L: the page does not count)
+      pos[0] = (page0 + q) * kPage;
+      pos[1] = n == 1 ? L : pos[0] + kPage;
       if (!ids_ok) {
-        if (sm.ids[q] < 0) live[0] = 0;
-        if (n == 2 && sm.ids[q + 1] < 0) live[kPair - 1] = 0;
+        if (sm.ids[q] < 0) pos[0] = L;
+        if (n == 2 && sm.ids[q + 1] < 0) pos[1] = L;
       }
-      const uint32_t st = smem_addr(sm.ring[warp][s][half]), step = half ? 0u - 2 * kQ4Slab : 2u * kQ4Slab;
-      // ---- scores: tokens r and r + 8 of head cq, of both pages
-      float sc[2 * kPair];
+      // every token of both pages counts for every column
+      const bool whole = max(pos[0], pos[1]) + kPage <= L - nq + 1;
+      const uint32_t st = smem_addr(slab_at(s, half)), step = half ? 0u - 2 * kQ4Slab : 2u * kQ4Slab;
+      // ---- scores: tokens r and r + 8 of the lane's columns, of both pages
+      float sc[kT][kCols][2 * kPair];
 #pragma unroll
       for (int u = 0; u < kPair; ++u) {
         const uint32_t ks = st + u * step;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        float c[kT][4];
+#pragma unroll
+        for (int y = 0; y < kT; ++y) c[y][0] = c[y][1] = c[y][2] = c[y][3] = 0.f;
         uint32_t ka[4], kb[4];
         ldmatrix4(ka, ks + ld_at);
         ldmatrix4(kb, ks + ld_at + 8 * kQ4Row);
@@ -343,52 +417,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; g < 4; ++g) {
           const uint32_t da = q4_dup_d(at(za, g)), oa = q4_dup_z(at(za, g));
           const uint32_t db = q4_dup_d(at(zb, g)), ob = q4_dup_z(at(zb, g));
-          mma16816(c, bf16x2_fma(q4_unit_pair<0>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<0>(kb[g]), db, ob),
-                   bf16x2_fma(q4_unit_pair<1>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<1>(kb[g]), db, ob), qb[g].x,
-                   qb[g].y);
-          mma16816(c, bf16x2_fma(q4_unit_pair<2>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<2>(kb[g]), db, ob),
-                   bf16x2_fma(q4_unit_pair<3>(ka[g]), da, oa), bf16x2_fma(q4_unit_pair<3>(kb[g]), db, ob), qb[g].z,
-                   qb[g].w);
+          const uint32_t a0 = bf16x2_fma(q4_unit_pair<0>(ka[g]), da, oa), a1 = bf16x2_fma(q4_unit_pair<0>(kb[g]), db, ob);
+          const uint32_t a2 = bf16x2_fma(q4_unit_pair<1>(ka[g]), da, oa), a3 = bf16x2_fma(q4_unit_pair<1>(kb[g]), db, ob);
+          const uint32_t a4 = bf16x2_fma(q4_unit_pair<2>(ka[g]), da, oa), a5 = bf16x2_fma(q4_unit_pair<2>(kb[g]), db, ob);
+          const uint32_t a6 = bf16x2_fma(q4_unit_pair<3>(ka[g]), da, oa), a7 = bf16x2_fma(q4_unit_pair<3>(kb[g]), db, ob);
+#pragma unroll
+          for (int y = 0; y < kT; ++y) {
+            mma16816(c[y], a0, a1, a2, a3, qb[y][g].x, qb[y][g].y);
+            mma16816(c[y], a4, a5, a6, a7, qb[y][g].z, qb[y][g].w);
+          }
         }
-        sc[2 * u] = c[0] * p.scale_log2;
-        sc[2 * u + 1] = c[2] * p.scale_log2;
+#pragma unroll
+        for (int y = 0; y < kT; ++y)
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            sc[y][x][2 * u] = c[y][x] * p.scale_log2;
+            sc[y][x][2 * u + 1] = c[y][2 + x] * p.scale_log2;
+          }
       }
-      const bool whole = live[0] == kPage && live[kPair - 1] == kPage;
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < kPair; ++u) {
-          if (r >= live[u]) sc[2 * u] = -INFINITY;
-          if (r + 8 >= live[u]) sc[2 * u + 1] = -INFINITY;
+        for (int y = 0; y < kT; ++y) {
+          const int vis = sees(y);
+#pragma unroll
+          for (int u = 0; u < kPair; ++u)
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) {
+              if (pos[u] + r >= vis) sc[y][x][2 * u] = -INFINITY;
+              if (pos[u] + r + 8 >= vis) sc[y][x][2 * u + 1] = -INFINITY;
+            }
         }
       }
-      float mx = fmaxf(sc[0], sc[1]);
-      if (kPair == 2) mx = fmaxf(mx, fmaxf(sc[2 * kPair - 2], sc[2 * kPair - 1]));
-      if (__any_sync(0xffffffffu, mx > m + kRescaleSlack)) {  // rare after the first pages
+      float mx[kT][kCols];
+      bool grow = false;
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (mx > m + kRescaleSlack) {
-          const float corr = fast_exp2(m - mx);  // m = -inf -> 0
-          m = mx;
-          nm = -mx;
-          l *= corr;
+      for (int y = 0; y < kT; ++y)
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) acc[g][x][y] *= corr;
+        for (int x = 0; x < kCols; ++x) {
+          mx[y][x] = fmaxf(fmaxf(sc[y][x][0], sc[y][x][1]), fmaxf(sc[y][x][2], sc[y][x][3]));
+          grow = grow || mx[y][x] > m[y][x] + kRescaleSlack;
         }
-      }
-      // weights as two bf16 each (leading bits, rest), transposed into the
-      // second product's B operand
-      uint32_t pb[2 * kPair];
+      if (__any_sync(0xffffffffu, grow)) {  // rare after the first pages
 #pragma unroll
-      for (int u = 0; u < 2 * kPair; ++u) {
-        const float w = fast_exp2(sc[u] + nm);
-        l += w;
-        const float h = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
-        pb[u] = movmatrix_trans(pack_bf16x2(h, w - h));
+        for (int y = 0; y < kT; ++y)
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            float t = mx[y][x];
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+            if (t > m[y][x] + kRescaleSlack) {
+              const float corr = fast_exp2(m[y][x] - t);  // m = -inf -> 0
+              m[y][x] = t;
+              nm[y][x] = -t;
+              l[y][x] *= corr;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int v = 0; v < 4; ++v)
+                    if (S::kOne || (v & 1) == x) acc[y][g][h][v] *= corr;
+            }
+          }
       }
+      // weights, transposed into the second product's B operand
+      uint32_t pb[kT][2 * kPair];
+#pragma unroll
+      for (int y = 0; y < kT; ++y)
+#pragma unroll
+        for (int u = 0; u < 2 * kPair; ++u) {
+          const float w0 = fast_exp2(sc[y][0][u] + nm[y][0]);
+          l[y][0] += w0;
+          if constexpr (S::kOne) {  // leading bits, rest
+            const float h = __uint_as_float(__float_as_uint(w0) & 0xffff0000u);
+            pb[y][u] = movmatrix_trans(pack_bf16x2(h, w0 - h));
+          } else {
+            const float w1 = fast_exp2(sc[y][kCols - 1][u] + nm[y][kCols - 1]);
+            l[y][kCols - 1] += w1;
+            pb[y][u] = movmatrix_trans(pack_bf16x2(w0, w1));
+          }
+        }
       // ---- output: dims of row r of each group's words, tokens 2 cq, 2 cq +
       // 1 and the same + 8
 #pragma unroll
@@ -399,23 +507,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ldmatrix4_trans(vb, vs + ld_at + 8 * kQ4Row);
         const uint32_t sp = vs + kQ4Codes + 32 * cq;
         uint4 z0 = lds128(sp), z1 = lds128(sp + 16), z2 = lds128(sp + 128), z3 = lds128(sp + 144);
-        if (!whole) {  // a token that does not count has weight 0: its values must be finite
+        if (!whole) {  // a token past the end has weight 0: its values must be finite
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          if (2 * cq >= live[u]) z0 = zero;
-          if (2 * cq + 1 >= live[u]) z1 = zero;
-          if (2 * cq + 8 >= live[u]) z2 = zero;
-          if (2 * cq + 9 >= live[u]) z3 = zero;
+          const int left = L - pos[u];
+          if (2 * cq >= left) z0 = zero;
+          if (2 * cq + 1 >= left) z1 = zero;
+          if (2 * cq + 8 >= left) z2 = zero;
+          if (2 * cq + 9 >= left) z3 = zero;
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const uint32_t da = __byte_perm(at(z0, g), at(z1, g), 0x5410), oa = __byte_perm(at(z0, g), at(z1, g), 0x7632);
           const uint32_t db = __byte_perm(at(z2, g), at(z3, g), 0x5410), ob = __byte_perm(at(z2, g), at(z3, g), 0x7632);
-          mma16816(acc[g][0], bf16x2_fma(q4_unit_pair<0>(va[g]), da, oa), bf16x2_fma(q4_unit_pair<1>(va[g]), da, oa),
-                   bf16x2_fma(q4_unit_pair<0>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<1>(vb[g]), db, ob), pb[2 * u],
-                   pb[2 * u + 1]);
-          mma16816(acc[g][1], bf16x2_fma(q4_unit_pair<2>(va[g]), da, oa), bf16x2_fma(q4_unit_pair<3>(va[g]), da, oa),
-                   bf16x2_fma(q4_unit_pair<2>(vb[g]), db, ob), bf16x2_fma(q4_unit_pair<3>(vb[g]), db, ob), pb[2 * u],
-                   pb[2 * u + 1]);
+          const uint32_t a0 = bf16x2_fma(q4_unit_pair<0>(va[g]), da, oa), a1 = bf16x2_fma(q4_unit_pair<1>(va[g]), da, oa);
+          const uint32_t a2 = bf16x2_fma(q4_unit_pair<0>(vb[g]), db, ob), a3 = bf16x2_fma(q4_unit_pair<1>(vb[g]), db, ob);
+          const uint32_t a4 = bf16x2_fma(q4_unit_pair<2>(va[g]), da, oa), a5 = bf16x2_fma(q4_unit_pair<3>(va[g]), da, oa);
+          const uint32_t a6 = bf16x2_fma(q4_unit_pair<2>(vb[g]), db, ob), a7 = bf16x2_fma(q4_unit_pair<3>(vb[g]), db, ob);
+#pragma unroll
+          for (int y = 0; y < kT; ++y) {
+            mma16816(acc[y][g][0], a0, a1, a2, a3, pb[y][2 * u], pb[y][2 * u + 1]);
+            mma16816(acc[y][g][1], a4, a5, a6, a7, pb[y][2 * u], pb[y][2 * u + 1]);
+          }
         }
       }
       q += n;
@@ -431,28 +543,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (gave_up) break;
 
-    // ---- this warp's part of the item: head cq, value 4 g + i is dim 32 g +
-    // 8 (r / 2) + r % 2 + 2 i, unnormalised
+    // ---- this warp's part of the item: in a column, value 4 g + i is dim 32 g
+    // + 8 (r / 2) + r % 2 + 2 i, unnormalised
+    Part<kCols> own[kT];
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    float4 x[4];
+    for (int y = 0; y < kT; ++y)
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      x[g] = make_float4(acc[g][0][0] + acc[g][0][1], acc[g][0][2] + acc[g][0][3], acc[g][1][0] + acc[g][1][1],
-                         acc[g][1][2] + acc[g][1][3]);
-    Merge mg;
+      for (int x = 0; x < kCols; ++x) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], o);
+        own[y].m[x] = m[y][x];
+        own[y].l[x] = l[y][x];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float(&c)[2][4] = acc[y][g];
+          own[y].o[4 * x + g] = S::kOne ? make_float4(c[0][0] + c[0][1], c[0][2] + c[0][3], c[1][0] + c[1][1],
+                                                      c[1][2] + c[1][3])
+                                        : make_float4(c[0][x], c[0][2 + x], c[1][x], c[1][2 + x]);
+        }
+      }
+    const int pages_r = (L + kPage - 1) / kPage;
+    const bool cut = it.p0 != 0 || it.n != pages_r;  // between CTAs
     const int wf = it.q_start / sw, wl = (it.q_start + it.n - 1) / sw;  // warps holding the item
-    if (wf == wl) {
-      mg.add(m, l, x);
-    } else {
+    if (wf != wl) {
       const int slot = it.q_start <= a ? 0 : 1;  // the warp's first item, or its last
       float4* mine = part_of(sm, warp, slot);
       __syncwarp();  // every lane has read the ring
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mine[32 * i + lane] = x[i];
-      if (r == 0) {
-        sm.part_m[warp][slot][cq] = m;
-        sm.part_l[warp][slot][cq] = l;
+      for (int y = 0; y < kT; ++y) {
+#pragma unroll
+        for (int v = 0; v < S::kVec; ++v) mine[(y * S::kVec + v) * 32 + lane] = own[y].o[v];
+        if (r == 0) {
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            sm.part_m[warp][slot][y * S::kTileCols + kCols * cq + x] = own[y].m[x];
+            sm.part_l[warp][slot][y * S::kTileCols + kCols * cq + x] = own[y].l[x];
+          }
+        }
       }
       __syncwarp();
       int last = 0;
@@ -462,61 +589,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence_block();
       }
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-      for (int w = wf; w <= wl; ++w) {  // in page order, whichever warp came last
-        const int sl = it.q_start <= w * sw ? 0 : 1;
-        float4 y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = part_of(sm, w, sl)[32 * i + lane];
-        mg.add(sm.part_m[w][sl][cq], sm.part_l[w][sl][cq], y);
-      }
     }
-    const size_t orow = (size_t)it.tok * p.num_q_heads + kvh * kGroup + cq;
-    if (it.p0 != 0 || it.n != pages_r) {
-      // the row is cut between CTAs: publish this one's piece; the last CTA
-      // to do so merges them
-      const float inv = mg.l > 0.f ? 1.f / mg.l : 0.f;
-      const float lse2 = mg.l > 0.f ? mg.m + log2f(mg.l) : -INFINITY;
-      const int b0 = it.A / plan.seg, b1 = (it.A + pages_r - 1) / plan.seg;  // segments holding the row
-      auto piece_at = [&](int bb) {
-        const int j = (bb == b0 && b0 * plan.seg < it.A) ? 1 : 0;  // a segment's last item, or its first
-        return ((size_t)(bb * Hkv + kvh) * 2 + j) * kGroup;
-      };
-      const size_t mine = piece_at(sidx);
-      if ((int64_t)(mine + kGroup) > p.piece_slots) {  // the host sized the workspace for fewer pieces
-        if (lane == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
+    // the pieces of a row cut between CTAs: segments b0 .. b1 hold it, each
+    // CTA's piece of it is its last item's or its first's
+    const int b0 = it.A / plan.seg, b1 = (it.A + pages_r - 1) / plan.seg;
+    constexpr int kSlots = kT * S::kTileCols;  // (piece, head) slots of the workspace per piece
+    auto piece_at = [&](int bb) {
+      return ((size_t)(bb * Hkv + kvh) * 2 + ((bb == b0 && b0 * plan.seg < it.A) ? 1 : 0)) * kSlots;
+    };
+    if (cut && (int64_t)(piece_at(sidx) + kSlots) > p.piece_slots) {  // the host sized the workspace for fewer
+      if (lane == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
+      continue;
+    }
+    auto output = [&](int y, const Part<kCols>& v) {
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) {
+        const int col = kCols * cq + x;  // of the tile
+        const int query = S::kOne ? 0 : 2 * y + (col >> 2), head = S::kOne ? col : col & 3;
+        const float inv = v.l[x] > 0.f ? 1.f / v.l[x] : 0.f;
+        float o[16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          o[4 * g] = v.o[4 * x + g].x * inv;
+          o[4 * g + 1] = v.o[4 * x + g].y * inv;
+          o[4 * g + 2] = v.o[4 * x + g].z * inv;
+          o[4 * g + 3] = v.o[4 * x + g].w * inv;
+        }
+        const size_t orow = (size_t)(it.tok + query) * p.num_q_heads + kvh * kGroup + head;
+        store_row(p.out + orow * kHeadDim, o, r, query < nq);
+        if (p.lse && r == 0 && query < nq)
+          p.lse[orow] = v.l[x] > 0.f ? (v.m[x] + log2f(v.l[x])) * kLn2 : -INFINITY;
+      }
+    };
+#pragma unroll
+    for (int y = 0; y < kT; ++y) {
+      if (wf != wl)  // in page order, whichever warp came last
+        merge_parts<kCols>(
+            own[y], wl - wf + 1, lane,
+            [&](int i, int c) {
+              return sm.part_m[wf + i][it.q_start <= (wf + i) * sw ? 0 : 1][y * S::kTileCols + kCols * cq + c];
+            },
+            [&](int i, int c) {
+              return sm.part_l[wf + i][it.q_start <= (wf + i) * sw ? 0 : 1][y * S::kTileCols + kCols * cq + c];
+            },
+            [&](int i) { return part_of(sm, wf + i, it.q_start <= (wf + i) * sw ? 0 : 1) + y * S::kVec * 32; });
+      if (!cut) {
+        output(y, own[y]);
         continue;
       }
+      const size_t mine = piece_at(sidx) + y * S::kTileCols;
       float4* dst = reinterpret_cast<float4*>(p.piece_o + mine * kHeadDim);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dst[32 * i + lane] =
-            make_float4(mg.o[4 * i] * inv, mg.o[4 * i + 1] * inv, mg.o[4 * i + 2] * inv, mg.o[4 * i + 3] * inv);
-      if (r == 0) p.piece_lse[mine + cq] = lse2;
-      __syncwarp();  // every lane's writes precede lane 0's release
-      int last = 0;
-      if (lane == 0) {
-        int* cnt = p.counters + (size_t)it.r * Hkv + kvh;
-        last = atom_add_acq_rel_gpu(cnt, 1) == b1 - b0;
-        if (last) *cnt = 0;  // every piece has arrived: ready for the next call
-      }
-      __syncwarp();  // lane 0's acquire orders the reads below
-      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-      Merge all;
-      for (int bb = b0; bb <= b1; ++bb) {
-        const size_t src = piece_at(bb);
-        const float4* y4 = reinterpret_cast<const float4*>(p.piece_o + src * kHeadDim);
-        float4 y[4];
+      for (int x = 0; x < kCols; ++x) {
+        const float inv = own[y].l[x] > 0.f ? 1.f / own[y].l[x] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __ldcg(y4 + 32 * i + lane);
-        all.add(__ldcg(p.piece_lse + src + cq), 1.f, y);
+        for (int g = 0; g < 4; ++g) {
+          const float4 v = own[y].o[4 * x + g];
+          dst[(4 * x + g) * 32 + lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
+        if (r == 0)
+          p.piece_lse[mine + kCols * cq + x] = own[y].l[x] > 0.f ? own[y].m[x] + log2f(own[y].l[x]) : -INFINITY;
       }
-      mg = all;
     }
-    const float inv = mg.l > 0.f ? 1.f / mg.l : 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mg.o[i] *= inv;
-    store_row(p.out + orow * kHeadDim, mg.o, r);
-    if (p.lse && r == 0) p.lse[orow] = mg.l > 0.f ? (mg.m + log2f(mg.l)) * kLn2 : -INFINITY;
+    if (!cut) continue;
+    __syncwarp();  // every lane's writes precede lane 0's release
+    int last = 0;
+    if (lane == 0) {
+      int* cnt = p.counters + (size_t)it.r * Hkv + kvh;
+      last = atom_add_acq_rel_gpu(cnt, 1) == b1 - b0;
+      if (last) *cnt = 0;  // every piece has arrived: ready for the next call
+    }
+    __syncwarp();  // lane 0's acquire orders the reads below
+    if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+#pragma unroll 1
+    for (int y = 0; y < kT; ++y) {
+      Part<kCols> all;
+      merge_parts<kCols>(
+          all, b1 - b0 + 1, lane,
+          [&](int i, int c) { return __ldcg(p.piece_lse + piece_at(b0 + i) + y * S::kTileCols + kCols * cq + c); },
+          [&](int, int) { return 1.f; },
+          [&](int i) {
+            return reinterpret_cast<const float4*>(p.piece_o + (piece_at(b0 + i) + y * S::kTileCols) * kHeadDim);
+          });
+      output(y, all);
+    }
   }
 
   if (gave_up && lane == 0) {
@@ -527,15 +683,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-std::atomic<bool> g_attr_set[kMaxDevices];
+std::atomic<bool> g_attr_set[6][kMaxDevices];
+
+template <int kTiles, class Plan>
+cudaError_t launch(const DecodeParams& p, const Plan& plan, int grid, bool overlap, std::atomic<bool>* done,
+                   cudaStream_t stream) {
+  constexpr int kSmem = (int)sizeof(Smem<kTiles>);
+  const cudaError_t e = set_smem_limit_once((const void*)decode_q4_kernel<kTiles, Plan>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_maybe_pdl(overlap, decode_q4_kernel<kTiles, Plan>, dim3(grid), dim3(Shape<kTiles>::kThreads), kSmem,
+                          stream, p, plan);
+}
+
+// The plan in the parameter block of the size it needs: a launch with a small
+// one takes 1.3 us less (its parameters are copied to the device and fetched by
+// every SM), and most batches fit it.
+template <int kTiles>
+cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int grid, bool overlap,
+                         std::atomic<bool>* done, cudaStream_t stream) {
+  const int segs = grid / p.num_kv_heads;
+  auto fill = [&](auto& d) {
+    d.n_rows = plan.n_rows;
+    d.seg = plan.seg;
+    d.total = plan.total;
+    for (int i = 0; i < plan.n_rows; ++i) d.row[i] = make_int4(plan.rows[i], plan.seq[i], plan.tok[i], n_q[i]);
+    for (int i = 0; i < segs; ++i) d.start[i] = make_int2(plan.first_row[i], plan.first_page[i]);
+  };
+  if (plan.n_rows <= 128 && segs <= 160) {
+    Q4Plan<128, 160> small;
+    fill(small);
+    return launch<kTiles>(p, small, grid, overlap, done, stream);
+  }
+  static thread_local Q4Plan<kPlanMaxRows, kPlanMaxCtas> large;
+  fill(large);
+  return launch<kTiles>(p, large, grid, overlap, done + kMaxDevices, stream);
+}
 
 }  // namespace
 
-cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, int grid, bool overlap,
-                             cudaStream_t stream) {
-  const cudaError_t e = set_smem_limit_once((const void*)decode_q4_kernel, (int)sizeof(Smem), g_attr_set);
-  if (e != cudaSuccess) return e;
-  return launch_maybe_pdl(overlap, decode_q4_kernel, dim3(grid), dim3(kThreads), sizeof(Smem), stream, p, plan);
+cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int tiles, int grid,
+                             bool overlap, cudaStream_t stream) {
+  std::atomic<bool>* done = &g_attr_set[0][0];
+  if (tiles == 0) return launch_tiles<0>(p, plan, n_q, grid, overlap, done, stream);
+  if (tiles <= 2) return launch_tiles<2>(p, plan, n_q, grid, overlap, done + 2 * kMaxDevices, stream);
+  return launch_tiles<3>(p, plan, n_q, grid, overlap, done + 4 * kMaxDevices, stream);
 }
 
 }  // namespace pa

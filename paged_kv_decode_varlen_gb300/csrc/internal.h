@@ -74,15 +74,19 @@ constexpr int kMinWarpSegPages = 8;
 constexpr int kWgWarps = 12;
 constexpr int kWgMaxPagesPerCta = 3072;
 constexpr int kWgMaxItemsPerCta = 192;
-// The decode kernel over q4 pages: one CTA of kQ4Warps warps per SM, a warp
-// segment each; pages and rows a segment may hold.
-#ifndef Q4_WARPS
-#define Q4_WARPS 16
-#endif
-constexpr int kQ4Warps = Q4_WARPS;
-constexpr int kQ4MaxPagesPerCta = 2040 / kQ4Warps * kQ4Warps;
+// The decode kernel over q4 pages: pages and rows a CTA's segment may hold.
+constexpr int kQ4MaxPagesPerCta = 2000;
 constexpr int kQ4MaxItemsPerCta = 192;
-static_assert(kQ4MaxPagesPerCta % kQ4Warps == 0 && kQ4MaxItemsPerCta % 32 == 0, "whole warp segments and table rounds");
+static_assert(kQ4MaxItemsPerCta % 32 == 0, "whole rounds of the item table");
+// Rows of up to kQ4DecodeQueries queries run it: tiles = 0 for one query, else
+// tiles of 8 columns (two queries of 4 heads): 2 for up to 4 queries, 3 for 5
+// and 6.  (A fourth tile's partial results would no longer fit beside the
+// rings.)
+constexpr int kQ4DecodeQueries = 6;
+constexpr int q4_decode_tiles(int n_q) { return n_q == 1 ? 0 : n_q <= 4 ? 2 : 3; }
+// Warps per CTA: as many as registers (tiles) and shared memory leave room for.
+constexpr int q4_decode_warps(int tiles) { return tiles == 0 ? 16 : 8; }
+static_assert(kQ4MaxPagesPerCta % 16 == 0, "whole warp segments");
 // Bytes of one (page, kv head) slab of K or V in bf16 (16 tokens x 128 dims).
 constexpr int kSlabBytesHost = 16 * 128 * 2;
 struct DecodePlan {
@@ -94,6 +98,16 @@ struct DecodePlan {
   int32_t tok[kPlanMaxRows];          // its query token (qo_indptr, from the host copy)
   int32_t first_row[kPlanMaxCtas];    // row (index d) holding a segment's first page
   int32_t first_page[kPlanMaxCtas];   // that page's index within its row
+};
+
+// The same plan as the q4 decode kernel takes it, for at most R rows and C
+// segments.
+template <int R, int C>
+struct Q4Plan {
+  int32_t n_rows, seg, total;
+  int32_t pad;
+  int4 row[R];    // request, seq_len, first query token, queries
+  int2 start[C];  // a segment's first row and that row's first page
 };
 
 // Decode step (self-planned launch): the kernel parameters carry only the
@@ -273,9 +287,10 @@ cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 // the warp-granular kernel (plan in whole warp segments of kWgWarps warps)
 cudaError_t launch_decode(const DecodeParams& p, const DecodePlan& plan, int grid, bool q8, bool overlap,
                           bool diag, bool cta_granular, cudaStream_t stream);
-// q4 pages, a plan in whole warp segments of kQ4Warps warps
-cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, int grid, bool overlap,
-                             cudaStream_t stream);
+// q4 pages: rows of n_q[i] queries (i: plan row), all of the class `tiles`; a
+// plan in whole warp segments of q4_decode_warps(tiles) warps
+cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int tiles, int grid,
+                             bool overlap, cudaStream_t stream);
 // warp_granular: the warp-granular kernel (grid: one CTA per SM at most; no
 // segment may hold more than kWgMaxItemsPerCta rows or kWgMaxPagesPerCta
 // pages), else the CTA-granular one (windows of rows)

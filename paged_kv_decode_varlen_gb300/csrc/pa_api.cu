@@ -543,6 +543,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
                 max_blocks_per_req);
   // classify rows and collect the plan inputs
   std::vector<int32_t> decode_rows;
+  std::vector<int32_t> q4_rows[2];  // q4 pages: rows of 2 .. 4 and of 5, 6 queries, which the decode kernel takes too
   int32_t active = 0, first_active = -1;
   int32_t max_len = 1;
   std::vector<std::pair<int32_t, int32_t>> tiles;  // (kv extent of the tile, item index) for ordering
@@ -571,6 +572,8 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     }
     if (qo_len == 1) {
       decode_rows.push_back(r);
+    } else if (q4 && qo_len > 1 && qo_len <= pa::kQ4DecodeQueries) {
+      q4_rows[pa::q4_decode_tiles(qo_len) == 2 ? 0 : 1].push_back(r);
     } else if (qo_len > 1) {
       const int32_t q_tile = q4 ? pa::kQ4TileTokens : pa::kPrefillQTile;
       for (int32_t j0 = 0; j0 < qo_len; j0 += q_tile) {
@@ -755,7 +758,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     }
   }
 
-  if (!decode_rows.empty()) {
+  if (!decode_rows.empty() || !q4_rows[0].empty() || !q4_rows[1].empty()) {
     pa::DecodeParams dp{};
     dp.q = static_cast<const uint16_t*>(q);
     dp.k_cache = static_cast<const uint16_t*>(k_cache);
@@ -788,6 +791,37 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     dp.err = err;
     static thread_local pa::DecodePlan plan;
     const int gcap = grid_cap(num_reqs, num_kv_heads, max_len);
+    if (q4) {
+      // one launch per class of rows (and per kPlanMaxRows rows; fewer where a
+      // segment would hold too many)
+      static thread_local int32_t n_q[pa::kPlanMaxRows];
+      bool overlap = tiles.empty();  // as below
+      for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows}) {
+        for (size_t d0 = 0; d0 < rows->size();) {
+          int n = (int)std::min(rows->size() - d0, (size_t)pa::kPlanMaxRows);
+          const int32_t* r0 = rows->data() + d0;
+          const int cls = pa::q4_decode_tiles(qo_indptr_host[r0[0] + 1] - qo_indptr_host[r0[0]]);
+          // a piece takes 4 (piece, head) slots of the workspace, or 8 per tile
+          const int64_t piece = cls == 0 ? PA_GQA_GROUP : 8 * cls;
+          const int cap = (int)std::min<int64_t>(gcap, wl.slots / (2 * piece));
+          int grid;
+          for (;; n = (n + 1) / 2) {
+            grid = plan_decode(r0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, cap, sm_count(),
+                               pa::q4_decode_warps(cls), pa::kQ4MaxPagesPerCta, pa::kQ4MaxItemsPerCta, plan);
+            if (grid >= 0 || n == 1) break;
+          }
+          if (grid < 0) return fail(PA_ERR_UNSUPPORTED, "no decode plan within the kernel limits");
+          d0 += (size_t)n;
+          if (grid == 0) continue;
+          for (int i = 0; i < n; ++i) n_q[i] = qo_indptr_host[r0[i] + 1] - qo_indptr_host[r0[i]];
+          s = run_launch(PA_KERNEL_DECODE, "decode_q4", stream,
+                         [&] { return pa::launch_decode_q4(dp, plan, n_q, cls, grid, overlap, stream); });
+          if (s != PA_OK) return s;
+          overlap = true;
+        }
+      }
+      return ok();
+    }
     // one launch per kPlanMaxRows decode rows (the plan travels as kernel
     // parameters); launches on one stream run in order and reuse the slots
     for (size_t d0 = 0; d0 < decode_rows.size(); d0 += pa::kPlanMaxRows) {
@@ -797,16 +831,6 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       // the tile kernel's tail, they made the step 1-2 us longer, not shorter.
       // Beside a concurrent prefix pass they start as soon as it has.
       const bool overlap = d0 > 0 || (P == 0 && tiles.empty()) || concurrent;
-      if (q4) {
-        const int grid = plan_decode(decode_rows.data() + d0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, gcap,
-                                     sm_count(), pa::kQ4Warps, pa::kQ4MaxPagesPerCta, pa::kQ4MaxItemsPerCta, plan);
-        if (grid < 0) return fail(PA_ERR_UNSUPPORTED, "no decode plan within the kernel limits");
-        if (grid == 0) continue;
-        s = run_launch(PA_KERNEL_DECODE, "decode_q4", stream,
-                       [&] { return pa::launch_decode_q4(dp, plan, grid, overlap, stream); });
-        if (s != PA_OK) return s;
-        continue;
-      }
       const bool diag = !q8 && g_decode_fault.load() != 0;
       bool cta_granular = false;
       const int grid = choose_decode_plan(decode_rows.data() + d0, n, seq_lens_host, qo_indptr_host, P, num_kv_heads,

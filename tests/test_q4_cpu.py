@@ -152,3 +152,35 @@ def test_attention_refusals(kw, status):
     n0 = lib.pa_launch_count()
     assert _attn(**kw) == status, lib.pa_last_error_message().decode()
     assert lib.pa_last_error_message().decode() != "" and lib.pa_launch_count() == n0
+
+
+def test_the_binding_refuses_shapes_types_and_places():
+    """Argument checks of the binding come before any call into the library;
+    CPU tensors are themselves refused."""
+    import torch
+    pool = torch.zeros(4, 2, 1280, dtype=torch.uint8)
+    rows = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int64)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    for bad in [(rows, rows, slots[:2], pool, pool), (rows, rows[:2], slots, pool, pool),
+                (rows, rows, slots, pool[..., :1152], pool[..., :1152]), (rows, rows, slots, pool, pool[:2])]:
+        with pytest.raises(ValueError):
+            b.pa_kv_append_q4(*bad, workspace=ws)
+    with pytest.raises(ValueError):
+        b.pa_kv_read_q4(slots[:, None], pool, pool, workspace=ws)
+    with pytest.raises(ValueError):
+        b.pa_kv_read_q4(slots, pool, pool, k_out=rows[:2], v_out=rows, workspace=ws)
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    one = torch.ones(2, dtype=torch.int32)
+    ind = torch.arange(3, dtype=torch.int32)
+    tab = torch.zeros(2, 1, dtype=torch.int32)
+    for kw in [dict(seq_lens_host=[1]), dict(qo_indptr_host=[0, 1]), dict(out=q[:1]),
+               dict(lse=torch.zeros(2, 4))]:
+        with pytest.raises(ValueError):
+            b.pa_attention_varlen_q4(q, pool, pool, tab, one, ind, 0.1, workspace=ws, **kw)
+    with pytest.raises(TypeError):
+        b._data(rows, torch.uint8, "rows", 0)
+    with pytest.raises(ValueError, match="current device"):
+        b._data(rows, torch.bfloat16, "rows", 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        b._data(rows.transpose(0, 1), torch.bfloat16, "rows", 0)
