@@ -8,8 +8,8 @@
 //
 // Work.  As in the bf16 decode kernel the rows' pages are laid end to end for
 // each kv head and cut into equal segments, one CTA per SM and segment; each
-// warp streams its share of the segment through a ring of its own (1280-byte
-// bulk copies, two pages at a time), so warps never wait for one another.  A
+// warp streams its share of the segment through a ring of its own (asynchronous
+// copies, two pages at a time), so warps never wait for one another.  A
 // row cut between warps is put together in shared memory by the last of them
 // to finish, a row cut between CTAs in the workspace by the last CTA; parts are
 // always added in page order, so results do not depend on who came last.
@@ -75,7 +75,6 @@ struct __align__(128) Smem {
   uint8_t ring[S::kWarps][S::kRingBytes > S::kPartBytes ? S::kRingBytes : S::kPartBytes];
   uint8_t part[S::kWarps][S::kPartBytes];  // a warp's part of its first item
   float part_m[S::kWarps][2][S::kT * S::kTileCols], part_l[S::kWarps][2][S::kT * S::kTileCols];
-  uint64_t full[S::kWarps][kStages];
   int32_t ids[kQ4MaxPagesPerCta];
   Item items[kQ4MaxItemsPerCta];
   int arrived[kQ4MaxItemsPerCta];  // warps done with their part of the item
@@ -92,6 +91,9 @@ __device__ __forceinline__ float4* part_of(Smem<kTiles>& sm, int warp, int slot)
   return reinterpret_cast<float4*>(slot == 0 ? sm.part[warp] : sm.ring[warp]);
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -160,18 +162,13 @@ struct Part {
 
 // Log-sum-exp merge of n parts, in order.  m_at(i, c), l_at(i, c): maximum and
 // weight sum of column c of this lane in part i; row(i): the part's vectors of
-// this lane at stride 32.  The eight lanes of a column read the maxima of eight
-// parts at a time; then the values of four parts are in flight at once.
+// this lane at stride 32.  The loads of a batch of parts are all in flight
+// before any is used.
 template <int kCols, class M, class L, class Row>
 __device__ __forceinline__ void merge_parts(Part<kCols>& out, int n, int lane, M&& m_at, L&& l_at, Row&& row) {
-  const int r = lane >> 2;
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
-    float mx = -INFINITY;
-    for (int i = r; i < n; i += 8) mx = fmaxf(mx, m_at(i, c));
-#pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    out.m[c] = mx;
+    out.m[c] = -INFINITY;
     out.l[c] = 0.f;
   }
 #pragma unroll
@@ -179,7 +176,7 @@ __device__ __forceinline__ void merge_parts(Part<kCols>& out, int n, int lane, M
   constexpr int kBatch = kCols == 1 ? 4 : 2;
   for (int i0 = 0; i0 < n; i0 += kBatch) {
     float4 x[kBatch][4 * kCols];
-    float w[kBatch][kCols];
+    float mi[kBatch][kCols], li[kBatch][kCols];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = min(i0 + u, n - 1);
@@ -188,21 +185,35 @@ __device__ __forceinline__ void merge_parts(Part<kCols>& out, int n, int lane, M
       for (int v = 0; v < 4 * kCols; ++v) x[u][v] = src[32 * v + lane];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const float f = (i0 + u >= n || out.m[c] == -INFINITY) ? 0.f : fast_exp2(m_at(i, c) - out.m[c]);
-        w[u][c] = f;
-        out.l[c] = fmaf(f, l_at(i, c), out.l[c]);
+        mi[u][c] = i0 + u < n ? m_at(i, c) : -INFINITY;
+        li[u][c] = l_at(i, c);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
+    for (int c = 0; c < kCols; ++c) {
+      float mx = out.m[c];
 #pragma unroll
-      for (int v = 0; v < 4 * kCols; ++v) {
-        const float f = w[u][v >> 2];
-        out.o[v].x = fmaf(f, x[u][v].x, out.o[v].x);
-        out.o[v].y = fmaf(f, x[u][v].y, out.o[v].y);
-        out.o[v].z = fmaf(f, x[u][v].z, out.o[v].z);
-        out.o[v].w = fmaf(f, x[u][v].w, out.o[v].w);
+      for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, mi[u][c]);
+      if (mx == -INFINITY) continue;  // every part so far is empty
+      const float f = fast_exp2(out.m[c] - mx);  // -inf -> 0
+      out.m[c] = mx;
+      out.l[c] *= f;
+#pragma unroll
+      for (int v = 4 * c; v < 4 * c + 4; ++v)
+        out.o[v] = make_float4(out.o[v].x * f, out.o[v].y * f, out.o[v].z * f, out.o[v].w * f);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float w = fast_exp2(mi[u][c] - mx);
+        out.l[c] = fmaf(w, li[u][c], out.l[c]);
+#pragma unroll
+        for (int v = 4 * c; v < 4 * c + 4; ++v) {
+          out.o[v].x = fmaf(w, x[u][v].x, out.o[v].x);
+          out.o[v].y = fmaf(w, x[u][v].y, out.o[v].y);
+          out.o[v].z = fmaf(w, x[u][v].z, out.o[v].z);
+          out.o[v].w = fmaf(w, x[u][v].w, out.o[v].w);
+        }
       }
+    }
   }
 }
 
@@ -218,13 +229,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   const int Hkv = p.num_kv_heads;
   const int kvh = b % Hkv, sidx = b / Hkv;
   const int S0 = sidx * plan.seg;
-  const int npg = min(plan.total, S0 + plan.seg) - S0;  // pages of this CTA's segment
+  const int npg = min(plan.total, S0 + plan.seg) - S0;  // pages of this CTA's segment (by_row: at most)
   if (npg <= 0) return;
-  if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[w][s], 1);
-    fence_mbar_init();
-  }
   for (int i = tid; i < kQ4MaxItemsPerCta; i += kThreads) sm.arrived[i] = 0;
   // ---- item table of the segment (one warp, 32 rows per round); it comes
   // from the kernel parameters alone, so it is built before the wait for the
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       const int p0 = (k0 + lane == 0) ? at.y : 0;
       int4 row = make_int4(0, 0, 0, 0);  // request, seq_len, first query token, queries
       int size = 0;
-      if (item < plan.n_rows) {
+      if (item < plan.n_rows && (!plan.by_row || item == at.x)) {
         row = plan.row[item];
         size = max((row.y + kPage - 1) / kPage - p0, 0);
       }
@@ -267,14 +273,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       if (lead < 32 || base_q >= npg) break;
     }
     if (lane == 0) {
-      if (base_q < npg) record_error(p.err, PA_ERR_DEVICE_INDEX);  // not planned on the host
+      if (base_q < npg && !plan.by_row) record_error(p.err, PA_ERR_DEVICE_INDEX);  // not planned on the host
       sm.n_items = n_it;
     }
   }
   __syncthreads();
   pdl_wait();
   const int n_items = sm.n_items;
-  if (n_items == 0) return;  // nothing covered (recorded above); no copy was issued
+  if (n_items == 0) return;  // nothing covered (recorded above)
   // ---- block ids of the segment's pages; a page with an id outside the pool
   // (or past the table) is recorded and skipped
   const int n_cov = sm.items[n_items - 1].q_start + sm.items[n_items - 1].n;
@@ -315,29 +321,39 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   const uint8_t* vbase = reinterpret_cast<const uint8_t*>(p.v_cache);
   // slab of the page `half` of stage s: K, then V one slab further
   auto slab_at = [&](int s, int half) { return sm.ring[warp] + (s * kPair + half) * (2 * kQ4Slab); };
-  // Pages a + 2 i and a + 2 i + 1 -> stage i % kStages.  Lanes 0 .. 3 issue the
-  // K and V slab of the two pages; a page with a bad id is fetched from block 0
-  // and does not count.
+  // Pages a + 2 i and a + 2 i + 1 -> stage i % kStages, one copy group per call
+  // (empty past the end).  A lane copies bytes 512 c + 16 lane of each page's
+  // two slabs laid end to end; a page with a bad id is fetched from block 0 and
+  // does not count.  (One bulk copy per slab instead: 246 us against 230 for 8
+  // rows of 131072 tokens; copies of 1280 bytes start too slowly.)
   const int n_pairs = (e - a + kPair - 1) / kPair;
   auto issue = [&](int i) {
-    if (lane < 2 * kPair) {
-      const int s = i % kStages, q = a + kPair * i + (lane >> 1);
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][s], (q + 1 < e ? 4 : 2) * kQ4Slab);
+#pragma unroll
+    for (int h = 0; h < kPair; ++h) {
+      const int q = a + kPair * i + h;
       if (q < e) {
-        const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab;
-        bulk_g2s(slab_at(s, lane >> 1) + (lane & 1) * kQ4Slab, ((lane & 1) ? vbase : kbase) + off, kQ4Slab,
-                 &sm.full[warp][s]);
+        const size_t off = ((size_t)max(sm.ids[q], 0) * Hkv + kvh) * kQ4Slab + 16 * lane;
+        const uint8_t* ks = kbase + off;
+        const uint8_t* vs = vbase + off;
+        const uint32_t dst = smem_addr(slab_at(i % kStages, h)) + 16 * lane;
+        static_assert(kQ4Slab == 1280, "five copies per lane, the third from both slabs");
+        copy16(dst, ks);
+        copy16(dst + 512, ks + 512);
+        copy16(dst + 1024, lane < 16 ? ks + 1024 : vs - 256);
+        copy16(dst + 1536, vs + 256);
+        copy16(dst + 2048, vs + 768);
       }
     }
+    cp_async_commit();
   };
-  for (int i = 0; i < min(n_pairs, kStages); ++i) issue(i);
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) issue(i);
 
   const int r = lane >> 2;   // token slot (r, r + 8) in the scores; dim row in the output
   const int cq = lane & 3;   // the lane's columns in scores and output: head cq, or 2 cq and 2 cq + 1
   // matrix-load address of lane l: matrix (group) l / 8, row (token) l % 8
   const uint32_t ld_at = (uint32_t)q4_code_at(lane & 7, lane >> 3);
-  int issued = min(n_pairs, kStages);
-  bool gave_up = false;
+  int issued = kStages;
 
   for (; k < n_items; ++k) {
     const Item& it = sm.items[k];
@@ -383,11 +399,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
     for (int q = i0; q < i1;) {
       const int j = q - a, i = j / kPair, s = i % kStages;
-      if (!mbar_wait_bounded(&sm.full[warp][s], (uint32_t)(i / kStages) & 1u)) {
-        record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
-        gave_up = true;
-        break;
-      }
+      cp_async_wait<kStages - 1>();  // this lane's copies of pair i
+      __syncwarp();                  // and the others'
       // two pages at once where the pair lies in the row, else one: page 0 is
       // q, page 1 its neighbour in the stage, of which no token counts then
       const int half = j & 1, n = (half == 0 && q + 1 < i1) ? 2 : 1;
@@ -534,14 +547,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       // the pair is done with: refill its stage
       if ((q - a) % kPair == 0) {
         __syncwarp();
-        if (issued < n_pairs) {
-          fence_proxy_async_smem();
-          issue(issued);
-          ++issued;
-        }
+        issue(issued);
+        ++issued;
       }
     }
-    if (gave_up) break;
 
     // ---- this warp's part of the item: in a column, value 4 g + i is dim 32 g
     // + 8 (r / 2) + r % 2 + 2 i, unnormalised
@@ -675,12 +684,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     }
   }
 
-  if (gave_up && lane == 0) {
-    // a wait ran out: let the last copies issued into each stage land
-    // (bounded), then leave
-    for (int i = max(0, issued - kStages); i < issued; ++i)
-      mbar_wait_bounded(&sm.full[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
-  }
 }
 
 std::atomic<bool> g_attr_set[6][kMaxDevices];
@@ -699,13 +702,14 @@ cudaError_t launch(const DecodeParams& p, const Plan& plan, int grid, bool overl
 // one takes 1.3 us less (its parameters are copied to the device and fetched by
 // every SM), and most batches fit it.
 template <int kTiles>
-cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int grid, bool overlap,
-                         std::atomic<bool>* done, cudaStream_t stream) {
+cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int grid, bool by_row,
+                         bool overlap, std::atomic<bool>* done, cudaStream_t stream) {
   const int segs = grid / p.num_kv_heads;
   auto fill = [&](auto& d) {
     d.n_rows = plan.n_rows;
     d.seg = plan.seg;
     d.total = plan.total;
+    d.by_row = by_row ? 1 : 0;
     for (int i = 0; i < plan.n_rows; ++i) d.row[i] = make_int4(plan.rows[i], plan.seq[i], plan.tok[i], n_q[i]);
     for (int i = 0; i < segs; ++i) d.start[i] = make_int2(plan.first_row[i], plan.first_page[i]);
   };
@@ -722,11 +726,11 @@ cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const in
 }  // namespace
 
 cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int tiles, int grid,
-                             bool overlap, cudaStream_t stream) {
+                             bool by_row, bool overlap, cudaStream_t stream) {
   std::atomic<bool>* done = &g_attr_set[0][0];
-  if (tiles == 0) return launch_tiles<0>(p, plan, n_q, grid, overlap, done, stream);
-  if (tiles <= 2) return launch_tiles<2>(p, plan, n_q, grid, overlap, done + 2 * kMaxDevices, stream);
-  return launch_tiles<3>(p, plan, n_q, grid, overlap, done + 4 * kMaxDevices, stream);
+  if (tiles == 0) return launch_tiles<0>(p, plan, n_q, grid, by_row, overlap, done, stream);
+  if (tiles <= 2) return launch_tiles<2>(p, plan, n_q, grid, by_row, overlap, done + 2 * kMaxDevices, stream);
+  return launch_tiles<3>(p, plan, n_q, grid, by_row, overlap, done + 4 * kMaxDevices, stream);
 }
 
 }  // namespace pa

@@ -105,7 +105,7 @@ struct DecodePlan {
 template <int R, int C>
 struct Q4Plan {
   int32_t n_rows, seg, total;
-  int32_t pad;
+  int32_t by_row;  // a segment holds pages of its first row only
   int4 row[R];    // request, seq_len, first query token, queries
   int2 start[C];  // a segment's first row and that row's first page
 };
@@ -290,7 +290,7 @@ cudaError_t launch_decode(const DecodeParams& p, const DecodePlan& plan, int gri
 // q4 pages: rows of n_q[i] queries (i: plan row), all of the class `tiles`; a
 // plan in whole warp segments of q4_decode_warps(tiles) warps
 cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int tiles, int grid,
-                             bool overlap, cudaStream_t stream);
+                             bool by_row, bool overlap, cudaStream_t stream);
 // warp_granular: the warp-granular kernel (grid: one CTA per SM at most; no
 // segment may hold more than kWgMaxItemsPerCta rows or kWgMaxPagesPerCta
 // pages), else the CTA-granular one (windows of rows)

@@ -399,6 +399,58 @@ int plan_decode(const int32_t* rows, int n, const int32_t* seq_lens_host, const 
   }
 }
 
+// A plan of the q4 decode kernel whose segments each hold pages of one row only
+// (segment boundaries at the rows' starts), for batches with few rows.  A CTA
+// takes ~0.06 us per page when the SMs are not all busy; a row cut between CTAs
+// costs ~2.6 us at its end and 0.25 us per piece (measured: one row of 513
+// tokens 7.7 us in one CTA against 9.6 in three; of 2048 tokens 9.7 us in four,
+// 11.0 in eight, 11.4 in one).  Of the segment lengths that fit max_seg segments
+// per kv head and whole warp segments (unit), and the plan given (made by
+// plan_decode), the cheapest by these is taken: replaces `plan` and returns its
+// grid, or 0 to keep the plan.
+int plan_row_segments(const int32_t* rows, int n, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
+                      int num_kv_heads, int max_seg, int unit, int max_pages, pa::DecodePlan& plan) {
+  if (n > max_seg) return 0;
+  int64_t total = 0;
+  int longest = 0;
+  for (int i = 0; i < n; ++i) {
+    const int pages = pages_of(seq_lens_host[rows[i]]);
+    total += pages;
+    longest = std::max(longest, pages);
+  }
+  auto cost = [](int seg, int pieces) { return 0.06 * seg + (pieces > 1 ? 2.6 + 0.25 * pieces : 0.0); };
+  // rows of a stream cut in equal segments take one piece more than they must
+  double best = cost(plan.seg, (longest + plan.seg - 1) / plan.seg + (n > 1 ? 1 : 0));
+  int best_seg = 0, best_n = 0;
+  for (int64_t seg = ((total + max_seg - 1) / max_seg + unit - 1) / unit * unit; seg <= max_pages && 0.06 * seg < best;
+       seg += unit) {
+    int64_t ns = 0;
+    for (int i = 0; i < n; ++i) ns += (pages_of(seq_lens_host[rows[i]]) + seg - 1) / seg;
+    if (ns > max_seg) continue;
+    const double c = cost((int)seg, (int)((longest + seg - 1) / seg));
+    if (c < best) {
+      best = c;
+      best_seg = (int)seg;
+      best_n = (int)ns;
+    }
+  }
+  if (best_seg == 0) return 0;
+  plan.n_rows = n;
+  plan.seg = best_seg;
+  plan.total = best_n * best_seg;
+  int sidx = 0;
+  for (int i = 0; i < n; ++i) {
+    plan.rows[i] = rows[i];
+    plan.seq[i] = seq_lens_host[rows[i]];
+    plan.tok[i] = qo_indptr_host[rows[i]];
+    for (int first = 0; first < pages_of(plan.seq[i]); first += best_seg, ++sidx) {
+      plan.first_row[sidx] = i;
+      plan.first_page[sidx] = first;
+    }
+  }
+  return best_n * num_kv_heads;
+}
+
 // The decode launch over rows[0..n): segments of whole pages for the
 // CTA-granular kernel; when they are long enough for four warp segments of
 // kMinWarpSegPages (or a pass runs beside the launch, or the timeout
@@ -813,9 +865,16 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
           if (grid < 0) return fail(PA_ERR_UNSUPPORTED, "no decode plan within the kernel limits");
           d0 += (size_t)n;
           if (grid == 0) continue;
+          const int row_grid =
+              g_forced_ctas.load() > 0
+                  ? 0
+                  : plan_row_segments(r0, n, seq_lens_host, qo_indptr_host, num_kv_heads,
+                                      std::min(std::min(sm_count(), cap) / num_kv_heads, pa::kPlanMaxCtas),
+                                      pa::q4_decode_warps(cls), pa::kQ4MaxPagesPerCta, plan);
+          if (row_grid > 0) grid = row_grid;
           for (int i = 0; i < n; ++i) n_q[i] = qo_indptr_host[r0[i] + 1] - qo_indptr_host[r0[i]];
           s = run_launch(PA_KERNEL_DECODE, "decode_q4", stream,
-                         [&] { return pa::launch_decode_q4(dp, plan, n_q, cls, grid, overlap, stream); });
+                         [&] { return pa::launch_decode_q4(dp, plan, n_q, cls, grid, row_grid > 0, overlap, stream); });
           if (s != PA_OK) return s;
           overlap = true;
         }

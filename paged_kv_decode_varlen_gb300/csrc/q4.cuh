@@ -46,9 +46,18 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-// A (D, Z) word -> (D, D) and (Z, Z).
-__device__ __forceinline__ uint32_t q4_dup_d(uint32_t dz) { return __byte_perm(dz, dz, 0x1010); }
-__device__ __forceinline__ uint32_t q4_dup_z(uint32_t dz) { return __byte_perm(dz, dz, 0x3232); }
+// A (D, Z) word -> (D, D) and (Z, Z); as moves of halves, which the FMA can take
+// as an operand's halves (a byte permute it cannot: 2.7 % of a long decode).
+__device__ __forceinline__ uint32_t q4_dup_d(uint32_t dz) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(dz));
+  return r;
+}
+__device__ __forceinline__ uint32_t q4_dup_z(uint32_t dz) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(dz));
+  return r;
+}
 
 // The eight values of a code word, as four bf16 pairs in dim order.
 __device__ __forceinline__ uint4 q4_word_values(uint32_t w, uint32_t dz) {
