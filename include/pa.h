@@ -187,6 +187,7 @@ pa_status pa_attention_varlen_q8(const void* q, const void* k_cache, const void*
  * with its scales in the slot's page.  Same arguments, validation and error
  * word as pa_kv_append; k_cache and v_cache are q4 pools (16-byte aligned).
  * With duplicate slots the stored row may mix the rows written to it.
+ * n_tokens * num_kv_heads must be below 2^31 (PA_ERR_UNSUPPORTED).
  */
 pa_status pa_kv_append_q4(const void* k_new, const void* v_new, const int64_t* slot_mapping, int64_t n_tokens,
                           void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
@@ -211,7 +212,8 @@ pa_status pa_kv_append_q4(const void* k_new, const void* v_new, const int64_t* s
  *                used.
  * n_tokens = 0 is valid and launches nothing.
  * Errors: PA_ERR_INVALID_ARG (n_tokens < 0, null or misaligned pointers),
- *   PA_ERR_UNSUPPORTED (shape), PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA.
+ *   PA_ERR_UNSUPPORTED (shape, or n_tokens * num_kv_heads >= 2^31),
+ *   PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA.
  */
 pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const void* k_cache, const void* v_cache,
                         int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void* k_out,

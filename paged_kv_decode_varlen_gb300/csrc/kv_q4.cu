@@ -11,7 +11,8 @@
 // Both kernels move bytes: a (token, kv head) row is 256 B of bf16 and 80 B of
 // a page, for K and for V.  Sixteen threads take one row, eight dims (one code
 // word) each: 16-byte accesses on the bf16 side, 64 contiguous bytes of codes
-// and 16 of scales on the other.
+// and 16 of scales on the other.  A thread has kRows rows in flight, since one
+// row is a chain of two loads (its slot, its bytes).
 #include "internal.h"
 #include "q4.cuh"
 
@@ -20,121 +21,198 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanesPerRow = kHeadDim / 8;  // 16: one code word each
-constexpr int kRowsPerCta = kThreads / kLanesPerRow;
+constexpr int kRowsPerPass = kThreads / kLanesPerRow;
 
-// One lane's 8 values -> its code word and its group's (D, Z) word; the
-// group's 32 values lie in 4 adjacent lanes of `mask`.
-__device__ __forceinline__ void quantize8_q4(const uint4& x, unsigned mask, uint32_t& codes, uint32_t& dz) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float v[8];
+// The least and greatest of a group's 32 values: 8 in each of 4 adjacent
+// lanes, as bf16 pairs.  Across lanes both travel in one word, (least,
+// -greatest), of which the lesser is kept.
+__device__ __forceinline__ void group_range(const uint4& x, float& lo, float& hi) {
+  auto b2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  const __nv_bfloat162 mn = __hmin2(__hmin2(b2(x.x), b2(x.y)), __hmin2(b2(x.z), b2(x.w)));
+  const __nv_bfloat162 mx = __hmax2(__hmax2(b2(x.x), b2(x.y)), __hmax2(b2(x.z), b2(x.w)));
+  __nv_bfloat162 m = __halves2bfloat162(__hmin(mn.x, mn.y), __hneg(__hmax(mx.x, mx.y)));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16lo(w[i]);
-    v[2 * i + 1] = bf16hi(w[i]);
-  }
-  float lo = v[0], hi = v[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
-  }
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-  }
-  const __nv_bfloat16 db = __float2bfloat16_rn(__fmul_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 16.f));
-  const float d = __bfloat162float(db);
-  const __nv_bfloat16 zb = __float2bfloat16_rn(__fsub_rn(lo, d));
-  const float z = __bfloat162float(zb);
-  codes = 0u;
-  if (d != 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = rintf(__fmul_rn(__fdiv_rn(__fsub_rn(v[i], z), d), 16.f) - 16.f);
-      codes |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * (i >> 1) + 16 * (i & 1));
-    }
-  }
-  dz = (uint32_t)__bfloat16_as_ushort(db) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
+  for (int o = 1; o <= 2; o <<= 1) m = __hmin2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  lo = __bfloat162float(m.x);
+  hi = -__bfloat162float(m.y);
 }
 
+// One lane's 8 values -> its code word and its group's (D, Z) word.
+__device__ __forceinline__ void quantize8_q4(const uint4& x, uint32_t& codes, uint32_t& dz) {
+  float lo, hi;
+  group_range(x, lo, hi);
+  const __nv_bfloat16 db = __float2bfloat16_rn(__fmul_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 16.f));
+  const __nv_bfloat16 zb = __float2bfloat16_rn(__fsub_rn(lo, __bfloat162float(db)));
+  dz = (uint32_t)__bfloat16_as_ushort(db) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
+  const float d = __bfloat162float(db) * 0.0625f, z = __bfloat162float(zb);  // a sixteenth of D: the step
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // n = (x - Z) / step rounded to an integer is 16 more than the code.  Clamped
+  // to [16, 31], it is rounded by adding 1.5 x 2^23 (binary32 keeps no fraction
+  // there) and left in the sum's low bits; four sums b_i = K + 16 + c_i add up to
+  // sum 16^i c_i and a constant.
+  constexpr uint32_t kBase = (0x4b400000u + 16u) * 0x1111u;
+  uint32_t half[2] = {0u, 0u};  // even and odd dims' codes
+  if (d >= 7.8886091e-31f && d <= 1.2676506e+30f) {  // 2^-100 .. 2^100: x - Z is between 0 and 48 steps
+    // (x - Z) / step rounded to nearest, from r = 1 / step rounded to nearest:
+    // one correction of t r by the exact remainder (Markstein, "Computation of
+    // elementary functions on the IBM RISC System/6000 processor", 1990).  A
+    // group shares the reciprocal, and pairs of values the instructions: the
+    // kernel is bound by issue (with a division per value 24 us for 7,021
+    // tokens, 17.6 us with this and no pairs).
+    const float r = __frcp_rn(d);
+    const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d), nz2 = make_float2(-z, -z);
+    const float2 magic = make_float2(12582912.f, 12582912.f);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const float2 t = __fadd2_rn(bf16x2_to_f2(w[i]), nz2);
+      float2 q = __fmul2_rn(t, r2);
+      q = __ffma2_rn(__ffma2_rn(q, nd2, t), r2, q);
+      q = make_float2(fminf(fmaxf(q.x, 16.f), 31.f), fminf(fmaxf(q.y, 16.f), 31.f));
+      q = __fadd2_rn(q, magic);
+      half[0] = half[0] * 16u + __float_as_uint(q.x);
+      half[1] = half[1] * 16u + __float_as_uint(q.y);
+    }
+    half[0] -= kBase;
+    half[1] -= kBase;
+  } else if (d != 0.f) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float v = e ? bf16hi(p) : bf16lo(p);
+        // 16 ((x - Z) / D): the quotient by D, as a step may be too small for binary32
+        const float n = __fmul_rn(__fdiv_rn(__fsub_rn(v, z), __bfloat162float(db)), 16.f);
+        half[e] |= (__float_as_uint(__fadd_rn(fminf(fmaxf(n, 16.f), 31.f), 12582912.f)) & 15u) << (4 * i);
+      }
+    }
+  }
+  codes = (half[0] & 0xffffu) | (half[1] << 16);
+}
+
+// Row indices fit 32 bits: 2^31 rows of bf16 would be 512 GiB.
+struct Row {
+  uint32_t row;   // token * kv heads + head
+  uint32_t tok;
+  int head;
+  bool exists;
+};
+template <int kRows>
+__device__ __forceinline__ Row row_of(int u, uint32_t rows, int num_kv_heads) {
+  Row x;
+  x.row = (blockIdx.x * kRows + u) * kRowsPerPass + threadIdx.x / kLanesPerRow;
+  x.exists = x.row < rows;
+  x.tok = x.row / (uint32_t)num_kv_heads;
+  x.head = (int)(x.row - x.tok * (uint32_t)num_kv_heads);
+  return x;
+}
+
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) kv_append_q4_kernel(const AppendParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t rows = p.n_tokens * p.num_kv_heads;
-  const int64_t stride = (int64_t)gridDim.x * kRowsPerCta;
+  const uint32_t rows = (uint32_t)(p.n_tokens * p.num_kv_heads);
   const int l = threadIdx.x % kLanesPerRow;
-  const unsigned mask = 0xffffu << (threadIdx.x & 16);  // the 16 lanes of this row
   uint8_t* kc = reinterpret_cast<uint8_t*>(p.k_cache);
   uint8_t* vc = reinterpret_cast<uint8_t*>(p.v_cache);
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kLanesPerRow; row < rows; row += stride) {
-    const int64_t tok = row / p.num_kv_heads;
-    const int h = (int)(row % p.num_kv_heads);
-    const int64_t slot = p.slot_mapping[tok];
-    if (slot < 0) continue;
-    const int64_t block = slot / kPage;
-    const int t = (int)(slot % kPage);
+  int64_t slot[kRows];
+  uint4 kx[kRows], vx[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const Row x = row_of<kRows>(u, rows, p.num_kv_heads);
+    slot[u] = x.exists ? p.slot_mapping[x.tok] : -1;
+    kx[u] = vx[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (x.exists) {
+      kx[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_new + (size_t)x.row * kHeadDim) + l);
+      vx[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_new + (size_t)x.row * kHeadDim) + l);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    if (__all_sync(0xffffffffu, slot[u] < 0)) continue;
+    const Row x = row_of<kRows>(u, rows, p.num_kv_heads);
+    uint32_t kcode, kdz, vcode, vdz;  // (whole warp: the groups' shuffles)
+    quantize8_q4(kx[u], kcode, kdz);
+    quantize8_q4(vx[u], vcode, vdz);
+    const int64_t block = slot[u] / kPage;
+    if (slot[u] < 0) continue;
     if (block >= p.num_blocks) {
       if (l == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
       continue;
     }
-    const size_t slab = ((size_t)block * p.num_kv_heads + h) * kQ4Slab;
+    const int t = (int)(slot[u] % kPage);
+    const size_t slab = ((size_t)block * p.num_kv_heads + x.head) * kQ4Slab;
     const size_t code_at = slab + q4_code_at(t, l >> 2) + 4 * (l & 3);
-    const size_t scale_at = slab + q4_scale_at(t, l >> 2);
-    const uint4 kx = reinterpret_cast<const uint4*>(p.k_new + row * kHeadDim)[l];
-    const uint4 vx = reinterpret_cast<const uint4*>(p.v_new + row * kHeadDim)[l];
-    uint32_t codes, dz;
-    quantize8_q4(kx, mask, codes, dz);
-    *reinterpret_cast<uint32_t*>(kc + code_at) = codes;
-    if ((l & 3) == 0) *reinterpret_cast<uint32_t*>(kc + scale_at) = dz;
-    quantize8_q4(vx, mask, codes, dz);
-    *reinterpret_cast<uint32_t*>(vc + code_at) = codes;
-    if ((l & 3) == 0) *reinterpret_cast<uint32_t*>(vc + scale_at) = dz;
+    *reinterpret_cast<uint32_t*>(kc + code_at) = kcode;
+    *reinterpret_cast<uint32_t*>(vc + code_at) = vcode;
+    if ((l & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(kc + slab + q4_scale_at(t, l >> 2)) = kdz;
+      *reinterpret_cast<uint32_t*>(vc + slab + q4_scale_at(t, l >> 2)) = vdz;
+    }
   }
 }
 
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const ReadParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t rows = p.n_tokens * p.num_kv_heads;
-  const int64_t stride = (int64_t)gridDim.x * kRowsPerCta;
+  const uint32_t rows = (uint32_t)(p.n_tokens * p.num_kv_heads);
   const int l = threadIdx.x % kLanesPerRow;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kLanesPerRow; row < rows; row += stride) {
-    const int64_t tok = row / p.num_kv_heads;
-    const int h = (int)(row % p.num_kv_heads);
-    const int64_t slot = p.slot_mapping[tok];
-    const int64_t block = slot / kPage;
-    uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
-    if (slot >= 0 && block < p.num_blocks) {
-      const int t = (int)(slot % kPage);
-      const size_t slab = ((size_t)block * p.num_kv_heads + h) * kQ4Slab;
+  int64_t slot[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const Row x = row_of<kRows>(u, rows, p.num_kv_heads);
+    slot[u] = x.exists ? p.slot_mapping[x.tok] : -1;
+  }
+  // codes and (D, Z) of K and of V; a slot outside the pool reads as zeros
+  uint32_t w[kRows][4];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const Row x = row_of<kRows>(u, rows, p.num_kv_heads);
+    const int64_t block = slot[u] / kPage;
+    w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
+    if (slot[u] >= 0 && block < p.num_blocks) {
+      const int t = (int)(slot[u] % kPage);
+      const size_t slab = ((size_t)block * p.num_kv_heads + x.head) * kQ4Slab;
       const size_t code_at = slab + q4_code_at(t, l >> 2) + 4 * (l & 3);
       const size_t scale_at = slab + q4_scale_at(t, l >> 2);
-      kx = q4_word_values(*reinterpret_cast<const uint32_t*>(p.k_cache + code_at),
-                          *reinterpret_cast<const uint32_t*>(p.k_cache + scale_at));
-      vx = q4_word_values(*reinterpret_cast<const uint32_t*>(p.v_cache + code_at),
-                          *reinterpret_cast<const uint32_t*>(p.v_cache + scale_at));
-    } else if (slot >= 0 && l == 0) {
+      w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache + code_at));
+      w[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache + scale_at));
+      w[u][2] = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache + code_at));
+      w[u][3] = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache + scale_at));
+    } else if (slot[u] >= 0 && l == 0) {
       record_error(p.err, PA_ERR_DEVICE_INDEX);
     }
-    reinterpret_cast<uint4*>(p.k_out + row * kHeadDim)[l] = kx;
-    reinterpret_cast<uint4*>(p.v_out + row * kHeadDim)[l] = vx;
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const Row x = row_of<kRows>(u, rows, p.num_kv_heads);
+    if (!x.exists) continue;
+    __stcs(reinterpret_cast<uint4*>(p.k_out + (size_t)x.row * kHeadDim) + l, q4_word_values(w[u][0], w[u][1]));
+    __stcs(reinterpret_cast<uint4*>(p.v_out + (size_t)x.row * kHeadDim) + l, q4_word_values(w[u][2], w[u][3]));
   }
 }
 
-unsigned grid_for(int64_t rows) {
-  const int64_t g = (rows + kRowsPerCta - 1) / kRowsPerCta;
-  return (unsigned)(g > 65535 ? 65535 : g);
+template <int kRows>
+dim3 grid_for(int64_t rows) {
+  return dim3((unsigned)((rows + kRows * kRowsPerPass - 1) / (kRows * kRowsPerPass)));
 }
 
 }  // namespace
 
+// A thread takes several rows only when there are CTAs enough for every SM
+// several times over; before that more CTAs are worth more.
+constexpr int64_t kFewRows = 16384;
+
 cudaError_t launch_kv_append_q4(const AppendParams& p, cudaStream_t stream) {
-  return launch_pdl(kv_append_q4_kernel, dim3(grid_for(p.n_tokens * p.num_kv_heads)), dim3(kThreads), 0, stream, p);
+  const int64_t rows = p.n_tokens * p.num_kv_heads;
+  return launch_pdl(kv_append_q4_kernel<1>, grid_for<1>(rows), dim3(kThreads), 0, stream, p);
 }
 
 cudaError_t launch_kv_read_q4(const ReadParams& p, cudaStream_t stream) {
-  return launch_pdl(kv_read_q4_kernel, dim3(grid_for(p.n_tokens * p.num_kv_heads)), dim3(kThreads), 0, stream, p);
+  const int64_t rows = p.n_tokens * p.num_kv_heads;
+  if (rows <= kFewRows) return launch_pdl(kv_read_q4_kernel<1>, grid_for<1>(rows), dim3(kThreads), 0, stream, p);
+  return launch_pdl(kv_read_q4_kernel<4>, grid_for<4>(rows), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace pa

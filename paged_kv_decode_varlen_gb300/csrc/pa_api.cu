@@ -964,6 +964,8 @@ pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const voi
     return fail(PA_ERR_INVALID_ARG, "tensors must be 16-byte aligned (slot_mapping 8, workspace 4)");
   if (workspace_bytes < PA_ERROR_WORD_BYTES)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %d bytes", workspace_bytes, PA_ERROR_WORD_BYTES);
+  if (n_tokens > INT32_MAX / num_kv_heads)
+    return fail(PA_ERR_UNSUPPORTED, "%lld tokens x %d heads: more than 2^31 rows", (long long)n_tokens, num_kv_heads);
   if (n_tokens == 0) return ok();
   pa::ReadParams p;
   p.slot_mapping = slot_mapping;
@@ -1021,6 +1023,8 @@ pa_status append(const void* k_new, const void* v_new, const int64_t* slot_mappi
     return fail(PA_ERR_INVALID_ARG, "tensors must be 16-byte aligned (slot_mapping 8, workspace 4)");
   if (workspace_bytes < PA_ERROR_WORD_BYTES)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %d bytes", workspace_bytes, PA_ERROR_WORD_BYTES);
+  if (pages == Pages::kQ4 && n_tokens > INT32_MAX / num_kv_heads)
+    return fail(PA_ERR_UNSUPPORTED, "%lld tokens x %d heads: more than 2^31 rows", (long long)n_tokens, num_kv_heads);
   if (n_tokens == 0) return ok();
   pa::AppendParams p;
   p.k_new = static_cast<const uint16_t*>(k_new);

@@ -105,6 +105,7 @@ def _read(**kw):
     (dict(P=32), b.PA_ERR_UNSUPPORTED),
     (dict(H=257), b.PA_ERR_UNSUPPORTED),
     (dict(wsb=255), b.PA_ERR_WORKSPACE_TOO_SMALL),
+    (dict(n=1 << 28), b.PA_ERR_UNSUPPORTED),   # 2^31 rows
 ])
 def test_write_and_read_refusals(call, kw, status):
     n0 = lib.pa_launch_count()
