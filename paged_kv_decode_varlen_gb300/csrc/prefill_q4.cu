@@ -10,31 +10,37 @@
 // tiles of 128 (8 pages).  The two tiles share every dequantised K and V tile,
 // and their softmaxes alternate on the tensor cores: while tile A's warps turn
 // scores into weights, B's products run.
-//   Bound.  Per key tile the four products of 128 x 128 x 128 take 2048 cycles
-// of the tensor cores, the exponentials of both tiles and the instructions of
-// all warps some 1900 of the schedulers', so neither waits long for the other.
+//   Bound.  Per key tile the products take 2560 cycles of the tensor cores, the
+// instructions of all warps some 2200 of the schedulers'.
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory
-// lane = row).  8: copies Q (TMA), owns the tensor memory, one thread issues
-// the products as their inputs become ready.  9-15: producers.  A unit of
-// their work is one page's K or V slab: each lane reads two 16-byte pieces of
-// codes (tokens t and t + 8 of one group) and their (D, Z), three units ahead,
-// and writes 64 bf16 values into the 128-byte-swizzled operand tile.  A key
-// tile is 16 units, dealt out to the seven warps in turn.  (Dequantised once
-// per CTA in registers: a second copy of the cache in bf16 is never made.)
+// lane = row).  8 and 9: issue the products of A and of B (8 also copies Q by
+// TMA and owns the tensor memory).  10-15: producers.  A unit of their work is
+// one page's K or V slab: each lane reads two 16-byte pieces of codes (tokens t
+// and t + 8 of one group) and their (D, Z), three units ahead, and writes 64
+// bf16 values into the 128-byte-swizzled operand tile.  A key tile is 16 units,
+// dealt out to the six warps in turn.  (Dequantised once per CTA in registers: a
+// second copy of the cache in bf16 is never made.)
+//   With the schedulers busy an issuing warp is slow (some 20 cycles per
+// instruction), so each query tile has its own, in a fixed order of few waits: one
+// warp that polled for whichever product was ready took 3000 cycles per round of
+// four.
 //
-// Tensor memory: scores of A and B (128 columns each), outputs of A and B (128
-// each).  A tile's weights (bf16 pairs, the A operand of the PV product)
-// overwrite its scores, so its next score product is issued only after its PV
-// product has completed.  The softmax takes the scores once, 32 columns at a
-// time, against a running maximum that is re-based only when it grows by more
-// than 2^8.  Weights are
-// rounded to bf16, as the tensor cores take them; their sum is kept in
-// binary32 from the unrounded ones, as are scores, maxima and outputs.
+// Tensor memory: per query tile two score buffers of 64 keys and the output,
+// 128 columns; that is all 512.  Scores are therefore made 64 keys at a time
+// (a sub-tile), and a sub-tile's weights (bf16 pairs, the A operand of the PV
+// product) overwrite its scores: the scores of sub-tile i + 1 are there when
+// the softmax has finished sub-tile i, and those of i + 2 follow the PV product
+// of i.  (With one buffer of 128 keys each score product waited for the PV
+// product before it: 4100 cycles per 128 keys against 2900, although 64 columns
+// of B make a score product read its Q tile at the shared memory's limit, 48
+// cycles for 32.)  The softmax takes the scores once, 32 columns at a time,
+// against a running maximum that is re-based only when it grows by more than
+// 2^8.  Weights are rounded to bf16, as the tensor cores take them; their sum is
+// kept in binary32 from the unrounded ones, as are scores, maxima and outputs.
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its
 // copies and products finish (bounded), frees its tensor memory and returns.
-#include <limits.h>
 #include <math.h>
 #include <stddef.h>
 
@@ -54,14 +60,15 @@ constexpr int kPagesPerTile = kKeys / kPage;
 constexpr int kHalf = 128 * 128;             // 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kKStages = 2, kVStages = 2;
-constexpr int kMmaWarp = 8, kProducer0 = 9, kProducers = 7;
+constexpr int kMmaWarp = 8, kProducer0 = 10, kProducers = 6;  // (kMmaWarp + 1: tile B)
 constexpr int kThreads = (kProducer0 + kProducers) * 32;
 constexpr int kUnits = 2 * kPagesPerTile;    // slabs of a key tile
 constexpr int kAhead = 3;                    // units a producer warp reads ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
 constexpr float kRescaleSlack = 8.f;
-constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys, false);
+constexpr int kSub = 64;                     // keys of a score product
+constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
 static_assert(kRows == 128 && kKeys == 128 && kQ4TileTokens == 2 * kTok, "tile shape");
 static_assert(2 * 32 * 16 == kQ4Codes, "two pieces of codes per lane");
@@ -74,8 +81,8 @@ struct __align__(1024) Smem {
   uint64_t bar_q;
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2], pv_done[2];  // per query tile, phase j for key tile j
-  uint64_t drained;  // every product issued has completed
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per query tile and buffer: phase i / 2 for sub-tile i
+  uint64_t drained[2];  // every product issued by a query tile's warp has completed
   uint64_t bad[8];   // byte u of entry j % 8: page u of key tile j has a block id outside the pool
   uint32_t tmem;
   int abort;
@@ -203,7 +210,7 @@ struct Job {
   const int32_t* table;
 };
 
-// Producer warp w: units w, w + 7, ... of the job (unit u: key tile u / 16, K
+// Producer warp w: units w, w + 6, ... of the job (unit u: key tile u / 16, K
 // pages 0 .. 7, then V pages 0 .. 7).
 __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const uint8_t* k_cache,
                                         const uint8_t* v_cache, int num_kv_heads, int64_t num_blocks, int n_tiles,
@@ -323,23 +330,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int n_tiles = (job.keys + kKeys - 1) / kKeys;
-  const int n_x = job.nq > kTok ? 2 : 1;  // query tiles
+  const int n_sub = (job.keys + kSub - 1) / kSub;  // sub-tiles, for both query tiles
+  const int n_x = job.nq > kTok ? 2 : 1;          // query tiles
   if (warp == kMmaWarp && lane == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&sm.k_full[s], kPagesPerTile);
-      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.k_empty[s], n_x);
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&sm.v_full[s], kPagesPerTile);
-      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.v_empty[s], n_x);
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], kRows);
-      mbar_init(&sm.pv_done[x], 1);
-    }
-    mbar_init(&sm.drained, 1);
+    for (int x = 0; x < 2; ++x)
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sm.s_full[x][b], 1);
+        mbar_init(&sm.p_full[x][b], kRows);
+        mbar_init(&sm.pv_done[x][b], 1);
+      }
+    for (int x = 0; x < 2; ++x) mbar_init(&sm.drained[x], 1);
     sm.abort = 0;
     fence_mbar_init();
     mbar_arrive_expect_tx(&sm.bar_q, n_x * kTileBytes);
@@ -360,66 +369,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducer0) {
     produce(sm, job, warp - kProducer0, reinterpret_cast<const uint8_t*>(p.k_cache),
             reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles, p.err);
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------- MMA issuer
-    // The whole warp runs this loop (so that descriptors and addresses are
+  } else if (warp >= kMmaWarp) {
+    // --------------------------------------------------------- MMA issuers
+    // The whole warp runs this (so that descriptors and addresses are
     // warp-uniform values) and one elected lane issues.
-    const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024);
-    const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
-    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto issue_s = [&](int x, int j, bool frees) {
-      const uint64_t qd = q_desc + (uint32_t)x * (kTileBytes >> 4), kd = k_desc + (uint32_t)(j % kKStages) * (kTileBytes >> 4);
-      const uint32_t on = elect_one();
-#pragma unroll
-      for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-        const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
-        mma_ss_if(on, tm + kColS + x * kKeys, qd + off, kd + off, kIdescS, ks > 0);
-      }
-      commit_if(on, &sm.s_full[x]);
-      if (frees) commit_if(on, &sm.k_empty[j % kKStages]);
-    };
-    auto issue_pv = [&](int x, int j, bool frees) {
-      const uint64_t vd = v_desc + (uint32_t)(j % kVStages) * (kTileBytes >> 4);
-      const uint32_t on = elect_one();
-#pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
-        mma_ts_if(on, tm + kColO + x * kHeadDim, tm + kColS + x * kKeys + 8 * ks, vd + ks * (2 * 1024 >> 4), kIdescO,
-                  (j > 0 || ks > 0) ? 1u : 0u);
-      commit_if(on, &sm.pv_done[x]);
-      if (frees) commit_if(on, &sm.v_empty[j % kVStages]);
-    };
-    bool ok = __all_sync(0xffffffffu, wait(sm, &sm.bar_q, 0, p.err) && wait(sm, &sm.k_full[0], 0, p.err));
-    if (ok) {
-      fence_after_sync();
-      for (int x = 0; x < n_x; ++x) issue_s(x, 0, x == n_x - 1);
-    }
-    // PV of tile A, then its next scores, then the same for B: A's softmax
-    // runs while B's products do.  (Taking whichever product was ready let the
-    // two tiles fall into step: both softmaxes, then all four products.)
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      for (int x = 0; ok && x < n_x; ++x) {
-        const bool last = x == n_x - 1;
-        ok = __all_sync(0xffffffffu, wait(sm, &sm.p_full[x], j & 1, p.err) &&
-                                         (x > 0 || wait(sm, &sm.v_full[j % kVStages], (j / kVStages) & 1, p.err)));
-        if (!ok) break;
+    const int x = warp - kMmaWarp;
+    if (x < n_x) {
+      const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
+      const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+      const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t t_s = tm + kColS + x * kKeys, t_o = tm + kColO + x * kHeadDim;
+      auto arrived = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
+      };
+      // scores of sub-tile i: 64 keys, half i & 1 of key tile i / 2
+      auto issue_s = [&](int i) {
+        const uint64_t kd =
+            k_desc + (uint32_t)((i >> 1) % kKStages) * (kTileBytes >> 4) + (uint32_t)(i & 1) * (kSub * 128 >> 4);
+        const uint32_t on = elect_one();
         fence_after_sync();
-        issue_pv(x, j, last);
-        if (j + 1 == n_tiles) continue;
-        const int j1 = j + 1;
-        // the weights lie where the scores go: PV first
-        ok = __all_sync(0xffffffffu, (x > 0 || wait(sm, &sm.k_full[j1 % kKStages], (j1 / kKStages) & 1, p.err)) &&
-                                         wait(sm, &sm.pv_done[x], j & 1, p.err));
-        if (!ok) break;
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
+          mma_ss_if(on, t_s + (i & 1) * kSub, q_desc + off, kd + off, kIdescS, ks > 0);
+        }
+        commit_if(on, &sm.s_full[x][i & 1]);
+        if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.k_empty[(i >> 1) % kKStages]);  // the tile's last use here
+      };
+      auto issue_pv = [&](int i) {
+        const uint64_t vd = v_desc + (uint32_t)((i >> 1) % kVStages) * (kTileBytes >> 4);
+        const uint32_t on = elect_one();
         fence_after_sync();
-        issue_s(x, j1, last);
+#pragma unroll
+        for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
+          mma_ts_if(on, t_o, t_s + (i & 1) * kSub + 8 * ks,
+                    vd + (uint32_t)((i & 1) * (kSub / 16) + ks) * (2 * 1024 >> 4), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
+        commit_if(on, &sm.pv_done[x][i & 1]);
+        if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.v_empty[(i >> 1) % kVStages]);
+      };
+      bool ok = arrived(&sm.bar_q, 0) && arrived(&sm.k_full[0], 0);
+      if (ok) {
+        issue_s(0);
+        if (n_sub > 1) issue_s(1);
       }
+      for (int i = 0; ok && i < n_sub; ++i) {
+        const int j = i >> 1;
+        ok = ((i & 1) || arrived(&sm.v_full[j % kVStages], j / kVStages)) && arrived(&sm.p_full[x][i & 1], j);
+        if (!ok) break;
+        issue_pv(i);
+        if (i + 2 >= n_sub) continue;
+        // the weights lie where the scores of sub-tile i + 2 go
+        ok = ((i & 1) || arrived(&sm.k_full[(j + 1) % kKStages], (j + 1) / kKStages)) &&
+             arrived(&sm.pv_done[x][i & 1], j);
+        if (ok) issue_s(i + 2);
+      }
+      // every product issued has completed before the tensor memory is freed,
+      // and Q has landed before the CTA leaves: a commit tracks all of them
+      commit_if(elect_one(), &sm.drained[x]);
+      mbar_wait_bounded(&sm.drained[x], 0);
+      mbar_wait_bounded(&sm.bar_q, 0);
     }
-    // every product issued has completed before the tensor memory is freed,
-    // and Q has landed before the CTA leaves: a commit tracks all of them
-    commit_if(elect_one(), &sm.drained);
-    mbar_wait_bounded(&sm.drained, 0);
-    mbar_wait_bounded(&sm.bar_q, 0);
     __syncwarp();
   } else if ((warp >> 2) < n_x) {
     // -------------------------------------------------------------- softmax
@@ -427,21 +437,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = threadIdx.x & 127;  // 4 * token + head in group
     const int pos = job.pos0 + x * kTok + (row >> 2);
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lane_base + kColS + x * kKeys, t_o = lane_base + kColO + x * kHeadDim;
+    const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    for (int j = 0; j < n_tiles; ++j) {
-      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x], j & 1, p.err));
+    for (int i = 0; i < n_sub; ++i) {
+      const uint32_t t_s = lane_base + kColS + x * kKeys + (i & 1) * kSub;
+      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x][i & 1], (i >> 1) & 1, p.err));
       if (!ok) break;
       fence_after_sync();
-      const int kbase = j * kKeys;
-      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&sm.bad[j & 7]);
+      const int kbase = i * kSub;
+      const uint32_t bad = reinterpret_cast<volatile uint32_t*>(&sm.bad[(i >> 1) & 7])[i & 1];  // bytes of its 4 pages
       // hidden keys: after the row's position, past the end, of a bad page
-      const bool masked = kbase + kKeys - 1 > job.pos0 + x * kTok || kbase + kKeys > job.keys || bad != 0u;
-      const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the tile before the first hidden one
+      const bool masked = kbase + kSub - 1 > job.pos0 + x * kTok || kbase + kSub > job.keys || bad != 0u;
+      const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the sub-tile before the first hidden one
       const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
-      // One pass over the scores in quarters of 32 keys, the next quarter's
+      // One pass over the scores, 32 keys at a time, the next ones'
       // load in flight: its maximum, then its weights, against the running
       // maximum; when that has to be re-based (rare after the first tile) the
       // output and the weights stored so far are rescaled.
@@ -449,63 +460,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t buf[2][32];
       tmem_ld32_async(t_s, buf[0]);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < 2; ++h) {
         uint32_t(&c)[32] = buf[h & 1];
         wait_ld(c);
-        if (h < 3) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
+        if (h < 1) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
         if (masked) {
-          const uint32_t pages = (uint32_t)(bad >> (16 * h));  // bytes of pages 2 h and 2 h + 1
+          const uint32_t pages = bad >> (16 * h);  // bytes of pages 2 h and 2 h + 1
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * h + i >= seen || (pages & (i < 16 ? 0xffu : 0xff00u))) c[i] = hide;
+          for (int y = 0; y < 32; ++y)
+            if (32 * h + y >= seen || (pages & (y < 16 ? 0xffu : 0xff00u))) c[y] = hide;
         }
         float mx[4];  // independent chains, over scores of the sign of the scale
         float mt;
         if (scale >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(c[i]), __uint_as_float(c[i + 4]));
+          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(__uint_as_float(c[y]), __uint_as_float(c[y + 4]));
 #pragma unroll
-          for (int i = 8; i < 32; i += 2)
-            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(c[i]), __uint_as_float(c[i + 1])));
+          for (int y = 8; y < 32; y += 2)
+            mx[(y >> 1) & 3] = fmaxf(mx[(y >> 1) & 3], fmaxf(__uint_as_float(c[y]), __uint_as_float(c[y + 1])));
           mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fminf(__uint_as_float(c[i]), __uint_as_float(c[i + 4]));
+          for (int y = 0; y < 4; ++y) mx[y] = fminf(__uint_as_float(c[y]), __uint_as_float(c[y + 4]));
 #pragma unroll
-          for (int i = 8; i < 32; i += 2)
-            mx[(i >> 1) & 3] = fminf(mx[(i >> 1) & 3], fminf(__uint_as_float(c[i]), __uint_as_float(c[i + 1])));
+          for (int y = 8; y < 32; y += 2)
+            mx[(y >> 1) & 3] = fminf(mx[(y >> 1) & 3], fminf(__uint_as_float(c[y]), __uint_as_float(c[y + 1])));
           mt = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale;
         }
         const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
         if (__any_sync(0xffffffffu, grow)) {
-          if (h < 3) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
+          if (h < 1) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
           const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
           if (grow) m_run = mt;
           l_run *= corr;
           const float2 c2 = make_float2(corr, corr);
           ls[0] = __fmul2_rn(ls[0], c2);
           ls[1] = __fmul2_rn(ls[1], c2);
-          // O is stable: this tile's scores were issued after PV of tile j - 1
-          rescale(t_o, t_s, h, j > 0, corr);
+          if (i > 0) {  // O is stable once PV of the sub-tile before is done
+            ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(i - 1) & 1], ((i - 1) >> 1) & 1, p.err));
+            if (!ok) break;
+            fence_after_sync();
+          }
+          rescale(t_o, t_s, h, i > 0, corr);
         }
         const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
         const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1])), sc2, nm2);
+        for (int y = 0; y < 16; ++y) {
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
           const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-          ls[i & 1] = __fadd2_rn(ls[i & 1], e);
-          w[i] = pack_bf16x2(e.x, e.y);
+          ls[y & 1] = __fadd2_rn(ls[y & 1], e);
+          w[y] = pack_bf16x2(e.x, e.y);
         }
         store16(t_s + 16 * h, w);  // weights over scores already read
       }
+      if (!ok) break;
       l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       wait_st();
       fence_before_sync();  // the tensor-memory accesses above precede the arrive
-      mbar_arrive(&sm.p_full[x]);
+      mbar_arrive(&sm.p_full[x][i & 1]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x], (n_tiles - 1) & 1, p.err));
+    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(n_sub - 1) & 1], ((n_sub - 1) >> 1) & 1, p.err));
     if (ok) {
       fence_after_sync();
       // bf16 rows through the tile's Q buffer (its last score product is
