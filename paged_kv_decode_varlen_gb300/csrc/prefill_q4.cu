@@ -35,8 +35,7 @@
 // product before it: 4100 cycles per 128 keys against 2900, although 64 columns
 // of B make a score product read its Q tile at the shared memory's limit, 48
 // cycles for 32.)  The softmax takes the scores once, 32 columns at a time,
-// against a running maximum that is re-based only when it grows by more than
-// 2^8.  Weights are rounded to bf16, as the tensor cores take them; their sum is
+// against a reference that is re-based only when weights get large.  Weights are rounded to bf16, as the tensor cores take them; their sum is
 // kept in binary32 from the unrounded ones, as are scores, maxima and outputs.
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its
@@ -66,7 +65,7 @@ constexpr int kUnits = 2 * kPagesPerTile;    // slabs of a key tile
 constexpr int kAhead = 3;                    // units a producer warp reads ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
-constexpr float kRescaleSlack = 8.f;
+constexpr float kMaxSum = 1024.f;  // of 32 weights, before their row's reference is raised
 constexpr int kSub = 64;                     // keys of a score product
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
@@ -233,9 +232,18 @@ __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const u
     return b;
   };
   int ids = load_ids(0), ids_next = load_ids(32);
-  uint4 code[kAhead][2];
+  // Row t of a page, 16-byte chunk c of its 64-dim half at c ^ (t & 7).  The
+  // words of groups 2 and 3 are taken in the order 2, 3, 0, 1, so that the eight
+  // lanes of a store phase (2 tokens x 4 groups) meet eight chunks.
+  const int swap = g & 2;
+  uint32_t at[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    at[x] = (g >> 1) * kHalf + t * 128 + (((((g & 1) << 2) + (x ^ swap)) ^ (t & 7)) << 4);
+  const uint32_t code_at = 16 * lane + 4 * swap, dz_at = q4_scale_at(t, g);
+  uint2 code[kAhead][2][2];  // per piece: words 0, 1 and words 2, 3 (in the order taken)
   uint32_t dz[kAhead][2];
-  int id_of[kAhead];
+  bool bad[kAhead];
   // unit n into slot d; a key past the end, or of a page outside the pool, becomes 0
   auto fetch = [&](int n, int d) {
     if (n > 0 && (n & 31) == 0) {
@@ -243,32 +251,28 @@ __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const u
       ids_next = load_ids(n + 32);
     }
     const int id = __shfl_sync(0xffffffffu, ids, n & 31);
-    id_of[d] = id;
-    code[d][0] = code[d][1] = make_uint4(0u, 0u, 0u, 0u);
-    dz[d][0] = dz[d][1] = 0u;
-    if (id < 0) return;
     const int u = w + kProducers * n;
     const int left = job.keys - ((u / kUnits) * kPagesPerTile + (u & (kPagesPerTile - 1))) * kPage;
-    const uint8_t* slab = ((u & kPagesPerTile) ? v_cache : k_cache) + ((size_t)id * num_kv_heads + job.kvh) * kQ4Slab;
-    const uint4* c = reinterpret_cast<const uint4*>(slab) + lane;
-    const uint32_t* z = reinterpret_cast<const uint32_t*>(slab + q4_scale_at(t, g));
-    if (t < left) {
-      code[d][0] = __ldg(c);
-      dz[d][0] = __ldg(z);
+    const uint8_t* slab =
+        ((u & kPagesPerTile) ? v_cache : k_cache) + ((size_t)max(id, 0) * num_kv_heads + job.kvh) * kQ4Slab;
+    bad[d] = id == -2;
+    auto load = [&](int y) {  // tokens t + 8 y
+      code[d][y][0] = __ldg(reinterpret_cast<const uint2*>(slab + 512 * y + code_at));
+      code[d][y][1] = __ldg(reinterpret_cast<const uint2*>(slab + 512 * y + (code_at ^ 8u)));
+      dz[d][y] = __ldg(reinterpret_cast<const uint32_t*>(slab + 8 * 4 * kQ4Groups * y + dz_at));
+    };
+    if (id >= 0 && left >= kPage) {
+      load(0);
+      load(1);
+      return;
     }
-    if (t + 8 < left) {
-      code[d][1] = __ldg(c + 32);
-      dz[d][1] = __ldg(z + 8 * kQ4Groups);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      code[d][y][0] = code[d][y][1] = make_uint2(0u, 0u);
+      dz[d][y] = 0u;
+      if (id >= 0 && t + 8 * y < left) load(y);
     }
   };
-  // Row t of a page, 16-byte chunk c of its 64-dim half at c ^ (t & 7).  The
-  // words of groups 2 and 3 are stored in the order 2, 3, 0, 1, so that the
-  // eight lanes of a store phase (2 tokens x 4 groups) meet eight chunks.
-  const int swap = g & 2;
-  uint32_t at[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    at[x] = (g >> 1) * kHalf + t * 128 + (((((g & 1) << 2) + (x ^ swap)) ^ (t & 7)) << 4);
 #pragma unroll
   for (int d = 0; d < kAhead; ++d) fetch(d, d);
   for (int n0 = 0; w + kProducers * n0 < n_units; n0 += kAhead) {
@@ -278,16 +282,15 @@ __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const u
       if (u >= n_units) return;
       const int j = u / kUnits, pg = u & (kPagesPerTile - 1), s = j % kKStages;
       const bool is_v = u & kPagesPerTile;
-      if (!is_v && lane == 0) reinterpret_cast<volatile uint8_t*>(&sm.bad[j & 7])[pg] = id_of[d] == -2;
+      if (!is_v && lane == 0) reinterpret_cast<volatile uint8_t*>(&sm.bad[j & 7])[pg] = bad[d];
       if (j >= kKStages &&
           !__all_sync(0xffffffffu, wait(sm, is_v ? &sm.v_empty[s] : &sm.k_empty[s], ((j / kKStages) - 1) & 1, err)))
         return;
       const uint32_t dst = smem_addr(is_v ? sm.v[s] : sm.k[s]) + pg * (kPage * 128);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const uint4 c = code[d][y];
         const uint32_t z = dz[d][y];
-        const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+        const uint32_t word[4] = {code[d][y][0].x, code[d][y][0].y, code[d][y][1].x, code[d][y][1].y};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint4 val = q4_word_values(word[x], z);
@@ -452,11 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = kbase + kSub - 1 > job.pos0 + x * kTok || kbase + kSub > job.keys || bad != 0u;
       const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the sub-tile before the first hidden one
       const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
-      // One pass over the scores, 32 keys at a time, the next ones'
-      // load in flight: its maximum, then its weights, against the running
-      // maximum; when that has to be re-based (rare after the first tile) the
-      // output and the weights stored so far are rescaled.
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // One pass over the scores, 32 keys at a time, the next ones' load in
+      // flight.  The weights are taken against the row's reference m_run first;
+      // only when their sum shows that it lies too low (or there is none yet)
+      // the maximum is looked for, m_run re-based to it, and the output and the
+      // weights stored so far rescaled.  After a row's first keys that is rare.
+      float2 ls = make_float2(0.f, 0.f);
       uint32_t buf[2][32];
       tmem_ld32_async(t_s, buf[0]);
 #pragma unroll
@@ -470,32 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 32; ++y)
             if (32 * h + y >= seen || (pages & (y < 16 ? 0xffu : 0xff00u))) c[y] = hide;
         }
-        float mx[4];  // independent chains, over scores of the sign of the scale
-        float mt;
-        if (scale >= 0.f) {
+        uint32_t w[16];
+        float2 sum;
+        for (bool again = false;; again = true) {
+          const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+          const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(__uint_as_float(c[y]), __uint_as_float(c[y + 4]));
-#pragma unroll
-          for (int y = 8; y < 32; y += 2)
-            mx[(y >> 1) & 3] = fmaxf(mx[(y >> 1) & 3], fmaxf(__uint_as_float(c[y]), __uint_as_float(c[y + 1])));
-          mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        } else {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fminf(__uint_as_float(c[y]), __uint_as_float(c[y + 4]));
-#pragma unroll
-          for (int y = 8; y < 32; y += 2)
-            mx[(y >> 1) & 3] = fminf(mx[(y >> 1) & 3], fminf(__uint_as_float(c[y]), __uint_as_float(c[y + 1])));
-          mt = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * scale;
-        }
-        const bool grow = mt > m_run + kRescaleSlack;  // always true for the first finite maximum
-        if (__any_sync(0xffffffffu, grow)) {
+          for (int y = 0; y < 16; ++y) {
+            const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
+            const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+            s2[y & 1] = __fadd2_rn(s2[y & 1], e);
+            w[y] = pack_bf16x2(e.x, e.y);
+          }
+          sum = __fadd2_rn(s2[0], s2[1]);
+          const bool low = sum.x + sum.y > kMaxSum || m_run == -INFINITY;
+          if (again || !__any_sync(0xffffffffu, low)) break;
           if (h < 1) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
+          float mt = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < 32; ++y) mt = fmaxf(mt, __uint_as_float(c[y]) * scale);
+          const bool grow = low && mt > m_run;
           const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
           if (grow) m_run = mt;
           l_run *= corr;
-          const float2 c2 = make_float2(corr, corr);
-          ls[0] = __fmul2_rn(ls[0], c2);
-          ls[1] = __fmul2_rn(ls[1], c2);
+          ls = __fmul2_rn(ls, make_float2(corr, corr));
           if (i > 0) {  // O is stable once PV of the sub-tile before is done
             ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(i - 1) & 1], ((i - 1) >> 1) & 1, p.err));
             if (!ok) break;
@@ -503,20 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           rescale(t_o, t_s, h, i > 0, corr);
         }
-        const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
-        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-        uint32_t w[16];
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
-          const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-          ls[y & 1] = __fadd2_rn(ls[y & 1], e);
-          w[y] = pack_bf16x2(e.x, e.y);
-        }
+        ls = __fadd2_rn(ls, sum);
         store16(t_s + 16 * h, w);  // weights over scores already read
       }
       if (!ok) break;
-      l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+      l_run += ls.x + ls.y;
       wait_st();
       fence_before_sync();  // the tensor-memory accesses above precede the arrive
       mbar_arrive(&sm.p_full[x][i & 1]);
