@@ -38,8 +38,8 @@ namespace pa {
 namespace {
 
 constexpr int kPair = 2;     // pages per stage
-constexpr int kStages = 2;   // stages in flight per warp
 constexpr float kRescaleSlack = 8.f;  // the running max is re-based when it grows by more than 2^8
+constexpr float kNoMax = 1e30f;
 
 struct Item {        // one row's pages within this CTA's segment
   int32_t q_start;  // first page of the item in the segment
@@ -64,6 +64,7 @@ struct Shape {
   static constexpr int kWarps = q4_decode_warps(kTiles);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kPartBytes = kT * kVec * 32 * 16;
+  static constexpr int kStages = 2;                // stages in flight per warp (a power of two)
   static constexpr int kRingBytes = kStages * kPair * 2 * kQ4Slab;
 };
 
@@ -221,7 +222,7 @@ template <int kTiles, class Plan>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     decode_q4_kernel(const DecodeParams p, const __grid_constant__ Plan plan) {
   using S = Shape<kTiles>;
-  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kT = S::kT, kCols = S::kCols;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kT = S::kT, kCols = S::kCols, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<kTiles>& sm = *reinterpret_cast<Smem<kTiles>*>(smem_raw);
   const int b = blockIdx.x;
@@ -278,7 +279,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     }
   }
   __syncthreads();
-  pdl_wait();
+  // Beside a tile kernel (p.beside) this launch starts once every CTA of that
+  // kernel has passed its own wait, so the kernels before it are complete;
+  // waiting here would wait for the tile kernel itself.
+  if (!p.beside) pdl_wait();
   const int n_items = sm.n_items;
   if (n_items == 0) return;  // nothing covered (recorded above)
   // ---- block ids of the segment's pages; a page with an id outside the pool
@@ -353,10 +357,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   const int cq = lane & 3;   // the lane's columns in scores and output: head cq, or 2 cq and 2 cq + 1
   // matrix-load address of lane l: matrix (group) l / 8, row (token) l % 8
   const uint32_t ld_at = (uint32_t)q4_code_at(lane & 7, lane >> 3);
-  int issued = kStages;
 
   for (; k < n_items; ++k) {
-    const Item& it = sm.items[k];
+    const Item it = sm.items[k];
     const int i0 = max(it.q_start, a), i1 = min(it.q_start + it.n, e);
     if (i0 >= i1) break;  // past this warp's pages
     const int L = it.L, nq = it.nq;
@@ -386,15 +389,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[y][g][x][i] = 0.f;
-    // per column: running max (the same in the column's 8 lanes), minus it (0
-    // before the first key), and the sum of this lane's own weights
-    float m[kT][kCols], nm[kT][kCols], l[kT][kCols];
+    // per column: minus the running max (the same in the column's 8 lanes; a
+    // huge number before the first key, so that nothing weighs anything) and
+    // the sum of this lane's own weights
+    float nm[kT][kCols], l[kT][kCols];
 #pragma unroll
     for (int y = 0; y < kT; ++y)
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        m[y][c] = -INFINITY;
-        nm[y][c] = l[y][c] = 0.f;
+        nm[y][c] = kNoMax;
+        l[y][c] = 0.f;
       }
 
     for (int q = i0; q < i1;) {
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < kCols; ++x) {
           mx[y][x] = fmaxf(fmaxf(sc[y][x][0], sc[y][x][1]), fmaxf(sc[y][x][2], sc[y][x][3]));
-          grow = grow || mx[y][x] > m[y][x] + kRescaleSlack;
+          grow = grow || mx[y][x] + nm[y][x] > kRescaleSlack;
         }
       if (__any_sync(0xffffffffu, grow)) {  // rare after the first pages
 #pragma unroll
@@ -478,9 +482,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             float t = mx[y][x];
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            if (t > m[y][x] + kRescaleSlack) {
-              const float corr = fast_exp2(m[y][x] - t);  // m = -inf -> 0
-              m[y][x] = t;
+            if (t + nm[y][x] > kRescaleSlack) {
+              const float corr = fast_exp2(-nm[y][x] - t);  // the first time 0
               nm[y][x] = -t;
               l[y][x] *= corr;
 #pragma unroll
@@ -547,8 +550,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       // the pair is done with: refill its stage
       if ((q - a) % kPair == 0) {
         __syncwarp();
-        issue(issued);
-        ++issued;
+        issue((q - a) / kPair - 1 + kStages);
       }
     }
 
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       for (int x = 0; x < kCols; ++x) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], o);
-        own[y].m[x] = m[y][x];
+        own[y].m[x] = nm[y][x] == kNoMax ? -INFINITY : -nm[y][x];
         own[y].l[x] = l[y][x];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -683,7 +685,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       output(y, all);
     }
   }
-
+  // beside a tile kernel: this launch completes after it
+  if (p.beside) pdl_wait();
 }
 
 std::atomic<bool> g_attr_set[6][kMaxDevices];

@@ -75,7 +75,7 @@ constexpr int kWgWarps = 12;
 constexpr int kWgMaxPagesPerCta = 3072;
 constexpr int kWgMaxItemsPerCta = 192;
 // The decode kernel over q4 pages: pages and rows a CTA's segment may hold.
-constexpr int kQ4MaxPagesPerCta = 2000;
+constexpr int kQ4MaxPagesPerCta = 1992;
 constexpr int kQ4MaxItemsPerCta = 192;
 static_assert(kQ4MaxItemsPerCta % 32 == 0, "whole rounds of the item table");
 // Rows of up to kQ4DecodeQueries queries run it: tiles = 0 for one query, else
@@ -85,8 +85,8 @@ static_assert(kQ4MaxItemsPerCta % 32 == 0, "whole rounds of the item table");
 constexpr int kQ4DecodeQueries = 6;
 constexpr int q4_decode_tiles(int n_q) { return n_q == 1 ? 0 : n_q <= 4 ? 2 : 3; }
 // Warps per CTA: as many as registers (tiles) and shared memory leave room for.
-constexpr int q4_decode_warps(int tiles) { return tiles == 0 ? 16 : 8; }
-static_assert(kQ4MaxPagesPerCta % 16 == 0, "whole warp segments");
+constexpr int q4_decode_warps(int tiles) { return tiles == 0 ? 12 : 8; }
+static_assert(kQ4MaxPagesPerCta % 12 == 0 && kQ4MaxPagesPerCta % 8 == 0, "whole warp segments");
 // Bytes of one (page, kv head) slab of K or V in bf16 (16 tokens x 128 dims).
 constexpr int kSlabBytesHost = 16 * 128 * 2;
 struct DecodePlan {

@@ -328,6 +328,19 @@ int prefill_alone_ctas(const std::vector<int32_t>& job_tiles, int sms) {
   return (int)best_g;
 }
 
+// Whether the tile jobs of a q4 batch (rows of many queries; `jobs` CTAs, one
+// per SM, the longest of key_tiles tiles) run beside the decode launch, which
+// then has the other SMs: where that ends sooner than the jobs first and the
+// decode launch on every SM after them.  Measured rates: a job ~5 us and 1.9 us
+// per key tile (1.2 with one query tile), the decode launch ~9 us and 37 GB/s
+// per SM.
+bool q4_tiles_beside(int64_t jobs, int64_t key_tiles, bool two_tiles, int64_t decode_slabs, int sms) {
+  if (jobs == 0 || decode_slabs == 0 || jobs > sms - 8) return false;
+  const double tiles_us = 5.0 + (two_tiles ? 1.9 : 1.2) * (double)key_tiles;
+  auto decode_us = [&](int64_t n) { return 9.0 + (double)decode_slabs * 2 * PA_Q4_SLAB_BYTES / ((double)n * 37e3); };
+  return std::max(tiles_us, decode_us(sms - jobs)) + 2.0 < tiles_us + decode_us(sms);
+}
+
 // Plan one persistent decode launch over decode rows rows[0..n): fills
 // plan, returns the grid size (0 when there is nothing to do, -1 when no
 // valid plan exists within the limits).  The grid is n_seg x Hkv CTAs.
@@ -723,6 +736,29 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     }
   }
 
+  // q4 pages: the tile jobs beside the (one) decode launch
+  const int q4_jobs = q4 ? (int)std::min<int64_t>((int64_t)tiles.size() * num_kv_heads, INT32_MAX) : 0;
+  bool q4_beside = false;
+  if (q4_jobs > 0 && g_prefill_ctas.load() >= 0 && g_forced_ctas.load() <= 0) {
+    const std::vector<int32_t>* one = nullptr;
+    int classes = 0;
+    for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows})
+      if (!rows->empty()) {
+        one = rows;
+        ++classes;
+      }
+    if (classes == 1 && one->size() <= (size_t)pa::kPlanMaxRows) {
+      int64_t pages = 0;
+      int32_t extent = 0;
+      bool two_tiles = false;
+      for (int32_t r : *one) pages += pages_of(seq_lens_host[r]);
+      for (const auto& t : tiles) extent = std::max(extent, t.first);
+      for (int32_t r : item_req) two_tiles = two_tiles || qo_indptr_host[r + 1] - qo_indptr_host[r] > pa::kPrefillQTile;
+      q4_beside = q4_tiles_beside(q4_jobs, (extent + pa::kTcKeyTile - 1) / pa::kTcKeyTile, two_tiles,
+                                  pages * num_kv_heads, sm_count());
+    }
+  }
+
   int prefill_ctas = 0;  // CTAs of the prefill launch (0: one per job)
   if (!tiles.empty()) {
     // longest key extent first, so the big tiles do not form the tail
@@ -847,7 +883,9 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       // one launch per class of rows (and per kPlanMaxRows rows; fewer where a
       // segment would hold too many)
       static thread_local int32_t n_q[pa::kPlanMaxRows];
-      bool overlap = tiles.empty();  // as below
+      bool overlap = tiles.empty() || q4_beside;  // as below
+      dp.beside = q4_beside ? 1 : 0;
+      const int slots = q4_beside ? sm_count() - q4_jobs : sm_count();
       for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows}) {
         for (size_t d0 = 0; d0 < rows->size();) {
           int n = (int)std::min(rows->size() - d0, (size_t)pa::kPlanMaxRows);
@@ -858,7 +896,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
           const int cap = (int)std::min<int64_t>(gcap, wl.slots / (2 * piece));
           int grid;
           for (;; n = (n + 1) / 2) {
-            grid = plan_decode(r0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, cap, sm_count(),
+            grid = plan_decode(r0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, cap, slots,
                                pa::q4_decode_warps(cls), pa::kQ4MaxPagesPerCta, pa::kQ4MaxItemsPerCta, plan);
             if (grid >= 0 || n == 1) break;
           }
@@ -869,7 +907,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
               g_forced_ctas.load() > 0
                   ? 0
                   : plan_row_segments(r0, n, seq_lens_host, qo_indptr_host, num_kv_heads,
-                                      std::min(std::min(sm_count(), cap) / num_kv_heads, pa::kPlanMaxCtas),
+                                      std::min(std::min(slots, cap) / num_kv_heads, pa::kPlanMaxCtas),
                                       pa::q4_decode_warps(cls), pa::kQ4MaxPagesPerCta, plan);
           if (row_grid > 0) grid = row_grid;
           for (int i = 0; i < n; ++i) n_q[i] = qo_indptr_host[r0[i] + 1] - qo_indptr_host[r0[i]];
@@ -877,6 +915,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
                          [&] { return pa::launch_decode_q4(dp, plan, n_q, cls, grid, row_grid > 0, overlap, stream); });
           if (s != PA_OK) return s;
           overlap = true;
+          dp.beside = 0;  // (a further launch waits for this one)
         }
       }
       return ok();
