@@ -197,6 +197,15 @@ struct PrefillItems {
   int32_t q_start[kMaxPrefillItems];
 };
 
+// The tile kernel's items over q4 pages: (request, first query token, its
+// position, queries), up to N of them.
+template <int N>
+struct Q4Items {
+  int32_t count;
+  int32_t pad[3];
+  int4 item[N];
+};
+
 struct PrefillParams {
   const uint16_t* q;
   const uint16_t* k_cache;
@@ -296,9 +305,10 @@ cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, cons
 // pages), else the CTA-granular one (windows of rows)
 cudaError_t launch_decode_step(const DecodeParams& p, const StepPlan& plan, int grid, bool warp_granular,
                                cudaStream_t stream);
-// q4 pages: one CTA per (item of kQ4TileTokens queries, kv head)
-cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const CUtensorMap& q_map,
-                              cudaStream_t stream);
+// q4 pages: (item of kQ4TileTokens queries, kv head) jobs on ctas CTAs; rows[i]
+// is item i's (request, first query token, its position, queries)
+cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows,
+                              const CUtensorMap& q_map, int ctas, cudaStream_t stream);
 // ctas: CTAs of the launch (0: one per (item, kv head) job; fewer run
 // several jobs each)
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, const TcMaps& maps, int ctas,

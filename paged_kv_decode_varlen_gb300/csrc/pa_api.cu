@@ -613,6 +613,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   int32_t max_len = 1;
   std::vector<std::pair<int32_t, int32_t>> tiles;  // (kv extent of the tile, item index) for ordering
   static thread_local pa::PrefillItems items;
+  static thread_local int4 q4_items[pa::kMaxPrefillItems];
   std::vector<int32_t> item_req, item_q0;
   for (int r = 0; r < num_reqs; ++r) {
     const int32_t qo_len = qo_indptr_host[r + 1] - qo_indptr_host[r];
@@ -836,10 +837,14 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         const int32_t idx = tiles[base + i].second;
         items.req[i] = item_req[idx];
         items.q_start[i] = item_q0[idx];
+        const int32_t r = item_req[idx], qo0 = qo_indptr_host[r], c = qo_indptr_host[r + 1] - qo0;
+        q4_items[i] = make_int4(r, qo0 + item_q0[idx], seq_lens_host[r] - c + item_q0[idx],
+                                std::min(pa::kQ4TileTokens, c - item_q0[idx]));
       }
       s = run_launch(PA_KERNEL_PREFILL, "prefill", stream,
                      [&] {
-                       return q4 ? pa::launch_prefill_q4(pp, items, maps.q, stream)
+                       return q4 ? pa::launch_prefill_q4(pp, items, q4_items, maps.q,
+                                                         std::min(items.count * num_kv_heads, sm_count()), stream)
                                  : pa::launch_prefill(pp, items, maps, prefill_ctas, stream);
                      });
       if (s != PA_OK) return s;

@@ -5,9 +5,13 @@
 // h + j and attends to keys 0 .. h + j; scores, softmax and output as in
 // decode_q4.cu, keys and values the bf16 numbers that the codes stand for.
 //
-// Work.  One CTA per (64 query tokens, kv head): two query tiles A and B of 32
-// tokens x 4 heads = 128 rows, the M of one tcgen05.mma each, against key
-// tiles of 128 (8 pages).  The two tiles share every dequantised K and V tile,
+// Work.  A job is 64 query tokens of a row for one kv head: two query tiles A
+// and B of 32 tokens x 4 heads = 128 rows, the M of one tcgen05.mma each (B is
+// left out of a job of up to 32), against key tiles of 128 (8 pages).  One CTA
+// per SM runs its share of the jobs one after another without a barrier between
+// them: rings, phases and buffers are indexed by running counts, so the next
+// job's Q, first key tiles and first scores are made while the softmax warps
+// finish this one (8 prompts of 100 to 1000 tokens: 56 us with a CTA per job).  The two tiles share every dequantised K and V tile,
 // and their softmaxes alternate on the tensor cores: while tile A's warps turn
 // scores into weights, B's products run.
 //   Bound.  Per key tile the products take 2560 cycles of the tensor cores, the
@@ -74,10 +78,11 @@ static_assert(2 * 32 * 16 == kQ4Codes, "two pieces of codes per lane");
 static_assert(kKStages == kVStages, "one ring depth");
 
 struct __align__(1024) Smem {
-  uint8_t q[2][kTileBytes];  // then each tile's output rows on their way out
+  uint8_t q[2][kTileBytes];
   uint8_t k[kKStages][kTileBytes];
   uint8_t v[kVStages][kTileBytes];
-  uint64_t bar_q;
+  uint64_t q_full, q_free;  // a job's Q has landed; its last scores are done
+  uint64_t o_free[2];       // the softmax warps have read a job's output
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per query tile and buffer: phase i / 2 for sub-tile i
@@ -207,17 +212,44 @@ struct Job {
   int32_t pos0;  // position of the first
   int32_t keys;  // keys its last query sees
   const int32_t* table;
+  int32_t n_tiles, n_sub;  // key tiles; sub-tiles of 64 keys (for both query tiles)
+  int32_t n_x;             // query tiles
 };
 
+// The CTA's jobs: job b of every round of gridDim.x jobs, in reverse order on
+// odd rounds (the items come longest first).  Calls f(job) until it returns
+// false.
+template <class Items, class F>
+__device__ __forceinline__ void for_each_job(const PrefillParams& p, const Items& items, F&& f) {
+  const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
+  for (int base = 0, odd = 0; base < n; base += G, odd ^= 1) {
+    const int u = base + (odd ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (u >= n) continue;
+    const int it = u / p.num_kv_heads;
+    const int4 item = items.item[it];  // request, first query token, its position, queries
+    Job job;
+    job.tok0 = item.y;
+    job.nq = item.w;
+    job.kvh = u - it * p.num_kv_heads;
+    job.pos0 = item.z;
+    job.keys = item.z + item.w;
+    job.table = p.block_tables + (size_t)item.x * p.max_blocks_per_req;
+    job.n_tiles = (job.keys + kKeys - 1) / kKeys;
+    job.n_sub = (job.keys + kSub - 1) / kSub;
+    job.n_x = job.nq > kTok ? 2 : 1;
+    if (!f(job)) return;
+  }
+}
+
 // Producer warp w: units w, w + 6, ... of the job (unit u: key tile u / 16, K
-// pages 0 .. 7, then V pages 0 .. 7).
-__device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const uint8_t* k_cache,
-                                        const uint8_t* v_cache, int num_kv_heads, int64_t num_blocks, int n_tiles,
-                                        int* err) {
+// pages 0 .. 7, then V pages 0 .. 7); J0: the CTA's key tiles before the job's.
+// False after a timeout.
+__device__ __forceinline__ bool produce(Smem& sm, const Job& job, int w, int J0, const uint8_t* k_cache,
+                                        const uint8_t* v_cache, int num_kv_heads, int64_t num_blocks, int* err) {
   const int lane = threadIdx.x & 31;
   const int t = lane >> 2, g = (lane & 3) ^ ((t >> 1) & 3);  // tokens t and t + 8 of group g
   const int last_page = (job.keys - 1) / kPage;
-  const int n_units = n_tiles * kUnits;
+  const int n_units = job.n_tiles * kUnits;
   // block id of the warp's unit n (lane l of a batch: unit 32 B + l), a batch
   // ahead; -1: past the row's keys, -2: outside the pool
   auto load_ids = [&](int n0) -> int {
@@ -279,13 +311,13 @@ __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const u
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
       const int n = n0 + d, u = w + kProducers * n;
-      if (u >= n_units) return;
-      const int j = u / kUnits, pg = u & (kPagesPerTile - 1), s = j % kKStages;
+      if (u >= n_units) return true;
+      const int j = J0 + u / kUnits, pg = u & (kPagesPerTile - 1), s = j % kKStages;
       const bool is_v = u & kPagesPerTile;
       if (!is_v && lane == 0) reinterpret_cast<volatile uint8_t*>(&sm.bad[j & 7])[pg] = bad[d];
       if (j >= kKStages &&
           !__all_sync(0xffffffffu, wait(sm, is_v ? &sm.v_empty[s] : &sm.k_empty[s], ((j / kKStages) - 1) & 1, err)))
-        return;
+        return false;
       const uint32_t dst = smem_addr(is_v ? sm.v[s] : sm.k[s]) + pg * (kPage * 128);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -305,60 +337,38 @@ __device__ __forceinline__ void produce(Smem& sm, const Job& job, int w, const u
       if (lane == 0) mbar_arrive(is_v ? &sm.v_full[s] : &sm.k_full[s]);
     }
   }
+  return true;
 }
 
+template <class Items>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_q4_kernel(const PrefillParams p, const __grid_constant__ PrefillItems items,
+    prefill_q4_kernel(const PrefillParams p, const __grid_constant__ Items items,
                       const __grid_constant__ CUtensorMap q_map) {
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  pdl_wait();
-  pdl_launch_dependents();
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  Job job;
-  {
-    const int it = blockIdx.x / p.num_kv_heads;
-    const int r = items.req[it], j0 = items.q_start[it];
-    const int qo0 = p.qo_indptr[r], c = p.qo_indptr[r + 1] - qo0;
-    job.tok0 = qo0 + j0;
-    job.nq = min(kQ4TileTokens, c - j0);
-    job.kvh = blockIdx.x % p.num_kv_heads;
-    job.pos0 = p.seq_lens[r] - c + j0;
-    job.keys = job.pos0 + job.nq;
-    job.table = p.block_tables + (size_t)r * p.max_blocks_per_req;
-  }
-  // metadata that differ from the host plan: record and skip the job
-  if (job.nq <= 0 || job.pos0 < 0 || (job.keys - 1) / kPage >= p.max_blocks_per_req) {
-    if (threadIdx.x == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
-    return;
-  }
-  const int n_tiles = (job.keys + kKeys - 1) / kKeys;
-  const int n_sub = (job.keys + kSub - 1) / kSub;  // sub-tiles, for both query tiles
-  const int n_x = job.nq > kTok ? 2 : 1;          // query tiles
   if (warp == kMmaWarp && lane == 0) {
-    mbar_init(&sm.bar_q, 1);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_free, 2);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&sm.k_full[s], kPagesPerTile);
-      mbar_init(&sm.k_empty[s], n_x);
+      mbar_init(&sm.k_empty[s], 2);
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&sm.v_full[s], kPagesPerTile);
-      mbar_init(&sm.v_empty[s], n_x);
+      mbar_init(&sm.v_empty[s], 2);
     }
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sm.s_full[x][b], 1);
         mbar_init(&sm.p_full[x][b], kRows);
         mbar_init(&sm.pv_done[x][b], 1);
       }
-    for (int x = 0; x < 2; ++x) mbar_init(&sm.drained[x], 1);
+      mbar_init(&sm.o_free[x], kRows);
+      mbar_init(&sm.drained[x], 1);
+    }
     sm.abort = 0;
     fence_mbar_init();
-    mbar_arrive_expect_tx(&sm.bar_q, n_x * kTileBytes);
-    for (int x = 0; x < n_x; ++x) {
-      tma_load_3d(sm.q[x], &q_map, 0, job.kvh * kGroup, job.tok0 + x * kTok, &sm.bar_q);
-      tma_load_3d(sm.q[x] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + x * kTok, &sm.bar_q);
-    }
   }
   if (warp == kMmaWarp) {
     __syncwarp();
@@ -368,89 +378,153 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sm.tmem;
+  // nothing above touches what an earlier kernel may write (the jobs come with
+  // the parameters)
+  pdl_wait();
+  pdl_launch_dependents();
 
   if (warp >= kProducer0) {
-    produce(sm, job, warp - kProducer0, reinterpret_cast<const uint8_t*>(p.k_cache),
-            reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, n_tiles, p.err);
+    int J0 = 0;
+    for_each_job(p, items, [&](const Job& job) {
+      const bool ok = produce(sm, job, warp - kProducer0, J0, reinterpret_cast<const uint8_t*>(p.k_cache),
+                              reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, p.err);
+      J0 += job.n_tiles;
+      return ok;
+    });
   } else if (warp >= kMmaWarp) {
     // --------------------------------------------------------- MMA issuers
     // The whole warp runs this (so that descriptors and addresses are
     // warp-uniform values) and one elected lane issues.
     const int x = warp - kMmaWarp;
-    if (x < n_x) {
-      const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
-      const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
-      const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t t_s = tm + kColS + x * kKeys, t_o = tm + kColO + x * kHeadDim;
-      auto arrived = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
-      };
-      // scores of sub-tile i: 64 keys, half i & 1 of key tile i / 2
-      auto issue_s = [&](int i) {
-        const uint64_t kd =
-            k_desc + (uint32_t)((i >> 1) % kKStages) * (kTileBytes >> 4) + (uint32_t)(i & 1) * (kSub * 128 >> 4);
-        const uint32_t on = elect_one();
-        fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
-          mma_ss_if(on, t_s + (i & 1) * kSub, q_desc + off, kd + off, kIdescS, ks > 0);
+    const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
+    const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t t_s = tm + kColS + x * kKeys, t_o = tm + kColO + x * kHeadDim;
+    auto arrived = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
+    };
+    // Q of a job (its n-th): after the last scores of the job before
+    auto load_q = [&](const Job& job) {
+      const uint32_t on = elect_one();
+      if (on) {
+        mbar_arrive_expect_tx(&sm.q_full, job.n_x * kTileBytes);
+        for (int y = 0; y < job.n_x; ++y) {
+          tma_load_3d(sm.q[y], &q_map, 0, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
+          tma_load_3d(sm.q[y] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
         }
-        commit_if(on, &sm.s_full[x][i & 1]);
-        if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.k_empty[(i >> 1) % kKStages]);  // the tile's last use here
-      };
-      auto issue_pv = [&](int i) {
-        const uint64_t vd = v_desc + (uint32_t)((i >> 1) % kVStages) * (kTileBytes >> 4);
-        const uint32_t on = elect_one();
-        fence_after_sync();
+      }
+      __syncwarp();
+    };
+    // running counts: key tiles, jobs, this query tile's sub-tiles and jobs
+    int J0 = 0, n_job = 0, I0 = 0, n_own = 0;
+    bool ok = true;
+    for_each_job(p, items, [&](const Job& job) {
+      if (x == 0) {
+        ok = n_job == 0 || arrived(&sm.q_free, n_job - 1);
+        if (ok) load_q(job);
+      }
+      if (x < job.n_x) {
+        const int n_sub = job.n_sub;
+        // scores of sub-tile i: 64 keys, half i & 1 of the job's key tile i / 2
+        auto issue_s = [&](int i) {
+          const int J = J0 + (i >> 1), b = (I0 + i) & 1;
+          const uint64_t kd = k_desc + (uint32_t)(J % kKStages) * (kTileBytes >> 4) + (uint32_t)(i & 1) * (kSub * 128 >> 4);
+          const uint32_t on = elect_one();
+          fence_after_sync();
 #pragma unroll
-        for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
-          mma_ts_if(on, t_o, t_s + (i & 1) * kSub + 8 * ks,
-                    vd + (uint32_t)((i & 1) * (kSub / 16) + ks) * (2 * 1024 >> 4), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
-        commit_if(on, &sm.pv_done[x][i & 1]);
-        if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.v_empty[(i >> 1) % kVStages]);
-      };
-      bool ok = arrived(&sm.bar_q, 0) && arrived(&sm.k_full[0], 0);
-      if (ok) {
-        issue_s(0);
-        if (n_sub > 1) issue_s(1);
+          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
+            mma_ss_if(on, t_s + b * kSub, q_desc + off, kd + off, kIdescS, ks > 0);
+          }
+          commit_if(on, &sm.s_full[x][b]);
+          if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.k_empty[J % kKStages]);  // the tile's last use here
+          if (i == n_sub - 1) commit_if(on, &sm.q_free);
+        };
+        auto issue_pv = [&](int i) {
+          const int J = J0 + (i >> 1), b = (I0 + i) & 1;
+          const uint64_t vd = v_desc + (uint32_t)(J % kVStages) * (kTileBytes >> 4);
+          const uint32_t on = elect_one();
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
+            mma_ts_if(on, t_o, t_s + b * kSub + 8 * ks, vd + (uint32_t)((i & 1) * (kSub / 16) + ks) * (2 * 1024 >> 4),
+                      kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
+          commit_if(on, &sm.pv_done[x][b]);
+          if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.v_empty[J % kVStages]);
+        };
+        // before the scores of sub-tile i: its key tile, and the PV product of
+        // the sub-tile whose weights lie where they go
+        auto may_score = [&](int i) {
+          const int J = J0 + (i >> 1), I = I0 + i;
+          return ((i & 1) || arrived(&sm.k_full[J % kKStages], J / kKStages)) &&
+                 (I < 2 || arrived(&sm.pv_done[x][I & 1], (I >> 1) - 1));
+        };
+        ok = ok && arrived(&sm.q_full, n_job);
+        for (int i = 0; ok && i < min(n_sub, 2); ++i)
+          if ((ok = may_score(i))) issue_s(i);
+        // the first PV product overwrites the output of this tile's job before
+        ok = ok && (n_own == 0 || arrived(&sm.o_free[x], n_own - 1));
+        for (int i = 0; ok && i < n_sub; ++i) {
+          const int J = J0 + (i >> 1), I = I0 + i;
+          ok = ((i & 1) || arrived(&sm.v_full[J % kVStages], J / kVStages)) && arrived(&sm.p_full[x][I & 1], I >> 1);
+          if (!ok) break;
+          issue_pv(i);
+          if (i + 2 < n_sub && (ok = may_score(i + 2))) issue_s(i + 2);
+        }
+        I0 += n_sub;
+        n_own += 1;
+      } else {
+        // a job without this tile: every phase is waited for in turn all the
+        // same (a wait by parity tells a phase only from its neighbours), and
+        // every stage given back
+        auto pass = [&](uint64_t* full, uint64_t* empty, int phase) {
+          ok = ok && arrived(full, phase);
+          if (ok && lane == 0) mbar_arrive(empty);
+          __syncwarp();
+        };
+        pass(&sm.q_full, &sm.q_free, n_job);
+        for (int j = 0; j < job.n_tiles; ++j) {
+          const int J = J0 + j;
+          pass(&sm.k_full[J % kKStages], &sm.k_empty[J % kKStages], J / kKStages);
+          pass(&sm.v_full[J % kVStages], &sm.v_empty[J % kVStages], J / kVStages);
+        }
       }
-      for (int i = 0; ok && i < n_sub; ++i) {
-        const int j = i >> 1;
-        ok = ((i & 1) || arrived(&sm.v_full[j % kVStages], j / kVStages)) && arrived(&sm.p_full[x][i & 1], j);
-        if (!ok) break;
-        issue_pv(i);
-        if (i + 2 >= n_sub) continue;
-        // the weights lie where the scores of sub-tile i + 2 go
-        ok = ((i & 1) || arrived(&sm.k_full[(j + 1) % kKStages], (j + 1) / kKStages)) &&
-             arrived(&sm.pv_done[x][i & 1], j);
-        if (ok) issue_s(i + 2);
-      }
-      // every product issued has completed before the tensor memory is freed,
-      // and Q has landed before the CTA leaves: a commit tracks all of them
-      commit_if(elect_one(), &sm.drained[x]);
-      mbar_wait_bounded(&sm.drained[x], 0);
-      mbar_wait_bounded(&sm.bar_q, 0);
-    }
+      J0 += job.n_tiles;
+      n_job += 1;
+      return ok;
+    });
+    // every product issued has completed before the tensor memory is freed (a
+    // commit tracks all of them), and Q has landed before the CTA leaves
+    commit_if(elect_one(), &sm.drained[x]);
+    mbar_wait_bounded(&sm.drained[x], 0);
+    if (x == 0 && n_job > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(n_job - 1) & 1u);
     __syncwarp();
-  } else if ((warp >> 2) < n_x) {
+  } else {
     // -------------------------------------------------------------- softmax
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;  // 4 * token + head in group
-    const int pos = job.pos0 + x * kTok + (row >> 2);
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
-    float m_run = -INFINITY, l_run = 0.f;
+    int J0 = 0, I0 = 0;  // running counts: key tiles, this query tile's sub-tiles
     bool ok = true;
-    for (int i = 0; i < n_sub; ++i) {
-      const uint32_t t_s = lane_base + kColS + x * kKeys + (i & 1) * kSub;
-      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x][i & 1], (i >> 1) & 1, p.err));
+    for_each_job(p, items, [&](const Job& job) {
+    if (x >= job.n_x) {
+      J0 += job.n_tiles;
+      return true;
+    }
+    const int pos = job.pos0 + x * kTok + (row >> 2);
+    float m_run = -INFINITY, l_run = 0.f;
+    for (int i = 0; i < job.n_sub; ++i) {
+      const int I = I0 + i;
+      const uint32_t t_s = lane_base + kColS + x * kKeys + (I & 1) * kSub;
+      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x][I & 1], (I >> 1) & 1, p.err));
       if (!ok) break;
       fence_after_sync();
       const int kbase = i * kSub;
-      const uint32_t bad = reinterpret_cast<volatile uint32_t*>(&sm.bad[(i >> 1) & 7])[i & 1];  // bytes of its 4 pages
+      // bytes of its 4 pages
+      const uint32_t bad = reinterpret_cast<volatile uint32_t*>(&sm.bad[(J0 + (i >> 1)) & 7])[i & 1];
       // hidden keys: after the row's position, past the end, of a bad page
       const bool masked = kbase + kSub - 1 > job.pos0 + x * kTok || kbase + kSub > job.keys || bad != 0u;
       const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the sub-tile before the first hidden one
@@ -500,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= corr;
           ls = __fmul2_rn(ls, make_float2(corr, corr));
           if (i > 0) {  // O is stable once PV of the sub-tile before is done
-            ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(i - 1) & 1], ((i - 1) >> 1) & 1, p.err));
+            ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(I - 1) & 1], ((I - 1) >> 1) & 1, p.err));
             if (!ok) break;
             fence_after_sync();
           }
@@ -513,47 +587,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       l_run += ls.x + ls.y;
       wait_st();
       fence_before_sync();  // the tensor-memory accesses above precede the arrive
-      mbar_arrive(&sm.p_full[x][i & 1]);
+      mbar_arrive(&sm.p_full[x][I & 1]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(n_sub - 1) & 1], ((n_sub - 1) >> 1) & 1, p.err));
-    if (ok) {
-      fence_after_sync();
-      // bf16 rows through the tile's Q buffer (its last score product is
-      // done): 256 B per row, 16-byte chunk c at c ^ (row & 15)
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      uint8_t* stg = sm.q[x];
+    const int I1 = I0 + job.n_sub - 1;
+    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err));
+    if (!ok) return false;
+    fence_after_sync();
+    // the row straight from the tensor memory
+    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    const int tok = x * kTok + (row >> 2);
+    const size_t orow = (size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3);
+    uint16_t* out = p.out + orow * kHeadDim;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        tmem_ld32(t_o + 32 * c, o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(stg + row * 256 + (((4 * c + i) ^ (row & 15)) << 4)) =
-              make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+    for (int c = 0; c < 4; ++c) {
+      float o[32];
+      tmem_ld32(t_o + 32 * c, o);
+      if (c == 3) {
+        fence_before_sync();  // the tensor-memory reads above precede the arrive
+        mbar_arrive(&sm.o_free[x]);
       }
-      const int tok = x * kTok + (row >> 2);
-      if (p.lse && tok < job.nq)
-        p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
-            l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
-    }
-    if (x == 0)
-      asm volatile("bar.sync 1, %0;" ::"n"(kRows) : "memory");
-    else
-      asm volatile("bar.sync 2, %0;" ::"n"(kRows) : "memory");
-    if (!*reinterpret_cast<volatile int*>(&sm.abort)) {
-#pragma unroll 4
-      for (int i = 0; i < kRows * 16 / kRows; ++i) {  // 16 threads write one 256-byte row
-        const int L = i * kRows + row;
-        const int rr = L >> 4, c = L & 15;
-        const int tok = x * kTok + (rr >> 2);
-        if (tok >= job.nq) continue;
-        const size_t orow = (size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (rr & 3);
-        *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 8 * c) =
-            *reinterpret_cast<const uint4*>(sm.q[x] + rr * 256 + ((c ^ (rr & 15)) << 4));
+      if (tok >= job.nq) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(o[16 * h + 2 * y] * inv, o[16 * h + 2 * y + 1] * inv);
+        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c + 16 * h);  // (out is 16-byte aligned, not 32)
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
+    if (p.lse && tok < job.nq) p.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+    J0 += job.n_tiles;
+    I0 += job.n_sub;
+    return true;
+    });
   }
   fence_before_sync();
   __syncthreads();
@@ -561,21 +629,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-std::atomic<bool> g_attr_set[kMaxDevices];
+std::atomic<bool> g_attr_set[2][kMaxDevices];
+
+template <int N>
+cudaError_t launch(const PrefillParams& p, const PrefillItems& items, const int4* rows, const CUtensorMap& q_map, int ctas,
+                   std::atomic<bool>* done, cudaStream_t stream) {
+  static thread_local Q4Items<N> d;
+  d.count = items.count;
+  for (int i = 0; i < items.count; ++i) d.item[i] = rows[i];
+  const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel<Q4Items<N>>, (int)kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_q4_kernel<Q4Items<N>>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, d, q_map);
+}
 
 }  // namespace
 
-cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const CUtensorMap& q_map,
-                              cudaStream_t stream) {
+cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows,
+                              const CUtensorMap& q_map, int ctas, cudaStream_t stream) {
   if (items.count <= 0) return cudaSuccess;
-  const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel, (int)kSmemBytes, g_attr_set);
-  if (e != cudaSuccess) return e;
   // a zero scale (every score 0) as 2^-100, so that a hidden score scales to
-  // -inf: scores of finite inputs stay below 2^-60 and weigh 1 as before
+  // -inf: scores of q and k whose products stay below 2^40 are below 2^-60 then
+  // and weigh 1 as before
   PrefillParams pp = p;
   if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
-  return launch_pdl(prefill_q4_kernel, dim3((unsigned)(items.count * p.num_kv_heads)), dim3(kThreads), kSmemBytes,
-                    stream, pp, items, q_map);
+  if (items.count <= 96) return launch<96>(pp, items, rows, q_map, ctas, g_attr_set[0], stream);
+  return launch<kMaxPrefillItems>(pp, items, rows, q_map, ctas, g_attr_set[1], stream);
 }
 
 }  // namespace pa

@@ -180,12 +180,21 @@ MANY = {
     "chunk_tile_edges": ([128, 129, 160, 257, 96], [32, 33, 31, 64, 65], 1),
     "mixed": ([900, 40, 1, 2000, 513, 77], [100, 1, 1, 1, 7, 0], 2),
     "idle_rows": ([50, 0, 30, 70, 9], [0, 0, 3, 0, 1], 2),
+    # more jobs than SMs, of one and of two query tiles in every order
+    "jobs_in_turn": ([int(x) for x in np.random.default_rng(6).integers(7, 200, 40)],
+                     [int(x) for x in np.random.default_rng(7).integers(7, 100, 40)], 8),
+    "jobs_in_turn_late": ([int(x) for x in np.random.default_rng(8).integers(400, 900, 24)],
+                          [int(x) for x in np.random.default_rng(9).integers(7, 140, 24)], 8),
+    "two_to_six_queries": ([40, 2, 333, 16, 17, 90, 3000, 6, 128], [2, 2, 3, 4, 5, 6, 6, 6, 4], 3),
+    "few_queries_many_rows": ([int(x) for x in np.random.default_rng(10).integers(6, 60, 300)],
+                              [int(x) for x in np.random.default_rng(11).integers(0, 7, 300)], 2),
 }
 
 
 @pytest.mark.parametrize("name", sorted(MANY))
 def test_rows_with_several_queries(name):
     seq, qo, Hkv = MANY[name]
+    qo = [min(a, b) for a, b in zip(seq, qo)]
     c = Case(seq, qo, Hkv, seed=len(name))
     ws = B.new_workspace(B.pa_attention_workspace_size(len(seq), sum(qo), 4 * Hkv, 128, max(seq)), DEV)
     c.check(*c.run(workspace=ws), what=name)
