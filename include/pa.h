@@ -224,6 +224,13 @@ pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const voi
  * chunked-prefill and verify rows alike: every K and V element is the bf16
  * value its code stands for, the rest of the definition, the arguments, the
  * workspace (pa_attention_workspace_size) and the errors are unchanged.
+ * A workspace that only q4 calls use needs no zero-filling (apart from the
+ * error word), and may come from calls of other sizes; the partial results
+ * that a call leaves in it are no zeros for the other entry points' counters.
+ * Weights are rounded to bf16 before they meet V in rows of several queries;
+ * in rows of one they carry 16 bits, unless ceil(seq_len / 16) * num_kv_heads
+ * exceeds a million.  Scores of rows with many queries must stay below 2^30 in
+ * magnitude.
  */
 pa_status pa_attention_varlen_q4(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
                                  const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,

@@ -9,6 +9,7 @@ module raises ImportError (there is no fallback path).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -230,8 +231,16 @@ _current_device = torch.cuda.current_device
 
 def _stream_handle(stream, device):
     if stream is not None:
+        if stream.device_index != device:
+            raise ValueError("stream must belong to the current device")
         return stream.cuda_stream
     return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream):
+    """Tensors made in this context are made on `stream` (None: the current
+    one), so that they are ordered with the call that uses them there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _data(t, dtype, name, device):
@@ -266,7 +275,8 @@ def pa_kv_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, workspace=None
         raise ValueError("inconsistent shapes")
     dev = _current_device()
     if workspace is None:
-        workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
+        with _on(stream):
+            workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
     _check(_lib.pa_kv_append_q4(_data(k_new, torch.bfloat16, "k_new", dev), _data(v_new, torch.bfloat16, "v_new", dev),
                                 _data(slot_mapping, torch.int64, "slot_mapping", dev), N,
                                 _data(k_cache, torch.uint8, "k_cache", dev), _data(v_cache, torch.uint8, "v_cache", dev),
@@ -283,15 +293,16 @@ def pa_kv_read_q4(slot_mapping, k_cache, v_cache, k_out=None, v_out=None, worksp
     if v_cache.shape != k_cache.shape or slab != PA_Q4_SLAB_BYTES or slot_mapping.dim() != 1:
         raise ValueError("inconsistent shapes")
     N = slot_mapping.shape[0]
-    if k_out is None:
-        k_out = torch.empty((N, Hkv, 128), dtype=torch.bfloat16, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty((N, Hkv, 128), dtype=torch.bfloat16, device=k_cache.device)
+    if k_out is None or v_out is None:
+        with _on(stream):
+            k_out, v_out = (torch.empty((N, Hkv, 128), dtype=torch.bfloat16, device=k_cache.device) if t is None else t
+                            for t in (k_out, v_out))
     if k_out.shape != (N, Hkv, 128) or v_out.shape != (N, Hkv, 128):
         raise ValueError("k_out and v_out must be [N, Hkv, 128]")
     dev = _current_device()
     if workspace is None:
-        workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
+        with _on(stream):
+            workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
     _check(_lib.pa_kv_read_q4(_data(slot_mapping, torch.int64, "slot_mapping", dev), N,
                               _data(k_cache, torch.uint8, "k_cache", dev), _data(v_cache, torch.uint8, "v_cache", dev),
                               nb, 16, Hkv, 128, _data(k_out, torch.bfloat16, "k_out", dev),
@@ -314,17 +325,20 @@ def pa_attention_varlen_q4(q, k_cache, v_cache, block_tables, seq_lens, qo_indpt
     slh, slh_at = _host_data(seq_lens if seq_lens_host is None else seq_lens_host, R, "seq_lens_host")
     qih, qih_at = _host_data(qo_indptr if qo_indptr_host is None else qo_indptr_host, R + 1, "qo_indptr_host")
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if lse is None and return_lse:
-        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            lse = torch.empty((total_q, Hq), dtype=torch.float32, device=q.device)
     elif lse is not None and lse.shape != (total_q, Hq):
         raise ValueError("lse must be [total_q, Hq]")
     dev = _current_device()
     if workspace is None:
         max_len = int(slh.max()) if R else 1
-        workspace = new_workspace(pa_attention_workspace_size(R, total_q, Hq, D, max_len), q.device)
+        with _on(stream):
+            workspace = new_workspace(pa_attention_workspace_size(R, total_q, Hq, D, max_len), q.device)
     _check(_lib.pa_attention_varlen_q4(_data(q, torch.bfloat16, "q", dev), _data(k_cache, torch.uint8, "k_cache", dev),
                                        _data(v_cache, torch.uint8, "v_cache", dev), nb,
                                        _data(block_tables, torch.int32, "block_tables", dev), block_tables.shape[1],

@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stddef.h>
 
+#include <chrono>
+
 #include "internal.h"
 #include "q4.cuh"
 
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int kPair = 2;     // pages per stage
 constexpr float kRescaleSlack = 8.f;  // the running max is re-based when it grows by more than 2^8
-constexpr float kNoMax = 1e30f;
+constexpr float kNoMax = 3.402823466e38f;  // the greatest binary32: any score is above its negative
 
 struct Item {        // one row's pages within this CTA's segment
   int32_t q_start;  // first page of the item in the segment
@@ -353,6 +355,34 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
   for (int i = 0; i < kStages; ++i) issue(i);
 
+  // The pieces of a row cut between CTAs lie in the workspace: segments b0 ..
+  // b1 hold the row, and each CTA's piece of it is its last item's or its
+  // first's.  The pieces that have arrived are counted in a word beside the
+  // first one, tag << 16 | count.  Every CTA of the row makes sure before it
+  // adds its piece that the word carries this launch's tag, so what the workspace
+  // held before (from calls of other shapes, or not cleared) does not matter.
+  constexpr int kSlots = q4_piece_slots(kTiles);
+  auto first_seg = [&](const Item& it) { return it.A / plan.seg; };
+  auto piece_at = [&](const Item& it, int bb) {
+    const int b0 = first_seg(it);
+    return ((size_t)(bb * Hkv + kvh) * 2 + ((bb == b0 && b0 * plan.seg < it.A) ? 1 : 0)) * kSlots;
+  };
+  auto cut = [&](const Item& it) { return it.p0 != 0 || it.n != (it.L + kPage - 1) / kPage; };
+  // (the host sized the workspace: never false)
+  auto piece_fits = [&](const Item& it) { return (int64_t)(piece_at(it, sidx) + kSlots) <= p.piece_slots; };
+  auto word_of = [&](const Item& it) {
+    return reinterpret_cast<unsigned long long*>(p.piece_lse + piece_at(it, first_seg(it)) + kSlots - 2);
+  };
+  if (lane < 2 && n_items > lane) {  // (while the first pages are on their way)
+    const Item& it = sm.items[lane == 0 ? n_items - 1 : 0];
+    if (it.q_start / sw == warp && cut(it) && piece_fits(it)) {  // the item's first warp
+      unsigned long long* word = word_of(it);
+      const unsigned long long was = *reinterpret_cast<volatile unsigned long long*>(word);
+      if (was >> 16 != plan.tag) atomicCAS(word, was, (unsigned long long)plan.tag << 16);
+    }
+  }
+  __syncwarp();
+
   const int r = lane >> 2;   // token slot (r, r + 8) in the scores; dim row in the output
   const int cq = lane & 3;   // the lane's columns in scores and output: head cq, or 2 cq and 2 cq + 1
   // matrix-load address of lane l: matrix (group) l / 8, row (token) l % 8
@@ -573,8 +603,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                                         : make_float4(c[0][x], c[0][2 + x], c[1][x], c[1][2 + x]);
         }
       }
-    const int pages_r = (L + kPage - 1) / kPage;
-    const bool cut = it.p0 != 0 || it.n != pages_r;  // between CTAs
+    const bool is_cut = cut(it);  // between CTAs
     const int wf = it.q_start / sw, wl = (it.q_start + it.n - 1) / sw;  // warps holding the item
     if (wf != wl) {
       const int slot = it.q_start <= a ? 0 : 1;  // the warp's first item, or its last
@@ -601,14 +630,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       }
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
     }
-    // the pieces of a row cut between CTAs: segments b0 .. b1 hold it, each
-    // CTA's piece of it is its last item's or its first's
-    const int b0 = it.A / plan.seg, b1 = (it.A + pages_r - 1) / plan.seg;
-    constexpr int kSlots = kT * S::kTileCols;  // (piece, head) slots of the workspace per piece
-    auto piece_at = [&](int bb) {
-      return ((size_t)(bb * Hkv + kvh) * 2 + ((bb == b0 && b0 * plan.seg < it.A) ? 1 : 0)) * kSlots;
-    };
-    if (cut && (int64_t)(piece_at(sidx) + kSlots) > p.piece_slots) {  // the host sized the workspace for fewer
+    const int b0 = first_seg(it), b1 = (it.A + (L + kPage - 1) / kPage - 1) / plan.seg;
+    if (is_cut && !piece_fits(it)) {
       if (lane == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
       continue;
     }
@@ -644,11 +667,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
               return sm.part_l[wf + i][it.q_start <= (wf + i) * sw ? 0 : 1][y * S::kTileCols + kCols * cq + c];
             },
             [&](int i) { return part_of(sm, wf + i, it.q_start <= (wf + i) * sw ? 0 : 1) + y * S::kVec * 32; });
-      if (!cut) {
+      if (!is_cut) {
         output(y, own[y]);
         continue;
       }
-      const size_t mine = piece_at(sidx) + y * S::kTileCols;
+      const size_t mine = piece_at(it, sidx) + y * S::kTileCols;
       float4* dst = reinterpret_cast<float4*>(p.piece_o + mine * kHeadDim);
 #pragma unroll
       for (int x = 0; x < kCols; ++x) {
@@ -662,13 +685,13 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
           p.piece_lse[mine + kCols * cq + x] = own[y].l[x] > 0.f ? own[y].m[x] + log2f(own[y].l[x]) : -INFINITY;
       }
     }
-    if (!cut) continue;
+    if (!is_cut) continue;
     __syncwarp();  // every lane's writes precede lane 0's release
     int last = 0;
     if (lane == 0) {
-      int* cnt = p.counters + (size_t)it.r * Hkv + kvh;
-      last = atom_add_acq_rel_gpu(cnt, 1) == b1 - b0;
-      if (last) *cnt = 0;  // every piece has arrived: ready for the next call
+      unsigned long long* word = word_of(it);
+      last = (int)(atom_add_acq_rel_gpu(word, 1ull) & 0xffffu) == b1 - b0;
+      if (last) *word = 0;  // every piece has arrived: ready for the next replay with this tag
     }
     __syncwarp();  // lane 0's acquire orders the reads below
     if (!__shfl_sync(0xffffffffu, last, 0)) continue;
@@ -677,19 +700,33 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       Part<kCols> all;
       merge_parts<kCols>(
           all, b1 - b0 + 1, lane,
-          [&](int i, int c) { return __ldcg(p.piece_lse + piece_at(b0 + i) + y * S::kTileCols + kCols * cq + c); },
+          [&](int i, int c) { return __ldcg(p.piece_lse + piece_at(it, b0 + i) + y * S::kTileCols + kCols * cq + c); },
           [&](int, int) { return 1.f; },
           [&](int i) {
-            return reinterpret_cast<const float4*>(p.piece_o + (piece_at(b0 + i) + y * S::kTileCols) * kHeadDim);
+            return reinterpret_cast<const float4*>(p.piece_o + (piece_at(it, b0 + i) + y * S::kTileCols) * kHeadDim);
           });
       output(y, all);
     }
   }
-  // beside a tile kernel: this launch completes after it
+  // beside a tile kernel: this launch completes after it (the last thing that
+  // the warps with pages do; one of them is enough)
   if (p.beside) pdl_wait();
 }
 
 std::atomic<bool> g_attr_set[6][kMaxDevices];
+
+// A tag that no earlier launch of this process has had, and that other data
+// are as good as never: 47 bits of a scrambled count (the finalizer of the
+// splitmix64 generator), never 0.
+uint64_t next_tag() {
+  static std::atomic<uint64_t> count{
+      (uint64_t)std::chrono::system_clock::now().time_since_epoch().count()};
+  uint64_t z = count.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  z ^= z >> 31;
+  return z >> 17 | uint64_t(1) << 47;
+}
 
 template <int kTiles, class Plan>
 cudaError_t launch(const DecodeParams& p, const Plan& plan, int grid, bool overlap, std::atomic<bool>* done,
@@ -713,6 +750,7 @@ cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const in
     d.seg = plan.seg;
     d.total = plan.total;
     d.by_row = by_row ? 1 : 0;
+    d.tag = next_tag();
     for (int i = 0; i < plan.n_rows; ++i) d.row[i] = make_int4(plan.rows[i], plan.seq[i], plan.tok[i], n_q[i]);
     for (int i = 0; i < segs; ++i) d.start[i] = make_int2(plan.first_row[i], plan.first_page[i]);
   };

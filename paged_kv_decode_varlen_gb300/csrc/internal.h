@@ -86,6 +86,9 @@ constexpr int kQ4DecodeQueries = 6;
 constexpr int q4_decode_tiles(int n_q) { return n_q == 1 ? 0 : n_q <= 4 ? 2 : 3; }
 // Warps per CTA: as many as registers (tiles) and shared memory leave room for.
 constexpr int q4_decode_warps(int tiles) { return tiles == 0 ? 12 : 8; }
+// (piece, head) slots of the workspace that a piece of a row cut between CTAs
+// takes: its columns, and a 64-bit word in two of the lse slots.
+constexpr int q4_piece_slots(int tiles) { return (tiles == 0 ? PA_GQA_GROUP : 8 * tiles) + 2; }
 static_assert(kQ4MaxPagesPerCta % 12 == 0 && kQ4MaxPagesPerCta % 8 == 0, "whole warp segments");
 // Bytes of one (page, kv head) slab of K or V in bf16 (16 tokens x 128 dims).
 constexpr int kSlabBytesHost = 16 * 128 * 2;
@@ -106,6 +109,7 @@ template <int R, int C>
 struct Q4Plan {
   int32_t n_rows, seg, total;
   int32_t by_row;  // a segment holds pages of its first row only
+  uint64_t tag;    // marks this launch's words in the workspace (48 bits)
   int4 row[R];    // request, seq_len, first query token, queries
   int2 start[C];  // a segment's first row and that row's first page
 };

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <memory>
 #include <vector>
 
@@ -328,6 +329,20 @@ int prefill_alone_ctas(const std::vector<int32_t>& job_tiles, int sms) {
   return (int)best_g;
 }
 
+// CTAs of a q4 decode launch, of those that gcap and the workspace's slots allow.
+int q4_grid_cap(int gcap, int64_t slots, int tiles) {
+  return (int)std::min<int64_t>(gcap, slots / (2 * pa::q4_piece_slots(tiles)));  // two pieces a CTA
+}
+
+// Whether a row of L keys fits a q4 decode launch (in any batch: a workspace
+// is no smaller for more rows).  Those that do not, a million pages over all
+// kv heads, run on the tile kernel.
+bool q4_row_fits(int32_t L, int tiles, int num_kv_heads) {
+  const int gcap = grid_cap(1, num_kv_heads, L);
+  const int segs = q4_grid_cap(gcap, layout_for_grid(1, num_kv_heads, pa::kHeadDim, gcap).slots, tiles) / num_kv_heads;
+  return pages_of(L) <= (int64_t)segs * pa::kQ4MaxPagesPerCta;
+}
+
 // Whether the tile jobs of a q4 batch (rows of many queries; `jobs` CTAs, one
 // per SM, the longest of key_tiles tiles) run beside the decode launch, which
 // then has the other SMs: where that ends sooner than the jobs first and the
@@ -636,11 +651,13 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         return fail(PA_ERR_INVALID_ARG, "request %d: the shared prefix (%d pages) must be cached before its %d queries",
                     r, prefix_pages, qo_len);
     }
-    if (qo_len == 1) {
+    const bool decodes = !q4 || (qo_len <= pa::kQ4DecodeQueries &&
+                                 q4_row_fits(L, pa::q4_decode_tiles(qo_len), num_kv_heads));
+    if (qo_len == 1 && decodes) {
       decode_rows.push_back(r);
-    } else if (q4 && qo_len > 1 && qo_len <= pa::kQ4DecodeQueries) {
+    } else if (q4 && qo_len > 1 && decodes) {
       q4_rows[pa::q4_decode_tiles(qo_len) == 2 ? 0 : 1].push_back(r);
-    } else if (qo_len > 1) {
+    } else if (qo_len >= 1) {
       const int32_t q_tile = q4 ? pa::kQ4TileTokens : pa::kPrefillQTile;
       for (int32_t j0 = 0; j0 < qo_len; j0 += q_tile) {
         tiles.push_back({L - qo_len + std::min(qo_len, j0 + q_tile), (int32_t)item_req.size()});
@@ -896,9 +913,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
           int n = (int)std::min(rows->size() - d0, (size_t)pa::kPlanMaxRows);
           const int32_t* r0 = rows->data() + d0;
           const int cls = pa::q4_decode_tiles(qo_indptr_host[r0[0] + 1] - qo_indptr_host[r0[0]]);
-          // a piece takes 4 (piece, head) slots of the workspace, or 8 per tile
-          const int64_t piece = cls == 0 ? PA_GQA_GROUP : 8 * cls;
-          const int cap = (int)std::min<int64_t>(gcap, wl.slots / (2 * piece));
+          const int cap = q4_grid_cap(gcap, wl.slots, cls);
           int grid;
           for (;; n = (n + 1) / 2) {
             grid = plan_decode(r0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, cap, slots,
@@ -1044,9 +1059,13 @@ pa_status pa_attention_varlen_q4(const void* q, const void* k_cache, const void*
                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                  float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                                  pa_stream_t stream) {
-  return attention(q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_req, seq_lens, qo_indptr,
-                   seq_lens_host, qo_indptr_host, num_reqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size,
-                   0, sm_scale, out, lse, workspace, workspace_bytes, stream, Pages::kQ4);
+  try {
+    return attention(q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_req, seq_lens, qo_indptr,
+                     seq_lens_host, qo_indptr_host, num_reqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size,
+                     0, sm_scale, out, lse, workspace, workspace_bytes, stream, Pages::kQ4);
+  } catch (const std::bad_alloc&) {  // of the plan's host arrays
+    return fail(PA_ERR_UNSUPPORTED, "no host memory for the plan of %d requests", num_reqs);
+  }
 }
 
 }  // extern "C"

@@ -606,16 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before_sync();  // the tensor-memory reads above precede the arrive
         mbar_arrive(&sm.o_free[x]);
       }
-      if (tok >= job.nq) continue;
+      if (tok < job.nq) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[8];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(o[16 * h + 2 * y] * inv, o[16 * h + 2 * y + 1] * inv);
-        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c + 16 * h);  // (out is 16-byte aligned, not 32)
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(o[16 * h + 2 * y] * inv, o[16 * h + 2 * y + 1] * inv);
+          uint4* dst = reinterpret_cast<uint4*>(out + 32 * c + 16 * h);  // (out is 16-byte aligned, not 32)
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
+      __syncwarp();  // the next load takes the whole warp
     }
     if (p.lse && tok < job.nq) p.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     J0 += job.n_tiles;

@@ -368,3 +368,160 @@ def test_calls_on_two_streams_with_workspaces_of_their_own():
         for out, lse in runs:
             c.check(out, lse)
             assert torch.equal(out, runs[0][0])
+
+
+# --------------------------------------------- calls that a rule sends elsewhere
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, -1e-44])
+def test_zero_negative_and_tiny_scales(scale):
+    c = Case([300, 33, 150, 70], [1, 4, 90, 40], 2, seed=51)
+    c.b.sm_scale = scale
+    out, lse = c.run()
+    c.b.sm_scale = abs(scale)
+    if scale < 0:  # for the oracle the sign goes to q
+        c.b.q[:] ^= np.uint16(0x8000)
+    c.check(out, lse, f"scale {scale}")
+
+
+@pytest.mark.parametrize("qo,scale", [(1, 1e36), (2, 1e36), (6, 1e36), (7, 1e6), (40, 1e6)])
+def test_very_large_scores(qo, scale):
+    """A row's first query of a whole prompt sees one key: the output is its
+    value (to the rounding of the weight and of the output, 2^-8 each), lse its
+    score."""
+    c = Case([qo, qo], [qo, qo], 2, seed=52)
+    c.b.sm_scale = scale
+    out, lse = c.run()
+    k, v, q = (oracle.bf16_to_f64(x) for x in (q4.unpack(c.hk), q4.unpack(c.hv), c.b.q))
+    got = oracle.bf16_to_f64(bf16_host(out))
+    for r in range(2):
+        blk = int(c.b.block_tables[r, 0])
+        for h in range(8):
+            key, val = k[blk, h // 4, 0], v[blk, h // 4, 0]
+            assert np.all(np.abs(got[r * qo, h] - val) <= 2.0 ** -7 * np.abs(val) * (1 + 2.0 ** -6))
+            score = scale * float(q[r * qo, h] @ key)
+            # 128 products and sums in binary32, then the scale's roundings
+            assert abs(float(lse[r * qo, h]) - score) <= 2.0 ** -16 * scale * float(np.abs(q[r * qo, h]) @ np.abs(key))
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("qo", [[1, 1], [5, 5], [90, 40]])
+def test_views_at_sixteen_byte_offsets(qo):
+    c = Case([200, 61], qo if qo[1] <= 61 else [90, 40], 2, seed=54)
+    want, want_lse = c.run()
+    d, total = c.dev, int(c.b.qo_indptr[-1])
+
+    def shifted(t, fill=0):
+        buf = torch.full((t.numel() + 8,), fill, dtype=t.dtype, device=DEV)
+        view = buf[8:].view(t.shape)  # 16 bytes of bf16
+        return buf, view
+
+    _, q = shifted(d["q"])
+    q.copy_(d["q"])
+    obuf, out = shifted(want, 7)
+    pools = []
+    for pool in (c.kc, c.vc):
+        buf = torch.empty(pool.numel() + 16, dtype=torch.uint8, device=DEV)
+        pools.append(buf[16:].view(pool.shape))
+        pools[-1].copy_(pool)
+    got, lse = B.pa_attention_varlen_q4(q, pools[0], pools[1], d["tables"], d["seq"], d["ind"], c.b.sm_scale, out=out,
+                                        return_lse=True)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse) and got.shape[0] == total
+    assert bool((obuf[:8] == 7).all())
+
+
+def test_tile_jobs_beside_the_decode_launch_or_before_it():
+    c = Case([1500, 1200, 900, 800, 300, 700], [100, 1, 1, 1, 1, 1], 2, seed=55)
+    out, lse = c.run()
+    c.check(out, lse, "as planned")
+    B.pa_set_prefill_ctas(-1)
+    try:
+        first, first_lse = c.run()
+        torch.cuda.synchronize()
+    finally:
+        B.pa_set_prefill_ctas(0)
+    c.check(first, first_lse, "one after the other")
+    assert torch.equal(first[:100], out[:100])  # the tile jobs' own rows do not depend on it
+
+
+def test_results_do_not_depend_on_what_the_workspace_held():
+    sizes = [([900, 1500], [1, 1]), ([300] * 70, [1] * 70), ([4000], [5]), ([64, 2000, 31], [64, 1, 3])]
+    cases = [Case(s, q, 2, seed=56 + i) for i, (s, q) in enumerate(sizes)]
+    need = max(B.pa_attention_workspace_size(len(s), sum(q), 8, 128, max(s)) for s, q in sizes)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device=DEV)
+    ws[:B.PA_ERROR_WORD_BYTES] = 0
+    clean = [c.run() for c in cases]
+    for _ in range(2):
+        for c, (out, lse) in zip(cases, clean):
+            got, got_lse = c.run(workspace=ws)
+            assert torch.equal(got, out) and torch.equal(got_lse, lse)
+    ws[B.PA_ERROR_WORD_BYTES:] = 0xff
+    for c, (out, _) in zip(reversed(cases), reversed(clean)):
+        assert torch.equal(c.run(workspace=ws)[0], out)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+
+
+def test_two_graphs_share_a_workspace():
+    cases = [Case([2500, 40], [1, 1], 2, seed=61), Case([700, 650, 90], [3, 1, 20], 2, seed=62)]
+    ws = B.new_workspace(max(B.pa_attention_workspace_size(len(c.b.seq_lens), int(c.b.qo_indptr[-1]), 8, 128, 2500)
+                             for c in cases), DEV)
+    want = [c.run() for c in cases]
+    outs, graphs = [], []
+    for c in cases:
+        out, lse = torch.empty_like(c.dev["q"]), torch.empty(c.dev["q"].shape[:2], device=DEV)
+        c.run(out=out, lse=lse, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(out=out, lse=lse, workspace=ws)
+        outs.append((out, lse))
+        graphs.append(g)
+    for order in ([0, 1], [1, 0, 0, 1, 1]):
+        for out, lse in outs:
+            out.zero_()
+            lse.zero_()
+        for i in order:
+            graphs[i].replay()
+        for (out, lse), (w, wl) in zip(outs, want):
+            assert torch.equal(out, w) and torch.equal(lse, wl)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+
+
+def test_rows_behind_the_last_sequence_stay():
+    c = Case([77, 130, 20], [1, 40, 3], 2, seed=63)
+    want, want_lse = c.run()
+    total = want.shape[0]
+    big = torch.full((total + 90, 8, 128), -5.0, dtype=torch.bfloat16, device=DEV)
+    biglse = torch.full((total + 90, 8), -5.0, device=DEV)
+    c.run(out=big[:total], lse=biglse[:total])
+    assert torch.equal(big[:total], want) and torch.equal(biglse[:total], want_lse)
+    assert bool((big[total:] == -5).all()) and bool((biglse[total:] == -5).all())
+    kc, vc = _pool_pair(4, 2)
+    k = bf16_dev(_rows(np.random.default_rng(64), 9, 2))
+    B.pa_kv_append_q4(k, k, torch.arange(9, device=DEV), kc, vc)
+    buf = torch.full((15, 2, 128), -5.0, dtype=torch.bfloat16, device=DEV)
+    B.pa_kv_read_q4(torch.arange(9, device=DEV), kc, vc, k_out=buf[:9], v_out=torch.empty_like(k))
+    assert bool((buf[9:] == -5).all()) and not bool((buf[:9] == -5).all())
+
+
+@pytest.mark.parametrize("qo", [1, 6])
+def test_rows_of_a_million_pages(qo):
+    """A table that names eight blocks over and over: every key counts as often
+    as its block is named, so the output is that of the eight blocks and lse is
+    greater by the logarithm of their number."""
+    Hkv, times = 256, 1100  # 8800 pages x 256 heads: no decode plan
+    c = Case([128], [qo], Hkv, seed=65)
+    out, lse = c.run()
+    q = c.dev["q"]
+    tables = c.dev["tables"][:, :8].repeat(1, times).contiguous()
+    L = 128 * times
+    seq = torch.tensor([L], dtype=torch.int32, device=DEV)
+    ind = torch.tensor([0, qo], dtype=torch.int32, device=DEV)
+    got, got_lse = B.pa_attention_varlen_q4(q, c.kc, c.vc, tables, seq, ind, c.b.sm_scale, return_lse=True)
+    # the last query sees every key.  Each output is off by at most its weights'
+    # rounding (2^-8 of max |v|) and half of its own (2^-8): twice that, and the
+    # sums of 140800 weights in binary32, in steps of 64 (2^-24 each)
+    a, b = got[-1].double(), out[-1].double()
+    v = oracle.bf16_to_f64(q4.unpack(c.hv))[c.b.block_tables[0, :8]]
+    big = float(np.abs(v).max())
+    assert float((a - b).abs().max()) <= (4 * 2.0 ** -8 + 2.0 ** -12) * big
+    assert float((got_lse[-1] - lse[-1] - np.log(times)).abs().max()) <= 2.0 ** -12
