@@ -310,9 +310,10 @@ cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, cons
 cudaError_t launch_decode_step(const DecodeParams& p, const StepPlan& plan, int grid, bool warp_granular,
                                cudaStream_t stream);
 // q4 pages: (item of kQ4TileTokens queries, kv head) jobs on ctas CTAs; rows[i]
-// is item i's (request, first query token, its position, queries)
-cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows,
-                              const CUtensorMap& q_map, int ctas, cudaStream_t stream);
+// is item i's (request, first query token, its position, queries), maps.q and
+// maps.k the tensor maps of q (boxes of 32 tokens) and of out (of one)
+cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows, const TcMaps& maps,
+                              int ctas, cudaStream_t stream);
 // ctas: CTAs of the launch (0: one per (item, kv head) job; fewer run
 // several jobs each)
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, const TcMaps& maps, int ctas,

@@ -523,15 +523,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tiled map of q ([total_q][Hq][128] bf16, boxes 64 x 4 heads x 32 tokens),
-// 128-byte swizzled; out-of-range q tokens read as 0.
-pa_status make_q_map(const void* q, int32_t total_q, int32_t num_q_heads, CUtensorMap& m) {
+// Tiled map of q or out ([total_q][Hq][128] bf16, boxes 64 x 4 heads x
+// box_tokens), 128-byte swizzled; out-of-range q tokens read as 0.
+pa_status make_q_map(const void* q, int32_t total_q, int32_t num_q_heads, int box_tokens, CUtensorMap& m) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint32_t estr[3] = {1, 1, 1};
   const cuuint64_t qdims[3] = {(cuuint64_t)pa::kHeadDim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
   const cuuint64_t qstrides[2] = {(cuuint64_t)pa::kHeadDim * 2, (cuuint64_t)num_q_heads * pa::kHeadDim * 2};
-  const cuuint32_t qbox[3] = {64, (cuuint32_t)pa::kGroup, (cuuint32_t)pa::kPrefillQTile};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)pa::kGroup, (cuuint32_t)box_tokens};
   const CUresult r = enc(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), qdims, qstrides, qbox, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -546,7 +546,7 @@ pa_status make_tc_maps(const void* q, int32_t total_q, int32_t num_q_heads, cons
   const int64_t rows = num_blocks * num_kv_heads * pa::kPage;
   if (rows >= (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "pool of %lld rows: too many for the tile kernels",
                                                (long long)rows);
-  const pa_status s = make_q_map(q, total_q, num_q_heads, m.q);
+  const pa_status s = make_q_map(q, total_q, num_q_heads, pa::kPrefillQTile, m.q);
   if (s != PA_OK) return s;
   const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   const cuuint32_t estr[2] = {1, 1};
@@ -684,8 +684,9 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   float* prefix_lse = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_lse) : nullptr;
   static thread_local pa::TcMaps maps;
   if (P > 0 || !tiles.empty()) {
-    s = q4 ? make_q_map(q, total_q, num_q_heads, maps.q)
+    s = q4 ? make_q_map(q, total_q, num_q_heads, pa::kPrefillQTile, maps.q)
            : make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
+    if (s == PA_OK && q4) s = make_q_map(out, total_q, num_q_heads, 32 / pa::kGroup, maps.k);
     if (s != PA_OK) return s;
   }
 
@@ -860,7 +861,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       }
       s = run_launch(PA_KERNEL_PREFILL, "prefill", stream,
                      [&] {
-                       return q4 ? pa::launch_prefill_q4(pp, items, q4_items, maps.q,
+                       return q4 ? pa::launch_prefill_q4(pp, items, q4_items, maps,
                                                          std::min(items.count * num_kv_heads, sm_count()), stream)
                                  : pa::launch_prefill(pp, items, maps, prefill_ctas, stream);
                      });

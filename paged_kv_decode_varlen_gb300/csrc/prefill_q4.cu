@@ -70,6 +70,7 @@ constexpr int kAhead = 3;                    // units a producer warp reads ahea
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
 constexpr float kMaxSum = 1024.f;  // of 32 weights, before their row's reference is raised
+constexpr int kOutTok = 32 / kGroup;         // query tokens of a softmax warp
 constexpr int kSub = 64;                     // keys of a score product
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
@@ -81,6 +82,7 @@ struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kKStages][kTileBytes];
   uint8_t v[kVStages][kTileBytes];
+  uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 dims at a time
   uint64_t q_full, q_free;  // a job's Q has landed; its last scores are done
   uint64_t o_free[2];       // the softmax warps have read a job's output
   uint64_t k_full[kKStages], k_empty[kKStages];
@@ -205,6 +207,19 @@ __device__ __noinline__ void rescale(uint32_t t_o, uint32_t t_p, int quarters, b
   wait_st();
 }
 
+// A box of a tensor map from shared to global memory, in the thread's current
+// group of bulk copies; groups; and waits for all of the thread's groups to have
+// read shared memory / to have been written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 struct Job {
   int32_t tok0;  // first query token of the job
   int32_t nq;    // its query tokens (1 .. 64)
@@ -217,17 +232,24 @@ struct Job {
 };
 
 // The CTA's jobs: job b of every round of gridDim.x jobs, in reverse order on
-// odd rounds (the items come longest first).  Calls f(job) until it returns
-// false.
-template <class Items, class F>
-__device__ __forceinline__ void for_each_job(const PrefillParams& p, const Items& items, F&& f) {
-  const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
-  for (int base = 0, odd = 0; base < n; base += G, odd ^= 1) {
+// odd rounds (the items come longest first).
+template <class Items>
+struct Jobs {
+  const PrefillParams& p;
+  const Items& items;
+  int base, odd;
+  __device__ __forceinline__ Jobs(const PrefillParams& p_, const Items& items_) : p(p_), items(items_), base(0), odd(0) {}
+  __device__ __forceinline__ bool next(Job& job) {
+    const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
     const int u = base + (odd ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    if (u >= n) continue;
+    if (u >= n) {  // (a last round that has no job for this CTA)
+      base = n;
+      return false;
+    }
+    base += G;
+    odd ^= 1;
     const int it = u / p.num_kv_heads;
     const int4 item = items.item[it];  // request, first query token, its position, queries
-    Job job;
     job.tok0 = item.y;
     job.nq = item.w;
     job.kvh = u - it * p.num_kv_heads;
@@ -237,9 +259,9 @@ __device__ __forceinline__ void for_each_job(const PrefillParams& p, const Items
     job.n_tiles = (job.keys + kKeys - 1) / kKeys;
     job.n_sub = (job.keys + kSub - 1) / kSub;
     job.n_x = job.nq > kTok ? 2 : 1;
-    if (!f(job)) return;
+    return true;
   }
-}
+};
 
 // Producer warp w: units w, w + 6, ... of the job (unit u: key tile u / 16, K
 // pages 0 .. 7, then V pages 0 .. 7); J0: the CTA's key tiles before the job's.
@@ -343,7 +365,7 @@ __device__ __forceinline__ bool produce(Smem& sm, const Job& job, int w, int J0,
 template <class Items>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const PrefillParams p, const __grid_constant__ Items items,
-                      const __grid_constant__ CUtensorMap q_map) {
+                      const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap out_map) {
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -384,13 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp >= kProducer0) {
+    Jobs<Items> jobs(p, items);
+    Job job;
     int J0 = 0;
-    for_each_job(p, items, [&](const Job& job) {
-      const bool ok = produce(sm, job, warp - kProducer0, J0, reinterpret_cast<const uint8_t*>(p.k_cache),
-                              reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, p.err);
+    while (jobs.next(job) &&
+           produce(sm, job, warp - kProducer0, J0, reinterpret_cast<const uint8_t*>(p.k_cache),
+                   reinterpret_cast<const uint8_t*>(p.v_cache), p.num_kv_heads, p.num_blocks, p.err))
       J0 += job.n_tiles;
-      return ok;
-    });
   } else if (warp >= kMmaWarp) {
     // --------------------------------------------------------- MMA issuers
     // The whole warp runs this (so that descriptors and addresses are
@@ -404,10 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto arrived = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
     };
-    // Q of a job (its n-th): after the last scores of the job before
+    // running counts: key tiles, jobs, this query tile's sub-tiles and jobs, Qs loaded
+    int J0 = 0, n_job = 0, I0 = 0, n_own = 0, n_q = 0;
+    // Q of a job: after the last scores of the job before
     auto load_q = [&](const Job& job) {
-      const uint32_t on = elect_one();
-      if (on) {
+      n_q += 1;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&sm.q_full, job.n_x * kTileBytes);
         for (int y = 0; y < job.n_x; ++y) {
           tma_load_3d(sm.q[y], &q_map, 0, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
@@ -416,14 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    // running counts: key tiles, jobs, this query tile's sub-tiles and jobs
-    int J0 = 0, n_job = 0, I0 = 0, n_own = 0;
-    bool ok = true;
-    for_each_job(p, items, [&](const Job& job) {
-      if (x == 0) {
-        ok = n_job == 0 || arrived(&sm.q_free, n_job - 1);
-        if (ok) load_q(job);
-      }
+    Jobs<Items> jobs(p, items);
+    Job job, next;
+    bool more = jobs.next(job), ok = true;
+    if (x == 0 && more) load_q(job);
+    while (more && ok) {
       if (x < job.n_x) {
         const int n_sub = job.n_sub;
         // scores of sub-tile i: 64 keys, half i & 1 of the job's key tile i / 2
@@ -463,10 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && arrived(&sm.q_full, n_job);
         for (int i = 0; ok && i < min(n_sub, 2); ++i)
           if ((ok = may_score(i))) issue_s(i);
+        more = jobs.next(next);
         // the first PV product overwrites the output of this tile's job before
         ok = ok && (n_own == 0 || arrived(&sm.o_free[x], n_own - 1));
         for (int i = 0; ok && i < n_sub; ++i) {
           const int J = J0 + (i >> 1), I = I0 + i;
+          if (x == 0 && more && i == n_sub - 1) {  // the next job's Q, while the softmax has the last scores
+            ok = arrived(&sm.q_free, n_job);
+            if (!ok) break;
+            load_q(next);
+          }
           ok = ((i & 1) || arrived(&sm.v_full[J % kVStages], J / kVStages)) && arrived(&sm.p_full[x][I & 1], I >> 1);
           if (!ok) break;
           issue_pv(i);
@@ -489,16 +516,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           pass(&sm.k_full[J % kKStages], &sm.k_empty[J % kKStages], J / kKStages);
           pass(&sm.v_full[J % kVStages], &sm.v_empty[J % kVStages], J / kVStages);
         }
+        more = jobs.next(next);
       }
       J0 += job.n_tiles;
       n_job += 1;
-      return ok;
-    });
+      job = next;
+    }
     // every product issued has completed before the tensor memory is freed (a
     // commit tracks all of them), and Q has landed before the CTA leaves
     commit_if(elect_one(), &sm.drained[x]);
     mbar_wait_bounded(&sm.drained[x], 0);
-    if (x == 0 && n_job > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(n_job - 1) & 1u);
+    if (n_q > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(n_q - 1) & 1u);
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
@@ -508,11 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
     int J0 = 0, I0 = 0;  // running counts: key tiles, this query tile's sub-tiles
-    bool ok = true;
-    for_each_job(p, items, [&](const Job& job) {
+    Jobs<Items> jobs(p, items);
+    Job job;
+    bool more = jobs.next(job), ok = true;
+    while (more) {
     if (x >= job.n_x) {
       J0 += job.n_tiles;
-      return true;
+      more = jobs.next(job);
+      continue;
     }
     const int pos = job.pos0 + x * kTok + (row >> 2);
     float m_run = -INFINITY, l_run = 0.f;
@@ -589,41 +620,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before_sync();  // the tensor-memory accesses above precede the arrive
       mbar_arrive(&sm.p_full[x][I & 1]);
     }
+    if (!ok) break;
     const int I1 = I0 + job.n_sub - 1;
-    if (ok) ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err));
-    if (!ok) return false;
+    if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
     fence_after_sync();
-    // the row straight from the tensor memory
+    // The output, 64 dims at a time, through shared memory (128-byte swizzle)
+    // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored
+    // by the threads, 16 bytes of a row each, an instruction touches 32 lines:
+    // 6000 cycles for a job's last 128 rows against .)
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
     const int tok = x * kTok + (row >> 2);
-    const size_t orow = (size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3);
-    uint16_t* out = p.out + orow * kHeadDim;
+    const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
+    uint8_t* stg = sm.out[warp];
+    uint32_t o[2][32];
+    tmem_ld32_async(t_o, o[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float o[32];
-      tmem_ld32(t_o + 32 * c, o);
-      if (c == 3) {
+    for (int h = 0; h < 2; ++h) {
+      if (lane == 0) bulk_wait_read();  // what was staged before has been read
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        wait_ld(o[c]);
+        if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+        uint32_t w[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+          w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+      }
+      if (h == 1) {
         fence_before_sync();  // the tensor-memory reads above precede the arrive
         mbar_arrive(&sm.o_free[x]);
       }
-      if (tok < job.nq) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(o[16 * h + 2 * y] * inv, o[16 * h + 2 * y + 1] * inv);
-          uint4* dst = reinterpret_cast<uint4*>(out + 32 * c + 16 * h);  // (out is 16-byte aligned, not 32)
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (tok_w + kOutTok <= job.nq) {
+        if (lane == 0) {
+          tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
+          bulk_commit();
+        }
+      } else {  // the row's last tokens
+#pragma unroll 1
+        for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
+          const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
+          *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
+              *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
         }
       }
-      __syncwarp();  // the next load takes the whole warp
     }
-    if (p.lse && tok < job.nq) p.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+    if (p.lse && tok < job.nq)
+      p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
+          l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     J0 += job.n_tiles;
     I0 += job.n_sub;
-    return true;
-    });
+    more = jobs.next(job);
+    }
+    if (lane == 0) bulk_wait_all();  // the stores have been written
+    __syncwarp();
   }
   fence_before_sync();
   __syncthreads();
@@ -634,28 +690,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 std::atomic<bool> g_attr_set[2][kMaxDevices];
 
 template <int N>
-cudaError_t launch(const PrefillParams& p, const PrefillItems& items, const int4* rows, const CUtensorMap& q_map, int ctas,
+cudaError_t launch(const PrefillParams& p, const PrefillItems& items, const int4* rows, const TcMaps& maps, int ctas,
                    std::atomic<bool>* done, cudaStream_t stream) {
   static thread_local Q4Items<N> d;
   d.count = items.count;
   for (int i = 0; i < items.count; ++i) d.item[i] = rows[i];
   const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel<Q4Items<N>>, (int)kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_q4_kernel<Q4Items<N>>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, d, q_map);
+  return launch_pdl(prefill_q4_kernel<Q4Items<N>>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, d, maps.q, maps.k);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows,
-                              const CUtensorMap& q_map, int ctas, cudaStream_t stream) {
+                              const TcMaps& maps, int ctas, cudaStream_t stream) {
   if (items.count <= 0) return cudaSuccess;
   // a zero scale (every score 0) as 2^-100, so that a hidden score scales to
   // -inf: scores of q and k whose products stay below 2^40 are below 2^-60 then
   // and weigh 1 as before
   PrefillParams pp = p;
   if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
-  if (items.count <= 96) return launch<96>(pp, items, rows, q_map, ctas, g_attr_set[0], stream);
-  return launch<kMaxPrefillItems>(pp, items, rows, q_map, ctas, g_attr_set[1], stream);
+  if (items.count <= 96) return launch<96>(pp, items, rows, maps, ctas, g_attr_set[0], stream);
+  return launch<kMaxPrefillItems>(pp, items, rows, maps, ctas, g_attr_set[1], stream);
 }
 
 }  // namespace pa
