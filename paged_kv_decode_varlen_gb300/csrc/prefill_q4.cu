@@ -11,17 +11,22 @@
 // per SM runs its share of the jobs one after another without a barrier between
 // them: rings, phases and buffers are indexed by running counts, so the next
 // job's Q, first key tiles and first scores are made while the softmax warps
-// finish this one (8 prompts of 100 to 1000 tokens: 56 us with a CTA per job).  The two tiles share every dequantised K and V tile,
-// and their softmaxes alternate on the tensor cores: while tile A's warps turn
-// scores into weights, B's products run.
-//   Bound.  Per key tile the products take 2560 cycles of the tensor cores, the
-// instructions of all warps some 2200 of the schedulers'.
+// finish this one (8 prompts of 100 to 1000 tokens, 32 heads: 43.7 us, where a
+// CTA per job took 56).  The two tiles share every dequantised K and V tile.
+//   Bound.  Per key tile of 128 the products take 2560 cycles of the tensor
+// cores, the instructions of all warps some 2200 of the schedulers'; the whole
+// takes some 3400 (4 chunks of 512 tokens behind 4096 to 8192: 174 us, 1117
+// TFLOP/s): a warp that issues products or turns scores into weights waits for
+// its turn among four on a scheduler.  The loops of the three roles fill the
+// instruction cache, so code counts: a third slot of read-ahead in the producers
+// costs 5 % of the prompts' time, two loops kept apart in the issuing warps save
+// 8 % against a merged one.
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory
 // lane = row).  8 and 9: issue the products of A and of B (8 also copies Q by
 // TMA and owns the tensor memory).  10-15: producers.  A unit of their work is
 // one page's K or V slab: each lane reads two 16-byte pieces of codes (tokens t
-// and t + 8 of one group) and their (D, Z), three units ahead, and writes 64
+// and t + 8 of one group) and their (D, Z), two units ahead, and writes 64
 // bf16 values into the 128-byte-swizzled operand tile.  A key tile is 16 units,
 // dealt out to the six warps in turn.  (Dequantised once per CTA in registers: a
 // second copy of the cache in bf16 is never made.)
@@ -36,11 +41,12 @@
 // product) overwrite its scores: the scores of sub-tile i + 1 are there when
 // the softmax has finished sub-tile i, and those of i + 2 follow the PV product
 // of i.  (With one buffer of 128 keys each score product waited for the PV
-// product before it: 4100 cycles per 128 keys against 2900, although 64 columns
-// of B make a score product read its Q tile at the shared memory's limit, 48
-// cycles for 32.)  The softmax takes the scores once, 32 columns at a time,
-// against a reference that is re-based only when weights get large.  Weights are rounded to bf16, as the tensor cores take them; their sum is
-// kept in binary32 from the unrounded ones, as are scores, maxima and outputs.
+// product before it: 206 us for the late chunks against 186 at that step,
+// although 64 columns of B make a score product read its Q tile at the shared
+// memory's limit, 48 cycles for 32.)  The softmax takes the scores once, 32
+// columns at a time, against a reference that is re-based only when weights get
+// large.  Weights are rounded to bf16, as the tensor cores take them; their sum
+// is kept in binary32 from the unrounded ones, as are scores, maxima and outputs.
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its
 // copies and products finish (bounded), frees its tensor memory and returns.
@@ -66,7 +72,7 @@ constexpr int kKStages = 2, kVStages = 2;
 constexpr int kMmaWarp = 8, kProducer0 = 10, kProducers = 6;  // (kMmaWarp + 1: tile B)
 constexpr int kThreads = (kProducer0 + kProducers) * 32;
 constexpr int kUnits = 2 * kPagesPerTile;    // slabs of a key tile
-constexpr int kAhead = 3;                    // units a producer warp reads ahead
+constexpr int kAhead = 2;                    // units a producer warp reads ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
 constexpr float kMaxSum = 1024.f;  // of 32 weights, before their row's reference is raised
@@ -368,7 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap out_map) {
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // roles by warp: hardware warp 0 is role 8 (the issuing warps first: 43.7 us
+  // against 44.3 for the prompts above; a role keeps its warp number modulo 4,
+  // which names its tensor-memory lanes)
+  const int warp = __shfl_sync(0xffffffffu, (((int)threadIdx.x >> 5) + kMmaWarp) & 15, 0), lane = threadIdx.x & 31;
   if (warp == kMmaWarp && lane == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_free, 2);
@@ -625,9 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
     fence_after_sync();
     // The output, 64 dims at a time, through shared memory (128-byte swizzle)
-    // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored
-    // by the threads, 16 bytes of a row each, an instruction touches 32 lines:
-    // 6000 cycles for a job's last 128 rows against .)
+    // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
+    // threads, 16 bytes of a row each, an instruction touches 32 lines: a job's
+    // end took 6000 cycles against 2600, the prompts above 52 us against 47.)
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
     const int tok = x * kTok + (row >> 2);
     const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
