@@ -64,6 +64,9 @@ struct Shape {
   static constexpr int kVec = kCols * 4;           // float4 of output values per lane and tile
   static constexpr int kTileCols = kOne ? 4 : 8;   // columns of a tile
   static constexpr int kWarps = q4_decode_warps(kTiles);
+  // pages computed at once (several queries: one, for shorter code and no spilled
+  // registers, 70.5 us against 71.6 for 64 rows of 5 queries and 2300 tokens)
+  static constexpr int kU = kOne ? 2 : 1;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kPartBytes = kT * kVec * 32 * 16;
   static constexpr int kStages = 2;                // stages in flight per warp (a power of two)
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       __syncwarp();                  // and the others'
       // two pages at once where the pair lies in the row, else one: page 0 is
       // q, page 1 its neighbour in the stage, of which no token counts then
-      const int half = j & 1, n = (half == 0 && q + 1 < i1) ? 2 : 1;
+      const int half = j & 1, n = (S::kU == 2 && half == 0 && q + 1 < i1) ? 2 : 1;
       int pos[kPair];  // row position of each page's first token (L: the page does not count)
       pos[0] = (page0 + q) * kPage;
       pos[1] = n == 1 ? L : pos[0] + kPage;
@@ -446,16 +449,19 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         if (n == 2 && sm.ids[q + 1] < 0) pos[1] = L;
       }
       // every token of both pages counts for every column
-      const bool whole = max(pos[0], pos[1]) + kPage <= L - nq + 1;
+      const bool whole = (S::kU == 2 ? max(pos[0], pos[1]) : pos[0]) + kPage <= L - nq + 1;
       const uint32_t st = smem_addr(slab_at(s, half)), step = half ? 0u - 2 * kQ4Slab : 2u * kQ4Slab;
       // ---- scores: tokens r and r + 8 of the lane's columns, of both pages
-      float sc[kT][kCols][2 * kPair];
+      float sc[kT][kCols][2 * S::kU];
 #pragma unroll
-      for (int u = 0; u < kPair; ++u) {
+      for (int u = 0; u < S::kU; ++u) {
         const uint32_t ks = st + u * step;
         float c[kT][4];
 #pragma unroll
         for (int y = 0; y < kT; ++y) c[y][0] = c[y][1] = c[y][2] = c[y][3] = 0.f;
+        float c2[kT][4];  // a second accumulator: two shorter chains of products
+#pragma unroll
+        for (int y = 0; y < kT; ++y) c2[y][0] = c2[y][1] = c2[y][2] = c2[y][3] = 0.f;
         uint32_t ka[4], kb[4];
         ldmatrix4(ka, ks + ld_at);
         ldmatrix4(kb, ks + ld_at + 8 * kQ4Row);
@@ -471,15 +477,15 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < kT; ++y) {
             mma16816(c[y], a0, a1, a2, a3, qb[y][g].x, qb[y][g].y);
-            mma16816(c[y], a4, a5, a6, a7, qb[y][g].z, qb[y][g].w);
+            mma16816(c2[y], a4, a5, a6, a7, qb[y][g].z, qb[y][g].w);
           }
         }
 #pragma unroll
         for (int y = 0; y < kT; ++y)
 #pragma unroll
           for (int x = 0; x < kCols; ++x) {
-            sc[y][x][2 * u] = c[y][x] * p.scale_log2;
-            sc[y][x][2 * u + 1] = c[y][2 + x] * p.scale_log2;
+            sc[y][x][2 * u] = (c[y][x] + c2[y][x]) * p.scale_log2;
+            sc[y][x][2 * u + 1] = (c[y][2 + x] + c2[y][2 + x]) * p.scale_log2;
           }
       }
       if (!whole) {
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         for (int y = 0; y < kT; ++y) {
           const int vis = sees(y);
 #pragma unroll
-          for (int u = 0; u < kPair; ++u)
+          for (int u = 0; u < S::kU; ++u)
 #pragma unroll
             for (int x = 0; x < kCols; ++x) {
               if (pos[u] + r >= vis) sc[y][x][2 * u] = -INFINITY;
@@ -501,7 +507,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       for (int y = 0; y < kT; ++y)
 #pragma unroll
         for (int x = 0; x < kCols; ++x) {
-          mx[y][x] = fmaxf(fmaxf(sc[y][x][0], sc[y][x][1]), fmaxf(sc[y][x][2], sc[y][x][3]));
+          mx[y][x] = fmaxf(sc[y][x][0], sc[y][x][1]);
+          if constexpr (S::kU == 2) mx[y][x] = fmaxf(mx[y][x], fmaxf(sc[y][x][2], sc[y][x][3]));
           grow = grow || mx[y][x] + nm[y][x] > kRescaleSlack;
         }
       if (__any_sync(0xffffffffu, grow)) {  // rare after the first pages
@@ -527,11 +534,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
           }
       }
       // weights, transposed into the second product's B operand
-      uint32_t pb[kT][2 * kPair];
+      uint32_t pb[kT][2 * S::kU];
 #pragma unroll
       for (int y = 0; y < kT; ++y)
 #pragma unroll
-        for (int u = 0; u < 2 * kPair; ++u) {
+        for (int u = 0; u < 2 * S::kU; ++u) {
           const float w0 = fast_exp2(sc[y][0][u] + nm[y][0]);
           l[y][0] += w0;
           if constexpr (S::kOne) {  // leading bits, rest
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       // ---- output: dims of row r of each group's words, tokens 2 cq, 2 cq +
       // 1 and the same + 8
 #pragma unroll
-      for (int u = 0; u < kPair; ++u) {
+      for (int u = 0; u < S::kU; ++u) {
         const uint32_t vs = st + u * step + kQ4Slab;
         uint32_t va[4], vb[4];
         ldmatrix4_trans(va, vs + ld_at);
@@ -738,9 +745,9 @@ cudaError_t launch(const DecodeParams& p, const Plan& plan, int grid, bool overl
                           stream, p, plan);
 }
 
-// The plan in the parameter block of the size it needs: a launch with a small
-// one takes 1.3 us less (its parameters are copied to the device and fetched by
-// every SM), and most batches fit it.
+// The plan in a parameter block of the size it needs, 24 KiB or 3: four short
+// rows 7.1 us with the small one against 7.2 to 7.3, and up to 1.4 us less on the
+// host; most batches fit it.
 template <int kTiles>
 cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int grid, bool by_row,
                          bool overlap, std::atomic<bool>* done, cudaStream_t stream) {

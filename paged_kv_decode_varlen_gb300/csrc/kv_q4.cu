@@ -200,9 +200,12 @@ dim3 grid_for(int64_t rows) {
 
 }  // namespace
 
-// A thread takes several rows only when there are CTAs enough for every SM
-// several times over; before that more CTAs are worth more.
-constexpr int64_t kFewRows = 16384;
+// The read-back takes four rows per thread, for their loads in flight together,
+// only when there are CTAs enough for every SM several times over; before that
+// more CTAs are worth more (8 heads: 4096 tokens 4.3 us with one row per thread,
+// 5.9 with four; 8192 tokens 8.6 and 8.8; 16384 tokens 18.6 and 16.5; 131072
+// tokens 133 and 109).
+constexpr int64_t kFewRows = 65536;
 
 cudaError_t launch_kv_append_q4(const AppendParams& p, cudaStream_t stream) {
   const int64_t rows = p.n_tokens * p.num_kv_heads;

@@ -719,6 +719,7 @@ cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items,
   // and weigh 1 as before
   PrefillParams pp = p;
   if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
+  // (parameters of the size needed, as in the decode launch)
   if (items.count <= 96) return launch<96>(pp, items, rows, maps, ctas, g_attr_set[0], stream);
   return launch<kMaxPrefillItems>(pp, items, rows, maps, ctas, g_attr_set[1], stream);
 }
