@@ -201,14 +201,25 @@ struct PrefillItems {
   int32_t q_start[kMaxPrefillItems];
 };
 
-// The tile kernel's items over q4 pages: (request, first query token, its
-// position, queries), up to N of them.
+// Key ranges of the tile jobs over q4 pages, when few jobs would leave SMs idle:
+// each item is listed once per range of `tiles` key tiles (0: whole), and each
+// (listed item, kv head) leaves `rows` rows of partial outputs in piece_o (512
+// bytes each) and piece_lse.
+struct Q4Split {
+  int32_t tiles, rows;
+  float* piece_o;
+  float* piece_lse;
+};
+// The tile kernel's items over q4 pages, up to N of them: request, first query
+// token, its position, queries + 256 x key range.
 template <int N>
 struct Q4Items {
   int32_t count;
-  int32_t pad[3];
+  int32_t pad;
+  Q4Split split;
   int4 item[N];
 };
+constexpr int kQ4FewItems = 160;  // a batch of split items has no more
 
 struct PrefillParams {
   const uint16_t* q;
@@ -312,8 +323,11 @@ cudaError_t launch_decode_step(const DecodeParams& p, const StepPlan& plan, int 
 // q4 pages: (item of kQ4TileTokens queries, kv head) jobs on ctas CTAs; rows[i]
 // is item i's (request, first query token, its position, queries), maps.q and
 // maps.k the tensor maps of q (boxes of 32 tokens) and of out (of one)
-cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows, const TcMaps& maps,
-                              int ctas, cudaStream_t stream);
+cudaError_t launch_prefill_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
+                              const TcMaps& maps, int ctas, cudaStream_t stream);
+// ... and the outputs of split items from their ranges' parts
+cudaError_t launch_merge_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
+                            cudaStream_t stream);
 // ctas: CTAs of the launch (0: one per (item, kv head) job; fewer run
 // several jobs each)
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, const TcMaps& maps, int ctas,

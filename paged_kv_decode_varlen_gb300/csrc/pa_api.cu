@@ -343,18 +343,53 @@ bool q4_row_fits(int32_t L, int tiles, int num_kv_heads) {
   return pages_of(L) <= (int64_t)segs * pa::kQ4MaxPagesPerCta;
 }
 
-// Whether the tile jobs of a q4 batch (rows of many queries; `jobs` CTAs, one
-// per SM, the longest of key_tiles tiles) run beside the decode launch, which
-// then has the other SMs: where that ends sooner than the jobs first and the
-// decode launch on every SM after them.  Measured rates: a job ~5 us and 1.9 us
-// per key tile (1.2 with one query tile), the decode launch ~9 us and 37 GB/s
-// per SM.  (32 decode rows and a chunk of 512 tokens, 2048 to 4096 keys each: a
-// step of 54 us beside, 74 one after the other.)
-bool q4_tiles_beside(int64_t jobs, int64_t key_tiles, bool two_tiles, int64_t decode_slabs, int sms) {
-  if (jobs == 0 || decode_slabs == 0 || jobs > sms - 8) return false;
-  const double tiles_us = 5.0 + (two_tiles ? 1.9 : 1.2) * (double)key_tiles;
-  auto decode_us = [&](int64_t n) { return 9.0 + (double)decode_slabs * 2 * PA_Q4_SLAB_BYTES / ((double)n * 37e3); };
-  return std::max(tiles_us, decode_us(sms - jobs)) + 2.0 < tiles_us + decode_us(sms);
+// How the tile jobs of a q4 batch (rows of many queries) run: whole or in ranges
+// of `split` key tiles, and beside the decode launch or before it.
+struct Q4TilePlan {
+  int split = 0;  // key tiles of a range (0: whole items)
+  bool beside = false;
+  int64_t jobs = 0;  // (item or its range, kv head)
+};
+
+// job_tiles: key tiles of every item.  Ranges where few items would leave SMs
+// idle: their parts (part_cap of them fit the workspace) are merged by a kernel
+// of their own.  Beside the decode launch (may_beside), one CTA per job, which
+// then has the other SMs, where that ends sooner than one after the other.
+// Measured rates: a job ~5 us and 1.9 us per key tile (1.2 with one query tile),
+// a merge ~4 us, the decode launch ~9 us and 37 GB/s per SM.  (SPLITFIG;
+// 32 decode rows and a chunk of 512 tokens, 2048 to 4096 keys each: a step of 54
+// us beside, 74 one after the other.)
+Q4TilePlan plan_q4_tiles(const std::vector<int32_t>& job_tiles, bool two_tiles, int num_kv_heads, int64_t part_cap,
+                         bool may_beside, int64_t decode_slabs, int sms) {
+  Q4TilePlan best;
+  if (job_tiles.empty()) return best;
+  const int64_t longest = *std::max_element(job_tiles.begin(), job_tiles.end());
+  const double rate = two_tiles ? 1.9 : 1.2;
+  auto decode_us = [&](int64_t n) {
+    return decode_slabs == 0 ? 0.0 : 9.0 + (double)decode_slabs * 2 * PA_Q4_SLAB_BYTES / ((double)n * 37e3);
+  };
+  double best_us = 0;
+  int64_t last = 0;
+  for (int64_t parts = 1; parts <= longest; ++parts) {
+    const int64_t tiles = (longest + parts - 1) / parts;
+    if (tiles == last) continue;
+    last = tiles;
+    int64_t jobs = 0;
+    for (int32_t t : job_tiles) jobs += (t + tiles - 1) / tiles;
+    jobs *= num_kv_heads;
+    if (parts > 1 && jobs > std::min<int64_t>({part_cap, sms, pa::kQ4FewItems})) break;
+    const double us = 5.0 + rate * (double)tiles + (parts > 1 ? 4.0 : 0.0);
+    for (int beside = 0; beside < 2; ++beside) {
+      if (beside && !(may_beside && decode_slabs > 0 && jobs <= sms - 8)) continue;
+      const double all = beside ? std::max(us, decode_us(sms - jobs)) + 2.0 : us + decode_us(sms);
+      if (best.jobs > 0 && all >= best_us) continue;
+      best_us = all;
+      best.split = parts > 1 ? (int)tiles : 0;
+      best.beside = beside != 0;
+      best.jobs = jobs;
+    }
+  }
+  return best;
 }
 
 // Plan one persistent decode launch over decode rows rows[0..n): fills
@@ -756,28 +791,48 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     }
   }
 
-  // q4 pages: the tile jobs beside the (one) decode launch
-  const int q4_jobs = q4 ? (int)std::min<int64_t>((int64_t)tiles.size() * num_kv_heads, INT32_MAX) : 0;
-  bool q4_beside = false;
-  if (q4_jobs > 0 && g_prefill_ctas.load() >= 0 && g_forced_ctas.load() <= 0) {
+  // q4 pages: the tile jobs beside the (one) decode launch, and in key ranges
+  Q4TilePlan q4_plan;
+  pa::Q4Split q4_split{};
+  if (q4 && !tiles.empty()) {
     const std::vector<int32_t>* one = nullptr;
-    int classes = 0;
+    int classes = 0, cls = 0;
     for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows})
       if (!rows->empty()) {
         one = rows;
         ++classes;
+        cls = std::max(cls, pa::q4_decode_tiles(qo_indptr_host[(*rows)[0] + 1] - qo_indptr_host[(*rows)[0]]));
       }
-    if (classes == 1 && one->size() <= (size_t)pa::kPlanMaxRows) {
-      int64_t pages = 0;
-      int32_t extent = 0;
-      bool two_tiles = false;
-      for (int32_t r : *one) pages += pages_of(seq_lens_host[r]);
-      for (const auto& t : tiles) extent = std::max(extent, t.first);
-      for (int32_t r : item_req) two_tiles = two_tiles || qo_indptr_host[r + 1] - qo_indptr_host[r] > pa::kPrefillQTile;
-      q4_beside = q4_tiles_beside(q4_jobs, (extent + pa::kTcKeyTile - 1) / pa::kTcKeyTile, two_tiles,
-                                  pages * num_kv_heads, sm_count());
+    int64_t slabs = 0;
+    for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows})
+      for (int32_t r : *rows) slabs += (int64_t)pages_of(seq_lens_host[r]) * num_kv_heads;
+    bool two_tiles = false;
+    for (int32_t r : item_req) two_tiles = two_tiles || qo_indptr_host[r + 1] - qo_indptr_host[r] > pa::kPrefillQTile;
+    std::vector<int32_t> job_tiles;
+    for (const auto& t : tiles) job_tiles.push_back((t.first + pa::kTcKeyTile - 1) / pa::kTcKeyTile);
+    // the parts lie behind what a decode launch beside the jobs writes
+    const int part_rows = (two_tiles ? 2 : 1) * pa::kPrefillQTile * pa::kGroup;
+    const int64_t low = classes > 0 ? (int64_t)2 * sm_count() * pa::q4_piece_slots(cls) : 0;
+    const bool fits = slabs <= (int64_t)sm_count() / 2 * pa::kQ4MaxPagesPerCta;  // (a longer stream takes more pieces)
+    const int64_t part_cap = fits ? std::max<int64_t>(0, (wl.slots - low) / part_rows) : 0;
+    q4_plan = plan_q4_tiles(job_tiles, two_tiles, num_kv_heads, part_cap,
+                            classes == 1 && one->size() <= (size_t)pa::kPlanMaxRows && g_prefill_ctas.load() >= 0 &&
+                                g_forced_ctas.load() <= 0,
+                            slabs, sm_count());
+    if (q4_plan.split > 0) {
+      q4_split.tiles = q4_plan.split;
+      q4_split.rows = part_rows;
+      const int64_t first = wl.slots - q4_plan.jobs * part_rows;
+      q4_split.piece_o = reinterpret_cast<float*>(ws + wl.piece_o) + first * pa::kHeadDim;
+      q4_split.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse) + first;
     }
   }
+  pa::PrefillParams pp{};
+  int q4_count = 0;
+  auto merge_q4 = [&] {
+    return run_launch(PA_KERNEL_MERGE, "merge_q4", stream,
+                      [&] { return pa::launch_merge_q4(pp, q4_count, q4_items, q4_split, stream); });
+  };
 
   int prefill_ctas = 0;  // CTAs of the prefill launch (0: one per job)
   if (!tiles.empty()) {
@@ -831,7 +886,6 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         prefill_ctas = std::min(prefill_alone_ctas(job_tiles, sm_count()), jobs - 1);
       }
     }
-    pa::PrefillParams pp;
     pp.q = static_cast<const uint16_t*>(q);
     pp.k_cache = static_cast<const uint16_t*>(k_cache);
     pp.v_cache = static_cast<const uint16_t*>(v_cache);
@@ -856,16 +910,25 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         const int32_t idx = tiles[base + i].second;
         items.req[i] = item_req[idx];
         items.q_start[i] = item_q0[idx];
-        const int32_t r = item_req[idx], qo0 = qo_indptr_host[r], c = qo_indptr_host[r + 1] - qo0;
-        q4_items[i] = make_int4(r, qo0 + item_q0[idx], seq_lens_host[r] - c + item_q0[idx],
-                                std::min(pa::kQ4TileTokens, c - item_q0[idx]));
+      }
+      if (q4) {
+        q4_count = 0;
+        for (size_t i = 0; i < n; ++i) {
+          const int32_t r = items.req[i], j0 = items.q_start[i], qo0 = qo_indptr_host[r], c = qo_indptr_host[r + 1] - qo0;
+          const int32_t nq = std::min(pa::kQ4TileTokens, c - j0), pos = seq_lens_host[r] - c + j0;
+          const int32_t key_tiles = (pos + nq + pa::kTcKeyTile - 1) / pa::kTcKeyTile;
+          const int ranges = q4_split.tiles > 0 ? (key_tiles + q4_split.tiles - 1) / q4_split.tiles : 1;
+          for (int k = 0; k < ranges; ++k) q4_items[q4_count++] = make_int4(r, qo0 + j0, pos, nq | k << 8);
+        }
       }
       s = run_launch(PA_KERNEL_PREFILL, "prefill", stream,
                      [&] {
-                       return q4 ? pa::launch_prefill_q4(pp, items, q4_items, maps,
-                                                         std::min(items.count * num_kv_heads, sm_count()), stream)
+                       return q4 ? pa::launch_prefill_q4(pp, q4_count, q4_items, q4_split, maps,
+                                                         (int)std::min<int64_t>((int64_t)q4_count * num_kv_heads,
+                                                                                sm_count()), stream)
                                  : pa::launch_prefill(pp, items, maps, prefill_ctas, stream);
                      });
+      if (s == PA_OK && q4_split.tiles > 0 && !q4_plan.beside) s = merge_q4();
       if (s != PA_OK) return s;
     }
   }
@@ -907,15 +970,17 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       // one launch per class of rows (and per kPlanMaxRows rows; fewer where a
       // segment would hold too many)
       static thread_local int32_t n_q[pa::kPlanMaxRows];
-      bool overlap = tiles.empty() || q4_beside;  // as below
-      dp.beside = q4_beside ? 1 : 0;
-      const int slots = q4_beside ? sm_count() - q4_jobs : sm_count();
+      bool overlap = tiles.empty() || q4_plan.beside;  // as below
+      dp.beside = q4_plan.beside ? 1 : 0;
+      const int slots = q4_plan.beside ? sm_count() - (int)q4_plan.jobs : sm_count();
+      // beside jobs in key ranges, whose parts take the workspace's end
+      if (q4_plan.beside && q4_split.tiles > 0) dp.piece_slots -= q4_plan.jobs * q4_split.rows;
       for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows}) {
         for (size_t d0 = 0; d0 < rows->size();) {
           int n = (int)std::min(rows->size() - d0, (size_t)pa::kPlanMaxRows);
           const int32_t* r0 = rows->data() + d0;
           const int cls = pa::q4_decode_tiles(qo_indptr_host[r0[0] + 1] - qo_indptr_host[r0[0]]);
-          const int cap = q4_grid_cap(gcap, wl.slots, cls);
+          const int cap = q4_grid_cap(gcap, dp.piece_slots, cls);
           int grid;
           for (;; n = (n + 1) / 2) {
             grid = plan_decode(r0, n, seq_lens_host, qo_indptr_host, 0, num_kv_heads, cap, slots,
@@ -940,7 +1005,8 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
           dp.beside = 0;  // (a further launch waits for this one)
         }
       }
-      return ok();
+      if (q4_plan.beside && q4_split.tiles > 0) s = merge_q4();
+      return s == PA_OK ? ok() : s;
     }
     // one launch per kPlanMaxRows decode rows (the plan travels as kernel
     // parameters); launches on one stream run in order and reuse the slots

@@ -226,7 +226,8 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-struct Job {
+struct Job {  // (split: positions and keys from the range's first key on)
+  int32_t slot;  // (listed item, kv head)
   int32_t tok0;  // first query token of the job
   int32_t nq;    // its query tokens (1 .. 64)
   int32_t kvh;
@@ -239,7 +240,7 @@ struct Job {
 
 // The CTA's jobs: job b of every round of gridDim.x jobs, in reverse order on
 // odd rounds (the items come longest first).
-template <class Items>
+template <class Items, bool kSplit>
 struct Jobs {
   const PrefillParams& p;
   const Items& items;
@@ -256,12 +257,19 @@ struct Jobs {
     odd ^= 1;
     const int it = u / p.num_kv_heads;
     const int4 item = items.item[it];  // request, first query token, its position, queries
+    job.slot = u;
     job.tok0 = item.y;
-    job.nq = item.w;
+    job.nq = kSplit ? item.w & 0xff : item.w;
     job.kvh = u - it * p.num_kv_heads;
     job.pos0 = item.z;
-    job.keys = item.z + item.w;
+    job.keys = item.z + job.nq;
     job.table = p.block_tables + (size_t)item.x * p.max_blocks_per_req;
+    if constexpr (kSplit) {
+      const int key0 = (item.w >> 8) * items.split.tiles * kKeys;
+      job.pos0 -= key0;
+      job.keys = min(job.keys - key0, items.split.tiles * kKeys);
+      job.table += key0 / kPage;
+    }
     job.n_tiles = (job.keys + kKeys - 1) / kKeys;
     job.n_sub = (job.keys + kSub - 1) / kSub;
     job.n_x = job.nq > kTok ? 2 : 1;
@@ -368,7 +376,7 @@ __device__ __forceinline__ bool produce(Smem& sm, const Job& job, int w, int J0,
   return true;
 }
 
-template <class Items>
+template <class Items, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const PrefillParams p, const __grid_constant__ Items items,
                       const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap out_map) {
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp >= kProducer0) {
-    Jobs<Items> jobs(p, items);
+    Jobs<Items, kSplit> jobs(p, items);
     Job job;
     int J0 = 0;
     while (jobs.next(job) &&
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    Jobs<Items> jobs(p, items);
+    Jobs<Items, kSplit> jobs(p, items);
     Job job, next;
     bool more = jobs.next(job), ok = true;
     if (x == 0 && more) load_q(job);
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
     int J0 = 0, I0 = 0;  // running counts: key tiles, this query tile's sub-tiles
-    Jobs<Items> jobs(p, items);
+    Jobs<Items, kSplit> jobs(p, items);
     Job job;
     bool more = jobs.next(job), ok = true;
     while (more) {
@@ -633,56 +641,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int I1 = I0 + job.n_sub - 1;
     if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
     fence_after_sync();
-    // The output, 64 dims at a time, through shared memory (128-byte swizzle)
-    // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
-    // threads, 16 bytes of a row each, an instruction touches 32 lines: a job's
-    // end took 6000 cycles against 2600, the prompts above 52 us against 47.)
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-    const int tok = x * kTok + (row >> 2);
-    const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
-    uint8_t* stg = sm.out[warp];
-    uint32_t o[2][32];
-    tmem_ld32_async(t_o, o[0]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (lane == 0) bulk_wait_read();  // what was staged before has been read
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        wait_ld(o[c]);
-        if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
-        uint32_t w[16];
-#pragma unroll
-        for (int y = 0; y < 16; ++y)
-          w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+    if constexpr (kSplit) {
+      // the row's part of this key range, 4 dims of 32 rows at a time
+      const size_t at = (size_t)job.slot * items.split.rows + x * kRows;
+      float4* dst = reinterpret_cast<float4*>(items.split.piece_o + at * kHeadDim) + row;
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim / 16; ++c) {
+        uint32_t o[16];
+        load16(t_o + 16 * c, o);
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
-              make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+          dst[(4 * c + y) * kRows] =
+              make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
+                          __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
       }
-      if (h == 1) {
-        fence_before_sync();  // the tensor-memory reads above precede the arrive
-        mbar_arrive(&sm.o_free[x]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (tok_w + kOutTok <= job.nq) {
-        if (lane == 0) {
-          tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
-          bulk_commit();
+      fence_before_sync();  // the tensor-memory reads above precede the arrive
+      mbar_arrive(&sm.o_free[x]);
+      items.split.piece_lse[at + row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+    } else {
+      // The output, 64 dims at a time, through shared memory (128-byte swizzle)
+      // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
+      // threads, 16 bytes of a row each, an instruction touches 32 lines: a job's
+      // end took 6000 cycles against 2600, the prompts above 52 us against 47.)
+      const int tok = x * kTok + (row >> 2);
+      const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
+      uint8_t* stg = sm.out[warp];
+      uint32_t o[2][32];
+      tmem_ld32_async(t_o, o[0]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (lane == 0) bulk_wait_read();  // what was staged before has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          wait_ld(o[c]);
+          if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+          uint32_t w[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y)
+            w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
         }
-      } else {  // the row's last tokens
+        if (h == 1) {
+          fence_before_sync();  // the tensor-memory reads above precede the arrive
+          mbar_arrive(&sm.o_free[x]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (tok_w + kOutTok <= job.nq) {
+          if (lane == 0) {
+            tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
+            bulk_commit();
+          }
+        } else {  // the row's last tokens
 #pragma unroll 1
-        for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
-          const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
-          *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
-              *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+          for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
+            const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
+            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
+                *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+          }
         }
       }
+      if (p.lse && tok < job.nq)
+        p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
+            l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     }
-    if (p.lse && tok < job.nq)
-      p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
-          l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
     J0 += job.n_tiles;
     I0 += job.n_sub;
     more = jobs.next(job);
@@ -696,32 +723,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-std::atomic<bool> g_attr_set[2][kMaxDevices];
+// The outputs of split items: the log-sum-exp merge of their key ranges' parts,
+// in order.  A CTA takes 32 dims of a query tile's 128 rows (a thread 8 dims of a
+// row at a time, 16 dims in all): the parts lie as 4 dims of neighbouring rows,
+// so a warp reads 512 bytes at once.
+template <class Items>
+__global__ void __launch_bounds__(256) merge_q4_kernel(const PrefillParams p, const __grid_constant__ Items items) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int u = blockIdx.x, x = blockIdx.y, row = threadIdx.x & 127;
+  const int it = u / p.num_kv_heads, kvh = u - it * p.num_kv_heads;
+  const int4 item = items.item[it];
+  const int nq = item.w & 0xff, tok = x * kTok + (row >> 2);
+  if (item.w >> 8 || tok >= nq) return;  // not the item's first range, not a query
+  const int n_tiles = (item.z + nq + kKeys - 1) / kKeys;
+  const int n = (n_tiles + items.split.tiles - 1) / items.split.tiles;
+  const size_t stride = (size_t)p.num_kv_heads * items.split.rows;  // rows from a range to the next
+  const size_t at = (size_t)u * items.split.rows + x * kRows;
+  const float* lse = items.split.piece_lse + at + row;
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(lse + i * stride));
+  float l = 0.f;
+  if (m > -INFINITY) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) l += fast_exp2(__ldcg(lse + i * stride) - m);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t orow = (size_t)(item.y + tok) * p.num_q_heads + kvh * kGroup + (row & 3);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = blockIdx.z * 4 + 2 * (threadIdx.x >> 7) + h;  // dims 8 c .. 8 c + 7
+    const float4* src = reinterpret_cast<const float4*>(items.split.piece_o + at * kHeadDim) + 2 * c * kRows + row;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = l > 0.f ? fast_exp2(__ldcg(lse + i * stride) - m) * inv : 0.f;
+      const float4 a = __ldcg(src + i * stride * (kHeadDim / 4)), b = __ldcg(src + i * stride * (kHeadDim / 4) + kRows);
+      o[0] = fmaf(w, a.x, o[0]);
+      o[1] = fmaf(w, a.y, o[1]);
+      o[2] = fmaf(w, a.z, o[2]);
+      o[3] = fmaf(w, a.w, o[3]);
+      o[4] = fmaf(w, b.x, o[4]);
+      o[5] = fmaf(w, b.y, o[5]);
+      o[6] = fmaf(w, b.z, o[6]);
+      o[7] = fmaf(w, b.w, o[7]);
+    }
+    *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 8 * c) = make_uint4(
+        pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+  }
+  if (p.lse && blockIdx.z == 0 && threadIdx.x < 128) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+std::atomic<bool> g_attr_set[3][kMaxDevices];
 
 template <int N>
-cudaError_t launch(const PrefillParams& p, const PrefillItems& items, const int4* rows, const TcMaps& maps, int ctas,
-                   std::atomic<bool>* done, cudaStream_t stream) {
+const Q4Items<N>& fill(int count, const int4* rows, const Q4Split& split) {
   static thread_local Q4Items<N> d;
-  d.count = items.count;
-  for (int i = 0; i < items.count; ++i) d.item[i] = rows[i];
-  const cudaError_t e = set_smem_limit_once((const void*)prefill_q4_kernel<Q4Items<N>>, (int)kSmemBytes, done);
+  d.count = count;
+  d.split = split;
+  for (int i = 0; i < count; ++i) d.item[i] = rows[i];
+  return d;
+}
+
+template <int N, bool kSplit>
+cudaError_t launch(const PrefillParams& p, int count, const int4* rows, const Q4Split& split, const TcMaps& maps, int ctas,
+                   std::atomic<bool>* done, cudaStream_t stream) {
+  auto kernel = prefill_q4_kernel<Q4Items<N>, kSplit>;
+  const cudaError_t e = set_smem_limit_once((const void*)kernel, (int)kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_q4_kernel<Q4Items<N>>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, d, maps.q, maps.k);
+  return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, fill<N>(count, rows, split),
+                    maps.q, maps.k);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_q4(const PrefillParams& p, const PrefillItems& items, const int4* rows,
+cudaError_t launch_prefill_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
                               const TcMaps& maps, int ctas, cudaStream_t stream) {
-  if (items.count <= 0) return cudaSuccess;
+  if (count <= 0) return cudaSuccess;
   // a zero scale (every score 0) as 2^-100, so that a hidden score scales to
   // -inf: scores of q and k whose products stay below 2^40 are below 2^-60 then
   // and weigh 1 as before
   PrefillParams pp = p;
   if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
+  if (split.tiles > 0) {
+    if (count > kQ4FewItems) return cudaErrorInvalidValue;
+    return launch<kQ4FewItems, true>(pp, count, rows, split, maps, ctas, g_attr_set[2], stream);
+  }
   // (parameters of the size needed, as in the decode launch)
-  if (items.count <= 96) return launch<96>(pp, items, rows, maps, ctas, g_attr_set[0], stream);
-  return launch<kMaxPrefillItems>(pp, items, rows, maps, ctas, g_attr_set[1], stream);
+  if (count <= kQ4FewItems) return launch<kQ4FewItems, false>(pp, count, rows, split, maps, ctas, g_attr_set[0], stream);
+  return launch<kMaxPrefillItems, false>(pp, count, rows, split, maps, ctas, g_attr_set[1], stream);
+}
+
+cudaError_t launch_merge_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
+                            cudaStream_t stream) {
+  if (count <= 0) return cudaSuccess;
+  if (count > kQ4FewItems) return cudaErrorInvalidValue;
+  return launch_pdl(merge_q4_kernel<Q4Items<kQ4FewItems>>,
+                    dim3((unsigned)(count * p.num_kv_heads), (unsigned)(split.rows / kRows), 4), dim3(256), 0, stream, p,
+                    fill<kQ4FewItems>(count, rows, split));
 }
 
 }  // namespace pa

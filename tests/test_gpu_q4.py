@@ -525,3 +525,51 @@ def test_rows_of_a_million_pages(qo):
     big = float(np.abs(v).max())
     assert float((a - b).abs().max()) <= (4 * 2.0 ** -8 + 2.0 ** -12) * big
     assert float((got_lse[-1] - lse[-1] - np.log(times)).abs().max()) <= 2.0 ** -12
+
+
+# few tile jobs and many keys: the keys are cut into ranges
+RANGES = {
+    "one_chunk": ([3000], [20], 2),
+    "two_tiles": ([5000, 700], [64, 9], 1),
+    "many_ranges": ([20000], [7], 8),
+    "ends_inside_a_page": ([4097, 2049], [33, 10], 3),
+    "a_whole_prompt": ([600], [600], 1),
+    "ranges_that_early_queries_do_not_see": ([260, 1030], [200, 130], 1),
+    "beside_decode_rows": ([9000, 900, 30, 2000], [40, 1, 1, 1], 2),
+    "beside_verify_rows": ([6000, 900, 30, 0, 2000], [12, 5, 5, 0, 5], 4),
+    "before_two_kinds_of_rows": ([7000, 900, 30], [70, 5, 1], 2),
+}
+
+
+@pytest.mark.parametrize("name", sorted(RANGES))
+def test_few_jobs_over_many_keys(name):
+    seq, qo, Hkv = RANGES[name]
+    c = Case(seq, qo, Hkv, seed=70 + len(name))
+    need = B.pa_attention_workspace_size(len(seq), sum(qo), 4 * Hkv, 128, max(seq))
+    ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device=DEV)  # and nothing behind what was asked for
+    ws[:B.PA_ERROR_WORD_BYTES] = 0
+    B.pa_trace_enable(True)
+    try:
+        out, lse = c.run(workspace=ws)
+        kinds = [k for k, _ in B.pa_trace_read()]
+    finally:
+        B.pa_trace_enable(False)
+    c.check(out, lse, what=name)
+    assert kinds.count("prefill") == 1 and kinds.count("merge") == 1, kinds
+    again, again_lse = c.run(workspace=ws)
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0 and bool((ws[need:] == 0xff).all())
+
+
+def test_ranges_with_a_page_outside_the_pool_and_hidden_ones():
+    c = Case([3000], [20], 2, seed=90)
+    c.dev["tables"][0, 5] = -7
+    ws = B.new_workspace(B.pa_attention_workspace_size(1, 20, 8, 128, 3000), DEV)
+    out, lse = c.run(workspace=ws)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == B.PA_ERR_DEVICE_INDEX
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+    c.dev["tables"].fill_(10 ** 8)
+    out, lse = c.run()
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all())
