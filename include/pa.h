@@ -549,7 +549,7 @@ typedef enum {
   PA_KERNEL_DECODE = 2,
   PA_KERNEL_COMBINE = 3, /* reserved: the split merge is fused into PA_KERNEL_DECODE */
   PA_KERNEL_PREFILL = 4,
-  PA_KERNEL_MERGE = 5,
+  PA_KERNEL_MERGE = 5,       /* pa_merge_lse; key ranges of pa_attention_varlen_q4 */
   PA_KERNEL_PREFIX = 6,      /* shared-prefix pass of pa_attention_varlen_shared_prefix */
   PA_KERNEL_PREFIX_MERGE = 7, /* merge of that pass's key-chunk partials */
   PA_KERNEL_COPY_BLOCKS = 8,  /* pa_copy_blocks */

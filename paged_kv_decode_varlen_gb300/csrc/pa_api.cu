@@ -346,48 +346,66 @@ bool q4_row_fits(int32_t L, int tiles, int num_kv_heads) {
 // How the tile jobs of a q4 batch (rows of many queries) run: whole or in ranges
 // of `split` key tiles, and beside the decode launch or before it.
 struct Q4TilePlan {
-  int split = 0;  // key tiles of a range (0: whole items)
+  int32_t queries = 0;  // of an item
+  int split = 0;        // key tiles of a range (0: whole items)
   bool beside = false;
-  int64_t jobs = 0;  // (item or its range, kv head)
+  int64_t jobs = 0;     // (item or its range, kv head)
+  double us = 0;        // estimate
 };
 
-// job_tiles: key tiles of every item.  Ranges where few items would leave SMs
-// idle: their parts (part_cap of them fit the workspace) are merged by a kernel
-// of their own.  Beside the decode launch (may_beside), one CTA per job, which
-// then has the other SMs, where that ends sooner than one after the other.
-// Measured rates: a job ~5 us and 1.9 us per key tile (1.2 with one query tile),
-// a merge ~4 us, the decode launch ~9 us and 37 GB/s per SM.  (SPLITFIG;
-// 32 decode rows and a chunk of 512 tokens, 2048 to 4096 keys each: a step of 54
-// us beside, 74 one after the other.)
-Q4TilePlan plan_q4_tiles(const std::vector<int32_t>& job_tiles, bool two_tiles, int num_kv_heads, int64_t part_cap,
-                         bool may_beside, int64_t decode_slabs, int sms) {
+// rows: the batch's rows for the tile kernel.  Items of 64 queries, two query
+// tiles that share every key tile, or of 32 where these would leave SMs idle; then
+// key ranges, whose parts (as many as part_slots rows of the workspace hold) a
+// kernel of their own merges.  Beside the decode launch (may_beside), one CTA per
+// job, which then has the other SMs, where that ends sooner than one after the
+// other.  Measured rates: a CTA's first job ~5 us, each further one ~3.5, and 1.8 us
+// per key tile (1.55 with one query tile), a merge ~4 us, the decode launch ~9 us
+// and 37 GB/s per SM.  (One chunk of 20 tokens behind 6000, 8 kv heads: 22 us in
+// ranges, 78 in whole items; of 200 behind 1800: 26 us in items of 32 and ranges,
+// 35 in items of 64; of 512 behind 3500: 55 and 62; 32 decode rows and a chunk of
+// 512 tokens, 2048 to 4096 keys each: a step of 54 us beside, 74 one after the
+// other.)
+Q4TilePlan plan_q4_tiles(const std::vector<int32_t>& rows, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
+                         int num_kv_heads, int64_t part_slots, bool may_beside, int64_t decode_slabs, int sms) {
   Q4TilePlan best;
-  if (job_tiles.empty()) return best;
-  const int64_t longest = *std::max_element(job_tiles.begin(), job_tiles.end());
-  const double rate = two_tiles ? 1.9 : 1.2;
   auto decode_us = [&](int64_t n) {
     return decode_slabs == 0 ? 0.0 : 9.0 + (double)decode_slabs * 2 * PA_Q4_SLAB_BYTES / ((double)n * 37e3);
   };
-  double best_us = 0;
-  int64_t last = 0;
-  for (int64_t parts = 1; parts <= longest; ++parts) {
-    const int64_t tiles = (longest + parts - 1) / parts;
-    if (tiles == last) continue;
-    last = tiles;
-    int64_t jobs = 0;
-    for (int32_t t : job_tiles) jobs += (t + tiles - 1) / tiles;
-    jobs *= num_kv_heads;
-    if (parts > 1 && jobs > std::min<int64_t>({part_cap, sms, pa::kQ4FewItems})) break;
-    const double us = 5.0 + rate * (double)tiles + (parts > 1 ? 4.0 : 0.0);
-    for (int beside = 0; beside < 2; ++beside) {
-      if (beside && !(may_beside && decode_slabs > 0 && jobs <= sms - 8)) continue;
-      const double all = beside ? std::max(us, decode_us(sms - jobs)) + 2.0 : us + decode_us(sms);
-      if (best.jobs > 0 && all >= best_us) continue;
-      best_us = all;
-      best.split = parts > 1 ? (int)tiles : 0;
-      best.beside = beside != 0;
-      best.jobs = jobs;
+  for (int32_t queries = pa::kQ4TileTokens; queries >= pa::kPrefillQTile; queries -= pa::kPrefillQTile) {
+    std::vector<int32_t> item_tiles;
+    bool two_tiles = false;
+    int64_t longest = 0, total = 0;
+    for (int32_t r : rows) {
+      const int32_t c = qo_indptr_host[r + 1] - qo_indptr_host[r];
+      two_tiles = two_tiles || std::min(c, queries) > pa::kPrefillQTile;
+      for (int32_t j0 = 0; j0 < c; j0 += queries) {
+        const int32_t t = (seq_lens_host[r] - c + std::min(c, j0 + queries) + pa::kTcKeyTile - 1) / pa::kTcKeyTile;
+        item_tiles.push_back(t);
+        longest = std::max<int64_t>(longest, t);
+        total += t;
+      }
     }
+    const double rate = two_tiles ? 1.8 : 1.55;
+    const int64_t part_cap = part_slots / ((two_tiles ? 2 : 1) * pa::kPrefillQTile * pa::kGroup);
+    int64_t last = 0;
+    for (int64_t parts = 1; parts <= longest; ++parts) {
+      const int64_t tiles = (longest + parts - 1) / parts;
+      if (tiles == last) continue;
+      last = tiles;
+      int64_t jobs = 0;
+      for (int32_t t : item_tiles) jobs += (t + tiles - 1) / tiles;
+      jobs *= num_kv_heads;
+      if (parts > 1 && jobs > std::min<int64_t>({part_cap, sms, pa::kQ4FewItems})) break;
+      const double us = 5.0 + 3.5 * (double)((jobs - 1) / sms) + (parts > 1 ? 4.0 : 0.0) +
+                        rate * std::max((double)tiles, jobs > sms ? (double)total * num_kv_heads / sms : 0.0);
+      for (int beside = 0; beside < 2; ++beside) {
+        if (beside && !(may_beside && decode_slabs > 0 && jobs <= sms - 8)) continue;
+        const double all = beside ? std::max(us, decode_us(sms - jobs)) + 2.0 : us + decode_us(sms);
+        if (best.jobs > 0 && all >= best.us) continue;
+        best = Q4TilePlan{queries, parts > 1 ? (int)tiles : 0, beside != 0, jobs, all};
+      }
+    }
+    if (!two_tiles) break;  // items of 32 would be the same
   }
   return best;
 }
@@ -666,6 +684,15 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   static thread_local pa::PrefillItems items;
   static thread_local int4 q4_items[pa::kMaxPrefillItems];
   std::vector<int32_t> item_req, item_q0;
+  std::vector<int32_t> q4_tile_rows;  // q4 pages: rows of the tile kernel
+  auto add_items = [&](int32_t r, int32_t q_tile) {  // a row's query tiles
+    const int32_t qo_len = qo_indptr_host[r + 1] - qo_indptr_host[r];
+    for (int32_t j0 = 0; j0 < qo_len; j0 += q_tile) {
+      tiles.push_back({seq_lens_host[r] - qo_len + std::min(qo_len, j0 + q_tile), (int32_t)item_req.size()});
+      item_req.push_back(r);
+      item_q0.push_back(j0);
+    }
+  };
   for (int r = 0; r < num_reqs; ++r) {
     const int32_t qo_len = qo_indptr_host[r + 1] - qo_indptr_host[r];
     const int32_t L = seq_lens_host[r];
@@ -693,13 +720,10 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       decode_rows.push_back(r);
     } else if (q4 && qo_len > 1 && decodes) {
       q4_rows[pa::q4_decode_tiles(qo_len) == 2 ? 0 : 1].push_back(r);
-    } else if (qo_len >= 1) {
-      const int32_t q_tile = q4 ? pa::kQ4TileTokens : pa::kPrefillQTile;
-      for (int32_t j0 = 0; j0 < qo_len; j0 += q_tile) {
-        tiles.push_back({L - qo_len + std::min(qo_len, j0 + q_tile), (int32_t)item_req.size()});
-        item_req.push_back(r);
-        item_q0.push_back(j0);
-      }
+    } else if (q4 && qo_len >= 1) {
+      q4_tile_rows.push_back(r);
+    } else if (qo_len > 1) {
+      add_items(r, pa::kPrefillQTile);
     }
   }
   const WorkspaceLayout wl = layout(num_reqs, num_q_heads, head_dim, max_len);
@@ -719,7 +743,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   float* prefix_o = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_o) : nullptr;
   float* prefix_lse = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_lse) : nullptr;
   static thread_local pa::TcMaps maps;
-  if (P > 0 || !tiles.empty()) {
+  if (P > 0 || !tiles.empty() || !q4_tile_rows.empty()) {
     s = q4 ? make_q_map(q, total_q, num_q_heads, pa::kPrefillQTile, maps.q)
            : make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
     if (s == PA_OK && q4) s = make_q_map(out, total_q, num_q_heads, 32 / pa::kGroup, maps.k);
@@ -791,34 +815,35 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
     }
   }
 
-  // q4 pages: the tile jobs beside the (one) decode launch, and in key ranges
+  // q4 pages: the tile kernel's items
   Q4TilePlan q4_plan;
   pa::Q4Split q4_split{};
-  if (q4 && !tiles.empty()) {
+  if (!q4_tile_rows.empty()) {
     const std::vector<int32_t>* one = nullptr;
     int classes = 0, cls = 0;
-    for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows})
-      if (!rows->empty()) {
-        one = rows;
-        ++classes;
-        cls = std::max(cls, pa::q4_decode_tiles(qo_indptr_host[(*rows)[0] + 1] - qo_indptr_host[(*rows)[0]]));
-      }
     int64_t slabs = 0;
-    for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows})
+    for (const std::vector<int32_t>* rows : {&q4_rows[1], &q4_rows[0], &decode_rows}) {
+      if (rows->empty()) continue;
+      one = rows;
+      ++classes;
+      cls = std::max(cls, pa::q4_decode_tiles(qo_indptr_host[(*rows)[0] + 1] - qo_indptr_host[(*rows)[0]]));
       for (int32_t r : *rows) slabs += (int64_t)pages_of(seq_lens_host[r]) * num_kv_heads;
-    bool two_tiles = false;
-    for (int32_t r : item_req) two_tiles = two_tiles || qo_indptr_host[r + 1] - qo_indptr_host[r] > pa::kPrefillQTile;
-    std::vector<int32_t> job_tiles;
-    for (const auto& t : tiles) job_tiles.push_back((t.first + pa::kTcKeyTile - 1) / pa::kTcKeyTile);
-    // the parts lie behind what a decode launch beside the jobs writes
-    const int part_rows = (two_tiles ? 2 : 1) * pa::kPrefillQTile * pa::kGroup;
+    }
+    // parts lie behind what a decode launch beside the jobs writes, one wave of
+    // CTAs (a longer stream takes more)
     const int64_t low = classes > 0 ? (int64_t)2 * sm_count() * pa::q4_piece_slots(cls) : 0;
-    const bool fits = slabs <= (int64_t)sm_count() / 2 * pa::kQ4MaxPagesPerCta;  // (a longer stream takes more pieces)
-    const int64_t part_cap = fits ? std::max<int64_t>(0, (wl.slots - low) / part_rows) : 0;
-    q4_plan = plan_q4_tiles(job_tiles, two_tiles, num_kv_heads, part_cap,
+    const bool fits = slabs <= (int64_t)sm_count() / 2 * pa::kQ4MaxPagesPerCta;
+    q4_plan = plan_q4_tiles(q4_tile_rows, seq_lens_host, qo_indptr_host, num_kv_heads,
+                            fits ? std::max<int64_t>(0, wl.slots - low) : 0,
                             classes == 1 && one->size() <= (size_t)pa::kPlanMaxRows && g_prefill_ctas.load() >= 0 &&
                                 g_forced_ctas.load() <= 0,
                             slabs, sm_count());
+    bool two_tiles = false;
+    for (int32_t r : q4_tile_rows) {
+      add_items(r, q4_plan.queries);
+      two_tiles = two_tiles || std::min(qo_indptr_host[r + 1] - qo_indptr_host[r], q4_plan.queries) > pa::kPrefillQTile;
+    }
+    const int part_rows = (two_tiles ? 2 : 1) * pa::kPrefillQTile * pa::kGroup;
     if (q4_plan.split > 0) {
       q4_split.tiles = q4_plan.split;
       q4_split.rows = part_rows;
@@ -915,7 +940,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
         q4_count = 0;
         for (size_t i = 0; i < n; ++i) {
           const int32_t r = items.req[i], j0 = items.q_start[i], qo0 = qo_indptr_host[r], c = qo_indptr_host[r + 1] - qo0;
-          const int32_t nq = std::min(pa::kQ4TileTokens, c - j0), pos = seq_lens_host[r] - c + j0;
+          const int32_t nq = std::min(q4_plan.queries, c - j0), pos = seq_lens_host[r] - c + j0;
           const int32_t key_tiles = (pos + nq + pa::kTcKeyTile - 1) / pa::kTcKeyTile;
           const int ranges = q4_split.tiles > 0 ? (key_tiles + q4_split.tiles - 1) / q4_split.tiles : 1;
           for (int k = 0; k < ranges; ++k) q4_items[q4_count++] = make_int4(r, qo0 + j0, pos, nq | k << 8);
