@@ -220,6 +220,7 @@ struct Q4Items {
   int4 item[N];
 };
 constexpr int kQ4FewItems = 160;  // a batch of split items has no more
+constexpr int kQ4MaxRanges = 32;
 
 struct PrefillParams {
   const uint16_t* q;

@@ -388,7 +388,7 @@ Q4TilePlan plan_q4_tiles(const std::vector<int32_t>& rows, const int32_t* seq_le
     const double rate = two_tiles ? 1.8 : 1.55;
     const int64_t part_cap = part_slots / ((two_tiles ? 2 : 1) * pa::kPrefillQTile * pa::kGroup);
     int64_t last = 0;
-    for (int64_t parts = 1; parts <= longest; ++parts) {
+    for (int64_t parts = 1; parts <= std::min<int64_t>(longest, pa::kQ4MaxRanges); ++parts) {
       const int64_t tiles = (longest + parts - 1) / parts;
       if (tiles == last) continue;
       last = tiles;

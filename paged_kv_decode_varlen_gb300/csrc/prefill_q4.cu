@@ -227,7 +227,6 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 struct Job {  // (split: positions and keys from the range's first key on)
-  int32_t slot;  // (listed item, kv head)
   int32_t tok0;  // first query token of the job
   int32_t nq;    // its query tokens (1 .. 64)
   int32_t kvh;
@@ -239,7 +238,7 @@ struct Job {  // (split: positions and keys from the range's first key on)
 };
 
 // The CTA's jobs: job b of every round of gridDim.x jobs, in reverse order on
-// odd rounds (the items come longest first).
+// odd rounds (the items come longest first).  kSplit: job b, the only round.
 template <class Items, bool kSplit>
 struct Jobs {
   const PrefillParams& p;
@@ -247,6 +246,7 @@ struct Jobs {
   int base, odd;
   __device__ __forceinline__ Jobs(const PrefillParams& p_, const Items& items_) : p(p_), items(items_), base(0), odd(0) {}
   __device__ __forceinline__ bool next(Job& job) {
+    if (kSplit && base > 0) return false;  // one job per CTA
     const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
     const int u = base + (odd ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (u >= n) {  // (a last round that has no job for this CTA)
@@ -257,7 +257,6 @@ struct Jobs {
     odd ^= 1;
     const int it = u / p.num_kv_heads;
     const int4 item = items.item[it];  // request, first query token, its position, queries
-    job.slot = u;
     job.tok0 = item.y;
     job.nq = kSplit ? item.w & 0xff : item.w;
     job.kvh = u - it * p.num_kv_heads;
@@ -644,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
     if constexpr (kSplit) {
       // the row's part of this key range, 4 dims of 32 rows at a time
-      const size_t at = (size_t)job.slot * items.split.rows + x * kRows;
+      const size_t at = (size_t)blockIdx.x * items.split.rows + x * kRows;
       float4* dst = reinterpret_cast<float4*>(items.split.piece_o + at * kHeadDim) + row;
 #pragma unroll 1
       for (int c = 0; c < kHeadDim / 16; ++c) {
@@ -724,55 +723,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The outputs of split items: the log-sum-exp merge of their key ranges' parts,
-// in order.  A CTA takes 32 dims of a query tile's 128 rows (a thread 8 dims of a
-// row at a time, 16 dims in all): the parts lie as 4 dims of neighbouring rows,
-// so a warp reads 512 bytes at once.
+// in order.  A CTA takes 32 dims of a query tile's 128 rows, a thread 16 dims of a
+// row.  The parts lie as 4 dims of neighbouring rows, so a warp reads 512 bytes at
+// once; the ranges' weights are shared by the CTA, so that nothing but the parts'
+// loads, four ranges at a time, stands in the way of the sums.
 template <class Items>
 __global__ void __launch_bounds__(256) merge_q4_kernel(const PrefillParams p, const __grid_constant__ Items items) {
+  __shared__ float weight[kQ4MaxRanges][kRows];
   pdl_launch_dependents();
   pdl_wait();
   const int u = blockIdx.x, x = blockIdx.y, row = threadIdx.x & 127;
   const int it = u / p.num_kv_heads, kvh = u - it * p.num_kv_heads;
   const int4 item = items.item[it];
   const int nq = item.w & 0xff, tok = x * kTok + (row >> 2);
-  if (item.w >> 8 || tok >= nq) return;  // not the item's first range, not a query
+  if (item.w >> 8 || x * kTok >= nq) return;  // not the item's first range, no such query tile
   const int n_tiles = (item.z + nq + kKeys - 1) / kKeys;
   const int n = (n_tiles + items.split.tiles - 1) / items.split.tiles;
   const size_t stride = (size_t)p.num_kv_heads * items.split.rows;  // rows from a range to the next
   const size_t at = (size_t)u * items.split.rows + x * kRows;
-  const float* lse = items.split.piece_lse + at + row;
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(lse + i * stride));
-  float l = 0.f;
-  if (m > -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) l += fast_exp2(__ldcg(lse + i * stride) - m);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
   const size_t orow = (size_t)(item.y + tok) * p.num_q_heads + kvh * kGroup + (row & 3);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = blockIdx.z * 4 + 2 * (threadIdx.x >> 7) + h;  // dims 8 c .. 8 c + 7
-    const float4* src = reinterpret_cast<const float4*>(items.split.piece_o + at * kHeadDim) + 2 * c * kRows + row;
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+  if (threadIdx.x < kRows) {
+    const float* lse = items.split.piece_lse + at + row;
+    float m = -INFINITY;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
-      const float w = l > 0.f ? fast_exp2(__ldcg(lse + i * stride) - m) * inv : 0.f;
-      const float4 a = __ldcg(src + i * stride * (kHeadDim / 4)), b = __ldcg(src + i * stride * (kHeadDim / 4) + kRows);
-      o[0] = fmaf(w, a.x, o[0]);
-      o[1] = fmaf(w, a.y, o[1]);
-      o[2] = fmaf(w, a.z, o[2]);
-      o[3] = fmaf(w, a.w, o[3]);
-      o[4] = fmaf(w, b.x, o[4]);
-      o[5] = fmaf(w, b.y, o[5]);
-      o[6] = fmaf(w, b.z, o[6]);
-      o[7] = fmaf(w, b.w, o[7]);
+      const float v = __ldcg(lse + i * stride);
+      weight[i][row] = v;
+      m = fmaxf(m, v);
     }
-    *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 8 * c) = make_uint4(
-        pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    float l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const float w = m > -INFINITY ? fast_exp2(weight[i][row] - m) : 0.f;
+      weight[i][row] = w;
+      l += w;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    for (int i = 0; i < n; ++i) weight[i][row] *= inv;
+    if (p.lse && blockIdx.z == 0 && tok < nq) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
-  if (p.lse && blockIdx.z == 0 && threadIdx.x < 128) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  __syncthreads();
+  const int c = blockIdx.z * 8 + 4 * (threadIdx.x >> 7);  // dims 4 c .. 4 c + 15
+  const float4* src = reinterpret_cast<const float4*>(items.split.piece_o + at * kHeadDim) + c * kRows + row;
+  float4 o[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float w = weight[i][row];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float4 a = __ldcg(src + i * stride * (kHeadDim / 4) + v * kRows);
+      o[v] = make_float4(fmaf(w, a.x, o[v].x), fmaf(w, a.y, o[v].y), fmaf(w, a.z, o[v].z), fmaf(w, a.w, o[v].w));
+    }
+  }
+  if (tok >= nq) return;
+#pragma unroll
+  for (int v = 0; v < 4; v += 2)
+    *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 4 * (c + v)) =
+        make_uint4(pack_bf16x2(o[v].x, o[v].y), pack_bf16x2(o[v].z, o[v].w), pack_bf16x2(o[v + 1].x, o[v + 1].y),
+                   pack_bf16x2(o[v + 1].z, o[v + 1].w));
 }
 
 std::atomic<bool> g_attr_set[3][kMaxDevices];
