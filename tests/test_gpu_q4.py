@@ -573,3 +573,26 @@ def test_ranges_with_a_page_outside_the_pool_and_hidden_ones():
     c.dev["tables"].fill_(10 ** 8)
     out, lse = c.run()
     assert not bool(out.any()) and bool(torch.isneginf(lse).all())
+
+
+def test_captured_key_ranges_replay_beside_other_work():
+    c = Case([3000, 500, 40], [20, 1, 1], 2, seed=91)
+    want, want_lse = c.run()
+    ws = B.new_workspace(B.pa_attention_workspace_size(3, 22, 8, 128, 3000), DEV)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    c.run(out=out, lse=lse, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(out=out, lse=lse, workspace=ws)
+    other = Case([1200] * 3, [1, 30, 4], 2, seed=92)
+    other_want = other.run()[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        with torch.cuda.stream(side):
+            other_out = other.run(stream=side)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(other_out, other_want)
+    assert B.pa_get_device_error(ws) == 0
