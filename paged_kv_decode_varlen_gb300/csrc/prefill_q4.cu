@@ -556,162 +556,162 @@ __global__ void __launch_bounds__(kThreads, 1)
     Job job;
     bool more = jobs.next(job), ok = true;
     while (more) {
-    if (x >= job.n_x) {
-      J0 += job.n_tiles;
-      more = jobs.next(job);
-      continue;
-    }
-    const int pos = job.pos0 + x * kTok + (row >> 2);
-    float m_run = -INFINITY, l_run = 0.f;
-    for (int i = 0; i < job.n_sub; ++i) {
-      const int I = I0 + i;
-      const uint32_t t_s = lane_base + kColS + x * kKeys + (I & 1) * kSub;
-      ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x][I & 1], (I >> 1) & 1, p.err));
-      if (!ok) break;
-      fence_after_sync();
-      const int kbase = i * kSub;
-      // bytes of its 4 pages
-      const uint32_t bad = reinterpret_cast<volatile uint32_t*>(&sm.bad[(J0 + (i >> 1)) & 7])[i & 1];
-      // hidden keys: after the row's position, past the end, of a bad page
-      const bool masked = kbase + kSub - 1 > job.pos0 + x * kTok || kbase + kSub > job.keys || bad != 0u;
-      const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the sub-tile before the first hidden one
-      const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
-      // One pass over the scores, 32 keys at a time, the next ones' load in
-      // flight.  The weights are taken against the row's reference m_run first;
-      // only when their sum shows that it lies too low (or there is none yet)
-      // the maximum is looked for, m_run re-based to it, and the output and the
-      // weights stored so far rescaled.  After a row's first keys that is rare.
-      float2 ls = make_float2(0.f, 0.f);
-      uint32_t buf[2][32];
-      tmem_ld32_async(t_s, buf[0]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t(&c)[32] = buf[h & 1];
-        wait_ld(c);
-        if (h < 1) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
-        if (masked) {
-          const uint32_t pages = bad >> (16 * h);  // bytes of pages 2 h and 2 h + 1
-#pragma unroll
-          for (int y = 0; y < 32; ++y)
-            if (32 * h + y >= seen || (pages & (y < 16 ? 0xffu : 0xff00u))) c[y] = hide;
-        }
-        uint32_t w[16];
-        float2 sum;
-        for (bool again = false;; again = true) {
-          const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
-          const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
-            const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-            s2[y & 1] = __fadd2_rn(s2[y & 1], e);
-            w[y] = pack_bf16x2(e.x, e.y);
-          }
-          sum = __fadd2_rn(s2[0], s2[1]);
-          const bool low = sum.x + sum.y > kMaxSum || m_run == -INFINITY;
-          if (again || !__any_sync(0xffffffffu, low)) break;
-          if (h < 1) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
-          float mt = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < 32; ++y) mt = fmaxf(mt, __uint_as_float(c[y]) * scale);
-          const bool grow = low && mt > m_run;
-          const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
-          if (grow) m_run = mt;
-          l_run *= corr;
-          ls = __fmul2_rn(ls, make_float2(corr, corr));
-          if (i > 0) {  // O is stable once PV of the sub-tile before is done
-            ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(I - 1) & 1], ((I - 1) >> 1) & 1, p.err));
-            if (!ok) break;
-            fence_after_sync();
-          }
-          rescale(t_o, t_s, h, i > 0, corr);
-        }
-        ls = __fadd2_rn(ls, sum);
-        store16(t_s + 16 * h, w);  // weights over scores already read
+      if (x >= job.n_x) {
+        J0 += job.n_tiles;
+        more = jobs.next(job);
+        continue;
       }
-      if (!ok) break;
-      l_run += ls.x + ls.y;
-      wait_st();
-      fence_before_sync();  // the tensor-memory accesses above precede the arrive
-      mbar_arrive(&sm.p_full[x][I & 1]);
-    }
-    if (!ok) break;
-    const int I1 = I0 + job.n_sub - 1;
-    if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
-    fence_after_sync();
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-    if constexpr (kSplit) {
-      // the row's part of this key range, 4 dims of 32 rows at a time
-      const size_t at = (size_t)blockIdx.x * items.split.rows + x * kRows;
-      float4* dst = reinterpret_cast<float4*>(items.split.piece_o + at * kHeadDim) + row;
-#pragma unroll 1
-      for (int c = 0; c < kHeadDim / 16; ++c) {
-        uint32_t o[16];
-        load16(t_o + 16 * c, o);
+      const int pos = job.pos0 + x * kTok + (row >> 2);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = 0; i < job.n_sub; ++i) {
+        const int I = I0 + i;
+        const uint32_t t_s = lane_base + kColS + x * kKeys + (I & 1) * kSub;
+        ok = __all_sync(0xffffffffu, wait(sm, &sm.s_full[x][I & 1], (I >> 1) & 1, p.err));
+        if (!ok) break;
+        fence_after_sync();
+        const int kbase = i * kSub;
+        // bytes of its 4 pages
+        const uint32_t bad = reinterpret_cast<volatile uint32_t*>(&sm.bad[(J0 + (i >> 1)) & 7])[i & 1];
+        // hidden keys: after the row's position, past the end, of a bad page
+        const bool masked = kbase + kSub - 1 > job.pos0 + x * kTok || kbase + kSub > job.keys || bad != 0u;
+        const int seen = min(pos, job.keys - 1) - kbase + 1;  // keys of the sub-tile before the first hidden one
+        const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
+        // One pass over the scores, 32 keys at a time, the next ones' load in
+        // flight.  The weights are taken against the row's reference m_run first;
+        // only when their sum shows that it lies too low (or there is none yet)
+        // the maximum is looked for, m_run re-based to it, and the output and the
+        // weights stored so far rescaled.  After a row's first keys that is rare.
+        float2 ls = make_float2(0.f, 0.f);
+        uint32_t buf[2][32];
+        tmem_ld32_async(t_s, buf[0]);
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          dst[(4 * c + y) * kRows] =
-              make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
-                          __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
-      }
-      fence_before_sync();  // the tensor-memory reads above precede the arrive
-      mbar_arrive(&sm.o_free[x]);
-      items.split.piece_lse[at + row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
-    } else {
-      // The output, 64 dims at a time, through shared memory (128-byte swizzle)
-      // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
-      // threads, 16 bytes of a row each, an instruction touches 32 lines: a job's
-      // end took 6000 cycles against 2600, the prompts above 52 us against 47.)
-      const int tok = x * kTok + (row >> 2);
-      const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
-      uint8_t* stg = sm.out[warp];
-      uint32_t o[2][32];
-      tmem_ld32_async(t_o, o[0]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t(&c)[32] = buf[h & 1];
+          wait_ld(c);
+          if (h < 1) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
+          if (masked) {
+            const uint32_t pages = bad >> (16 * h);  // bytes of pages 2 h and 2 h + 1
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (lane == 0) bulk_wait_read();  // what was staged before has been read
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          wait_ld(o[c]);
-          if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+            for (int y = 0; y < 32; ++y)
+              if (32 * h + y >= seen || (pages & (y < 16 ? 0xffu : 0xff00u))) c[y] = hide;
+          }
           uint32_t w[16];
+          float2 sum;
+          for (bool again = false;; again = true) {
+            const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+            const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int y = 0; y < 16; ++y)
-            w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+            for (int y = 0; y < 16; ++y) {
+              const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
+              const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+              s2[y & 1] = __fadd2_rn(s2[y & 1], e);
+              w[y] = pack_bf16x2(e.x, e.y);
+            }
+            sum = __fadd2_rn(s2[0], s2[1]);
+            const bool low = sum.x + sum.y > kMaxSum || m_run == -INFINITY;
+            if (again || !__any_sync(0xffffffffu, low)) break;
+            if (h < 1) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
+            float mt = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < 32; ++y) mt = fmaxf(mt, __uint_as_float(c[y]) * scale);
+            const bool grow = low && mt > m_run;
+            const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
+            if (grow) m_run = mt;
+            l_run *= corr;
+            ls = __fmul2_rn(ls, make_float2(corr, corr));
+            if (i > 0) {  // O is stable once PV of the sub-tile before is done
+              ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(I - 1) & 1], ((I - 1) >> 1) & 1, p.err));
+              if (!ok) break;
+              fence_after_sync();
+            }
+            rescale(t_o, t_s, h, i > 0, corr);
+          }
+          ls = __fadd2_rn(ls, sum);
+          store16(t_s + 16 * h, w);  // weights over scores already read
+        }
+        if (!ok) break;
+        l_run += ls.x + ls.y;
+        wait_st();
+        fence_before_sync();  // the tensor-memory accesses above precede the arrive
+        mbar_arrive(&sm.p_full[x][I & 1]);
+      }
+      if (!ok) break;
+      const int I1 = I0 + job.n_sub - 1;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
+      fence_after_sync();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      if constexpr (kSplit) {
+        // the row's part of this key range, 4 dims of 32 rows at a time
+        const size_t at = (size_t)blockIdx.x * items.split.rows + x * kRows;
+        float4* dst = reinterpret_cast<float4*>(items.split.piece_o + at * kHeadDim) + row;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim / 16; ++c) {
+          uint32_t o[16];
+          load16(t_o + 16 * c, o);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
-                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+            dst[(4 * c + y) * kRows] =
+                make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
+                            __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
         }
-        if (h == 1) {
-          fence_before_sync();  // the tensor-memory reads above precede the arrive
-          mbar_arrive(&sm.o_free[x]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (tok_w + kOutTok <= job.nq) {
-          if (lane == 0) {
-            tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
-            bulk_commit();
+        fence_before_sync();  // the tensor-memory reads above precede the arrive
+        mbar_arrive(&sm.o_free[x]);
+        items.split.piece_lse[at + row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+      } else {
+        // The output, 64 dims at a time, through shared memory (128-byte swizzle)
+        // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
+        // threads, 16 bytes of a row each, an instruction touches 32 lines: a job's
+        // end took 6000 cycles against 2600, the prompts above 52 us against 47.)
+        const int tok = x * kTok + (row >> 2);
+        const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
+        uint8_t* stg = sm.out[warp];
+        uint32_t o[2][32];
+        tmem_ld32_async(t_o, o[0]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) bulk_wait_read();  // what was staged before has been read
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            wait_ld(o[c]);
+            if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+            uint32_t w[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
           }
-        } else {  // the row's last tokens
+          if (h == 1) {
+            fence_before_sync();  // the tensor-memory reads above precede the arrive
+            mbar_arrive(&sm.o_free[x]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (tok_w + kOutTok <= job.nq) {
+            if (lane == 0) {
+              tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
+              bulk_commit();
+            }
+          } else {  // the row's last tokens
 #pragma unroll 1
-          for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
-            const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
-            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
-                *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+            for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
+              const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
+              *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
+                  *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+            }
           }
         }
+        if (p.lse && tok < job.nq)
+          p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
+              l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
       }
-      if (p.lse && tok < job.nq)
-        p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
-            l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
-    }
-    J0 += job.n_tiles;
-    I0 += job.n_sub;
-    more = jobs.next(job);
+      J0 += job.n_tiles;
+      I0 += job.n_sub;
+      more = jobs.next(job);
     }
     if (lane == 0) bulk_wait_all();  // the stores have been written
     __syncwarp();
