@@ -176,7 +176,8 @@ pa_status pa_attention_varlen_q8(const void* q, const void* k_cache, const void*
  * value, D = bf16(16 ((hi - lo) / 15)), Z = bf16(lo - D), code = 16 ((x - Z) /
  * D) - 16 rounded to the nearest integer (ties to even) and clamped to
  * [0, 15]; all codes 0 when D is 0 (a group of equal values is kept exactly).
- * Inputs must be finite and at most 2^126 in magnitude; a group with others
+ * Inputs must be finite and at most 2^125 in magnitude (a greater x - Z may
+ * overflow, which costs its code up to a step); a group with infinities or NaN
  * gets unspecified bytes (no other group is touched).
  */
 #define PA_Q4_SLAB_BYTES (PA_BLOCK_SIZE * PA_HEAD_DIM / 2 + PA_BLOCK_SIZE * (PA_HEAD_DIM / 32) * 4) /* 1280 */

@@ -64,6 +64,20 @@ def test_quantisation_error_is_half_a_step():
     assert np.all(np.abs(got - v).reshape(40, 2, 4, 32) <= bound[..., None])
 
 
+def test_the_largest_inputs_are_within_half_a_step():
+    rng = np.random.default_rng(5)
+    x = np.clip(rng.standard_normal((60, 1, 128)) * 2.0 ** 124.5, -2.0 ** 125, 2.0 ** 125).astype(np.float32)
+    bits = W.f32_to_bf16_bits(x)
+    pool = np.zeros((4, 1, q4.SLAB), np.uint8)
+    q4.append(bits, np.arange(60), pool)
+    got = _value(q4.unpack(pool))[np.arange(60) // 16, :, np.arange(60) % 16].reshape(60, 4, 32)
+    v = _value(bits).reshape(60, 4, 32)
+    # the bound of the test above
+    d = (v.max(-1) - v.min(-1)) * 16 / 15 * (1 + 2.0 ** -8)
+    bound = d / 32 + 2.0 ** -8 * (np.abs(v.min(-1)) + 2 * d) + 2.0 ** -8 * np.abs(v).max(-1)
+    assert np.all(np.abs(got - v) <= bound[..., None])
+
+
 def test_equal_values_are_exact_and_codes_span_the_range():
     x = np.full((1, 1, 128), 0x4049, np.uint16)
     pool = np.zeros((1, 1, q4.SLAB), np.uint8)
