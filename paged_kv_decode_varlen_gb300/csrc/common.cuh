@@ -142,12 +142,6 @@ __device__ __forceinline__ int atom_add_acq_rel_gpu(int* addr, int v) {
   return old;
 }
 
-__device__ __forceinline__ unsigned long long atom_add_acq_rel_gpu(unsigned long long* addr, unsigned long long v) {
-  unsigned long long old;
-  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
-  return old;
-}
-
 // Acquire load at GPU scope (pairs with a release by another CTA).
 __device__ __forceinline__ int ld_acquire_gpu(const int* addr) {
   int v;

@@ -141,6 +141,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// As atom_add_acq_rel_gpu of common.cuh, on 64 bits (here, since that file is
+// part of the bf16 decode kernel's measured source).
+__device__ __forceinline__ unsigned long long atom_add64_acq_rel_gpu(unsigned long long* addr, unsigned long long v) {
+  unsigned long long old;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
+  return old;
+}
 __device__ __forceinline__ uint32_t at(const uint4& v, int g) { return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w; }
 
 // An output row (head of this lane, 16 dims per lane as described at the
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int last = 0;
     if (lane == 0) {
       unsigned long long* word = word_of(it);
-      last = (int)(atom_add_acq_rel_gpu(word, 1ull) & 0xffffu) == b1 - b0;
+      last = (int)(atom_add64_acq_rel_gpu(word, 1ull) & 0xffffu) == b1 - b0;
       if (last) *word = 0;  // every piece has arrived: ready for the next replay with this tag
     }
     __syncwarp();  // lane 0's acquire orders the reads below
