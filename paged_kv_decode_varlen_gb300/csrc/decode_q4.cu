@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       Part<kCols> all;
       merge_parts<kCols>(
           all, b1 - b0 + 1, lane,
-          [&](int i, int c) { return __ldcg(p.piece_lse + piece_at(it, b0 + i) + y * S::kTileCols + kCols * cq + c); },
+          [&](int i, int c) { return load_cg(p.piece_lse + piece_at(it, b0 + i) + y * S::kTileCols + kCols * cq + c); },
           [&](int, int) { return 1.f; },
           [&](int i) {
             return reinterpret_cast<const float4*>(p.piece_o + (piece_at(it, b0 + i) + y * S::kTileCols) * kHeadDim);

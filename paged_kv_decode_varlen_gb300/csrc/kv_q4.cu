@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_q4_kernel(const AppendPara
     slot = p.slot_mapping[tok];
     const uint4* k = reinterpret_cast<const uint4*>(p.k_new + (size_t)row * kHeadDim) + 4 * group + word;
     const uint4* v = reinterpret_cast<const uint4*>(p.v_new + (size_t)row * kHeadDim) + 4 * group + word;
-    k0 = __ldcs(k);
-    k1 = __ldcs(k + 2);
-    v0 = __ldcs(v);
-    v1 = __ldcs(v + 2);
+    k0 = load_cs(k);
+    k1 = load_cs(k + 2);
+    v0 = load_cs(v);
+    v1 = load_cs(v + 2);
   }
   if (__all_sync(0xffffffffu, slot < 0)) return;
   uint32_t kcode[2], kdz, vcode[2], vdz;  // (whole warp: the groups' shuffles)
@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const ReadParams p
       const size_t slab = ((size_t)block * p.num_kv_heads + x.head) * kQ4Slab;
       const size_t code_at = slab + q4_code_at(t, l >> 2) + 4 * (l & 3);
       const size_t scale_at = slab + q4_scale_at(t, l >> 2);
-      w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache + code_at));
-      w[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache + scale_at));
-      w[u][2] = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache + code_at));
-      w[u][3] = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache + scale_at));
+      w[u][0] = load_cg(reinterpret_cast<const uint32_t*>(p.k_cache + code_at));
+      w[u][1] = load_cg(reinterpret_cast<const uint32_t*>(p.k_cache + scale_at));
+      w[u][2] = load_cg(reinterpret_cast<const uint32_t*>(p.v_cache + code_at));
+      w[u][3] = load_cg(reinterpret_cast<const uint32_t*>(p.v_cache + scale_at));
     } else if (slot[u] >= 0 && l == 0) {
       record_error(p.err, PA_ERR_DEVICE_INDEX);
     }

@@ -324,9 +324,9 @@ __device__ __forceinline__ bool produce(Smem& sm, const Job& job, int w, int J0,
         ((u & kPagesPerTile) ? v_cache : k_cache) + ((size_t)max(id, 0) * num_kv_heads + job.kvh) * kQ4Slab;
     bad[d] = id == -2;
     auto load = [&](int y) {  // tokens t + 8 y
-      code[d][y][0] = __ldg(reinterpret_cast<const uint2*>(slab + 512 * y + code_at));
-      code[d][y][1] = __ldg(reinterpret_cast<const uint2*>(slab + 512 * y + (code_at ^ 8u)));
-      dz[d][y] = __ldg(reinterpret_cast<const uint32_t*>(slab + 8 * 4 * kQ4Groups * y + dz_at));
+      code[d][y][0] = load_cg(reinterpret_cast<const uint2*>(slab + 512 * y + code_at));
+      code[d][y][1] = load_cg(reinterpret_cast<const uint2*>(slab + 512 * y + (code_at ^ 8u)));
+      dz[d][y] = load_cg(reinterpret_cast<const uint32_t*>(slab + 8 * 4 * kQ4Groups * y + dz_at));
     };
     if (id >= 0 && left >= kPage) {
       load(0);
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(256) merge_q4_kernel(const PrefillParams p, co
     float m = -INFINITY;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
-      const float v = __ldcg(lse + i * stride);
+      const float v = load_cg(lse + i * stride);
       weight[i][row] = v;
       m = fmaxf(m, v);
     }
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(256) merge_q4_kernel(const PrefillParams p, co
     const float w = weight[i][row];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float4 a = __ldcg(src + i * stride * (kHeadDim / 4) + v * kRows);
+      const float4 a = load_cg(src + i * stride * (kHeadDim / 4) + v * kRows);
       o[v] = make_float4(fmaf(w, a.x, o[v].x), fmaf(w, a.y, o[v].y), fmaf(w, a.z, o[v].z), fmaf(w, a.w, o[v].w));
     }
   }

@@ -26,6 +26,44 @@ constexpr int kQ4Codes = kPage * kQ4Row;             // code bytes of a slab
 constexpr int kQ4Slab = PA_Q4_SLAB_BYTES;
 static_assert(kQ4Slab == kQ4Codes + kPage * kQ4Groups * 4 && kQ4Slab % 16 == 0, "codes, then (D, Z) pairs");
 
+// Loads of what an earlier kernel of the stream may have written (a pool, new
+// rows, partial results), as the coherent loads that they have to be: a q4 kernel
+// is launched while the one before it may still run, so ld.global.nc, which wants
+// memory that nobody writes while the kernel runs, might give what was there
+// before.  Volatile, so that none is moved above the wait for that kernel; they
+// pass L1, which none of them would use twice.  (.cs: read once.)
+__device__ __forceinline__ uint32_t load_cg(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load_cg(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_cg(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_cs(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Byte of token t's 16 code bytes of group g, and of its (D, Z) pair.
 __device__ __forceinline__ int q4_code_at(int t, int g) { return t * kQ4Row + ((g ^ ((t >> 1) & 3)) << 4); }
 __device__ __forceinline__ int q4_scale_at(int t, int g) { return kQ4Codes + (t * kQ4Groups + g) * 4; }
