@@ -231,7 +231,8 @@ pa_status pa_kv_read_q4(const int64_t* slot_mapping, int64_t n_tokens, const voi
  * Weights are rounded to bf16 before they meet V in rows of several queries;
  * in rows of one they carry 16 bits, unless ceil(seq_len / 16) * num_kv_heads
  * exceeds a million.  Scores of rows with many queries must stay below 2^30 in
- * magnitude.
+ * magnitude.  A (query, head) with a NaN among its scores has NaN in its out row
+ * and its lse, and changes no other.
  */
 pa_status pa_attention_varlen_q4(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
                                  const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,

@@ -183,8 +183,9 @@ struct Part {
   float4 o[4 * kCols];
 };
 
-// Log-sum-exp merge of n parts, in order.  m_at(i, c), l_at(i, c): maximum and
-// weight sum of column c of this lane in part i; row(i): the part's vectors of
+// Log-sum-exp merge of n parts, in order.  m_at(i, c), l_at(i, c): maximum (-inf:
+// nothing counts, NaN: nor does any other part) and weight sum of column c of
+// this lane in part i; row(i): the part's vectors of
 // this lane at stride 32.  The loads of a batch of parts are all in flight
 // before any is used.
 template <int kCols, class M, class L, class Row>
@@ -216,7 +217,7 @@ __device__ __forceinline__ void merge_parts(Part<kCols>& out, int n, int lane, M
     for (int c = 0; c < kCols; ++c) {
       float mx = out.m[c];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, mi[u][c]);
+      for (int u = 0; u < kBatch; ++u) mx = max_nan(mx, mi[u][c]);
       if (mx == -INFINITY) continue;  // every part so far is empty
       const float f = fast_exp2(out.m[c] - mx);  // -inf -> 0
       out.m[c] = mx;
@@ -617,7 +618,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       for (int x = 0; x < kCols; ++x) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], o);
-        own[y].m[x] = nm[y][x] == kNoMax ? -INFINITY : -nm[y][x];
+        // (without a maximum the sum is 0, or NaN from scores that were NaN)
+        own[y].m[x] = nm[y][x] == kNoMax ? l[y][x] - INFINITY : -nm[y][x];
         own[y].l[x] = l[y][x];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       for (int x = 0; x < kCols; ++x) {
         const int col = kCols * cq + x;  // of the tile
         const int query = S::kOne ? 0 : 2 * y + (col >> 2), head = S::kOne ? col : col & 3;
-        const float inv = v.l[x] > 0.f ? 1.f / v.l[x] : 0.f;
+        const float inv = v.l[x] == 0.f ? 0.f : 1.f / v.l[x];
         float o[16];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         const size_t orow = (size_t)(it.tok + query) * p.num_q_heads + kvh * kGroup + head;
         store_row(p.out + orow * kHeadDim, o, r, query < nq);
         if (p.lse && r == 0 && query < nq)
-          p.lse[orow] = v.l[x] > 0.f ? (v.m[x] + log2f(v.l[x])) * kLn2 : -INFINITY;
+          p.lse[orow] = lse_log2(v.m[x], v.l[x]) * kLn2;
       }
     };
 #pragma unroll
@@ -699,14 +701,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       float4* dst = reinterpret_cast<float4*>(p.piece_o + mine * kHeadDim);
 #pragma unroll
       for (int x = 0; x < kCols; ++x) {
-        const float inv = own[y].l[x] > 0.f ? 1.f / own[y].l[x] : 0.f;
+        const float inv = own[y].l[x] == 0.f ? 0.f : 1.f / own[y].l[x];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float4 v = own[y].o[4 * x + g];
           dst[(4 * x + g) * 32 + lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
         }
         if (r == 0)
-          p.piece_lse[mine + kCols * cq + x] = own[y].l[x] > 0.f ? own[y].m[x] + log2f(own[y].l[x]) : -INFINITY;
+          p.piece_lse[mine + kCols * cq + x] = lse_log2(own[y].m[x], own[y].l[x]);
       }
     }
     if (!is_cut) continue;

@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int I1 = I0 + job.n_sub - 1;
       if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
       fence_after_sync();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if constexpr (kSplit) {
         // the row's part of this key range, 4 dims of 32 rows at a time
         const size_t at = (size_t)blockIdx.x * items.split.rows + x * kRows;
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_before_sync();  // the tensor-memory reads above precede the arrive
         mbar_arrive(&sm.o_free[x]);
-        items.split.piece_lse[at + row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+        items.split.piece_lse[at + row] = lse_log2(m_run, l_run);
       } else {
         // The output, 64 dims at a time, through shared memory (128-byte swizzle)
         // and out by TMA, the warp's 8 tokens x 4 heads x 64 dims.  (Stored by the
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (p.lse && tok < job.nq)
           p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] =
-              l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+              lse_log2(m_run, l_run) * kLn2;
       }
       J0 += job.n_tiles;
       I0 += job.n_sub;
@@ -749,17 +749,17 @@ __global__ void __launch_bounds__(256) merge_q4_kernel(const PrefillParams p, co
     for (int i = 0; i < n; ++i) {
       const float v = load_cg(lse + i * stride);
       weight[i][row] = v;
-      m = fmaxf(m, v);
+      m = max_nan(m, v);
     }
     float l = 0.f;
     for (int i = 0; i < n; ++i) {
-      const float w = m > -INFINITY ? fast_exp2(weight[i][row] - m) : 0.f;
+      const float w = m == -INFINITY ? 0.f : fast_exp2(weight[i][row] - m);
       weight[i][row] = w;
       l += w;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     for (int i = 0; i < n; ++i) weight[i][row] *= inv;
-    if (p.lse && blockIdx.z == 0 && tok < nq) p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && blockIdx.z == 0 && tok < nq) p.lse[orow] = lse_log2(m, l) * kLn2;
   }
   __syncthreads();
   const int c = blockIdx.z * 8 + 4 * (threadIdx.x >> 7);  // dims 4 c .. 4 c + 15

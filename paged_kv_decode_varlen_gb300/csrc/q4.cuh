@@ -16,6 +16,8 @@
 // neighbouring dims.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 
 namespace pa {
@@ -63,6 +65,18 @@ __device__ __forceinline__ uint4 load_cs(const uint4* p) {
                : "memory");
   return v;
 }
+
+// The greater of two, NaN if one is: merging parts, a NaN of one shows in all.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// log2 sum_t 2^(s_t) from a maximum (or any reference) and the sum of weights
+// against it; -inf without a weight (the sum of a row that has one is never 0),
+// NaN where a score was.
+__device__ __forceinline__ float lse_log2(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
 // Byte of token t's 16 code bytes of group g, and of its (D, Z) pair.
 __device__ __forceinline__ int q4_code_at(int t, int g) { return t * kQ4Row + ((g ^ ((t >> 1) & 3)) << 4); }
