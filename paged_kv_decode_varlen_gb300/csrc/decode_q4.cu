@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         last = atomicAdd(&sm.arrived[k], 1) == wl - wf;
         __threadfence_block();
       }
+      __syncwarp();  // lane 0's fence orders every lane's reads of the parts below (a shuffle orders no memory)
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
     }
     const int b0 = first_seg(it), b1 = (it.A + (L + kPage - 1) / kPage - 1) / plan.seg;
