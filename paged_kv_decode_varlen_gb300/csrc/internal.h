@@ -192,6 +192,14 @@ struct TcMaps {
   CUtensorMap v;
 };
 
+// Those of the tile kernel over q4 pages: q as above, and out as q with boxes of
+// kQ4OutTok tokens, the rows that a softmax warp stores at once.
+constexpr int kQ4OutTok = 32 / PA_GQA_GROUP;
+struct Q4Maps {
+  CUtensorMap q;
+  CUtensorMap out;
+};
+
 // Prefill work items: (request, first query of the tile) pairs, passed by
 // value in the kernel's parameter block.
 constexpr int kMaxPrefillItems = 1536;
@@ -321,11 +329,11 @@ cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, cons
 // pages), else the CTA-granular one (windows of rows)
 cudaError_t launch_decode_step(const DecodeParams& p, const StepPlan& plan, int grid, bool warp_granular,
                                cudaStream_t stream);
-// q4 pages: (item of kQ4TileTokens queries, kv head) jobs on ctas CTAs; rows[i]
-// is item i's (request, first query token, its position, queries), maps.q and
-// maps.k the tensor maps of q (boxes of 32 tokens) and of out (of one)
+// q4 pages: (item of up to kQ4TileTokens queries, kv head) jobs on ctas CTAs;
+// rows[i] is item i's (request, first query token, its position, queries + 256 x
+// key range).  With key ranges: one CTA per job, at most kQ4FewItems items
 cudaError_t launch_prefill_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
-                              const TcMaps& maps, int ctas, cudaStream_t stream);
+                              const Q4Maps& maps, int ctas, cudaStream_t stream);
 // ... and the outputs of split items from their ranges' parts
 cudaError_t launch_merge_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
                             cudaStream_t stream);
@@ -341,7 +349,7 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.
 constexpr int kPrefillQTile = 32;
 constexpr int kTcKeyTile = 128;
-// Query tokens per CTA of the tile kernel over q4 pages (two MMA tiles).
+// Most query tokens of a job of the tile kernel over q4 pages (two MMA tiles).
 constexpr int kQ4TileTokens = 2 * kPrefillQTile;
 // Decode kernel: pages a CTA may hold block ids for (bounds the segment).
 constexpr int kDecodeMaxPagesPerCta = 1024;

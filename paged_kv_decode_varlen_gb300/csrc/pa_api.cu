@@ -743,12 +743,14 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
   float* prefix_o = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_o) : nullptr;
   float* prefix_lse = P > 0 ? reinterpret_cast<float*>(ws + pl.prefix_lse) : nullptr;
   static thread_local pa::TcMaps maps;
-  if (P > 0 || !tiles.empty() || !q4_tile_rows.empty()) {
-    s = q4 ? make_q_map(q, total_q, num_q_heads, pa::kPrefillQTile, maps.q)
-           : make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
-    if (s == PA_OK && q4) s = make_q_map(out, total_q, num_q_heads, 32 / pa::kGroup, maps.k);
-    if (s != PA_OK) return s;
+  static thread_local pa::Q4Maps q4_maps;
+  if (!q4_tile_rows.empty()) {
+    s = make_q_map(q, total_q, num_q_heads, pa::kPrefillQTile, q4_maps.q);
+    if (s == PA_OK) s = make_q_map(out, total_q, num_q_heads, pa::kQ4OutTok, q4_maps.out);
+  } else if (P > 0 || !tiles.empty()) {
+    s = make_tc_maps(q, total_q, num_q_heads, k_cache, v_cache, num_blocks, num_kv_heads, maps);
   }
+  if (s != PA_OK) return s;
 
   // what the decode kernel folds in: the merged prefix partial, or the key-
   // chunk partials themselves when there is no prefill row to share them with
@@ -948,7 +950,7 @@ pa_status attention(const void* q, const void* k_cache, const void* v_cache, int
       }
       s = run_launch(PA_KERNEL_PREFILL, "prefill", stream,
                      [&] {
-                       return q4 ? pa::launch_prefill_q4(pp, q4_count, q4_items, q4_split, maps,
+                       return q4 ? pa::launch_prefill_q4(pp, q4_count, q4_items, q4_split, q4_maps,
                                                          (int)std::min<int64_t>((int64_t)q4_count * num_kv_heads,
                                                                                 sm_count()), stream)
                                  : pa::launch_prefill(pp, items, maps, prefill_ctas, stream);

@@ -5,9 +5,10 @@
 // h + j and attends to keys 0 .. h + j; scores, softmax and output as in
 // decode_q4.cu, keys and values the bf16 numbers that the codes stand for.
 //
-// Work.  A job is 64 query tokens of a row for one kv head: two query tiles A
-// and B of 32 tokens x 4 heads = 128 rows, the M of one tcgen05.mma each (B is
-// left out of a job of up to 32), against key tiles of 128 (8 pages).  One CTA
+// Work.  A job is up to 64 query tokens of a row for one kv head: two query tiles
+// A and B of 32 tokens x 4 heads = 128 rows, the M of one tcgen05.mma each (B is
+// left out of a job of up to 32, which the host also makes of longer rows where
+// jobs of 64 would leave SMs idle), against key tiles of 128 (8 pages).  One CTA
 // per SM runs its share of the jobs one after another without a barrier between
 // them: rings, phases and buffers are indexed by running counts, so the next
 // job's Q, first key tiles and first scores are made while the softmax warps
@@ -76,11 +77,12 @@ constexpr int kAhead = 2;                    // units a producer warp reads ahea
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 for tile B
 constexpr float kMaxSum = 1024.f;  // of 32 weights, before their row's reference is raised
-constexpr int kOutTok = 32 / kGroup;         // query tokens of a softmax warp
+constexpr int kOutTok = kQ4OutTok;           // query tokens of a softmax warp
 constexpr int kSub = 64;                     // keys of a score product
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
 static_assert(kRows == 128 && kKeys == 128 && kQ4TileTokens == 2 * kTok, "tile shape");
+static_assert(kOutTok * kGroup == 32 && 4 * kOutTok == kTok, "a softmax warp's 32 rows are whole tokens");
 static_assert(2 * 32 * 16 == kQ4Codes, "two pieces of codes per lane");
 static_assert(kKStages == kVStages, "one ring depth");
 
@@ -796,19 +798,19 @@ const Q4Items<N>& fill(int count, const int4* rows, const Q4Split& split) {
 }
 
 template <int N, bool kSplit>
-cudaError_t launch(const PrefillParams& p, int count, const int4* rows, const Q4Split& split, const TcMaps& maps, int ctas,
+cudaError_t launch(const PrefillParams& p, int count, const int4* rows, const Q4Split& split, const Q4Maps& maps, int ctas,
                    std::atomic<bool>* done, cudaStream_t stream) {
   auto kernel = prefill_q4_kernel<Q4Items<N>, kSplit>;
   const cudaError_t e = set_smem_limit_once((const void*)kernel, (int)kSmemBytes, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, fill<N>(count, rows, split),
-                    maps.q, maps.k);
+                    maps.q, maps.out);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_q4(const PrefillParams& p, int count, const int4* rows, const Q4Split& split,
-                              const TcMaps& maps, int ctas, cudaStream_t stream) {
+                              const Q4Maps& maps, int ctas, cudaStream_t stream) {
   if (count <= 0) return cudaSuccess;
   // a zero scale (every score 0) as 2^-100, so that a hidden score scales to
   // -inf: scores of q and k whose products stay below 2^40 are below 2^-60 then
