@@ -5,8 +5,10 @@
 // nearest even): lo, hi = min, max; D = bf16(16 ((hi - lo) / 15)); Z =
 // bf16(lo - D); code = rint(16 ((x - Z) / D) - 16) clamped to [0, 15], 0 when
 // D is 0.  The codes are taken against the rounded D and Z, so their rounding
-// only shifts the grid's ends (by at most 2^-9 of |lo| + 2 D) and adds no
-// error of its own inside it.
+// only shifts the grid's ends and adds no error of its own inside it.  A bf16 is
+// off by at most 2^-8 of the number: the lowest grid value, Z + D, lies within
+// 2^-8 |lo - D| of lo, the highest, Z + 31/16 D, within that and 2^-8 (hi - lo)
+// of hi, as 15/16 D is hi - lo but for D's rounding (binary32's aside).
 //
 // Both kernels move bytes: a (token, kv head) row is 256 B of bf16 and 80 B of
 // a page, for K and for V.  Read back, sixteen threads take one row, eight dims
