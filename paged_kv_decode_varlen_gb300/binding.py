@@ -240,8 +240,8 @@ def _stream_handle(stream, device):
 
 
 def _on(stream):
-    """Tensors made in this context are made on `stream` (None: the current
-    one), so that they are ordered with the call that uses them there."""
+    """Tensors made or fetched in this context are so on `stream` (None: the
+    current one), ordered with the call that uses them there."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
@@ -262,11 +262,13 @@ def _refuse(device, *tensors):
         _data(t, dtype, name, device)
 
 
-def _host_data(t, n, name):
-    """(int32 host tensor of n elements, its address) from a tensor or a
-    sequence; no copy when t is one already."""
+def _host_data(t, n, name, stream):
+    """(int32 host tensor of n elements, its address) from a tensor, fetched
+    behind the work of `stream` if it is on the device, or a sequence; no copy
+    when t is one already."""
     if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and not t.is_cuda and t.is_contiguous()):
-        t = _host_i32(t)
+        with _on(stream):
+            t = _host_i32(t)
     if t.shape != (n,):
         raise ValueError(f"{name} must have {n} elements")
     return t, t.data_ptr()
@@ -349,8 +351,8 @@ def pa_attention_varlen_q4(q, k_cache, v_cache, block_tables, seq_lens, qo_indpt
     if v_cache.shape != pool or slab != PA_Q4_SLAB_BYTES or qo_indptr.shape != (R + 1,) \
             or len(table) != 2 or table[0] != R:
         raise ValueError("inconsistent shapes")
-    slh, slh_at = _host_data(seq_lens if seq_lens_host is None else seq_lens_host, R, "seq_lens_host")
-    qih, qih_at = _host_data(qo_indptr if qo_indptr_host is None else qo_indptr_host, R + 1, "qo_indptr_host")
+    slh, slh_at = _host_data(seq_lens if seq_lens_host is None else seq_lens_host, R, "seq_lens_host", stream)
+    qih, qih_at = _host_data(qo_indptr if qo_indptr_host is None else qo_indptr_host, R + 1, "qo_indptr_host", stream)
     if out is None:
         with _on(stream):
             out = torch.empty_like(q)
