@@ -15,10 +15,12 @@
 // (one code word) each: 16-byte accesses on the bf16 side, 64 contiguous bytes of
 // codes and 16 of scales on the other, kRows rows per thread in flight, since one
 // row is a chain of two loads (its slot, its bytes).  Written, eight threads take
-// a row, two code words each: the arithmetic bounds that side, and what a group
-// needs once (its range, D, Z, the reciprocal) and a row (its slot, its place) is
-// then done by half as many threads (7,021 tokens, 8 kv heads, written and read
-// back: 17.0 us against 20.1 with sixteen; 64 tokens 3.7 against 3.5).
+// a row, two code words each: what a group needs once (its range, D, Z, the
+// reciprocal) and a row (its slot, its place) is then done by half as many threads
+// (7,021 tokens, 8 kv heads, written and read back: 17.2 us against 20.1 with
+// sixteen; 64 tokens 3.7 against 3.5).  What bounds that side: warps wait for their
+// own row's loads (the first stall), as a thread has one row and 46 % of the warp
+// slots are taken; the schedulers issue 63 % of the time.
 #include "internal.h"
 #include "q4.cuh"
 
@@ -65,9 +67,9 @@ __device__ __forceinline__ void quantize16_q4(const uint4& x, const uint4& y, ui
     // (x - Z) / step rounded to nearest, from r = 1 / step rounded to nearest:
     // one correction of t r by the exact remainder (Markstein, "Computation of
     // elementary functions on the IBM RISC System/6000 processor", 1990).  A
-    // group shares the reciprocal, and pairs of values the instructions: the
-    // kernel is bound by issue (7,021 tokens, when sixteen threads took a row:
-    // 24 us with a division per value, 17.6 with this and no pairs, 12.5 so).
+    // group shares the reciprocal, and pairs of values the instructions, which
+    // count (7,021 tokens, when sixteen threads took a row: 24 us with a division
+    // per value, 17.6 with this and no pairs, 12.5 so).
     const float r = __frcp_rn(d);
     const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d), nz2 = make_float2(-z, -z);
     const float2 magic = make_float2(12582912.f, 12582912.f);
@@ -221,9 +223,9 @@ dim3 grid_for(int64_t rows) {
 
 // The read-back takes four rows per thread, for their loads in flight together,
 // only when there are CTAs enough for every SM several times over; before that
-// more CTAs are worth more (8 heads: 4096 tokens 4.3 us with one row per thread,
-// 5.9 with four; 8192 tokens 8.6 and 8.8; 16384 tokens 18.6 and 16.5; 131072
-// tokens 133 and 109).
+// more CTAs are worth more (8 heads, captured: 4096 tokens 6.5 us with one row per
+// thread, 7.6 with four; 8192 tokens 10.7 and 10.2; 16384 tokens 18.9 and 16.5;
+// 131072 tokens 134 and 110).
 constexpr int64_t kFewRows = 65536;
 
 cudaError_t launch_kv_append_q4(const AppendParams& p, cudaStream_t stream) {

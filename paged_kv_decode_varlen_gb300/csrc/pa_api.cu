@@ -360,10 +360,15 @@ struct Q4TilePlan {
 // job, which then has the other SMs, where that ends sooner than one after the
 // other.  Measured rates: a CTA's first job ~5 us, each further one ~3.5, and 1.8 us
 // per key tile (1.55 with one query tile), a merge ~4 us, the decode launch ~9 us
-// and 37 GB/s per SM.  (One chunk of 20 tokens behind 6000, 8 kv heads: 22 us in
-// ranges, 78 in whole items; of 200 behind 1800: 26 us in items of 32 and ranges,
-// 35 in items of 64; of 512 behind 3500: 55 and 62; 32 decode rows and a chunk of
-// 512 tokens, 2048 to 4096 keys each: a step of 54 us beside, 74 one after the
+// and 37 GB/s per SM.  Beyond one wave of jobs the estimate takes the mean key
+// tiles per SM: a CTA runs whole jobs, so the busiest may have up to a job more,
+// which it does not see (4 chunks of 512 tokens, 4096 to 8192 keys, 8 kv heads:
+// 148 us estimated, 174 measured), and key ranges are looked at within one wave
+// only (3 chunks of 400 tokens, 3200 keys: 168 jobs, 93 us where even work would
+// take some 57).  (One chunk of 20 tokens behind 6000, 8 kv heads: 23 us in
+// ranges, 78 in whole items; of 200 behind 1800: 25 us in items of 32 and ranges,
+// 35 in items of 64; of 512 behind 3500: 56 and 62; 32 decode rows and a chunk of
+// 512 tokens, 2048 to 4096 keys each: a step of 57 us beside, 78 one after the
 // other.)
 Q4TilePlan plan_q4_tiles(const std::vector<int32_t>& rows, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
                          int num_kv_heads, int64_t part_slots, bool may_beside, int64_t decode_slabs, int sms) {

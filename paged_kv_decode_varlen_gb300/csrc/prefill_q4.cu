@@ -12,16 +12,17 @@
 // per SM runs its share of the jobs one after another without a barrier between
 // them: rings, phases and buffers are indexed by running counts, so the next
 // job's Q, first key tiles and first scores are made while the softmax warps
-// finish this one (8 prompts of 100 to 1000 tokens, 32 heads: 43.7 us, where a
+// finish this one (8 prompts of 100 to 1000 tokens, 32 heads: 44.0 us, where a
 // CTA per job took 56).  The two tiles share every dequantised K and V tile.
 //   Bound.  Per key tile of 128 the products take 2560 cycles of the tensor
-// cores, the instructions of all warps some 2200 of the schedulers'; the whole
-// takes some 3400 (4 chunks of 512 tokens behind 4096 to 8192: 174 us, 1117
-// TFLOP/s): a warp that issues products or turns scores into weights waits for
-// its turn among four on a scheduler.  The loops of the three roles fill the
-// instruction cache, so code counts: a third slot of read-ahead in the producers
-// costs 5 % of the prompts' time, two loops kept apart in the issuing warps save
-// 8 % against a merged one.
+// cores, the instructions of all warps some 2330 of the schedulers'; the whole
+// takes some 3400 (4 chunks of 512 tokens, 4096 to 8192 keys: 174 us, 1115
+// TFLOP/s, 24 us of it uneven work: 256 whole jobs on 152 SMs, the busiest of
+// which has 91 key tiles, the mean 77.5): a warp that issues products or turns
+// scores into weights waits for its turn among four on a scheduler.  The loops of
+// the three roles fill the instruction cache, so code counts: a third slot of
+// read-ahead in the producers costs 5 % of the prompts' time, two loops kept apart
+// in the issuing warps save 8 % against a merged one.
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory
 // lane = row).  8 and 9: issue the products of A and of B (8 also copies Q by
