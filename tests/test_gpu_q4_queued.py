@@ -104,3 +104,73 @@ def test_rounds_over_the_same_slots_see_their_own_rows(name, graph):
             assert torch.equal(a["before"][0], want[i - 1]["after"][0])
             assert not torch.equal(a["after"][0], a["before"][0])
     assert torch.equal(kc, end[0]) and torch.equal(vc, end[1])
+
+
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "captured"])
+@pytest.mark.parametrize("seq,qo", [([1500, 1200, 900, 800, 300, 700], [100, 1, 1, 1, 1, 1]),
+                                    ([6000, 900, 30, 2000], [12, 5, 5, 5])], ids=["decode_rows", "key_ranges_and_verify_rows"])
+def test_steps_rewrite_queries_tables_and_rows_in_place(seq, qo, graph):
+    """Tile jobs and decode rows of one call, which run beside one another: a
+    step's queries, block table and new rows are written over the last step's."""
+    Hkv, steps = 2, 8
+    rng = np.random.default_rng(9)
+    pages = [-(-L // 16) for L in seq]
+    total, blocks = sum(qo), sum(pages) + 9
+    kc, vc = B.new_q4_pool(blocks, Hkv, DEV), B.new_q4_pool(blocks, Hkv, DEV)
+    every = torch.arange(blocks * 16, device=DEV)
+    B.pa_kv_append_q4(bf16_dev(_rows(rng, blocks * 16, Hkv)), bf16_dev(_rows(rng, blocks * 16, Hkv)), every, kc, vc)
+    start = kc.clone(), vc.clone()
+    per_step = []
+    for _ in range(steps):
+        ids = rng.permutation(blocks).astype(np.int32)
+        tables = np.full((len(seq), max(pages)), -1, np.int32)
+        at, slots = 0, []
+        for r, (L, n, p) in enumerate(zip(seq, qo, pages)):
+            tables[r, :p] = ids[at:at + p]
+            at += p
+            t = np.arange(L - n, L)
+            slots.append(tables[r, t // 16].astype(np.int64) * 16 + t % 16)
+        per_step.append([bf16_dev(W.normal_bf16(rng, (total, 4 * Hkv, 128))), torch.from_numpy(tables).to(DEV),
+                         torch.from_numpy(np.concatenate(slots)).to(DEV), bf16_dev(_rows(rng, total, Hkv)),
+                         bf16_dev(_rows(rng, total, Hkv))])
+    q, tab, slot, k, v = (torch.empty_like(t) for t in per_step[0])
+    lens = torch.tensor(seq, dtype=torch.int32)
+    ind = torch.from_numpy(np.concatenate([[0], np.cumsum(qo)]).astype(np.int32))
+    lens_dev, ind_dev = lens.to(DEV), ind.to(DEV)
+    ws = B.new_workspace(B.pa_attention_workspace_size(len(seq), total, 4 * Hkv, 128, max(seq)), DEV)
+
+    def run(outs, between):
+        for new, (out, lse) in zip(per_step, outs):
+            for dst, src in zip((q, tab, slot, k, v), new):
+                dst.copy_(src)
+            between()
+            B.pa_kv_append_q4(k, v, slot, kc, vc, workspace=ws)
+            between()
+            B.pa_attention_varlen_q4(q, kc, vc, tab, lens_dev, ind_dev, 0.088, seq_lens_host=lens, qo_indptr_host=ind,
+                                     out=out, lse=lse, workspace=ws)
+            between()
+
+    def outputs():
+        return [(torch.zeros_like(q), torch.zeros(total, 4 * Hkv, device=DEV)) for _ in range(steps)]
+
+    def rewind():
+        kc.copy_(start[0])
+        vc.copy_(start[1])
+        torch.cuda.synchronize()
+
+    want, got = outputs(), outputs()
+    run(want, torch.cuda.synchronize)
+    rewind()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(got, lambda: None)
+        rewind()
+        g.replay()
+    else:
+        run(got, lambda: None)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+    for i, ((a, al), (b, bl)) in enumerate(zip(want, got)):
+        assert torch.equal(a, b) and torch.equal(al, bl), i
+    assert not torch.equal(want[0][0], want[1][0])
