@@ -73,7 +73,8 @@ typedef enum {
   PA_ERR_WORKSPACE_TOO_SMALL = 3, /* workspace_bytes below the *_workspace_size() query */
   PA_ERR_CUDA = 4,                /* a CUDA runtime call or launch failed */
   PA_ERR_DEVICE_INDEX = 5,        /* (error word) block id or slot outside the pool */
-  PA_ERR_DEVICE_TIMEOUT = 6       /* (error word) a bounded in-kernel wait gave up */
+  PA_ERR_DEVICE_TIMEOUT = 6,      /* (error word) a bounded in-kernel wait gave up */
+  PA_ERR_DEVICE_NO_BLOCKS = 7     /* (error word) pa_step_tables: the ring of free blocks ran out */
 } pa_status;
 
 #define PA_ABI_VERSION 1
@@ -486,6 +487,208 @@ pa_status pa_attention_varlen_noalloc(const void* q, const void* k_cache, const 
                                       int32_t* device_error, pa_stream_t stream);
 
 /*
+ * pa_step_tables -- a step's block tables, slots, positions and offsets, made on
+ * the device from the requests' lengths ("Inference optimisation", AI-infra book
+ * ch. 8, §8.3.1 and Fig. 8-10: a sequence that grows takes a new block from the
+ * free pool, its table maps logical to physical blocks), so that a decode loop
+ * needs no host between its steps.
+ *   Request r has c = cached_lens[r] tokens in the cache and brings n =
+ *   new_tokens[r] (0: it waits; negative: it has ended).
+ *   qo_indptr       the exclusive sums of n (0 for n < 0), and their total.
+ *   seq_lens[r]     c + n; 0 for a request that has ended.
+ *   Pages ceil(c / 16) .. ceil((c + n) / 16) - 1 of r are granted: their ids are
+ *   taken from the head of the ring of free blocks, in the order of requests and
+ *   pages, and written into block_tables[r].
+ *   Token j of r is row i = qo_indptr[r] + j of the step: positions[i] = c + j,
+ *   slot_mapping[i] = 16 block_tables[r, (c + j) / 16] + (c + j) % 16.  Rows from
+ *   the total to n_tokens are padding: slot -1, position 0.
+ *   Pages given back go to the ring's tail, in the order of requests and pages,
+ *   and are not granted before the next call.  Their table entries stay as they
+ *   are.  Of a request that has ended: all that it holds, except its first
+ *   shared_pages.  With window > 0, of a request with n > 0: pages j >= keep with
+ *   16 (j + 1) <= c - window + 1, which no query of this or a later step of
+ *   pa_attention_varlen_window sees, where keep = max(ceil(sink_tokens / 16),
+ *   shared_pages); first_page_out[r] is then the first page behind keep that it
+ *   still holds (first_page[r] where nothing was given back, 0 for a request
+ *   that has ended).
+ * new_tokens, cached_lens  [num_reqs] int32, device.
+ * first_page      [num_reqs] int32, device, or NULL for zeros: what the call
+ *                 before left in first_page_out (0 for a new request).
+ * block_tables    [num_reqs, max_blocks_per_req] int32, device, modified in place:
+ *                 only the entries of granted pages are written.
+ * free_ring       [num_blocks] int32, device, modified in place: the ids of the
+ *                 pool's free blocks, in a ring.
+ * free_state      [2] int32, device: the ring's head (0 .. num_blocks - 1) and the
+ *                 number of ids in it.
+ * window, sink_tokens, shared_pages  >= 0.  window = 0: nothing is given back
+ *                 but by ended requests (and sink_tokens is ignored).  The first
+ *                 shared_pages pages of every request are never given back (a
+ *                 prefix that others use too).  Other pages must belong to one
+ *                 request each.
+ * n_tokens        rows of slot_mapping and positions.
+ * seq_lens [num_reqs], qo_indptr [num_reqs + 1], positions [n_tokens] int32,
+ * slot_mapping [n_tokens] int64, free_state_out [2], first_page_out [num_reqs]
+ *                 int32 (or NULL when first_page is NULL and window is 0), device.
+ *                 seq_lens may be cached_lens, free_state_out free_state and
+ *                 first_page_out first_page: then a captured launch steps on at
+ *                 every replay.  Otherwise outputs must not overlap anything, and
+ *                 a call repeated on the same inputs gives the same again.
+ * workspace       device, >= PA_ERROR_WORD_BYTES bytes, 256-byte aligned, zero-filled
+ *                 before its first use: the error word, and a count that every call
+ *                 leaves at zero.  Calls sharing it must not run concurrently.
+ * Found on the device and recorded in the error word:
+ *   PA_ERR_DEVICE_INDEX: a row with c outside [0, PA_MAX_SEQ_LEN], or with more
+ *   than PA_MAX_SEQ_LEN tokens or max_blocks_per_req pages after the step, is
+ *   taken as one that waits (with seq_len 0 if c itself is out of these bounds).
+ *   If the new tokens of all rows exceed n_tokens, or free_state is out of its
+ *   range, or more pages would come back than the ring has places for, all rows
+ *   wait, and no page is granted or given back.  An id in the ring outside the
+ *   pool is granted as -1.
+ *   PA_ERR_DEVICE_NO_BLOCKS: the ring has fewer ids than pages are needed: the
+ *   pages it could not grant get the table entry -1, their tokens the slot -1.
+ * Errors: PA_ERR_INVALID_ARG (num_reqs outside [0, 65535], n_tokens < 0,
+ *   num_blocks outside [1, 2^31 - 1], a negative window, sink_tokens or
+ *   shared_pages, max_blocks_per_req < 1, null or misaligned pointers),
+ *   PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA.
+ */
+pa_status pa_step_tables(const int32_t* new_tokens, const int32_t* cached_lens, const int32_t* first_page,
+                         int32_t num_reqs, int32_t* block_tables, int32_t max_blocks_per_req, int32_t* free_ring,
+                         int64_t num_blocks, const int32_t* free_state, int32_t window, int32_t sink_tokens,
+                         int32_t shared_pages, int32_t n_tokens, int32_t* seq_lens, int32_t* qo_indptr,
+                         int64_t* slot_mapping, int32_t* positions, int32_t* free_state_out, int32_t* first_page_out,
+                         void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_rope_turns -- the rotation speeds of pa_qk_norm_rope, computed on the host:
+ * turns[i] = the fraction of a turn that pair i advances per position, inv_freq[i]
+ * / (2 pi) modulo 1, in units of 2^-64.  A position times this, modulo 2^64, is the
+ * pair's angle whatever the position: nothing is lost far into a context, where a
+ * binary32 angle would be off by whole radians.
+ * inv_freq, turns  [n] host arrays.  Errors: PA_ERR_INVALID_ARG (n outside
+ * [0, 64], null pointers, a speed that is not finite).
+ */
+pa_status pa_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/*
+ * pa_qk_norm_rope -- queries and keys of a layer, normalised for each head and
+ * rotated by their positions, in one pass (what a model does between the product
+ * that makes q, k and v and pa_kv_append).
+ *   For token i, head h and x = q[i, h, :] (k likewise):
+ *     y = x / sqrt(mean(x^2) + eps) * weight      (y = x with a NULL weight)
+ *     a, b = y[j], y[j + rotary_dim / 2]           (y[2 j], y[2 j + 1] if interleaved)
+ *     a', b' = a cos t - b sin t, b cos t + a sin t,   j = 0 .. rotary_dim / 2 - 1
+ *   with the angle t = positions[i] * inv_freq[j] (see pa_rope_turns); dims from
+ *   rotary_dim on are not rotated.  Arithmetic is binary32 throughout and each
+ *   result is rounded once to bf16.
+ * q, k           bf16, device, 16-byte aligned: token i's heads are contiguous,
+ *                [num_heads, head_dim] from element i * stride on; strides are in
+ *                elements, multiples of 8, at least num_heads * head_dim (a column
+ *                block of a fused product's rows has the stride of the whole row).
+ * positions      [n_tokens] int32, device (a negative one rotates backwards).
+ * q_weight, k_weight  [head_dim] float32, device, 16-byte aligned, or NULL.
+ * turns          [rotary_dim / 2] uint64, device, 8-byte aligned: pa_rope_turns.
+ * rotary_dim     0 .. head_dim, a multiple of 16 (0: no rotation; turns and
+ *                positions may then be NULL).
+ * interleaved    0 or 1.
+ * q_out, k_out   [n_tokens, num_heads, head_dim] bf16, 16-byte aligned.  q_out may
+ *                be q where q_stride is num_q_heads * head_dim (k_out likewise);
+ *                otherwise outputs must not overlap inputs.
+ * Errors: PA_ERR_INVALID_ARG (n_tokens < 0, strides, rotary_dim, interleaved, eps
+ *   negative or not finite, null or misaligned pointers), PA_ERR_UNSUPPORTED
+ *   (shape, or n_tokens x heads of 2^31 or more), PA_ERR_CUDA.
+ * n_tokens = 0 is valid and launches nothing.
+ */
+pa_status pa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+                          int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
+                          const uint64_t* turns, int32_t rotary_dim, int32_t interleaved, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, void* q_out, void* k_out, pa_stream_t stream);
+
+/*
+ * pa_qk_norm_rope_append -- pa_qk_norm_rope whose keys, and the values v beside
+ * them, go straight to their slots of the HND pools, as pa_kv_append would have
+ * put them there: one pass from the layer's product to the cache.
+ * v              as k, with a stride of its own; copied exactly.
+ * slot_mapping   [n_tokens] int64, device; negative: nothing is written to the
+ *                pools (the token's q_out row is).  Slots must be distinct.
+ * k_cache, v_cache  HND pools, 16-byte aligned, modified in place.
+ * workspace      device, >= PA_ERROR_WORD_BYTES bytes; only the error word is
+ *                used.  A slot >= num_blocks * 16 is skipped and recorded as
+ *                PA_ERR_DEVICE_INDEX.
+ * Errors: as pa_qk_norm_rope and pa_kv_append.
+ */
+pa_status pa_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                                 int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
+                                 const uint64_t* turns, int32_t rotary_dim, int32_t interleaved, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size, void* q_out, void* k_cache,
+                                 void* v_cache, int64_t num_blocks, void* workspace, size_t workspace_bytes,
+                                 pa_stream_t stream);
+
+/*
+ * pa_window_workspace_size -- bytes of device workspace that
+ * pa_attention_varlen_window and pa_decode_window need for a batch with at most
+ * these sizes (0 for negative arguments).
+ */
+size_t pa_window_workspace_size(int32_t num_reqs, int32_t total_q, int32_t num_q_heads, int32_t head_dim,
+                                int32_t window, int32_t sink_tokens);
+
+/*
+ * pa_attention_varlen_window -- pa_attention_varlen with a sliding window and
+ * first tokens that stay visible: the query at position p sees the keys
+ *     t <= p  with  t < sink_tokens  or  t > p - window
+ *   (its own and the window - 1 before it, and the first sink_tokens), the rest of
+ *   the definition, the arguments and the errors are pa_attention_varlen's, over
+ *   bf16 pools.  A window of seq_len or more is pa_attention_varlen.
+ *   Table entries of pages that hold no key which a query of the row's request
+ *   sees are never read: with pa_step_tables they are given back.  Keys and
+ *   values that no query of the request sees (slots behind its last token, tokens
+ *   behind its window) may hold anything, infinities and NaN included.  Infinities
+ *   and NaN in values that one query of a request sees may reach other queries
+ *   of the same request.
+ *   Weights are rounded to bf16 before they meet V in rows of more than two
+ *   queries; in rows of one or two they carry 16 bits.  A (query, head) with a NaN
+ *   among its scores has NaN in its out row and its lse, and changes no other.
+ * window         >= 1.
+ * sink_tokens    >= 0.
+ * workspace      >= pa_window_workspace_size(num_reqs, total_q, num_q_heads,
+ *                head_dim, window, sink_tokens) bytes, 256-byte aligned, zero-filled
+ *                before its first use, left reusable by every call; as
+ *                pa_attention_varlen otherwise.
+ * Errors: as pa_attention_varlen; PA_ERR_INVALID_ARG for window < 1 or
+ *   sink_tokens < 0.
+ */
+pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                                     const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                                     const int32_t* qo_indptr, const int32_t* seq_lens_host,
+                                     const int32_t* qo_indptr_host, int32_t num_reqs, int32_t total_q,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     float sm_scale, int32_t window, int32_t sink_tokens, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_decode_window -- pa_attention_varlen_window for a padded decode-only batch,
+ * planned on the device ("Inference optimisation", AI-infra book ch. 8, §8.2.4:
+ * graphs captured for a few padded shapes): the launch depends on the scalars
+ * alone, so that one captured in a CUDA graph serves every batch within them, and
+ * with pa_step_tables and pa_qk_norm_rope_append before it a decode layer runs
+ * without the host.
+ *   Row r is one request with query q[r], whose seq_lens[r] keys (its own token
+ *   among them) are in the cache.  seq_lens[r] = 0: padding; its out row is zero
+ *   and its lse -inf.  A row with seq_lens[r] outside [0, PA_MAX_SEQ_LEN] or more
+ *   than max_blocks_per_req pages is taken as padding and recorded as
+ *   PA_ERR_DEVICE_INDEX.
+ * q, out         [num_reqs, num_q_heads, head_dim] bf16; lse [num_reqs,
+ *                num_q_heads] float32 or NULL.
+ * workspace      >= pa_window_workspace_size(num_reqs, num_reqs, ...).
+ * Errors: as pa_attention_varlen_window; PA_ERR_UNSUPPORTED for num_reqs > 65535.
+ */
+pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                           const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                           int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, float sm_scale, int32_t window, int32_t sink_tokens, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * pa_merge_lse -- combine two partial attentions of the same queries over
  * disjoint key sets A and B.  The pages do not define this operation; it is
  * part of this library's interface so that a caller can split one request's
@@ -556,7 +759,9 @@ typedef enum {
   PA_KERNEL_PREFIX_MERGE = 7, /* merge of that pass's key-chunk partials */
   PA_KERNEL_COPY_BLOCKS = 8,  /* pa_copy_blocks */
   PA_KERNEL_DECODE_STEP = 9,  /* pa_decode_step */
-  PA_KERNEL_KV_READ = 10      /* pa_kv_read_q4 */
+  PA_KERNEL_KV_READ = 10,     /* pa_kv_read_q4 */
+  PA_KERNEL_STEP_TABLES = 11, /* pa_step_tables */
+  PA_KERNEL_NORM_ROPE = 12    /* pa_qk_norm_rope, pa_qk_norm_rope_append */
 } pa_kernel_kind;
 
 pa_status pa_set_decode_ctas(int32_t n);

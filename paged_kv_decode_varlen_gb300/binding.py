@@ -27,9 +27,10 @@ PA_ERR_WORKSPACE_TOO_SMALL = 3
 PA_ERR_CUDA = 4
 PA_ERR_DEVICE_INDEX = 5
 PA_ERR_DEVICE_TIMEOUT = 6
+PA_ERR_DEVICE_NO_BLOCKS = 7
 PA_ERROR_WORD_BYTES = 256
 KERNEL_KINDS = {1: "kv_append", 2: "decode", 3: "combine", 4: "prefill", 5: "merge", 6: "prefix", 7: "prefix_merge", 8: "copy_blocks",
-                9: "decode_step", 10: "kv_read"}
+                9: "decode_step", 10: "kv_read", 11: "step_tables", 12: "norm_rope"}
 
 
 class PAError(RuntimeError):
@@ -70,6 +71,17 @@ _SIGS = {
                                                  _i32, _i32, _i32, _f32, _P, _P, _P, _sz, _P]),
     "pa_attention_varlen_noalloc": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32,
                                            _i32, _f32, _P, _P, _P, _P]),
+    "pa_step_tables": (_i32, [_P, _P, _P, _i32, _P, _i32, _P, _i64, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _P, _P, _P, _P,
+                              _sz, _P]),
+    "pa_rope_turns": (_i32, [_P, _i32, _P]),
+    "pa_qk_norm_rope": (_i32, [_P, _i64, _P, _i64, _P, _i64, _P, _P, _f32, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _P]),
+    "pa_qk_norm_rope_append": (_i32, [_P, _i64, _P, _i64, _P, _i64, _P, _P, _i64, _P, _P, _f32, _P, _i32, _i32, _i32, _i32,
+                                      _i32, _i32, _P, _P, _P, _i64, _P, _sz, _P]),
+    "pa_window_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_attention_varlen_window": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
+                                          _f32, _i32, _i32, _P, _P, _P, _sz, _P]),
+    "pa_decode_window": (_i32, [_P, _P, _P, _i64, _P, _i32, _P, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _P, _P, _P,
+                                _sz, _P]),
     "pa_merge_lse": (_i32, [_P, _P, _P, _P, _P, _P, _i64, _i32, _i32, _P]),
     "pa_get_device_error": (_i32, [_P, ctypes.POINTER(_i32)]),
     "pa_clear_device_error": (_i32, [_P, _P]),
@@ -590,6 +602,245 @@ def pa_attention_varlen_noalloc(q, k_cache, v_cache, block_tables, seq_lens, qo_
                                             total_q, Hq, Hkv, D, P, float(sm_scale), _ptr(out), _ptr(lse),
                                             _ptr(device_error), _stream(stream)))
     return (out, lse) if (return_lse or lse is not None) else out
+
+
+def pa_step_tables(new_tokens, cached_lens, block_tables, free_ring, free_state, *, n_tokens=None, window=0, sink_tokens=0,
+                   shared_pages=0, first_page=None, seq_lens=None, qo_indptr=None, slot_mapping=None, positions=None,
+                   free_state_out=None, first_page_out=None, workspace=None, stream=None):
+    """A step's tables on the device from the requests' lengths (see
+    include/pa.h).  new_tokens, cached_lens int32 [R]; block_tables int32 [R,
+    max_blocks] and free_ring int32 [num_blocks] are updated in place; free_state
+    int32 [2].  n_tokens: rows of slot_mapping and positions (needed where
+    neither is given).  Outputs that are not given are made.  Returns (seq_lens,
+    qo_indptr, slot_mapping, positions, free_state_out, first_page_out)."""
+    R, = new_tokens.shape
+    table = block_tables.shape
+    if n_tokens is None:
+        if slot_mapping is None and positions is None:
+            raise ValueError("n_tokens is needed without slot_mapping or positions")
+        n_tokens = (positions if slot_mapping is None else slot_mapping).shape[0]
+    dev = _current_device()
+    if seq_lens is None or qo_indptr is None or slot_mapping is None or positions is None or free_state_out is None \
+            or first_page_out is None or workspace is None:
+        with _on(stream):
+            def made(t, n, dtype):
+                return torch.empty(n, dtype=dtype, device=new_tokens.device) if t is None else t
+            seq_lens, qo_indptr = made(seq_lens, R, _I32), made(qo_indptr, R + 1, _I32)
+            slot_mapping, positions = made(slot_mapping, n_tokens, _I64), made(positions, n_tokens, _I32)
+            free_state_out, first_page_out = made(free_state_out, 2, _I32), made(first_page_out, R, _I32)
+            if workspace is None:
+                workspace = new_workspace(PA_ERROR_WORD_BYTES, new_tokens.device)
+    if cached_lens.shape != (R,) or len(table) != 2 or table[0] != R or free_ring.dim() != 1 or free_state.shape != (2,) \
+            or seq_lens.shape != (R,) or qo_indptr.shape != (R + 1,) or slot_mapping.shape != (n_tokens,) \
+            or positions.shape != (n_tokens,) or free_state_out.shape != (2,) or first_page_out.shape != (R,) \
+            or (first_page is not None and first_page.shape != (R,)):
+        raise ValueError("inconsistent shapes")
+    i32 = [(new_tokens, "new_tokens"), (cached_lens, "cached_lens"), (block_tables, "block_tables"),
+           (free_ring, "free_ring"), (free_state, "free_state"), (seq_lens, "seq_lens"), (qo_indptr, "qo_indptr"),
+           (positions, "positions"), (free_state_out, "free_state_out"), (first_page_out, "first_page_out")]
+    if first_page is not None:
+        i32.append((first_page, "first_page"))
+    for t, name in i32:
+        _data(t, _I32, name, dev)
+    _refuse(dev, (slot_mapping, _I64, "slot_mapping"), (workspace, _U8, "workspace"))
+    status = _lib.pa_step_tables(new_tokens.data_ptr(), cached_lens.data_ptr(),
+                                 None if first_page is None else first_page.data_ptr(), R, block_tables.data_ptr(),
+                                 table[1], free_ring.data_ptr(), free_ring.shape[0], free_state.data_ptr(), int(window),
+                                 int(sink_tokens), int(shared_pages), n_tokens, seq_lens.data_ptr(), qo_indptr.data_ptr(),
+                                 slot_mapping.data_ptr(), positions.data_ptr(), free_state_out.data_ptr(),
+                                 first_page_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 _stream_handle(stream, dev))
+    if status:
+        _check(status)
+    return seq_lens, qo_indptr, slot_mapping, positions, free_state_out, first_page_out
+
+
+def pa_rope_turns(inv_freq) -> torch.Tensor:
+    """The rotation speeds inv_freq (radians per position, a host tensor or
+    sequence of up to 64) as pa_qk_norm_rope takes them: an int64 tensor on the host whose
+    bits are the unsigned fractions of a turn (see include/pa.h)."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    turns = torch.empty(f.shape[0], dtype=_I64)
+    _check(_lib.pa_rope_turns(f.data_ptr(), f.shape[0], turns.data_ptr()))
+    return turns
+
+
+def _heads(t, name, device):
+    """(address, token stride) of bf16 [N, H, 128], a token's heads side by side."""
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    s = t.stride()
+    if t.numel() and (s[2] != 1 or (t.shape[1] > 1 and s[1] != t.shape[2])):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    return t.data_ptr(), s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, device):
+    """The checks that the two calls of norms and rotations share; q_out is
+    made where it is not given."""
+    N, Hq, D = q.shape
+    if k.dim() != 3 or k.shape[0] != N or k.shape[2] != D or positions.shape != (N,) or turns.dim() != 1:
+        raise ValueError("inconsistent shapes")
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    _refuse(device, (positions, _I32, "positions"), (turns, _I64, "turns"), (q_out, _BF16, "q_out"))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if w.shape != (D,):
+                raise ValueError(f"{name} must be [head_dim]")
+            _data(w, _F32, name, device)
+    return q_out
+
+
+def pa_qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                    k_out=None, stream=None):
+    """q [N, Hq, 128] and k [N, Hkv, 128] bf16, normalised for each head (with
+    a weight) and rotated by positions int32 [N] at the speeds turns (pa_rope_turns,
+    on the device; 2 * len dims are rotated).  q and k may be columns of wider
+    rows.  Returns (q_out, k_out), contiguous bf16 (see include/pa.h)."""
+    dev = _current_device()
+    q_out = _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, dev)
+    if k_out is None:
+        with _on(stream):
+            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device)
+    elif k_out.shape != k.shape:
+        raise ValueError("k_out must have k's shape")
+    N, Hq, D = q.shape
+    (qp, qs), (kp, ks) = _heads(q, "q", dev), _heads(k, "k", dev)
+    status = _lib.pa_qk_norm_rope(qp, qs, kp, ks, positions.data_ptr(), N,
+                                  None if q_weight is None else q_weight.data_ptr(),
+                                  None if k_weight is None else k_weight.data_ptr(), float(eps), turns.data_ptr(),
+                                  2 * turns.shape[0], int(interleaved), Hq, k.shape[1], D, q_out.data_ptr(),
+                                  _data(k_out, _BF16, "k_out", dev), _stream_handle(stream, dev))
+    if status:
+        _check(status)
+    return q_out, k_out
+
+
+def pa_qk_norm_rope_append(q, k, v, positions, slot_mapping, turns, k_cache, v_cache, *, q_weight=None, k_weight=None,
+                           eps=1e-6, interleaved=False, q_out=None, workspace=None, stream=None):
+    """pa_qk_norm_rope whose keys, and the values v [N, Hkv, 128], go to
+    slot_mapping (int64 [N], negative = skip) of the HND pools.  Returns q_out
+    (see include/pa.h)."""
+    dev = _current_device()
+    q_out = _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, dev)
+    N, Hq, D = q.shape
+    nb, Hkv, P, D2 = pool = k_cache.shape
+    if v.shape != k.shape or v_cache.shape != pool or k.shape[1] != Hkv or D2 != D or slot_mapping.shape != (N,):
+        raise ValueError("inconsistent shapes")
+    if workspace is None:
+        with _on(stream):
+            workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
+    _refuse(dev, (slot_mapping, _I64, "slot_mapping"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
+            (workspace, _U8, "workspace"))
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
+    status = _lib.pa_qk_norm_rope_append(qp, qs, kp, ks, vp, vs, positions.data_ptr(), slot_mapping.data_ptr(), N,
+                                         None if q_weight is None else q_weight.data_ptr(),
+                                         None if k_weight is None else k_weight.data_ptr(), float(eps),
+                                         turns.data_ptr(), 2 * turns.shape[0], int(interleaved), Hq, Hkv, D, P,
+                                         q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb,
+                                         workspace.data_ptr(), workspace.numel(), _stream_handle(stream, dev))
+    if status:
+        _check(status)
+    return q_out
+
+
+def pa_window_workspace_size(num_reqs, total_q, num_q_heads, head_dim, window, sink_tokens) -> int:
+    return int(_lib.pa_window_workspace_size(num_reqs, total_q, num_q_heads, head_dim, window, sink_tokens))
+
+
+def pa_attention_varlen_window(q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, sm_scale, window, sink_tokens=0, *,
+                               seq_lens_host=None, qo_indptr_host=None, out=None, lse=None, workspace=None, stream=None,
+                               return_lse=False):
+    """pa_attention_varlen where a query sees its own key, the window - 1 before
+    it and the first sink_tokens (see include/pa.h)."""
+    shape, pool, table = q.shape, k_cache.shape, block_tables.shape
+    total_q, Hq, D = shape
+    nb, Hkv, P, D2 = pool
+    R = seq_lens.shape[0]
+    if v_cache.shape != pool or D2 != D or qo_indptr.shape != (R + 1,) or len(table) != 2 or table[0] != R:
+        raise ValueError("inconsistent shapes")
+    slh, slh_at = _host_data(seq_lens if seq_lens_host is None else seq_lens_host, R, "seq_lens_host", stream)
+    qih, qih_at = _host_data(qo_indptr if qo_indptr_host is None else qo_indptr_host, R + 1, "qo_indptr_host", stream)
+    dev = _current_device()
+    out, lse, workspace = _window_outputs(q, block_tables, out, lse, workspace, return_lse, R, window, sink_tokens, stream)
+    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is _BF16 and workspace.dtype is _U8
+            and block_tables.dtype is seq_lens.dtype is qo_indptr.dtype is _I32
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous() and qo_indptr.is_contiguous()
+            and out.is_contiguous() and workspace.is_contiguous()
+            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == seq_lens.get_device() == qo_indptr.get_device() == out.get_device() == workspace.get_device()):
+        _refuse(dev, (q, _BF16, "q"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
+                (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"), (qo_indptr, _I32, "qo_indptr"),
+                (out, _BF16, "out"), (workspace, _U8, "workspace"))
+    status = _lib.pa_attention_varlen_window(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(), table[1], seq_lens.data_ptr(),
+        qo_indptr.data_ptr(), slh_at, qih_at, R, total_q, Hq, Hkv, D, P, float(sm_scale), int(window), int(sink_tokens),
+        out.data_ptr(), None if lse is None else _data(lse, _F32, "lse", dev), workspace.data_ptr(), workspace.numel(),
+        _stream_handle(stream, dev))
+    if status:
+        _check(status)
+    return (out, lse) if lse is not None else out
+
+
+def _window_outputs(q, block_tables, out, lse, workspace, return_lse, R, window, sink_tokens, stream):
+    """out, lse (or None) and workspace of the calls with a window, made where
+    they are not given."""
+    total_q, Hq, D = q.shape
+    if out is None or workspace is None or (lse is None and return_lse):
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None and return_lse:
+                lse = torch.empty((total_q, Hq), dtype=_F32, device=q.device)
+            if workspace is None:
+                workspace = new_workspace(pa_window_workspace_size(R, total_q, Hq, D, window, sink_tokens), q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != (total_q, Hq):
+        raise ValueError("lse must be [total_q, Hq]")
+    return out, lse, workspace
+
+
+def pa_decode_window(q, k_cache, v_cache, block_tables, seq_lens, sm_scale, window, sink_tokens=0, *, out=None, lse=None,
+                     workspace=None, stream=None, return_lse=False):
+    """pa_attention_varlen_window of a padded decode-only batch, planned on the
+    device: q [R, Hq, 128], one query per row, seq_lens int32 [R] on the device (0 =
+    padding).  Nothing is read back to the host, so the call can be captured in a
+    CUDA graph (see include/pa.h)."""
+    pool, table = k_cache.shape, block_tables.shape
+    R, Hq, D = q.shape
+    nb, Hkv, P, D2 = pool
+    if v_cache.shape != pool or D2 != D or seq_lens.shape != (R,) or len(table) != 2 or table[0] != R:
+        raise ValueError("inconsistent shapes")
+    dev = _current_device()
+    out, lse, workspace = _window_outputs(q, block_tables, out, lse, workspace, return_lse, R, window, sink_tokens, stream)
+    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is _BF16 and workspace.dtype is _U8
+            and block_tables.dtype is seq_lens.dtype is _I32
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous() and out.is_contiguous()
+            and workspace.is_contiguous()
+            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == seq_lens.get_device() == out.get_device() == workspace.get_device()):
+        _refuse(dev, (q, _BF16, "q"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
+                (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"), (out, _BF16, "out"),
+                (workspace, _U8, "workspace"))
+    status = _lib.pa_decode_window(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(), table[1], seq_lens.data_ptr(), R,
+        Hq, Hkv, D, P, float(sm_scale), int(window), int(sink_tokens), out.data_ptr(),
+        None if lse is None else _data(lse, _F32, "lse", dev), workspace.data_ptr(), workspace.numel(),
+        _stream_handle(stream, dev))
+    if status:
+        _check(status)
+    return (out, lse) if lse is not None else out
 
 
 def pa_merge_lse(o_a, lse_a, o_b, lse_b, o_out=None, lse_out=None, stream=None):

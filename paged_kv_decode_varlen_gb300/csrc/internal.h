@@ -277,6 +277,77 @@ struct PrefixParams {
   int* err;
 };
 
+// A step's tables from the requests' lengths (pa_step_tables).
+struct TablesParams {
+  const int32_t* new_tokens;
+  const int32_t* cached_lens;
+  const int32_t* first_page;  // or null: zeros
+  int32_t num_reqs;
+  int32_t* block_tables;
+  int32_t max_blocks_per_req;
+  int32_t* free_ring;
+  int32_t num_blocks;
+  const int32_t* free_state;  // head, count
+  int32_t window, sink_tokens, shared_pages;
+  int32_t n_tokens;
+  int32_t* seq_lens;
+  int32_t* qo_indptr;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int32_t* free_state_out;
+  int32_t* first_page_out;  // or null
+  int* err;
+  int* arrived;  // CTAs of the launch that are done; zero between calls
+};
+
+// Norms and rotations of queries and keys; with pools the keys and the values go
+// to their slots, else the keys to k_out.
+struct RopeParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;  // append only
+  int64_t q_stride, k_stride, v_stride;  // elements from a token to the next
+  const int32_t* positions;
+  const int64_t* slot_mapping;  // append only
+  int64_t n_tokens;
+  const float* q_weight;  // or null: no norm
+  const float* k_weight;
+  float eps;
+  const uint64_t* turns;
+  int32_t rotary_dim;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  uint16_t* q_out;
+  uint16_t* k_out;    // no append
+  uint16_t* k_cache;  // append
+  uint16_t* v_cache;
+  int64_t num_blocks;
+  int* err;
+};
+
+// Attention with a window: a query at position p sees keys t <= p with t <
+// sink_tokens or t > p - window.
+struct WindowParams {
+  const uint16_t* q;
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  int64_t num_blocks;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_req;
+  const int32_t* seq_lens;
+  const int32_t* qo_indptr;  // or null: row r has the one query r
+  int32_t num_reqs;
+  int32_t total_q;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  float scale_log2;
+  int32_t window;
+  int32_t sink_tokens;
+  uint16_t* out;
+  float* lse;
+  int* err;
+};
+
 struct MergeParams {
   const uint16_t* o_a;
   const float* lse_a;
@@ -344,6 +415,9 @@ cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, co
 cudaError_t launch_prefix(const PrefixParams& p, int n_chunks, const TcMaps& maps, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixParams& p, int n_chunks, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
+cudaError_t launch_step_tables(const TablesParams& p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved, cudaStream_t stream);
+cudaError_t launch_window(const WindowParams& p, cudaStream_t stream);
 
 // Query tile of the tensor-core tile kernels (query tokens per CTA: with the
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.

@@ -1082,6 +1082,7 @@ const char* pa_status_string(int32_t s) {
     case PA_ERR_CUDA: return "PA_ERR_CUDA";
     case PA_ERR_DEVICE_INDEX: return "PA_ERR_DEVICE_INDEX";
     case PA_ERR_DEVICE_TIMEOUT: return "PA_ERR_DEVICE_TIMEOUT";
+    case PA_ERR_DEVICE_NO_BLOCKS: return "PA_ERR_DEVICE_NO_BLOCKS";
     default: return "PA_ERR_UNKNOWN";
   }
 }
@@ -1215,7 +1216,280 @@ pa_status append(const void* k_new, const void* v_new, const int64_t* slot_mappi
 
 }  // namespace
 
+namespace {
+
+// What the two entry points of norms and rotations check and launch.
+pa_status norm_rope(pa::RopeParams& p, bool append, int32_t interleaved, int32_t head_dim, int32_t block_size,
+                    cudaStream_t stream) {
+  if (p.n_tokens < 0) return fail(PA_ERR_INVALID_ARG, "n_tokens %lld < 0", (long long)p.n_tokens);
+  pa_status s = check_shape(p.num_q_heads, p.num_kv_heads, head_dim, block_size);
+  if (s != PA_OK) return s;
+  if (p.rotary_dim < 0 || p.rotary_dim > head_dim || p.rotary_dim % 16 != 0)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d: must be a multiple of 16 in [0, %d]", p.rotary_dim, head_dim);
+  if (interleaved != 0 && interleaved != 1) return fail(PA_ERR_INVALID_ARG, "interleaved %d (0 or 1)", interleaved);
+  if (!(p.eps >= 0.f && p.eps < INFINITY)) return fail(PA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  const int64_t qw = (int64_t)p.num_q_heads * head_dim, kw = (int64_t)p.num_kv_heads * head_dim;
+  if (p.q_stride < qw || p.k_stride < kw || p.q_stride % 8 != 0 || p.k_stride % 8 != 0 ||
+      (append && (p.v_stride < kw || p.v_stride % 8 != 0)))
+    return fail(PA_ERR_INVALID_ARG, "strides must be multiples of 8 and cover a token's heads");
+  if (p.n_tokens > INT32_MAX / (p.num_q_heads + 2 * p.num_kv_heads))
+    return fail(PA_ERR_UNSUPPORTED, "%lld tokens: more than 2^31 head rows", (long long)p.n_tokens);
+  if (p.n_tokens > 0 && (!p.q || !p.k || !p.q_out || (p.rotary_dim > 0 && (!p.positions || !p.turns)) ||
+                         (append ? !p.v || !p.slot_mapping : !p.k_out)))
+    return fail(PA_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.q_out, 16) || !aligned(p.k_out, 16) ||
+      !aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.q_weight, 16) || !aligned(p.k_weight, 16) ||
+      !aligned(p.turns, 8) || !aligned(p.slot_mapping, 8) || !aligned(p.positions, 4))
+    return fail(PA_ERR_INVALID_ARG, "tensors must be 16-byte aligned (turns and slot_mapping 8, positions 4)");
+  if (p.n_tokens == 0) return ok();
+  s = run_launch(PA_KERNEL_NORM_ROPE, "norm_rope", stream,
+                 [&] { return pa::launch_norm_rope(p, append, interleaved != 0, stream); });
+  return s == PA_OK ? ok() : s;
+}
+
+// Workspace of the attention with a window: the error word.
+size_t window_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return PA_ERROR_WORD_BYTES; }
+
+pa_status check_window(int32_t num_reqs, int64_t num_blocks, float sm_scale, int32_t window, int32_t sink_tokens) {
+  if (num_reqs < 0 || num_reqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_reqs %d outside [0, 65535]", num_reqs);
+  if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks must be positive");
+  if (!(fabsf(sm_scale) < INFINITY)) return fail(PA_ERR_INVALID_ARG, "sm_scale must be finite");
+  if (window < 1) return fail(PA_ERR_INVALID_ARG, "window %d < 1", window);
+  if (sink_tokens < 0) return fail(PA_ERR_INVALID_ARG, "sink_tokens %d < 0", sink_tokens);
+  return PA_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+pa_status pa_step_tables(const int32_t* new_tokens, const int32_t* cached_lens, const int32_t* first_page,
+                         int32_t num_reqs, int32_t* block_tables, int32_t max_blocks_per_req, int32_t* free_ring,
+                         int64_t num_blocks, const int32_t* free_state, int32_t window, int32_t sink_tokens,
+                         int32_t shared_pages, int32_t n_tokens, int32_t* seq_lens, int32_t* qo_indptr,
+                         int64_t* slot_mapping, int32_t* positions, int32_t* free_state_out, int32_t* first_page_out,
+                         void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (num_reqs < 0 || num_reqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_reqs %d outside [0, 65535]", num_reqs);
+  if (n_tokens < 0) return fail(PA_ERR_INVALID_ARG, "n_tokens %d < 0", n_tokens);
+  if (num_blocks < 1 || num_blocks > INT32_MAX)
+    return fail(PA_ERR_INVALID_ARG, "num_blocks %lld outside [1, 2^31 - 1]", (long long)num_blocks);
+  if (window < 0 || sink_tokens < 0 || shared_pages < 0)
+    return fail(PA_ERR_INVALID_ARG, "window, sink_tokens and shared_pages must not be negative");
+  if (max_blocks_per_req < 1) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_req must be positive");
+  if (!free_ring || !free_state || !free_state_out || !qo_indptr || !workspace ||
+      (num_reqs > 0 && (!new_tokens || !cached_lens || !block_tables || !seq_lens)) ||
+      (n_tokens > 0 && (!slot_mapping || !positions)) || ((first_page || window > 0) && num_reqs > 0 && !first_page_out))
+    return fail(PA_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned(new_tokens, 4) || !aligned(cached_lens, 4) || !aligned(first_page, 4) || !aligned(block_tables, 4) ||
+      !aligned(free_ring, 4) || !aligned(free_state, 4) || !aligned(seq_lens, 4) || !aligned(qo_indptr, 4) ||
+      !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(free_state_out, 4) || !aligned(first_page_out, 4) ||
+      !aligned(workspace, 256))
+    return fail(PA_ERR_INVALID_ARG, "arrays must be aligned to their elements, workspace to 256 bytes");
+  if (workspace_bytes < PA_ERROR_WORD_BYTES)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %d bytes", workspace_bytes, PA_ERROR_WORD_BYTES);
+  pa::TablesParams p;
+  p.new_tokens = new_tokens;
+  p.cached_lens = cached_lens;
+  p.first_page = first_page;
+  p.num_reqs = num_reqs;
+  p.block_tables = block_tables;
+  p.max_blocks_per_req = max_blocks_per_req;
+  p.free_ring = free_ring;
+  p.num_blocks = (int32_t)num_blocks;
+  p.free_state = free_state;
+  p.window = window;
+  p.sink_tokens = sink_tokens;
+  p.shared_pages = shared_pages;
+  p.n_tokens = n_tokens;
+  p.seq_lens = seq_lens;
+  p.qo_indptr = qo_indptr;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.free_state_out = free_state_out;
+  p.first_page_out = first_page_out;
+  p.err = static_cast<int*>(workspace);
+  p.arrived = static_cast<int*>(workspace) + PA_ERROR_WORD_BYTES / 8;  // in the error word's block, away from it
+  const pa_status s =
+      run_launch(PA_KERNEL_STEP_TABLES, "step_tables", stream, [&] { return pa::launch_step_tables(p, stream); });
+  return s == PA_OK ? ok() : s;
+}
+
+pa_status pa_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
+  if (n < 0 || n > PA_HEAD_DIM / 2) return fail(PA_ERR_INVALID_ARG, "n %d outside [0, %d]", n, PA_HEAD_DIM / 2);
+  if (n > 0 && (!inv_freq || !turns)) return fail(PA_ERR_INVALID_ARG, "null host pointer");
+  for (int32_t i = 0; i < n; ++i) {
+    if (!std::isfinite(inv_freq[i])) return fail(PA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+    const double t = inv_freq[i] / 6.283185307179586476925286766559;
+    const double units = std::ldexp(t - std::floor(t), 64);
+    turns[i] = units < 18446744073709551616.0 ? (uint64_t)units : 0;  // (a fraction rounded up to a whole turn)
+  }
+  return ok();
+}
+
+pa_status pa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+                          int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
+                          const uint64_t* turns, int32_t rotary_dim, int32_t interleaved, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, void* q_out, void* k_out, pa_stream_t stream) {
+  pa::RopeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.positions = positions;
+  p.n_tokens = n_tokens;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.turns = turns;
+  p.rotary_dim = rotary_dim;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  return norm_rope(p, false, interleaved, head_dim, PA_BLOCK_SIZE, stream);
+}
+
+pa_status pa_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                                 int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
+                                 const uint64_t* turns, int32_t rotary_dim, int32_t interleaved, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size, void* q_out, void* k_cache,
+                                 void* v_cache, int64_t num_blocks, void* workspace, size_t workspace_bytes,
+                                 pa_stream_t stream) {
+  if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks must be positive");
+  if (!k_cache || !v_cache || !workspace) return fail(PA_ERR_INVALID_ARG, "null cache or workspace pointer");
+  if (!aligned(workspace, 4)) return fail(PA_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+  if (workspace_bytes < PA_ERROR_WORD_BYTES)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %d bytes", workspace_bytes, PA_ERROR_WORD_BYTES);
+  pa::RopeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.n_tokens = n_tokens;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.turns = turns;
+  p.rotary_dim = rotary_dim;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_cache = static_cast<uint16_t*>(k_cache);
+  p.v_cache = static_cast<uint16_t*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.err = static_cast<int*>(workspace);
+  return norm_rope(p, true, interleaved, head_dim, block_size, stream);
+}
+
+size_t pa_window_workspace_size(int32_t num_reqs, int32_t total_q, int32_t num_q_heads, int32_t head_dim,
+                                int32_t window, int32_t sink_tokens) {
+  if (num_reqs < 0 || total_q < 0 || num_q_heads < 0 || head_dim < 0 || window < 0 || sink_tokens < 0) return 0;
+  return window_workspace(num_reqs, total_q, num_q_heads, window, sink_tokens);
+}
+
+pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                                     const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                                     const int32_t* qo_indptr, const int32_t* seq_lens_host,
+                                     const int32_t* qo_indptr_host, int32_t num_reqs, int32_t total_q,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     float sm_scale, int32_t window, int32_t sink_tokens, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status s = check_shape(num_q_heads, num_kv_heads, head_dim, block_size);
+  if (s == PA_OK) s = check_window(num_reqs, num_blocks, sm_scale, window, sink_tokens);
+  if (s != PA_OK) return s;
+  if (total_q < 0) return fail(PA_ERR_INVALID_ARG, "total_q %d < 0", total_q);
+  if (!seq_lens_host || !qo_indptr_host) return fail(PA_ERR_INVALID_ARG, "host metadata pointers are required");
+  if (!k_cache || !v_cache || !workspace || !seq_lens || !qo_indptr || (num_reqs > 0 && !block_tables) ||
+      (total_q > 0 && (!q || !out)))
+    return fail(PA_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(qo_indptr, 4))
+    return fail(PA_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned, workspace 256-byte aligned");
+  if (qo_indptr_host[0] != 0) return fail(PA_ERR_INVALID_ARG, "qo_indptr[0] = %d, must be 0", qo_indptr_host[0]);
+  if (qo_indptr_host[num_reqs] != total_q)
+    return fail(PA_ERR_INVALID_ARG, "qo_indptr[num_reqs] = %d != total_q = %d", qo_indptr_host[num_reqs], total_q);
+  for (int32_t r = 0; r < num_reqs; ++r) {
+    const int32_t n = qo_indptr_host[r + 1] - qo_indptr_host[r], L = seq_lens_host[r];
+    if (n < 0) return fail(PA_ERR_INVALID_ARG, "qo_indptr decreases at request %d", r);
+    if (L < 0 || L > PA_MAX_SEQ_LEN)
+      return fail(L < 0 ? PA_ERR_INVALID_ARG : PA_ERR_UNSUPPORTED, "seq_lens[%d] = %d outside [0, %d]", r, L,
+                  PA_MAX_SEQ_LEN);
+    if (n > L) return fail(PA_ERR_INVALID_ARG, "request %d: qo_len %d > seq_len %d", r, n, L);
+    if (pages_of(L) > max_blocks_per_req)
+      return fail(PA_ERR_INVALID_ARG, "request %d: %d pages > max_blocks_per_req %d", r, pages_of(L), max_blocks_per_req);
+  }
+  const size_t need = window_workspace(num_reqs, total_q, num_q_heads, window, sink_tokens);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (total_q == 0) return ok();
+  pa::WindowParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_cache = static_cast<const uint16_t*>(k_cache);
+  p.v_cache = static_cast<const uint16_t*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.block_tables = block_tables;
+  p.max_blocks_per_req = max_blocks_per_req;
+  p.seq_lens = seq_lens;
+  p.qo_indptr = qo_indptr;
+  p.num_reqs = num_reqs;
+  p.total_q = total_q;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.scale_log2 = sm_scale * pa::kLog2e;
+  p.window = window;
+  p.sink_tokens = sink_tokens;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = static_cast<int*>(workspace);
+  s = run_launch(PA_KERNEL_DECODE, "window", stream, [&] { return pa::launch_window(p, stream); });
+  return s == PA_OK ? ok() : s;
+}
+
+pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
+                           const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,
+                           int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, float sm_scale, int32_t window, int32_t sink_tokens, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status s = check_shape(num_q_heads, num_kv_heads, head_dim, block_size);
+  if (s == PA_OK) s = check_window(num_reqs, num_blocks, sm_scale, window, sink_tokens);
+  if (s != PA_OK) return s;
+  if (max_blocks_per_req < 1) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_req must be positive");
+  if (!k_cache || !v_cache || !workspace || (num_reqs > 0 && (!q || !out || !block_tables || !seq_lens)))
+    return fail(PA_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned, workspace 256-byte aligned");
+  const size_t need = window_workspace(num_reqs, num_reqs, num_q_heads, window, sink_tokens);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (num_reqs == 0) return ok();
+  pa::WindowParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_cache = static_cast<const uint16_t*>(k_cache);
+  p.v_cache = static_cast<const uint16_t*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.block_tables = block_tables;
+  p.max_blocks_per_req = max_blocks_per_req;
+  p.seq_lens = seq_lens;
+  p.num_reqs = num_reqs;
+  p.total_q = num_reqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.scale_log2 = sm_scale * pa::kLog2e;
+  p.window = window;
+  p.sink_tokens = sink_tokens;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = static_cast<int*>(workspace);
+  s = run_launch(PA_KERNEL_DECODE, "window", stream, [&] { return pa::launch_window(p, stream); });
+  return s == PA_OK ? ok() : s;
+}
 
 pa_status pa_copy_blocks(const int32_t* src_blocks, const int32_t* dst_blocks, int64_t n_pairs, void* k_cache,
                          void* v_cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,

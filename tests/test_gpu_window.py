@@ -1,0 +1,291 @@
+"""pa_attention_varlen_window and pa_decode_window through the C ABI against
+the definition in 64 bits.
+
+Whatever no query of a request sees is not a number here: slots behind the last
+token, tokens behind the window, blocks of no table; pages without a visible
+token have no block.
+
+Bounds, as for the other attention calls.  Scores: 128 products of bf16 numbers
+are exact in binary32; summing them and scaling rounds each at most 2^-24 relative
+some 136 times, so a score is off by at most DS = 2^-16 sm_scale max_t sum_d |q_d
+k_td|.  Then lse is off by at most DS plus a few roundings of its own, and every
+probability by a factor exp(2 DS).  The weights of rows with more than two queries
+are rounded to bf16 (2^-8 each) before they meet V, the others carry 16 bits; an
+output is rounded once to bf16.  With A = sum_t p_t |v_t|:
+  |out - ref| <= 2^-8 |ref| + (w + 4 DS + 2^-14) A,  w = 2^-8 or 2^-15.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import step
+from paged_kv_decode_varlen_gb300 import workloads as W
+from tests.util import bf16_dev, bf16_host
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from paged_kv_decode_varlen_gb300 import binding as B
+
+DEV = "cuda"
+
+
+class Case:
+    def __init__(self, seq, qo, window, sinks=0, Hkv=2, seed=0, scale=1 / np.sqrt(128), spare=3):
+        rng = np.random.default_rng(seed)
+        R = len(seq)
+        self.seq, self.qo = np.asarray(seq, np.int32), np.asarray(qo, np.int32)
+        self.ind = np.concatenate([[0], np.cumsum(self.qo)]).astype(np.int32)
+        self.window, self.sinks, self.Hkv, self.scale = window, sinks, Hkv, float(np.float32(scale))
+        pages = -(-self.seq // 16)
+        self.tables = np.full((R, max(1, int(pages.max(initial=1)))), -1, np.int32)
+        seen = []                                    # (row, token) that some query of the row sees
+        for r in range(R):
+            if qo[r]:
+                t = np.arange(seq[r])
+                seen.append((r, t[(t < sinks) | (t > seq[r] - qo[r] - window)]))
+        need = sorted({(r, int(j)) for r, t in seen for j in t // 16})
+        nb = len(need) + spare
+        perm = rng.permutation(nb)
+        for i, (r, j) in enumerate(need):
+            self.tables[r, j] = perm[i]
+        self.k = np.full((nb, Hkv, 16, 128), 0x7fc0, np.uint16)
+        self.v = self.k.copy()
+        self.v[:, :, ::3] = 0x7f80                   # infinities too
+        for r, t in seen:
+            at = (self.tables[r, t // 16], slice(None), t % 16)
+            self.k[at], self.v[at] = W.normal_bf16(rng, (len(t), Hkv, 128)), W.normal_bf16(rng, (len(t), Hkv, 128))
+        self.q = W.normal_bf16(rng, (int(self.ind[-1]), 4 * Hkv, 128))
+        self.d = dict(q=bf16_dev(self.q), k=bf16_dev(self.k), v=bf16_dev(self.v), tables=torch.from_numpy(self.tables).to(DEV),
+                      seq=torch.from_numpy(self.seq).to(DEV), ind=torch.from_numpy(self.ind).to(DEV))
+
+    def workspace(self):
+        return B.new_workspace(B.pa_window_workspace_size(len(self.seq), len(self.q), 4 * self.Hkv, 128, self.window,
+                                                          self.sinks), DEV)
+
+    def run(self, **kw):
+        d = self.d
+        return B.pa_attention_varlen_window(d["q"], d["k"], d["v"], d["tables"], d["seq"], d["ind"], self.scale, self.window,
+                                            self.sinks, seq_lens_host=torch.from_numpy(self.seq),
+                                            qo_indptr_host=torch.from_numpy(self.ind), return_lse=True, **kw)
+
+    def decode(self, **kw):
+        """The batch's rows of one query through the call that plans on the device."""
+        d = self.d
+        return B.pa_decode_window(d["q"], d["k"], d["v"], d["tables"], d["seq"], self.scale, self.window, self.sinks,
+                                  return_lse=True, **kw)
+
+    def check(self, out, lse, what="", rows=None):
+        ref, ref_lse, weight = step.attention_window(self.q, self.k, self.v, self.tables, self.seq, self.ind, self.scale,
+                                                     self.window, self.sinks)
+        kmax = np.nanmax(np.abs(oracle.bf16_to_f64(self.k)), initial=0)
+        ds = 2.0 ** -16 * abs(self.scale) * kmax * np.abs(oracle.bf16_to_f64(self.q)).sum(-1)
+        w = np.where(np.repeat(self.qo, self.qo) > 2, 2.0 ** -8, 2.0 ** -15)
+        tol = 2.0 ** -8 * np.abs(ref) + (w[:, None] + 4 * ds + 2.0 ** -14)[..., None] * weight
+        got = oracle.bf16_to_f64(bf16_host(out))
+        bad = ~(np.abs(got - ref) <= tol)
+        assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:5].tolist(),
+                               float(np.nanmax(np.abs(got - ref) / np.maximum(tol, 1e-30))))
+        lerr = np.abs(lse.cpu().double().numpy() - ref_lse)
+        assert np.all(lerr <= ds + 2.0 ** -20 * (1 + np.abs(ref_lse))), (what, float(lerr.max()))
+
+
+def rand(seed, n, lo, hi):
+    return [int(x) for x in np.random.default_rng(seed).integers(lo, hi + 1, n)]
+
+
+DECODE = {
+    "one_token": ([1], 1, 0, 1),
+    "window_of_one": ([1, 16, 17, 40], 1, 0, 2),
+    "window_of_one_and_sinks": ([1, 2, 16, 17, 40], 1, 3, 2),
+    "page_edges": (list(range(30, 68)), 17, 0, 1),
+    "page_edges_sinks": (list(range(30, 68)), 16, 16, 1),
+    "window_meets_sinks": (list(range(1, 60)), 20, 18, 1),
+    "sinks_alone_reach": ([100, 50, 7], 2, 200, 2),
+    "wide": ([100, 700, 16], 10 ** 6, 0, 2),
+    "widest": ([100, 700, 16], 2 ** 31 - 1, 2 ** 31 - 1, 2),
+    "three_heads": ([1000, 70, 300], 128, 4, 3),
+    "twelve_heads": ([129, 640, 1, 500], 100, 4, 12),
+    "eight_heads": ([17, 100, 2560, 513], 256, 4, 8),
+    "long_and_short": ([9000, 1, 40, 2100, 16], 4000, 5, 2),
+    "one_long": ([20000], 16000, 70, 1),
+    "many_rows": (rand(4, 300, 1, 200), 50, 4, 1),
+    "rows_over_one_launch": (rand(5, 1100, 1, 60), 20, 1, 1),
+    "as_the_batch": (rand(6, 64, 300, 3000), 512, 4, 8),
+}
+
+
+@pytest.mark.parametrize("name", sorted(DECODE))
+def test_decode_rows(name):
+    seq, window, sinks, Hkv = DECODE[name]
+    c = Case(seq, [1] * len(seq), window, sinks, Hkv, seed=len(name))
+    ws = c.workspace()
+    c.check(*c.run(workspace=ws), what=name)
+    c.check(*c.decode(workspace=ws), what=name + ", planned on the device")
+    c.check(*c.run(workspace=ws), what=name + ", the workspace again")
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+
+
+MANY = {
+    "two_queries": ([2, 300, 17, 16], [2, 2, 2, 2], 30, 0, 3),
+    "verify": ([700, 512, 90, 31], [5, 5, 5, 5], 64, 4, 8),
+    "three_to_nine": ([40, 333, 16, 17, 90, 3000, 9], [3, 4, 5, 6, 7, 8, 9], 50, 3, 2),
+    "eight_of_few": ([8, 9, 24, 100], [8, 8, 8, 8], 4, 1, 2),
+    "whole_prompts": ([1, 16, 17, 33, 129, 250], [1, 16, 17, 33, 129, 250], 40, 0, 2),
+    "whole_prompts_sinks": ([16, 17, 33, 129, 250], [16, 17, 33, 129, 250], 40, 20, 2),
+    "chunk_late": ([1500, 600], [70, 33], 200, 4, 1),
+    "chunk_narrow": ([500, 600], [170, 133], 5, 1, 2),
+    "chunk_wide": ([500, 600], [170, 133], 10 ** 6, 0, 2),
+    "chunk_tile_edges": ([128, 129, 160, 257, 96], [32, 33, 31, 64, 65], 64, 0, 1),
+    "window_is_a_tile": ([400, 513, 640], [64, 65, 100], 128, 128, 1),
+    "sinks_in_the_chunk": ([90, 300], [90, 300], 17, 130, 1),
+    "mixed": ([900, 40, 1, 2000, 513, 77], [100, 1, 1, 1, 7, 0], 300, 4, 2),
+    "idle_rows": ([50, 0, 30, 70, 9], [0, 0, 3, 0, 1], 10, 0, 2),
+    "jobs_in_turn": (rand(6, 40, 7, 400), rand(7, 40, 1, 100), 90, 4, 8),
+    "jobs_in_turn_late": (rand(8, 24, 400, 900), rand(9, 24, 7, 140), 333, 0, 8),
+    "long_window": ([6000], [40], 5000, 70, 1),
+    "few_queries_many_rows": (rand(10, 300, 9, 60), rand(11, 300, 0, 9), 20, 2, 2),
+}
+
+
+@pytest.mark.parametrize("name", sorted(MANY))
+def test_rows_with_several_queries(name):
+    seq, qo, window, sinks, Hkv = MANY[name]
+    qo = [min(a, b) for a, b in zip(seq, qo)]
+    c = Case(seq, qo, window, sinks, Hkv, seed=len(name))
+    ws = c.workspace()
+    c.check(*c.run(workspace=ws), what=name)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+
+
+def test_padding_rows():
+    c = Case([300, 0, 40, 0, 0, 1], [1] * 6, 64, 4, 2)
+    out, lse = c.decode()
+    assert not bool(out[[1, 3, 4]].any()) and bool(torch.isneginf(lse[[1, 3, 4]]).all())
+    live = [0, 2, 5]
+    d = Case([300, 0, 40, 0, 0, 1], [1, 0, 1, 0, 0, 1], 64, 4, 2)
+    d.q, d.d["q"] = c.q[live], c.d["q"][live].contiguous()
+    d.k, d.v, d.tables, d.d["k"], d.d["v"], d.d["tables"] = c.k, c.v, c.tables, c.d["k"], c.d["v"], c.d["tables"]
+    d.check(out[live], lse[live])
+
+
+@pytest.mark.parametrize("L", [-1, (1 << 20) + 1, 16 * 19 + 1, -(1 << 31), (1 << 31) - 1])
+def test_a_length_out_of_bounds_is_recorded(L):
+    c = Case([300, 64, 40], [1] * 3, 64, 4, 2)
+    want, _ = c.decode()
+    ws = c.workspace()
+    c.d["seq"][1] = L
+    out, lse = c.decode(workspace=ws)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == B.PA_ERR_DEVICE_INDEX
+    assert torch.equal(out[[0, 2]], want[[0, 2]]) and not bool(out[1].any()) and bool(torch.isneginf(lse[1]).all())
+
+
+@pytest.mark.parametrize("qo", [1, 5, 40])
+def test_a_block_outside_the_pool_is_recorded(qo):
+    c = Case([200, 90], [qo, qo], 70, 4, 2, seed=3)
+    want = c.run()[0]
+    c.d["tables"][1, 4] = 10 ** 6
+    c.tables[1, 4] = 10 ** 6
+    ws = c.workspace()
+    out, lse = c.run(workspace=ws)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == B.PA_ERR_DEVICE_INDEX
+    assert torch.equal(out[:qo], want[:qo])
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("qo", [1, 5, 40])
+def test_every_key_masked_gives_zero_and_minus_infinity(qo):
+    c = Case([40], [qo], 20, 4, 2, seed=5)
+    c.d["tables"].fill_(-1)
+    out, lse = c.run()
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("scale", [4.0, -0.3, 0.0])
+def test_scales(scale):
+    c = Case([400, 33, 120], [1, 9, 40], 100, 4, 2, seed=12, scale=scale)
+    c.check(*c.run())
+
+
+def test_without_lse():
+    c = Case([400, 33], [1, 9], 100, 4, 2, seed=12)
+    d = c.d
+    out, _ = c.run()
+    alone = B.pa_attention_varlen_window(d["q"], d["k"], d["v"], d["tables"], d["seq"], d["ind"], c.scale, 100, 4)
+    assert torch.equal(alone, out)
+
+
+@pytest.mark.parametrize("qo", [1, 4, 40])
+def test_a_query_that_is_not_a_number_shows_and_stays_in_its_row(qo):
+    c = Case([300, 90], [qo, qo], 100, 4, 2, seed=6)
+    want, want_lse = c.run()
+    c.d["q"][0, 3, 7] = float("nan")
+    out, lse = c.run()
+    keep = torch.ones(2 * qo, 8, dtype=torch.bool, device=DEV)
+    keep[0, 3] = False
+    assert bool(torch.isnan(out[0, 3]).all()) and bool(torch.isnan(lse[0, 3]))
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+
+
+def test_the_same_bits_again():
+    c = Case(rand(30, 40, 100, 3000), [1, 3, 9, 50] * 10, 700, 4, 4, seed=7)
+    ws = c.workspace()
+    out, lse = c.run(workspace=ws)
+    for _ in range(5):
+        o, l = c.run(workspace=ws)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_rows_behind_the_last_query_are_left():
+    c = Case([70, 200], [7, 40], 50, 4, 2, seed=8)
+    out = torch.full((60, 8, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    c.check(*c.run(out=out[:47]))
+    assert bool((out[47:] == 5.0).all())
+
+
+def test_a_captured_decode_takes_new_lengths():
+    """One captured launch over batches of other lengths, tables and queries,
+    its workspace shared with a second graph."""
+    R, Hkv, window, sinks = 24, 2, 200, 4
+    first = Case([1] * R, [1] * R, window, sinks, Hkv, seed=9)
+    nb = 1500
+    t = dict(q=torch.zeros(R, 4 * Hkv, 128, dtype=torch.bfloat16, device=DEV), k=torch.zeros(nb, Hkv, 16, 128, dtype=torch.bfloat16, device=DEV),
+             tables=torch.full((R, 200), -1, dtype=torch.int32, device=DEV), seq=torch.zeros(R, dtype=torch.int32, device=DEV))
+    t["v"] = torch.zeros_like(t["k"])
+    ws = first.workspace()
+    graphs = []
+    for _ in range(2):
+        graph, out = torch.cuda.CUDAGraph(), torch.empty_like(t["q"])
+        lse = torch.empty(R, 4 * Hkv, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            B.pa_decode_window(t["q"], t["k"], t["v"], t["tables"], t["seq"], first.scale, window, sinks, out=out, lse=lse,
+                               workspace=ws)
+        graphs.append((graph, out, lse))
+    for i in range(6):
+        c = Case(rand(40 + i, R, 1, [40, 3000][i % 2]), [1] * R, window, sinks, Hkv, seed=50 + i)
+        t["tables"][:, :c.tables.shape[1]].copy_(c.d["tables"])
+        for x in ("k", "v"):
+            t[x][:c.k.shape[0]].copy_(c.d[x])
+        t["q"].copy_(c.d["q"])
+        t["seq"].copy_(c.d["seq"])
+        graph, out, lse = graphs[i % 2]
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse, what=str(i))
+    assert B.pa_get_device_error(ws) == 0
+
+
+def test_on_a_stream_that_is_not_the_current_one():
+    c = Case([300, 45, 700], [1, 9, 4], 100, 4, 2, seed=10)
+    want, want_lse = c.run()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, lse = c.run(stream=side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
