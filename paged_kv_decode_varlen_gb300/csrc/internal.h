@@ -345,8 +345,18 @@ struct WindowParams {
   int32_t sink_tokens;
   uint16_t* out;
   float* lse;
+  // rows of a decode launch (at most kPlanMaxRows), and the segments that each is cut
+  // into (0: all rows' pages as one stream)
+  int32_t row0, rows, per_row;
+  float* piece_o;      // fp32 [2 x CTAs, piece_cols, D] of rows cut between CTAs
+  float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
+  int32_t piece_cols;  // (query, head) columns of a piece
+  int* counters;       // [num_reqs, Hkv, 2] pieces that have arrived; zero between calls
   int* err;
 };
+// Rows of up to this many queries run the decode kernel with a window.
+constexpr int kWindowDecodeQueries = 8;
+constexpr int kWindowMaxSms = 256;  // (workspace sizing; more SMs are not used)
 
 struct MergeParams {
   const uint16_t* o_a;
@@ -418,6 +428,8 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 cudaError_t launch_step_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved, cudaStream_t stream);
 cudaError_t launch_window(const WindowParams& p, cudaStream_t stream);
+// rows of up to `queries` queries on grid CTAs, a multiple of the kv heads
+cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream);
 
 // Query tile of the tensor-core tile kernels (query tokens per CTA: with the
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.

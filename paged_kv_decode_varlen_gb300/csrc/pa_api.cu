@@ -1247,8 +1247,40 @@ pa_status norm_rope(pa::RopeParams& p, bool append, int32_t interleaved, int32_t
   return s == PA_OK ? ok() : s;
 }
 
-// Workspace of the attention with a window: the error word.
-size_t window_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return PA_ERROR_WORD_BYTES; }
+// Workspace of the attention with a window: [error word | counts (num_reqs x Hkv x
+// 2 int32) | pieces of rows cut between CTAs, two per CTA (columns x D fp32) | their
+// lse].
+struct WindowLayout {
+  size_t counters, piece_o, piece_lse, total;
+  int32_t cols;
+};
+WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_heads) {
+  const int32_t hkv = std::max(num_q_heads / PA_GQA_GROUP, 1);
+  WindowLayout w;
+  w.cols = PA_GQA_GROUP * std::min(std::max(total_q, 1), pa::kWindowDecodeQueries);
+  const size_t slots = (size_t)2 * std::max(pa::kWindowMaxSms, hkv) * w.cols;
+  w.counters = PA_ERROR_WORD_BYTES;
+  w.piece_o = w.counters + align256((size_t)num_reqs * hkv * 2 * 4);
+  w.piece_lse = w.piece_o + slots * pa::kHeadDim * 4;
+  w.total = w.piece_lse + align256(slots * 4);
+  return w;
+}
+
+// The decode launches of rows 0 .. num_reqs - 1 (those of up to `queries` queries).
+// With at most as many rows as there are segments for a kv head, every row is cut into
+// segments of its own.
+pa_status window_decode(pa::WindowParams& p, int queries, cudaStream_t stream) {
+  const int nseg = std::max(1, std::min(sm_count(), pa::kWindowMaxSms) / p.num_kv_heads);
+  for (p.row0 = 0; p.row0 < p.num_reqs; p.row0 += pa::kPlanMaxRows) {
+    p.rows = std::min(p.num_reqs - p.row0, pa::kPlanMaxRows);
+    p.per_row = p.rows <= nseg ? nseg / p.rows : 0;
+    const pa_status s = run_launch(PA_KERNEL_DECODE, "decode_window", stream, [&] {
+      return pa::launch_decode_window(p, queries, nseg * p.num_kv_heads, stream);
+    });
+    if (s != PA_OK) return s;
+  }
+  return PA_OK;
+}
 
 pa_status check_window(int32_t num_reqs, int64_t num_blocks, float sm_scale, int32_t window, int32_t sink_tokens) {
   if (num_reqs < 0 || num_reqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_reqs %d outside [0, 65535]", num_reqs);
@@ -1389,7 +1421,7 @@ pa_status pa_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
 size_t pa_window_workspace_size(int32_t num_reqs, int32_t total_q, int32_t num_q_heads, int32_t head_dim,
                                 int32_t window, int32_t sink_tokens) {
   if (num_reqs < 0 || total_q < 0 || num_q_heads < 0 || head_dim < 0 || window < 0 || sink_tokens < 0) return 0;
-  return window_workspace(num_reqs, total_q, num_q_heads, window, sink_tokens);
+  return window_layout(num_reqs, total_q, num_q_heads).total;
 }
 
 pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
@@ -1414,6 +1446,7 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
   if (qo_indptr_host[0] != 0) return fail(PA_ERR_INVALID_ARG, "qo_indptr[0] = %d, must be 0", qo_indptr_host[0]);
   if (qo_indptr_host[num_reqs] != total_q)
     return fail(PA_ERR_INVALID_ARG, "qo_indptr[num_reqs] = %d != total_q = %d", qo_indptr_host[num_reqs], total_q);
+  int32_t few = 0, many = 0;  // most queries of a row for the decode kernel; rows of more
   for (int32_t r = 0; r < num_reqs; ++r) {
     const int32_t n = qo_indptr_host[r + 1] - qo_indptr_host[r], L = seq_lens_host[r];
     if (n < 0) return fail(PA_ERR_INVALID_ARG, "qo_indptr decreases at request %d", r);
@@ -1423,10 +1456,12 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
     if (n > L) return fail(PA_ERR_INVALID_ARG, "request %d: qo_len %d > seq_len %d", r, n, L);
     if (pages_of(L) > max_blocks_per_req)
       return fail(PA_ERR_INVALID_ARG, "request %d: %d pages > max_blocks_per_req %d", r, pages_of(L), max_blocks_per_req);
+    if (n <= pa::kWindowDecodeQueries) few = std::max(few, n);
+    else ++many;
   }
-  const size_t need = window_workspace(num_reqs, total_q, num_q_heads, window, sink_tokens);
-  if (workspace_bytes < need)
-    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  const WindowLayout wl = window_layout(num_reqs, total_q, num_q_heads);
+  if (workspace_bytes < wl.total)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, wl.total);
   if (total_q == 0) return ok();
   pa::WindowParams p{};
   p.q = static_cast<const uint16_t*>(q);
@@ -1446,8 +1481,14 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
   p.sink_tokens = sink_tokens;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
   p.err = static_cast<int*>(workspace);
-  s = run_launch(PA_KERNEL_DECODE, "window", stream, [&] { return pa::launch_window(p, stream); });
+  p.counters = reinterpret_cast<int*>(ws + wl.counters);
+  p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
+  p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
+  p.piece_cols = wl.cols;
+  if (many > 0) s = run_launch(PA_KERNEL_PREFILL, "window", stream, [&] { return pa::launch_window(p, stream); });
+  if (s == PA_OK && few > 0) s = window_decode(p, few, stream);
   return s == PA_OK ? ok() : s;
 }
 
@@ -1465,9 +1506,9 @@ pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cac
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
     return fail(PA_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned, workspace 256-byte aligned");
-  const size_t need = window_workspace(num_reqs, num_reqs, num_q_heads, window, sink_tokens);
-  if (workspace_bytes < need)
-    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  const WindowLayout wl = window_layout(num_reqs, num_reqs, num_q_heads);
+  if (workspace_bytes < wl.total)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, wl.total);
   if (num_reqs == 0) return ok();
   pa::WindowParams p{};
   p.q = static_cast<const uint16_t*>(q);
@@ -1486,8 +1527,13 @@ pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cac
   p.sink_tokens = sink_tokens;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
   p.err = static_cast<int*>(workspace);
-  s = run_launch(PA_KERNEL_DECODE, "window", stream, [&] { return pa::launch_window(p, stream); });
+  p.counters = reinterpret_cast<int*>(ws + wl.counters);
+  p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
+  p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
+  p.piece_cols = wl.cols;
+  s = window_decode(p, 1, stream);
   return s == PA_OK ? ok() : s;
 }
 

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kThreads) window_kernel(const WindowParams p) 
     j = tok - p.qo_indptr[r];
     n = p.qo_indptr[r + 1] - p.qo_indptr[r];
   }
+  if (n <= kWindowDecodeQueries) return;  // a row of the decode kernel
   int L = p.seq_lens[r];
   if (L < 0 || L > PA_MAX_SEQ_LEN || (L + kPage - 1) / kPage > p.max_blocks_per_req || (L > 0 && n > L)) {
     if (lane == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
