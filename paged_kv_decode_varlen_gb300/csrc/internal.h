@@ -230,6 +230,47 @@ struct Q4Items {
 constexpr int kQ4FewItems = 160;  // a batch of split items has no more
 constexpr int kQ4MaxRanges = 32;
 
+// Attention with a window: a query at position p sees keys t <= p with t <
+// sink_tokens or t > p - window.
+struct WindowParams {
+  const uint16_t* q;
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  int64_t num_blocks;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_req;
+  const int32_t* seq_lens;
+  const int32_t* qo_indptr;  // or null: row r has the one query r
+  int32_t num_reqs;
+  int32_t total_q;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  float scale_log2;
+  int32_t window;
+  int32_t sink_tokens;
+  uint16_t* out;
+  float* lse;
+  // rows of a decode launch (at most kPlanMaxRows), and the segments that each is cut
+  // into (0: all rows' pages as one stream)
+  int32_t row0, rows, per_row;
+  float* piece_o;      // fp32 [2 x CTAs, piece_cols, D] of rows cut between CTAs
+  float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
+  int32_t piece_cols;  // (query, head) columns of a piece
+  int* counters;       // [num_reqs, Hkv, 2] pieces that have arrived; zero between calls
+  int* err;
+};
+// Rows of up to this many queries run the decode kernel with a window.
+constexpr int kWindowDecodeQueries = 8;
+// The items of a tile launch: request, first query token, its position, queries (up to
+// kWindowTileTokens).
+constexpr int kWindowTileTokens = 64;
+struct WindowItems {
+  int32_t count;
+  int32_t pad[3];
+  int4 item[kMaxPrefillItems];
+};
+constexpr int kWindowMaxSms = 256;  // (workspace sizing; more SMs are not used)
+
 struct PrefillParams {
   const uint16_t* q;
   const uint16_t* k_cache;
@@ -325,39 +366,6 @@ struct RopeParams {
   int* err;
 };
 
-// Attention with a window: a query at position p sees keys t <= p with t <
-// sink_tokens or t > p - window.
-struct WindowParams {
-  const uint16_t* q;
-  const uint16_t* k_cache;
-  const uint16_t* v_cache;
-  int64_t num_blocks;
-  const int32_t* block_tables;
-  int32_t max_blocks_per_req;
-  const int32_t* seq_lens;
-  const int32_t* qo_indptr;  // or null: row r has the one query r
-  int32_t num_reqs;
-  int32_t total_q;
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
-  float scale_log2;
-  int32_t window;
-  int32_t sink_tokens;
-  uint16_t* out;
-  float* lse;
-  // rows of a decode launch (at most kPlanMaxRows), and the segments that each is cut
-  // into (0: all rows' pages as one stream)
-  int32_t row0, rows, per_row;
-  float* piece_o;      // fp32 [2 x CTAs, piece_cols, D] of rows cut between CTAs
-  float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
-  int32_t piece_cols;  // (query, head) columns of a piece
-  int* counters;       // [num_reqs, Hkv, 2] pieces that have arrived; zero between calls
-  int* err;
-};
-// Rows of up to this many queries run the decode kernel with a window.
-constexpr int kWindowDecodeQueries = 8;
-constexpr int kWindowMaxSms = 256;  // (workspace sizing; more SMs are not used)
-
 struct MergeParams {
   const uint16_t* o_a;
   const float* lse_a;
@@ -427,9 +435,12 @@ cudaError_t launch_prefix_merge(const PrefixParams& p, int n_chunks, cudaStream_
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 cudaError_t launch_step_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved, cudaStream_t stream);
-cudaError_t launch_window(const WindowParams& p, cudaStream_t stream);
 // rows of up to `queries` queries on grid CTAs, a multiple of the kv heads
 cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream);
+
+// (item, kv head) jobs of rows of more queries on ctas CTAs
+cudaError_t launch_prefill_window(const WindowParams& p, const WindowItems& items, const TcMaps& maps,
+                                  const CUtensorMap& out_map, int ctas, cudaStream_t stream);
 
 // Query tile of the tensor-core tile kernels (query tokens per CTA: with the
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.

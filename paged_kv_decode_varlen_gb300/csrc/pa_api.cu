@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "pa.h"
+#include "window.cuh"
 
 namespace {
 
@@ -1266,6 +1267,38 @@ WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_head
   return w;
 }
 
+// The tile launches of the rows of more than kWindowDecodeQueries queries.
+pa_status window_tiles(const pa::WindowParams& p, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
+                       cudaStream_t stream) {
+  static thread_local pa::TcMaps maps;
+  static thread_local CUtensorMap out_map;
+  pa_status s = make_tc_maps(p.q, p.total_q, p.num_q_heads, p.k_cache, p.v_cache, p.num_blocks, p.num_kv_heads, maps);
+  if (s == PA_OK) s = make_q_map(p.out, p.total_q, p.num_q_heads, pa::kQ4OutTok, out_map);
+  if (s != PA_OK) return s;
+  static thread_local pa::WindowItems items;
+  std::vector<std::pair<int32_t, int4>> all;  // (pages, item)
+  for (int32_t r = 0; r < p.num_reqs; ++r) {
+    const int32_t n = qo_indptr_host[r + 1] - qo_indptr_host[r];
+    if (n <= pa::kWindowDecodeQueries) continue;
+    for (int32_t j = 0; j < n; j += pa::kWindowTileTokens) {
+      const int32_t nq = std::min(n - j, pa::kWindowTileTokens), pos = seq_lens_host[r] - n + j;
+      all.push_back({pa::seen_pages(pos + nq, nq, p.window, p.sink_tokens).count(),
+                     make_int4(r, qo_indptr_host[r] + j, pos, nq)});
+    }
+  }
+  // the longest first, so that they do not form the tail
+  std::stable_sort(all.begin(), all.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
+  for (size_t base = 0; base < all.size(); base += pa::kMaxPrefillItems) {
+    items.count = (int32_t)std::min(all.size() - base, (size_t)pa::kMaxPrefillItems);
+    for (int32_t i = 0; i < items.count; ++i) items.item[i] = all[base + (size_t)i].second;
+    const int ctas = (int)std::min<int64_t>((int64_t)items.count * p.num_kv_heads, sm_count());
+    s = run_launch(PA_KERNEL_PREFILL, "prefill_window", stream,
+                   [&] { return pa::launch_prefill_window(p, items, maps, out_map, ctas, stream); });
+    if (s != PA_OK) return s;
+  }
+  return PA_OK;
+}
+
 // The decode launches of rows 0 .. num_reqs - 1 (those of up to `queries` queries).
 // With at most as many rows as there are segments for a kv head, every row is cut into
 // segments of its own.
@@ -1487,7 +1520,11 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
   p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
   p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
   p.piece_cols = wl.cols;
-  if (many > 0) s = run_launch(PA_KERNEL_PREFILL, "window", stream, [&] { return pa::launch_window(p, stream); });
+  try {
+    if (many > 0) s = window_tiles(p, seq_lens_host, qo_indptr_host, stream);
+  } catch (const std::bad_alloc&) {  // of the plan's host arrays
+    return fail(PA_ERR_UNSUPPORTED, "no host memory for the plan of %d requests", num_reqs);
+  }
   if (s == PA_OK && few > 0) s = window_decode(p, few, stream);
   return s == PA_OK ? ok() : s;
 }
