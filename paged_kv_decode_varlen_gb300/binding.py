@@ -630,23 +630,34 @@ def pa_step_tables(new_tokens, cached_lens, block_tables, free_ring, free_state,
             free_state_out, first_page_out = made(free_state_out, 2, _I32), made(first_page_out, R, _I32)
             if workspace is None:
                 workspace = new_workspace(PA_ERROR_WORD_BYTES, new_tokens.device)
-    if cached_lens.shape != (R,) or len(table) != 2 or table[0] != R or free_ring.dim() != 1 or free_state.shape != (2,) \
-            or seq_lens.shape != (R,) or qo_indptr.shape != (R + 1,) or slot_mapping.shape != (n_tokens,) \
-            or positions.shape != (n_tokens,) or free_state_out.shape != (2,) or first_page_out.shape != (R,) \
-            or (first_page is not None and first_page.shape != (R,)):
+    rows, tokens, two = new_tokens.shape, slot_mapping.shape, free_state.shape
+    if not (rows == cached_lens.shape == seq_lens.shape == first_page_out.shape and len(table) == 2 and table[0] == R
+            and free_ring.dim() == 1 and len(two) == 1 and two[0] == 2 and two == free_state_out.shape
+            and qo_indptr.shape == (R + 1,) and tokens == positions.shape == (n_tokens,)
+            and (first_page is None or first_page.shape == rows)):
         raise ValueError("inconsistent shapes")
-    i32 = [(new_tokens, "new_tokens"), (cached_lens, "cached_lens"), (block_tables, "block_tables"),
-           (free_ring, "free_ring"), (free_state, "free_state"), (seq_lens, "seq_lens"), (qo_indptr, "qo_indptr"),
-           (positions, "positions"), (free_state_out, "free_state_out"), (first_page_out, "first_page_out")]
-    if first_page is not None:
-        i32.append((first_page, "first_page"))
-    for t, name in i32:
-        _data(t, _I32, name, dev)
-    _refuse(dev, (slot_mapping, _I64, "slot_mapping"), (workspace, _U8, "workspace"))
+    fp = new_tokens if first_page is None else first_page
+    if not (new_tokens.dtype is cached_lens.dtype is block_tables.dtype is free_ring.dtype is free_state.dtype
+            is seq_lens.dtype is qo_indptr.dtype is positions.dtype is free_state_out.dtype is first_page_out.dtype
+            is fp.dtype is _I32 and slot_mapping.dtype is _I64 and workspace.dtype is _U8
+            and new_tokens.is_contiguous() and cached_lens.is_contiguous() and block_tables.is_contiguous()
+            and free_ring.is_contiguous() and free_state.is_contiguous() and seq_lens.is_contiguous()
+            and qo_indptr.is_contiguous() and positions.is_contiguous() and free_state_out.is_contiguous()
+            and first_page_out.is_contiguous() and fp.is_contiguous() and slot_mapping.is_contiguous()
+            and workspace.is_contiguous()
+            and dev == new_tokens.get_device() == cached_lens.get_device() == block_tables.get_device()
+            == free_ring.get_device() == free_state.get_device() == seq_lens.get_device() == qo_indptr.get_device()
+            == positions.get_device() == free_state_out.get_device() == first_page_out.get_device() == fp.get_device()
+            == slot_mapping.get_device() == workspace.get_device()):
+        _refuse(dev, (new_tokens, _I32, "new_tokens"), (cached_lens, _I32, "cached_lens"),
+                (block_tables, _I32, "block_tables"), (free_ring, _I32, "free_ring"), (free_state, _I32, "free_state"),
+                (seq_lens, _I32, "seq_lens"), (qo_indptr, _I32, "qo_indptr"), (positions, _I32, "positions"),
+                (free_state_out, _I32, "free_state_out"), (first_page_out, _I32, "first_page_out"),
+                (fp, _I32, "first_page"), (slot_mapping, _I64, "slot_mapping"), (workspace, _U8, "workspace"))
     status = _lib.pa_step_tables(new_tokens.data_ptr(), cached_lens.data_ptr(),
                                  None if first_page is None else first_page.data_ptr(), R, block_tables.data_ptr(),
-                                 table[1], free_ring.data_ptr(), free_ring.shape[0], free_state.data_ptr(), int(window),
-                                 int(sink_tokens), int(shared_pages), n_tokens, seq_lens.data_ptr(), qo_indptr.data_ptr(),
+                                 table[1], free_ring.data_ptr(), free_ring.shape[0], free_state.data_ptr(), window,
+                                 sink_tokens, shared_pages, n_tokens, seq_lens.data_ptr(), qo_indptr.data_ptr(),
                                  slot_mapping.data_ptr(), positions.data_ptr(), free_state_out.data_ptr(),
                                  first_page_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                  _stream_handle(stream, dev))
@@ -667,36 +678,34 @@ def pa_rope_turns(inv_freq) -> torch.Tensor:
     return turns
 
 
-def _heads(t, name, device):
-    """(address, token stride) of bf16 [N, H, 128], a token's heads side by side."""
-    if t.dtype is not _BF16:
-        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
-    s = t.stride()
-    if t.numel() and (s[2] != 1 or (t.shape[1] > 1 and s[1] != t.shape[2])):
-        raise ValueError(f"{name}: each token's heads must be contiguous")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, device):
-    """The checks that the two calls of norms and rotations share; q_out is
-    made where it is not given."""
+def _rope_refuse(dev, q, k, v, positions, turns, q_out, weights):
+    """Raise for what the calls of norms and rotations do not take (v may be k)."""
     N, Hq, D = q.shape
-    if k.dim() != 3 or k.shape[0] != N or k.shape[2] != D or positions.shape != (N,) or turns.dim() != 1:
+    if k.dim() != 3 or k.shape[0] != N or k.shape[2] != D or v.shape != k.shape or positions.shape != (N,) \
+            or turns.dim() != 1:
         raise ValueError("inconsistent shapes")
-    if q_out is None:
-        with _on(stream):
-            q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-    elif q_out.shape != q.shape:
+    if q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
-    _refuse(device, (positions, _I32, "positions"), (turns, _I64, "turns"), (q_out, _BF16, "q_out"))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+    for t, dtype, name in ((q, _BF16, "q"), (k, _BF16, "k"), (v, _BF16, "v"), (positions, _I32, "positions"),
+                           (turns, _I64, "turns")):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+            raise ValueError(f"{name}: each token's heads must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    _refuse(dev, (positions, _I32, "positions"), (turns, _I64, "turns"), (q_out, _BF16, "q_out"))
+    for w, name in weights:
         if w is not None:
             if w.shape != (D,):
                 raise ValueError(f"{name} must be [head_dim]")
-            _data(w, _F32, name, device)
-    return q_out
+            _data(w, _F32, name, dev)
+
+
+def _weight(w, D, dev):
+    """Whether a norm's weight is one that the kernels take."""
+    return w is None or (w.dtype is _F32 and w.shape == (D,) and w.is_contiguous() and w.get_device() == dev)
 
 
 def pa_qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -706,19 +715,30 @@ def pa_qk_norm_rope(q, k, positions, turns, *, q_weight=None, k_weight=None, eps
     on the device; 2 * len dims are rotated).  q and k may be columns of wider
     rows.  Returns (q_out, k_out), contiguous bf16 (see include/pa.h)."""
     dev = _current_device()
-    q_out = _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, dev)
-    if k_out is None:
+    if q_out is None or k_out is None:
         with _on(stream):
-            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device)
-    elif k_out.shape != k.shape:
-        raise ValueError("k_out must have k's shape")
-    N, Hq, D = q.shape
-    (qp, qs), (kp, ks) = _heads(q, "q", dev), _heads(k, "k", dev)
-    status = _lib.pa_qk_norm_rope(qp, qs, kp, ks, positions.data_ptr(), N,
+            q_out = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
+            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device) if k_out is None else k_out
+    N, Hq, D = shape = q.shape
+    (qs, qh, qe), (ks, kh, ke), kshape, tshape = q.stride(), k.stride(), k.shape, turns.shape
+    if not (len(kshape) == 3 and kshape[0] == N and kshape[2] == D and positions.shape == (N,) and len(tshape) == 1
+            and q_out.shape == shape and k_out.shape == kshape and qe == ke == 1 and qh == kh == D
+            and q.dtype is k.dtype is q_out.dtype is k_out.dtype is _BF16 and positions.dtype is _I32
+            and turns.dtype is _I64 and q_out.is_contiguous() and k_out.is_contiguous() and positions.is_contiguous()
+            and turns.is_contiguous() and _weight(q_weight, D, dev) and _weight(k_weight, D, dev)
+            and dev == q.get_device() == k.get_device() == q_out.get_device() == k_out.get_device()
+            == positions.get_device() == turns.get_device()):
+        _rope_refuse(dev, q, k, k, positions, turns, q_out, ((q_weight, "q_weight"), (k_weight, "k_weight")))
+        if k_out.shape != kshape:
+            raise ValueError("k_out must have k's shape")
+        _refuse(dev, (k_out, _BF16, "k_out"))
+    if N <= 1:  # (the stride of a dimension of one is anything)
+        qs, ks = Hq * D, kshape[1] * D
+    status = _lib.pa_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, positions.data_ptr(), N,
                                   None if q_weight is None else q_weight.data_ptr(),
-                                  None if k_weight is None else k_weight.data_ptr(), float(eps), turns.data_ptr(),
-                                  2 * turns.shape[0], int(interleaved), Hq, k.shape[1], D, q_out.data_ptr(),
-                                  _data(k_out, _BF16, "k_out", dev), _stream_handle(stream, dev))
+                                  None if k_weight is None else k_weight.data_ptr(), eps, turns.data_ptr(),
+                                  2 * tshape[0], interleaved, Hq, kshape[1], D, q_out.data_ptr(), k_out.data_ptr(),
+                                  _stream_handle(stream, dev))
     if status:
         _check(status)
     return q_out, k_out
@@ -730,23 +750,37 @@ def pa_qk_norm_rope_append(q, k, v, positions, slot_mapping, turns, k_cache, v_c
     slot_mapping (int64 [N], negative = skip) of the HND pools.  Returns q_out
     (see include/pa.h)."""
     dev = _current_device()
-    q_out = _rope_args(q, k, positions, turns, q_weight, k_weight, q_out, stream, dev)
-    N, Hq, D = q.shape
-    nb, Hkv, P, D2 = pool = k_cache.shape
-    if v.shape != k.shape or v_cache.shape != pool or k.shape[1] != Hkv or D2 != D or slot_mapping.shape != (N,):
-        raise ValueError("inconsistent shapes")
-    if workspace is None:
+    if q_out is None or workspace is None:
         with _on(stream):
-            workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device)
-    _refuse(dev, (slot_mapping, _I64, "slot_mapping"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
-            (workspace, _U8, "workspace"))
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
-    status = _lib.pa_qk_norm_rope_append(qp, qs, kp, ks, vp, vs, positions.data_ptr(), slot_mapping.data_ptr(), N,
-                                         None if q_weight is None else q_weight.data_ptr(),
-                                         None if k_weight is None else k_weight.data_ptr(), float(eps),
-                                         turns.data_ptr(), 2 * turns.shape[0], int(interleaved), Hq, Hkv, D, P,
-                                         q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb,
-                                         workspace.data_ptr(), workspace.numel(), _stream_handle(stream, dev))
+            q_out = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
+            workspace = new_workspace(PA_ERROR_WORD_BYTES, k_cache.device) if workspace is None else workspace
+    N, Hq, D = shape = q.shape
+    nb, Hkv, P, D2 = pool = k_cache.shape
+    (qs, qh, qe), (ks, kh, ke), (vs, vh, ve) = q.stride(), k.stride(), v.stride()
+    rows, tshape = positions.shape, turns.shape
+    if not (k.shape == v.shape == (N, Hkv, D) and D2 == D and v_cache.shape == pool and slot_mapping.shape == rows == (N,)
+            and len(tshape) == 1 and q_out.shape == shape and qe == ke == ve == 1 and qh == kh == vh == D
+            and q.dtype is k.dtype is v.dtype is q_out.dtype is k_cache.dtype is v_cache.dtype is _BF16
+            and positions.dtype is _I32 and turns.dtype is slot_mapping.dtype is _I64 and workspace.dtype is _U8
+            and q_out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and positions.is_contiguous() and turns.is_contiguous() and slot_mapping.is_contiguous()
+            and workspace.is_contiguous() and _weight(q_weight, D, dev) and _weight(k_weight, D, dev)
+            and dev == q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == k_cache.get_device()
+            == v_cache.get_device() == positions.get_device() == turns.get_device() == slot_mapping.get_device()
+            == workspace.get_device()):
+        _rope_refuse(dev, q, k, v, positions, turns, q_out, ((q_weight, "q_weight"), (k_weight, "k_weight")))
+        if v_cache.shape != pool or k.shape[1] != Hkv or D2 != D or slot_mapping.shape != (N,):
+            raise ValueError("inconsistent shapes")
+        _refuse(dev, (slot_mapping, _I64, "slot_mapping"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
+                (workspace, _U8, "workspace"))
+    if N <= 1:  # (the stride of a dimension of one is anything)
+        qs, ks, vs = Hq * D, Hkv * D, Hkv * D
+    status = _lib.pa_qk_norm_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+                                         slot_mapping.data_ptr(), N, None if q_weight is None else q_weight.data_ptr(),
+                                         None if k_weight is None else k_weight.data_ptr(), eps, turns.data_ptr(),
+                                         2 * tshape[0], interleaved, Hq, Hkv, D, P, q_out.data_ptr(), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), nb, workspace.data_ptr(), workspace.numel(),
+                                         _stream_handle(stream, dev))
     if status:
         _check(status)
     return q_out
@@ -783,7 +817,7 @@ def pa_attention_varlen_window(q, k_cache, v_cache, block_tables, seq_lens, qo_i
                 (out, _BF16, "out"), (workspace, _U8, "workspace"))
     status = _lib.pa_attention_varlen_window(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(), table[1], seq_lens.data_ptr(),
-        qo_indptr.data_ptr(), slh_at, qih_at, R, total_q, Hq, Hkv, D, P, float(sm_scale), int(window), int(sink_tokens),
+        qo_indptr.data_ptr(), slh_at, qih_at, R, total_q, Hq, Hkv, D, P, sm_scale, window, sink_tokens,
         out.data_ptr(), None if lse is None else _data(lse, _F32, "lse", dev), workspace.data_ptr(), workspace.numel(),
         _stream_handle(stream, dev))
     if status:
@@ -835,7 +869,7 @@ def pa_decode_window(q, k_cache, v_cache, block_tables, seq_lens, sm_scale, wind
                 (workspace, _U8, "workspace"))
     status = _lib.pa_decode_window(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(), table[1], seq_lens.data_ptr(), R,
-        Hq, Hkv, D, P, float(sm_scale), int(window), int(sink_tokens), out.data_ptr(),
+        Hq, Hkv, D, P, sm_scale, window, sink_tokens, out.data_ptr(),
         None if lse is None else _data(lse, _F32, "lse", dev), workspace.data_ptr(), workspace.numel(),
         _stream_handle(stream, dev))
     if status:

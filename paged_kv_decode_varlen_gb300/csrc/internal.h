@@ -338,7 +338,8 @@ struct TablesParams {
   int32_t* free_state_out;
   int32_t* first_page_out;  // or null
   int* err;
-  int* arrived;  // CTAs of the launch that are done; zero between calls
+  int32_t in_place;  // an output is the array it is made from
+  int* arrived;      // CTAs of the launch that are done; zero between calls
 };
 
 // Norms and rotations of queries and keys; with pools the keys and the values go

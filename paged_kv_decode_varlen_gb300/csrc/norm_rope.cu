@@ -11,142 +11,315 @@
 // a signed fraction of half a turn, go to sincospif: no range reduction, and as exact
 // at position 2^20 as at 1.
 //
+// Work.  A unit is a token and up to kHeads of its kv heads, with the 4 query heads of
+// each.  A warp takes units in turn: its lane 0 keeps the rows of the next kStages units
+// on their way to shared memory by bulk copies (three a unit: q, k, v), so that what is
+// in flight does not depend on how far the warp's arithmetic is.  8 lanes hold a row, 16
+// dims each, four rows at a time.  A unit's angles are computed once, two a lane, and
+// handed around by shuffles: each lane keeps the cosines and sines of its own dims in
+// registers for all rows.
 // Bound: HBM for many tokens (a token with 32 + 8 + 8 heads reads and writes 12 KiB
 // each), latency for few.
 #include "internal.h"
+
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kLanes = 8;  // per row, 16 dims each: [8 c, 8 c + 8) and [64 + 8 c, 64 + 8 c + 8)
-constexpr int kSlots = kThreads / kLanes;
-constexpr int kMaxTok = 32;  // tokens per CTA
+// (8191 tokens of 32 + 8 + 8 heads, 34.8 us, 5.6 TB/s.  Rows loaded by the lanes that
+// compute them, up to 12 ahead, 44 to 57 us: registers for what is in flight cost warps;
+// one unit in flight and 16 warps 35.5, three and 6 warps 38.9.)
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtas = 2;    // resident per SM
+constexpr int kStages = 2;  // units in flight per warp
+constexpr int kHeads = 8;   // kv heads of a unit
 
-__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// How dims pair up.  kFull: dim i with 64 + i.  kPairs: 2 i with 2 i + 1.  kPart: i with i
+// + half, for i < half < 64.
+enum class Mode { kFull, kPairs, kPart };
+
+// Lane c of a row's 8 holds dims [8 c, 8 c + 8) and [64 + 8 c, 64 + 8 c + 8): in pairs f[0
+// .. 3] and f[4 .. 7].
+__device__ __forceinline__ void unpack(const uint4& lo, const uint4& hi, float2 (&f)[8]) {
+  f[0] = bf16x2_to_f2(lo.x); f[1] = bf16x2_to_f2(lo.y); f[2] = bf16x2_to_f2(lo.z); f[3] = bf16x2_to_f2(lo.w);
+  f[4] = bf16x2_to_f2(hi.x); f[5] = bf16x2_to_f2(hi.y); f[6] = bf16x2_to_f2(hi.z); f[7] = bf16x2_to_f2(hi.w);
+}
+__device__ __forceinline__ uint4 pack4(const float2* f) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                    pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ float2 shfl2(float2 v, int from) {
+  return make_float2(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from));
+}
+
+// cos and sin of pair j's angle at `pos`; (1, 0) for a pair that is not rotated.
+__device__ __forceinline__ float2 angle(const RopeParams& p, int pos, int j, int half) {
+  float2 r = make_float2(1.f, 0.f);
+  if (j >= 0 && j < half) {
+    const uint64_t a = (uint64_t)(int64_t)pos * p.turns[j];
+    sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &r.y, &r.x);  // 2^-31: of half a turn
+  }
+  return r;
+}
+
+// The angles of a lane's dims.  kFull: of dims 8 c + i (and 64 + 8 c + i), pairs (2 u, 2 u +
+// 1) of i in c[u], s[u].  kPairs: of the pair f[u].  kPart: c[u], s[u] for f[u]; the sine's
+// sign is that of its partner's share.
+template <Mode kMode>
+struct Angles {
+  static constexpr int kN = kMode == Mode::kPart ? 8 : 4;
+  float2 c[kN], s[kN];
+};
+
+template <Mode kMode>
+__device__ __forceinline__ void make_angles(const RopeParams& p, int pos, Angles<kMode>& t) {
+  const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7, half = p.rotary_dim / 2;
+  if constexpr (kMode == Mode::kFull) {
+    // pairs 8 c + 2 r, + 1 here; lane (u, c) has those of c[u], s[u]
+    const float2 a = angle(p, pos, 8 * c + 2 * r, half), b = angle(p, pos, 8 * c + 2 * r + 1, half);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16lo(w[i]);
-    f[2 * i + 1] = bf16hi(w[i]);
+    for (int u = 0; u < 4; ++u) {
+      t.c[u] = shfl2(make_float2(a.x, b.x), 8 * u + c);
+      t.s[u] = shfl2(make_float2(a.y, b.y), 8 * u + c);
+    }
+  } else if constexpr (kMode == Mode::kPairs) {
+    // f[u] (u < 4) is pair 4 c + u, f[4 + u] pair 32 + 4 c + u: as c[u], s[u] = (that, this one's)
+    const float2 a = angle(p, pos, 4 * c + r, half), b = angle(p, pos, 32 + 4 * c + r, half);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      t.c[u] = shfl2(make_float2(a.x, b.x), 8 * u + c);
+      t.s[u] = shfl2(make_float2(a.y, b.y), 8 * u + c);
+    }
+  } else {
+    // chunks of 8 dims, e = c and 8 + c; with far = half / 8 chunk e < far pairs with e + far
+    const int far = half / 8;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int e = 8 * x + c;
+      const int j = e < far ? 8 * e : e < 2 * far ? 8 * (e - far) : -64;  // first pair of the chunk
+      const float2 a = angle(p, pos, j + 2 * r, half), b = angle(p, pos, j + 2 * r + 1, half);
+      const float sign = e < far ? -1.f : 1.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        t.c[4 * x + u] = shfl2(make_float2(a.x, b.x), 8 * u + c);
+        t.s[4 * x + u] = shfl2(make_float2(sign * a.y, sign * b.y), 8 * u + c);
+      }
+    }
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+
+template <Mode kMode>
+__device__ __forceinline__ void rotate(float2 (&f)[8], const Angles<kMode>& t, int half) {
+  auto neg = [](float2 v) { return make_float2(-v.x, -v.y); };
+  if constexpr (kMode == Mode::kFull) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float2 a = f[u], b = f[4 + u];
+      f[u] = __ffma2_rn(a, t.c[u], neg(__fmul2_rn(b, t.s[u])));
+      f[4 + u] = __ffma2_rn(b, t.c[u], __fmul2_rn(a, t.s[u]));
+    }
+  } else if constexpr (kMode == Mode::kPairs) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float c = u < 4 ? t.c[u & 3].x : t.c[u & 3].y, s = u < 4 ? t.s[u & 3].x : t.s[u & 3].y;
+      const float a = f[u].x, b = f[u].y;
+      f[u] = make_float2(fmaf(a, c, -b * s), fmaf(b, c, a * s));
+    }
+  } else {
+    const int lane = threadIdx.x & 31, c = lane & 7, far = half / 8;
+    float2 other[8];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int e = 8 * x + c;
+      const int pe = e < far ? e + far : e < 2 * far ? e - far : e;  // the partner's chunk
+      const int from = (lane & 24) + (pe & 7);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 a = shfl2(f[u], from), b = shfl2(f[4 + u], from);
+        other[4 * x + u] = pe >= 8 ? b : a;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) f[u] = __ffma2_rn(f[u], t.c[u], __fmul2_rn(other[u], t.s[u]));
+  }
 }
 
-template <bool kAppend, bool kInter>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p, int tok_per_cta) {
+// The weights of a lane's dims.
+__device__ __forceinline__ void load_weight(const float* w, float2 (&f)[8]) {
+  const int c = threadIdx.x & 7;
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    f[u] = w ? reinterpret_cast<const float2*>(w)[(u < 4 ? 4 * c : 28 + 4 * c) + u] : make_float2(1.f, 1.f);
+}
+
+// A row's 16 dims of this lane, normalised (weights w) and rotated.
+template <Mode kMode, bool kNorm>
+__device__ __forceinline__ void row16(uint4& lo, uint4& hi, const float2 (&w)[8], const Angles<kMode>& t, int half,
+                                      float eps) {
+  float2 f[8];
+  unpack(lo, hi, f);
+  if constexpr (kNorm) {
+    float2 s2 = __fmul2_rn(f[0], f[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s2 = __ffma2_rn(f[i], f[i], s2);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float q = rsqrtf(fmaf(ss, 1.f / kHeadDim, eps));
+    const float2 q2 = make_float2(q, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], w[i]), q2);
+  }
+  rotate<kMode>(f, t, half);
+  lo = pack4(f);
+  hi = pack4(f + 4);
+}
+
+// n rows of 256 bytes from shared memory (row i at src + 256 i) to dst + i * step
+// elements, on the way normalised with `weight` (null: not) and rotated.
+template <Mode kMode>
+__device__ __forceinline__ void rows_through(const uint8_t* src, int n, uint16_t* dst, size_t step, const float* weight,
+                                             const Angles<kMode>& t, int half, float eps) {
+  const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
+  const uint8_t* s = src + r * (kHeadDim * 2) + 16 * c;
+  uint16_t* d = dst + r * step + 8 * c;
+  auto go = [&](auto norm) {
+    float2 w[8];
+    if constexpr (decltype(norm)::value) load_weight(weight, w);
+#pragma unroll 2
+    for (int i = 0; i < n; i += 4, s += 4 * kHeadDim * 2, d += 4 * step) {
+      const bool live = i + r < n;
+      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+      if (live) {
+        lo = *reinterpret_cast<const uint4*>(s);
+        hi = *reinterpret_cast<const uint4*>(s + 128);
+      }
+      row16<kMode, decltype(norm)::value>(lo, hi, w, t, half, eps);
+      if (live) {
+        *reinterpret_cast<uint4*>(d) = lo;
+        *reinterpret_cast<uint4*>(d + 64) = hi;
+      }
+    }
+  };
+  if (weight) go(std::true_type{}); else go(std::false_type{});
+}
+
+template <bool kAppend>
+struct __align__(128) Smem {
+  uint8_t rows[kWarps][kStages][kHeads * (kGroup + (kAppend ? 2 : 1)) * kHeadDim * 2];
+  uint64_t full[kWarps][kStages];
+};
+
+template <bool kAppend, Mode kMode>
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(const RopeParams p, int heads) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<kAppend>& sm = *reinterpret_cast<Smem<kAppend>*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float2 cs[kMaxTok][kHeadDim / 2];  // cos, sin of (token, pair)
-  const int half = p.rotary_dim / 2;
-  const int64_t tok0 = (int64_t)blockIdx.x * tok_per_cta;
-  const int n_tok = (int)min((int64_t)tok_per_cta, p.n_tokens - tok0);
-  for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
-    const int t = i / half, j = i - t * half;
-    const uint64_t a = (uint64_t)(int64_t)p.positions[tok0 + t] * p.turns[j];
-    float s, c;
-    sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: of half a turn
-    cs[t][j] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int rows = p.num_q_heads + (kAppend ? 2 : 1) * p.num_kv_heads;
-  const int c = threadIdx.x % kLanes;
-  const unsigned lanes = 0xffu << (threadIdx.x & 24);  // of this row
-  for (int u = threadIdx.x / kLanes; u < n_tok * rows; u += kSlots) {
-    const int t = u / rows, h = u - t * rows;
-    const int64_t tok = tok0 + t;
-    const bool is_q = h < p.num_q_heads, is_v = h >= p.num_q_heads + p.num_kv_heads;
-    const int hk = is_q ? h : is_v ? h - p.num_q_heads - p.num_kv_heads : h - p.num_q_heads;
-    const uint16_t* src = (is_q ? p.q + tok * p.q_stride : is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride) +
-                          (size_t)hk * kHeadDim;
-    uint16_t* dst;
-    if (is_q) {
-      dst = p.q_out + (tok * p.num_q_heads + hk) * kHeadDim;
-    } else if constexpr (kAppend) {
-      const int64_t slot = p.slot_mapping[tok];
-      if (slot < 0) continue;
-      const int64_t block = slot / kPage;
-      if (block >= p.num_blocks) {
-        if (c == 0) record_error(p.err, PA_ERR_DEVICE_INDEX);
-        continue;
-      }
-      dst = (is_v ? p.v_cache : p.k_cache) + ((block * p.num_kv_heads + hk) * kPage + slot % kPage) * kHeadDim;
+  const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, half = p.rotary_dim / 2;
+  const int shares = (Hkv + heads - 1) / heads;  // units of a token
+  const int64_t units = p.n_tokens * shares, stride = (int64_t)gridDim.x * kWarps;
+  const int64_t first = (int64_t)blockIdx.x * kWarps + warp;
+  constexpr int kRow = kHeadDim * 2;
+  // unit u (the warp's k-th) on its way: q's rows, then k's, then v's (lane 0)
+  auto issue = [&](int64_t u, int k) {
+    if (u >= units) return;
+    const int64_t tok = u / shares;
+    const int h0 = (int)(u - tok * shares) * heads, n = min(heads, Hkv - h0);
+    uint64_t* bar = &sm.full[warp][k % kStages];
+    uint8_t* dst = sm.rows[warp][k % kStages];
+    mbar_arrive_expect_tx(bar, n * (kGroup + (kAppend ? 2 : 1)) * kRow);
+    bulk_g2s(dst, p.q + tok * p.q_stride + (size_t)h0 * kGroup * kHeadDim, n * kGroup * kRow, bar);
+    bulk_g2s(dst + n * kGroup * kRow, p.k + tok * p.k_stride + (size_t)h0 * kHeadDim, n * kRow, bar);
+    if constexpr (kAppend)
+      bulk_g2s(dst + n * (kGroup + 1) * kRow, p.v + tok * p.v_stride + (size_t)h0 * kHeadDim, n * kRow, bar);
+  };
+  if (lane == 0)
+    for (int k = 0; k < kStages; ++k) issue(first + k * stride, k);
+  int k = 0;
+  for (int64_t u = first; u < units; u += stride, ++k) {
+    const int64_t tok = u / shares;
+    const int h0 = (int)(u - tok * shares) * heads, n = min(heads, Hkv - h0);
+    int64_t slot = 0;
+    if constexpr (kAppend) slot = p.slot_mapping[tok];
+    Angles<kMode> t;
+    make_angles(p, p.rotary_dim > 0 ? p.positions[tok] : 0, t);
+    if (!mbar_wait_bounded(&sm.full[warp][k % kStages], (uint32_t)(k / kStages) & 1u)) {
+      record_error(p.err, PA_ERR_DEVICE_TIMEOUT);
+      // the copies in flight land before the warp leaves (bounded)
+      for (int j = k + 1; j < k + kStages; ++j)
+        if (first + j * stride < units) mbar_wait_bounded(&sm.full[warp][j % kStages], (uint32_t)(j / kStages) & 1u);
+      return;
+    }
+    const uint8_t* rows = sm.rows[warp][k % kStages];
+    rows_through(rows, n * kGroup, p.q_out + (tok * Hq + (size_t)h0 * kGroup) * kHeadDim, kHeadDim, p.q_weight, t, half,
+                 p.eps);
+    rows += n * kGroup * kRow;
+    if constexpr (!kAppend) {
+      rows_through(rows, n, p.k_out + (tok * Hkv + h0) * kHeadDim, kHeadDim, p.k_weight, t, half, p.eps);
     } else {
-      dst = p.k_out + (tok * p.num_kv_heads + hk) * kHeadDim;
+      const int64_t block = slot / kPage;
+      if (slot >= 0 && block < p.num_blocks) {
+        // a page's heads lie a slab apart
+        const size_t at = ((block * Hkv + h0) * kPage + slot % kPage) * kHeadDim;
+        constexpr size_t kStep = kPage * kHeadDim;
+        rows_through(rows, n, p.k_cache + at, kStep, p.k_weight, t, half, p.eps);
+        const int r = lane >> 4, c = lane & 15;
+        for (int i = r; i < n; i += 2)
+          *reinterpret_cast<uint4*>(p.v_cache + at + i * kStep + 8 * c) =
+              *reinterpret_cast<const uint4*>(rows + (n + i) * kRow + 16 * c);
+      } else if (slot >= 0 && lane == 0) {
+        record_error(p.err, PA_ERR_DEVICE_INDEX);
+      }
     }
-    uint4 lo = *reinterpret_cast<const uint4*>(src + 8 * c);
-    uint4 hi = *reinterpret_cast<const uint4*>(src + 64 + 8 * c);
-    if (!is_v) {
-      float y[16];
-      unpack8(lo, y);
-      unpack8(hi, y + 8);
-      const float* weight = is_q ? p.q_weight : p.k_weight;
-      if (weight) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(lanes, ss, o);
-        const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] *= r * weight[(i < 8 ? 8 * c : 56 + 8 * c) + i];
-      }
-      float z[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d = (i < 8 ? 8 * c : 56 + 8 * c) + i;
-        z[i] = y[i];
-        if constexpr (kInter) {
-          if (d < p.rotary_dim) {
-            const float2 w = cs[t][d / 2];
-            z[i] = (i & 1) ? fmaf(y[i], w.x, y[i ^ 1] * w.y) : fmaf(y[i], w.x, -y[i ^ 1] * w.y);
-          }
-        }
-      }
-      if constexpr (!kInter) {
-        // dims come in chunks of 8, chunk e = c or 8 + c; its partner lies half / 8
-        // chunks away
-        const int far = half / 8;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int e = 8 * s + c;
-          const bool low = e < far, turned = e < 2 * far;
-          const int pe = !turned ? e : low ? e + far : e - far;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int from = (threadIdx.x & 24) + (pe & 7);
-            const float p0 = __shfl_sync(lanes, y[i], from), p1 = __shfl_sync(lanes, y[8 + i], from);
-            const float other = pe >> 3 ? p1 : p0;
-            if (turned) {
-              const float2 w = cs[t][(low ? e : pe) * 8 + i];
-              z[8 * s + i] = fmaf(y[8 * s + i], w.x, low ? -other * w.y : other * w.y);
-            }
-          }
-        }
-      }
-      lo = pack8(z);
-      hi = pack8(z + 8);
+    __syncwarp();  // every lane has read the unit
+    if (lane == 0) {
+      fence_proxy_async_smem();
+      issue(u + kStages * stride, k + kStages);
     }
-    *reinterpret_cast<uint4*>(dst + 8 * c) = lo;
-    *reinterpret_cast<uint4*>(dst + 64 + 8 * c) = hi;
   }
+}
+
+std::atomic<bool> g_attr_set[2][3][kMaxDevices];
+
+template <bool kAppend, Mode kMode>
+cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
+  constexpr int64_t kResident = 152 * kCtas * kWarps;  // warps that the SMs hold at once
+  constexpr size_t kBytes = sizeof(Smem<kAppend>);
+  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "resident CTAs");
+  const cudaError_t e = set_smem_limit_once((const void*)norm_rope_kernel<kAppend, kMode>, (int)kBytes,
+                                            g_attr_set[kAppend][(int)kMode]);
+  if (e != cudaSuccess) return e;
+  // as many kv heads a unit as leave a unit to every warp
+  int heads = kHeads;
+  while (heads > 1 && p.n_tokens * ((p.num_kv_heads + heads - 1) / heads) < kResident) heads /= 2;
+  const int64_t units = p.n_tokens * ((p.num_kv_heads + heads - 1) / heads);
+  const int64_t warps = units < kResident ? units : kResident;
+  return launch_pdl(norm_rope_kernel<kAppend, kMode>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads),
+                    kBytes, stream, p, heads);
+}
+
+template <bool kAppend>
+cudaError_t launch_mode(const RopeParams& p, bool interleaved, cudaStream_t stream) {
+  if (interleaved) return launch<kAppend, Mode::kPairs>(p, stream);
+  if (p.rotary_dim == kHeadDim || p.rotary_dim == 0) return launch<kAppend, Mode::kFull>(p, stream);
+  return launch<kAppend, Mode::kPart>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved, cudaStream_t stream) {
-  const int rows = p.num_q_heads + (append ? 2 : 1) * p.num_kv_heads;
-  const int per = rows >= kSlots ? 1 : kSlots / rows;
-  const dim3 grid((unsigned)((p.n_tokens + per - 1) / per));
-  if (append)
-    return interleaved ? launch_pdl(norm_rope_kernel<true, true>, grid, dim3(kThreads), 0, stream, p, per)
-                       : launch_pdl(norm_rope_kernel<true, false>, grid, dim3(kThreads), 0, stream, p, per);
-  return interleaved ? launch_pdl(norm_rope_kernel<false, true>, grid, dim3(kThreads), 0, stream, p, per)
-                     : launch_pdl(norm_rope_kernel<false, false>, grid, dim3(kThreads), 0, stream, p, per);
+  return append ? launch_mode<true>(p, interleaved, stream) : launch_mode<false>(p, interleaved, stream);
 }
 
 }  // namespace pa

@@ -1372,6 +1372,7 @@ pa_status pa_step_tables(const int32_t* new_tokens, const int32_t* cached_lens, 
   p.positions = positions;
   p.free_state_out = free_state_out;
   p.first_page_out = first_page_out;
+  p.in_place = seq_lens == cached_lens || free_state_out == free_state || (first_page && first_page_out == first_page);
   p.err = static_cast<int*>(workspace);
   p.arrived = static_cast<int*>(workspace) + PA_ERROR_WORD_BYTES / 8;  // in the error word's block, away from it
   const pa_status s =

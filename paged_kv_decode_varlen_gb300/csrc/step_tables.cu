@@ -3,58 +3,58 @@
 //
 // What is computed: exclusive sums over the requests of their new tokens, of the
 // pages these need (ceil((c + n) / 16) - ceil(c / 16)) and of the pages given back,
-// and from them every token's, granted page's and returned page's place: three
-// flat lists, each entry of which finds its request by a search in the sums.
+// and from them every token's, granted page's and returned page's place.
 //
-// Bound: latency.  The lists are short (a decode step of 64 requests moves 3 KB, a
-// step of 8 Ki tokens 130 KB), so what counts is one launch and few dependent round
-// trips: lengths -> sums -> ring or table entry -> store.  Every CTA of the launch
-// makes all sums for itself from the lengths (R <= 1024: one load of each array
-// per thread) and takes its share of the three lists; no CTA waits for another.
-// The last one to arrive at a count writes what may lie where the others still had
-// to read (lengths, ring state), so that these outputs may be their inputs.
-#include "internal.h"
+// Bound: latency.  A decode step of 64 requests moves 3 KB, a step of 8 Ki tokens 130
+// KB, so what counts is one launch and few dependent round trips: lengths -> sums ->
+// ring or table entry -> store.  Every CTA of the launch makes all sums for itself from
+// the lengths and takes its share of the work; no CTA waits for another.
+//   A thread has one request (kMany: several, one after another).  A request of at most
+// one new token and one returned page is seen to by its own thread, whose table entry
+// is fetched while the sums are made.  The tokens and pages of the others are three flat
+// lists, each entry of which finds its request by a search in the sums: a prompt of
+// thousands of tokens is spread over all threads.
+//   Where an output is the array it is made from (lengths, ring state, first pages), the
+// last CTA to arrive at a count writes it, as the others may still have to read it.
+#include <type_traits>
 
 #include "common.cuh"
+#include "internal.h"
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-
 // One request's step.
 struct Row {
-  int cached, n;        // tokens before, new tokens
-  int had, has;         // pages before, after
-  int a_lo, a_hi;       // pages given back: [a_lo, a_hi), then [b_lo, b_hi)
+  int cached, n;   // tokens before, new tokens
+  int had, has;    // pages before, after
+  int a_lo, a_hi;  // pages given back: [a_lo, a_hi), then [b_lo, b_hi)
   int b_lo, b_hi;
-  int seq, first;       // what it holds after the step
+  int seq, first;  // what it holds after the step
+  bool bad, ended;
   __device__ __forceinline__ int granted() const { return has - had; }
   __device__ __forceinline__ int back() const { return a_hi - a_lo + (b_hi - b_lo); }
 };
 
-// `wait`: every row is taken as one that brings nothing.
-__device__ __forceinline__ Row row_of(const TablesParams& p, int r, bool wait, bool* bad) {
+// raw: the request's entry of new_tokens; wait: it is taken as one that brings nothing.
+__device__ __forceinline__ Row row_of(const TablesParams& p, int raw, int c, int first, bool wait) {
   Row w;
-  const int raw = p.new_tokens[r], c = p.cached_lens[r];
-  const int first = p.first_page ? max(p.first_page[r], 0) : 0;
+  first = max(first, 0);
   const int c_max = min(p.max_blocks_per_req, PA_MAX_SEQ_LEN / kPage) * kPage;
   const bool c_bad = c < 0 || c > c_max;
-  const bool n_bad = !c_bad && raw > c_max - c;
-  if (bad) *bad = c_bad || n_bad;
+  w.bad = c_bad || raw > c_max - c;  // (c_max - c does not overflow where c is not bad)
   w.cached = c_bad ? 0 : c;
-  w.n = (c_bad || n_bad || wait) ? 0 : max(raw, 0);
-  const bool ended = raw < 0 && !c_bad && !wait;
+  w.n = (w.bad || wait) ? 0 : max(raw, 0);
+  w.ended = raw < 0 && !c_bad && !wait;
   w.had = (w.cached + kPage - 1) / kPage;
   w.has = (w.cached + w.n + kPage - 1) / kPage;
-  const int sinks = p.window > 0 ? (int)(((int64_t)p.sink_tokens + kPage - 1) / kPage) : 0;
+  const int sinks = p.window > 0 ? p.sink_tokens / kPage + (p.sink_tokens % kPage != 0) : 0;
   const int keep = max(sinks, p.shared_pages);
   w.a_lo = w.a_hi = w.b_lo = w.b_hi = 0;
   w.seq = w.cached + w.n;
   w.first = first;
   const int from = max(first, keep);
-  if (ended) {
+  if (w.ended) {
     w.a_lo = min(p.shared_pages, w.had);
     w.a_hi = max(w.a_lo, min(keep, w.had));
     w.b_lo = min(from, w.had);
@@ -72,22 +72,31 @@ __device__ __forceinline__ Row row_of(const TablesParams& p, int r, bool wait, b
   return w;
 }
 
+// The three sums; T holds them for the requests of a launch (2^20 tokens and 2^16 pages
+// each at most: 32 bits for up to 1024 requests, 64 for more).
+template <class T>
 struct Sums {
-  int64_t tok, grant, back;
+  T tok, grant, back;
+  __device__ __forceinline__ Sums operator+(const Sums& b) const { return {tok + b.tok, grant + b.grant, back + b.back}; }
 };
-__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
-  return {a.tok + b.tok, a.grant + b.grant, a.back + b.back};
+template <class T>
+__device__ __forceinline__ Sums<T> shfl_up(const Sums<T>& a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.tok, o), __shfl_up_sync(0xffffffffu, a.grant, o),
+          __shfl_up_sync(0xffffffffu, a.back, o)};
 }
 
+constexpr int kMaxThreads = 1024;
+
+template <class T>
 struct Smem {
-  Sums warp[kWarps];
-  // start of each thread's first request in the three lists, and their ends
-  int tok[kThreads + 1], grant[kThreads + 1], back[kThreads + 1];
+  Sums<T> warp[32];
+  // start of each thread's first request in the three lists
+  int tok[kMaxThreads], grant[kMaxThreads], back[kMaxThreads];
+  int raw[kMaxThreads], cached[kMaxThreads], first[kMaxThreads];  // (one request per thread)
   int last;
 };
 
-// The thread whose requests hold entry i of a list: the last with start <= i among
-// `n` threads (of equal starts, the one that holds anything).
+// The thread whose requests hold entry i of a list: the last of n with start <= i.
 __device__ __forceinline__ int find(const int* start, int n, int i) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -97,56 +106,78 @@ __device__ __forceinline__ int find(const int* start, int n, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesParams p) {
+template <bool kMany>
+__global__ void __launch_bounds__(kMaxThreads, 1) step_tables_kernel(const TablesParams p) {
+  using T = typename std::conditional<kMany, int64_t, int32_t>::type;
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ Smem sm;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int R = p.num_reqs, per = (R + kThreads - 1) / kThreads;  // consecutive requests per thread
+  __shared__ Smem<T> sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_thr = (int)blockDim.x;
+  const int R = p.num_reqs, per = kMany ? (R + n_thr - 1) / n_thr : 1;  // consecutive requests per thread
   const int r0 = min(tid * per, R), r1 = min(r0 + per, R);
   const int head = p.free_state[0], count = p.free_state[1], cap = p.num_blocks;
+  auto load = [&](int r, bool wait) {
+    return row_of(p, p.new_tokens[r], p.cached_lens[r], p.first_page ? p.first_page[r] : 0, wait);
+  };
   // ---- sums over the requests
-  Sums own{0, 0, 0};
-  bool any_bad = false;
-  for (int r = r0; r < r1; ++r) {
-    bool bad;
-    const Row w = row_of(p, r, false, &bad);
-    any_bad = any_bad || bad;
-    own = own + Sums{w.n, w.granted(), w.back()};
+  Sums<T> own{0, 0, 0};
+  bool any_bad = false, listed = false;  // a request for the lists
+  Row mine{};  // the thread's request (!kMany)
+  bool small = false;
+  int entry = -1;  // its table entry of position `cached`
+  if constexpr (kMany) {
+    for (int r = r0; r < r1; ++r) {
+      const Row w = load(r, false);
+      any_bad = any_bad || w.bad;
+      own = own + Sums<T>{w.n, w.granted(), w.back()};
+    }
+    listed = true;
+  } else if (r0 < R) {
+    const int raw = p.new_tokens[r0], c = p.cached_lens[r0], first = p.first_page ? p.first_page[r0] : 0;
+    mine = row_of(p, raw, c, first, false);
+    small = !mine.ended && mine.n <= 1 && mine.back() <= 1;
+    if (small && mine.n == 1 && mine.granted() == 0)
+      entry = p.block_tables[(size_t)r0 * p.max_blocks_per_req + mine.cached / kPage];
+    sm.raw[tid] = raw;
+    sm.cached[tid] = c;
+    sm.first[tid] = first;
+    any_bad = mine.bad;
+    listed = !small;
+    own = Sums<T>{mine.n, mine.granted(), mine.back()};
   }
-  Sums incl = own;
+  Sums<T> incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums y{__shfl_up_sync(0xffffffffu, incl.tok, o), __shfl_up_sync(0xffffffffu, incl.grant, o),
-                 __shfl_up_sync(0xffffffffu, incl.back, o)};
+    const Sums<T> y = shfl_up(incl, o);
     if (lane >= o) incl = incl + y;
   }
   if (lane == 31) sm.warp[warp] = incl;
-  __syncthreads();
-  Sums before{0, 0, 0}, all{0, 0, 0};
-#pragma unroll 8
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = all;
-    all = all + sm.warp[w];
+  const bool lists = __syncthreads_or(listed) != 0;
+  Sums<T> w_incl = lane < n_thr / 32 ? sm.warp[lane] : Sums<T>{0, 0, 0};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums<T> y = shfl_up(w_incl, o);
+    if (lane >= o) w_incl = w_incl + y;
   }
-  before = before + incl;  // (inclusive)
+  auto of_lane = [&](int l) {
+    return Sums<T>{__shfl_sync(0xffffffffu, w_incl.tok, l), __shfl_sync(0xffffffffu, w_incl.grant, l),
+                   __shfl_sync(0xffffffffu, w_incl.back, l)};
+  };
+  const Sums<T> all = of_lane(31), prev = of_lane(max(warp - 1, 0));
+  const Sums<T> before = (warp > 0 ? prev : Sums<T>{0, 0, 0}) + incl;  // inclusive
   const bool state_bad = head < 0 || head >= cap || count < 0 || count > cap;
-  const int64_t left = max((int64_t)count - all.grant, (int64_t)0);
+  const int64_t left = max((int64_t)count - (int64_t)all.grant, (int64_t)0);
   // nothing is done where it could not be done in bounds
-  const bool wait = state_bad || all.tok > p.n_tokens || left + all.back > cap;
+  const bool wait = state_bad || all.tok > p.n_tokens || left + (int64_t)all.back > cap;
   const int total = wait ? 0 : (int)all.tok, grants = wait ? 0 : (int)all.grant, backs = wait ? 0 : (int)all.back;
-  const int given = state_bad ? 0 : min(grants, count);  // ids the ring can give
+  const int given = min(grants, max(count, 0));  // ids the ring can give
   if (blockIdx.x == 0 && any_bad) record_error(p.err, PA_ERR_DEVICE_INDEX);
   if (blockIdx.x == 0 && tid == 0) {
     if (wait) record_error(p.err, PA_ERR_DEVICE_INDEX);
     else if (given < grants) record_error(p.err, PA_ERR_DEVICE_NO_BLOCKS);
   }
-  sm.tok[tid] = wait ? 0 : (int)(before.tok - own.tok);
-  sm.grant[tid] = wait ? 0 : (int)(before.grant - own.grant);
-  sm.back[tid] = wait ? 0 : (int)(before.back - own.back);
-  __syncthreads();
-  const int used = (R + max(per, 1) - 1) / max(per, 1);  // threads that hold requests
-  const int step = (int)gridDim.x * kThreads, i0 = (int)blockIdx.x * kThreads + tid;
+  const int tok0 = wait ? 0 : (int)(before.tok - own.tok), grant0 = wait ? 0 : (int)(before.grant - own.grant),
+            back0 = wait ? 0 : (int)(before.back - own.back);
   // id of grant g, -1 if there is none
   auto granted_id = [&](int g) -> int {
     if (g >= given) return -1;
@@ -159,73 +190,96 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     }
     return id;
   };
-  // ---- tokens
-  for (int i = i0; i < p.n_tokens; i += step) {
-    int64_t slot = -1;
-    int pos = 0;
-    if (i < total) {
-      const int t = find(sm.tok, used, i);
-      int r = t * per, s = sm.tok[t], g = sm.grant[t];
-      Row w = row_of(p, r, false, nullptr);
-      while (i >= s + w.n) {  // (ends: the thread's requests hold entry i)
-        s += w.n;
-        g += w.granted();
-        w = row_of(p, ++r, false, nullptr);
+  auto give_back = [&](int i, int id) { p.free_ring[((int64_t)head + count + i) % cap] = id; };
+
+  if (!kMany && small && !wait && warp % (int)gridDim.x == (int)blockIdx.x) {
+    // a request of its own thread; its ring entry is one more round trip only where the
+    // token opens a page
+    if (mine.back() == 1)
+      give_back(back0, p.block_tables[(size_t)r0 * p.max_blocks_per_req + (mine.a_hi > mine.a_lo ? mine.a_lo : mine.b_lo)]);
+    if (mine.n == 1) {
+      if (mine.granted() == 1) {
+        entry = granted_id(grant0);
+        p.block_tables[(size_t)r0 * p.max_blocks_per_req + mine.had] = entry;
       }
-      pos = w.cached + (i - s);
-      const int page = pos / kPage;
+      p.slot_mapping[tok0] = entry >= 0 ? (int64_t)entry * kPage + mine.cached % kPage : -1;
+      p.positions[tok0] = mine.cached;
+    }
+  }
+  const int step = (int)gridDim.x * n_thr, i0 = (int)blockIdx.x * n_thr + tid;
+  if (lists && !wait) {
+    sm.tok[tid] = tok0;
+    sm.grant[tid] = grant0;
+    sm.back[tid] = back0;
+    __syncthreads();
+    const int used = (R + per - 1) / per;  // threads that hold requests
+    // entry i of a list (start: its sums; size: a request's share): its request r, whose
+    // entries begin at s, and the request's first grant
+    auto locate = [&](const int* start, auto size, int i, int& r, int& s, int& g, Row& w) -> bool {
+      const int t = find(start, used, i);
+      s = start[t];
+      g = sm.grant[t];
+      r = t * per;
+      if constexpr (kMany) {
+        w = load(r, false);
+        while (i >= s + size(w)) {  // (ends: the thread's requests hold entry i)
+          s += size(w);
+          g += w.granted();
+          w = load(++r, false);
+        }
+        return true;
+      } else {
+        w = row_of(p, sm.raw[t], sm.cached[t], sm.first[t], false);
+        return w.ended || w.n > 1 || w.back() > 1;  // (not seen to by its own thread)
+      }
+    };
+    int r, s, g;
+    Row w;
+    for (int i = i0; i < total; i += step) {
+      if (!locate(sm.tok, [](const Row& x) { return x.n; }, i, r, s, g, w)) continue;
+      const int pos = w.cached + (i - s), page = pos / kPage;
       const int id = page >= w.had ? granted_id(g + page - w.had) : p.block_tables[(size_t)r * p.max_blocks_per_req + page];
-      if (id >= 0) slot = (int64_t)id * kPage + pos % kPage;
+      p.slot_mapping[i] = id >= 0 ? (int64_t)id * kPage + pos % kPage : -1;
+      p.positions[i] = pos;
     }
-    p.slot_mapping[i] = slot;
-    p.positions[i] = pos;
+    for (int i = i0; i < grants; i += step)
+      if (locate(sm.grant, [](const Row& x) { return x.granted(); }, i, r, s, g, w))
+        p.block_tables[(size_t)r * p.max_blocks_per_req + w.had + (i - s)] = granted_id(i);
+    for (int i = i0; i < backs; i += step)  // (their entries are no granted ones)
+      if (locate(sm.back, [](const Row& x) { return x.back(); }, i, r, s, g, w)) {
+        const int a = w.a_hi - w.a_lo;
+        const int page = i - s < a ? w.a_lo + (i - s) : w.b_lo + (i - s - a);
+        give_back(i, p.block_tables[(size_t)r * p.max_blocks_per_req + page]);
+      }
   }
-  // ---- pages granted
-  for (int i = i0; i < grants; i += step) {
-    const int t = find(sm.grant, used, i);
-    int r = t * per, s = sm.grant[t];
-    Row w = row_of(p, r, false, nullptr);
-    while (i >= s + w.granted()) {
-      s += w.granted();
-      w = row_of(p, ++r, false, nullptr);
-    }
-    p.block_tables[(size_t)r * p.max_blocks_per_req + w.had + (i - s)] = granted_id(i);
+  for (int i = total + i0; i < p.n_tokens; i += step) {  // padding
+    p.slot_mapping[i] = -1;
+    p.positions[i] = 0;
   }
-  // ---- pages given back (their entries are no granted ones)
-  for (int i = i0; i < backs; i += step) {
-    const int t = find(sm.back, used, i);
-    int r = t * per, s = sm.back[t];
-    Row w = row_of(p, r, false, nullptr);
-    while (i >= s + w.back()) {
-      s += w.back();
-      w = row_of(p, ++r, false, nullptr);
-    }
-    const int a = w.a_hi - w.a_lo;
-    const int page = i - s < a ? w.a_lo + (i - s) : w.b_lo + (i - s - a);
-    p.free_ring[((int64_t)head + count + i) % cap] = p.block_tables[(size_t)r * p.max_blocks_per_req + page];
-  }
-  // ---- offsets
+  // ---- offsets, and what follows the step
   if (blockIdx.x == 0) {
-    int s = sm.tok[tid];
+    int s = tok0;
     for (int r = r0; r < r1; ++r) {
       p.qo_indptr[r] = s;
-      s += wait ? 0 : row_of(p, r, false, nullptr).n;
+      s += kMany ? load(r, wait).n : 0;
     }
     if (tid == 0) p.qo_indptr[R] = total;
   }
-  // ---- what the other CTAs read: written by the last one to get here
-  __syncthreads();
-  if (tid == 0) {
-    sm.last = 1;
-    if (gridDim.x > 1) {
+  if (p.in_place && gridDim.x > 1) {
+    // the other CTAs may still read what is written now: the last one to get here does
+    __syncthreads();
+    if (tid == 0) {
       sm.last = atom_add_acq_rel_gpu(p.arrived, 1) == (int)gridDim.x - 1;
       if (sm.last) *p.arrived = 0;
     }
+    __syncthreads();
+    if (!sm.last) return;
+  } else {
+    if (blockIdx.x > 0) return;
+    if (p.in_place) __syncthreads();  // (every thread has read its requests and the ring's state)
   }
-  __syncthreads();
-  if (!sm.last) return;
   for (int r = r0; r < r1; ++r) {
-    const Row w = row_of(p, r, wait, nullptr);
+    const Row w = kMany ? load(r, wait) : wait ? row_of(p, sm.raw[tid], sm.cached[tid], sm.first[tid], true) : mine;
     p.seq_lens[r] = w.seq;
     if (p.first_page_out) p.first_page_out[r] = w.first;
   }
@@ -238,10 +292,14 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
 }  // namespace
 
 cudaError_t launch_step_tables(const TablesParams& p, cudaStream_t stream) {
+  // a thread per request, and up to 1024 tokens a CTA
   const int64_t work = p.n_tokens > p.num_reqs ? p.n_tokens : p.num_reqs;
-  int64_t grid = (work + kThreads - 1) / kThreads;
+  const int threads = work <= 128 ? 128 : work <= 256 ? 256 : kMaxThreads;
+  int64_t grid = (p.n_tokens + kMaxThreads - 1) / kMaxThreads;
   grid = grid < 1 ? 1 : grid > 128 ? 128 : grid;
-  return launch_pdl(step_tables_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+  if (p.num_reqs > kMaxThreads)
+    return launch_pdl(step_tables_kernel<true>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
+  return launch_pdl(step_tables_kernel<false>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
 }
 
 }  // namespace pa
