@@ -50,24 +50,8 @@ template <int NT>
 struct Cfg {
   static constexpr int kQueries = NT == 1 ? 1 : 2 * NT;
   static constexpr int kCols = kQueries * kGroup;
-#ifndef W1
-#define W1 7
-#define S1 3
-#endif
-#ifndef W2
-#define W2 8
-#define S2 2
-#endif
-#ifndef W3
-#define W3 7
-#define S3 2
-#endif
-#ifndef W4
-#define W4 5
-#define S4 2
-#endif
-  static constexpr int kWarps = NT == 1 ? W1 : NT == 2 ? W2 : NT == 3 ? W3 : W4;
-  static constexpr int kStages = NT == 1 ? S1 : NT == 2 ? S2 : NT == 3 ? S3 : S4;
+  static constexpr int kWarps = NT <= 2 ? 8 : NT == 3 ? 4 : 5;
+  static constexpr int kStages = NT == 3 ? 3 : 2;
   static constexpr int kBufs = NT == 1 ? 2 : 1;
   static constexpr bool kQRegs = NT <= 2;  // q's fragments kept in registers
   static constexpr int kThreads = (kWarps + kMergeWarps + 1) * 32;

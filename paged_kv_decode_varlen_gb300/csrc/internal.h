@@ -257,6 +257,9 @@ struct WindowParams {
   float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
   int32_t piece_cols;  // (query, head) columns of a piece
   int* counters;       // [num_reqs, Hkv, 2] pieces that have arrived; zero between calls
+  // the tile kernel's parts of jobs cut between CTAs: [2 x CTAs][2 query tiles][128 rows]
+  float* part_o;    // ... x D fp32, 4 dims of neighbouring rows side by side
+  float* part_lse;  // log2 domain
   int* err;
 };
 // Rows of up to this many queries run the decode kernel with a window.
@@ -264,12 +267,22 @@ constexpr int kWindowDecodeQueries = 8;
 // The items of a tile launch: request, first query token, its position, queries (up to
 // kWindowTileTokens).
 constexpr int kWindowTileTokens = 64;
-struct WindowItems {
-  int32_t count;
-  int32_t pad[3];
-  int4 item[kMaxPrefillItems];
-};
 constexpr int kWindowMaxSms = 256;  // (workspace sizing; more SMs are not used)
+// ... and how the jobs (job u: item u / Hkv, kv head u % Hkv) are shared: whole, in
+// rounds of one per CTA, or CTA b from key tile start[b].y of job start[b].x to where CTA
+// b + 1 begins (no share is empty).
+struct WindowItems {
+  int32_t count, pad[3];
+  int4 item[kMaxPrefillItems];
+  int2 start[kWindowMaxSms + 1];
+};
+// A job that CTAs b0 .. b0 + parts - 1 have parts of, and where the first of these lies.
+struct WindowCut {
+  int32_t tok0, nq, kvh, b0, parts, slot0;
+};
+struct WindowCuts {
+  WindowCut cut[kWindowMaxSms];
+};
 
 struct PrefillParams {
   const uint16_t* q;
@@ -439,9 +452,12 @@ cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved,
 // rows of up to `queries` queries on grid CTAs, a multiple of the kv heads
 cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream);
 
-// (item, kv head) jobs of rows of more queries on ctas CTAs
-cudaError_t launch_prefill_window(const WindowParams& p, const WindowItems& items, const TcMaps& maps,
+// the (item, kv head) jobs of rows of more queries, shared by ctas CTAs
+cudaError_t launch_prefill_window(const WindowParams& p, const WindowItems& items, bool cut, const TcMaps& maps,
                                   const CUtensorMap& out_map, int ctas, cudaStream_t stream);
+
+// ... and the outputs of n cut jobs from their parts
+cudaError_t launch_merge_window(const WindowParams& p, const WindowCuts& cuts, int n, cudaStream_t stream);
 
 // Query tile of the tensor-core tile kernels (query tokens per CTA: with the
 // 4 heads of a GQA group, 128 rows = the MMA's M) and their key tile.

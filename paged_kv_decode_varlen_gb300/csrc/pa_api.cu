@@ -1249,10 +1249,11 @@ pa_status norm_rope(pa::RopeParams& p, bool append, int32_t interleaved, int32_t
 }
 
 // Workspace of the attention with a window: [error word | counts (num_reqs x Hkv x
-// 2 int32) | pieces of rows cut between CTAs, two per CTA (columns x D fp32) | their
-// lse].
+// 2 int32) | pieces of rows cut between CTAs, two per CTA (columns x D fp32) | their lse |
+// and for the tile kernel, parts of jobs cut between CTAs, two per CTA (2 x 128 rows x D
+// fp32) | their lse].
 struct WindowLayout {
-  size_t counters, piece_o, piece_lse, total;
+  size_t counters, piece_o, piece_lse, part_o, part_lse, total;
   int32_t cols;
 };
 WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_heads) {
@@ -1263,11 +1264,27 @@ WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_head
   w.counters = PA_ERROR_WORD_BYTES;
   w.piece_o = w.counters + align256((size_t)num_reqs * hkv * 2 * 4);
   w.piece_lse = w.piece_o + slots * pa::kHeadDim * 4;
-  w.total = w.piece_lse + align256(slots * 4);
+  // jobs of rows for the tile kernel: two parts a CTA
+  const size_t parts = total_q > pa::kWindowDecodeQueries ? (size_t)2 * std::min(sm_count(), pa::kWindowMaxSms) : 0;
+  w.part_o = w.piece_lse + align256(slots * 4);
+  w.part_lse = w.part_o + parts * 2 * 128 * pa::kHeadDim * 4;
+  w.total = w.part_lse + parts * 2 * 128 * 4;
   return w;
 }
 
-// The tile launches of the rows of more than kWindowDecodeQueries queries.
+// Key tiles of an item (request, first query token, its position, queries).
+int window_item_tiles(const pa::WindowParams& p, const int4& it) {
+  constexpr int kPages = pa::kTcKeyTile / pa::kPage;
+  return (pa::seen_pages(it.z + it.w, it.w, p.window, p.sink_tokens).count() + kPages - 1) / kPages;
+}
+// What a job costs beside its key tiles, in tiles.
+constexpr int kWindowJobCost = 3;
+// What cutting jobs costs beside: a share's ends are jobs of their own, their parts are
+// written and merged.
+constexpr int kWindowCutCost = 14;
+
+// The tile launches of the rows of more than kWindowDecodeQueries queries: the jobs' key
+// tiles as one stream, cut into equal shares.
 pa_status window_tiles(const pa::WindowParams& p, const int32_t* seq_lens_host, const int32_t* qo_indptr_host,
                        cudaStream_t stream) {
   static thread_local pa::TcMaps maps;
@@ -1276,24 +1293,80 @@ pa_status window_tiles(const pa::WindowParams& p, const int32_t* seq_lens_host, 
   if (s == PA_OK) s = make_q_map(p.out, p.total_q, p.num_q_heads, pa::kQ4OutTok, out_map);
   if (s != PA_OK) return s;
   static thread_local pa::WindowItems items;
-  std::vector<std::pair<int32_t, int4>> all;  // (pages, item)
+  std::vector<int4> all;
   for (int32_t r = 0; r < p.num_reqs; ++r) {
     const int32_t n = qo_indptr_host[r + 1] - qo_indptr_host[r];
     if (n <= pa::kWindowDecodeQueries) continue;
-    for (int32_t j = 0; j < n; j += pa::kWindowTileTokens) {
-      const int32_t nq = std::min(n - j, pa::kWindowTileTokens), pos = seq_lens_host[r] - n + j;
-      all.push_back({pa::seen_pages(pos + nq, nq, p.window, p.sink_tokens).count(),
-                     make_int4(r, qo_indptr_host[r] + j, pos, nq)});
-    }
+    for (int32_t j = 0; j < n; j += pa::kWindowTileTokens)
+      all.push_back(make_int4(r, qo_indptr_host[r] + j, seq_lens_host[r] - n + j, std::min(n - j, pa::kWindowTileTokens)));
   }
-  // the longest first, so that they do not form the tail
-  std::stable_sort(all.begin(), all.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
+  std::vector<std::pair<int32_t, int32_t>> order;  // (-key tiles, item) of a launch
+  std::vector<int64_t> before, load;               // cost of the items before; of a CTA's whole jobs; in key tiles
   for (size_t base = 0; base < all.size(); base += pa::kMaxPrefillItems) {
-    items.count = (int32_t)std::min(all.size() - base, (size_t)pa::kMaxPrefillItems);
-    for (int32_t i = 0; i < items.count; ++i) items.item[i] = all[base + (size_t)i].second;
-    const int ctas = (int)std::min<int64_t>((int64_t)items.count * p.num_kv_heads, sm_count());
+    const int count = (int)std::min(all.size() - base, (size_t)pa::kMaxPrefillItems);
+    const int64_t jobs = (int64_t)count * p.num_kv_heads;
+    before.assign(1, 0);
+    order.clear();
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+      const int n = window_item_tiles(p, all[base + (size_t)i]);
+      tiles += n;
+      order.push_back({-n, i});
+      before.push_back(before.back() + (int64_t)(n + kWindowJobCost) * p.num_kv_heads);
+    }
+    items.count = count;
+    // whole jobs, the longest first, in rounds of one per SM
+    const int sms = std::min(sm_count(), pa::kWindowMaxSms);
+    const int whole_ctas = (int)std::min<int64_t>(jobs, sms);
+    std::stable_sort(order.begin(), order.end());
+    load.assign((size_t)whole_ctas, 0);
+    for (int64_t u = 0; u < jobs; ++u) {
+      const int64_t rnd = u / whole_ctas, b = u % whole_ctas;
+      load[(size_t)((rnd & 1) ? whole_ctas - 1 - b : b)] += kWindowJobCost - order[(size_t)(u / p.num_kv_heads)].first;
+    }
+    // or a share of all key tiles per SM, three tiles at least where that cuts jobs
+    const int ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(jobs, tiles * p.num_kv_heads / 3));
+    if (*std::max_element(load.begin(), load.end()) <= before.back() / ctas + kWindowCutCost) {
+      for (int i = 0; i < count; ++i) items.item[i] = all[base + (size_t)order[(size_t)i].second];
+      s = run_launch(PA_KERNEL_PREFILL, "prefill_window", stream,
+                     [&] { return pa::launch_prefill_window(p, items, false, maps, out_map, whole_ctas, stream); });
+      if (s != PA_OK) return s;
+      continue;
+    }
+    for (int i = 0; i < count; ++i) items.item[i] = all[base + (size_t)i];
+    int n = 1;  // shares begun
+    items.start[0] = make_int2(0, 0);
+    for (int b = 1, i = 0; b < ctas; ++b) {
+      const int64_t at = before.back() * b / ctas;
+      while (before[(size_t)i + 1] <= at) ++i;
+      const int all_tiles = window_item_tiles(p, items.item[i]), cost = all_tiles + kWindowJobCost;
+      const int kvh = (int)((at - before[(size_t)i]) / cost), r = (int)((at - before[(size_t)i]) % cost);
+      int2 s = make_int2(i * p.num_kv_heads + kvh, std::max(r - kWindowJobCost, 0));
+      if (s.y < 2) s.y = 0;  // no part of a tile or two
+      else if (all_tiles - s.y < 2) s = make_int2(s.x + 1, 0);
+      const int2 last = items.start[n - 1];
+      if (s.x < (int)jobs && (s.x > last.x || (s.x == last.x && s.y > last.y))) items.start[n++] = s;
+    }
+    items.start[n] = make_int2((int)jobs, 0);
+    // the jobs that are cut: shares that begin inside one
+    static thread_local pa::WindowCuts cuts;
+    int n_cuts = 0;
+    for (int b = 1; b < n;) {
+      if (items.start[b].y == 0) {
+        ++b;
+        continue;
+      }
+      const int u = items.start[b].x, b0 = b - 1;
+      while (b < n && items.start[b].x == u) ++b;
+      const int4 it = items.item[u / p.num_kv_heads];
+      cuts.cut[n_cuts++] =
+          pa::WindowCut{it.y, it.w, u % p.num_kv_heads, b0, b - b0, 2 * b0 + (items.start[b0].x == u ? 0 : 1)};
+    }
     s = run_launch(PA_KERNEL_PREFILL, "prefill_window", stream,
-                   [&] { return pa::launch_prefill_window(p, items, maps, out_map, ctas, stream); });
+                   [&] { return pa::launch_prefill_window(p, items, true, maps, out_map, n, stream); });
+    if (s == PA_OK && n_cuts > 0)
+      s = run_launch(PA_KERNEL_MERGE, "merge_window", stream,
+                     [&] { return pa::launch_merge_window(p, cuts, n_cuts, stream); });
     if (s != PA_OK) return s;
   }
   return PA_OK;
@@ -1521,6 +1594,8 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
   p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
   p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
   p.piece_cols = wl.cols;
+  p.part_o = reinterpret_cast<float*>(ws + wl.part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse);
   try {
     if (many > 0) s = window_tiles(p, seq_lens_host, qo_indptr_host, stream);
   } catch (const std::bad_alloc&) {  // of the plan's host arrays

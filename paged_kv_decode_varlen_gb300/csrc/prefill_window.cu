@@ -8,9 +8,13 @@
 // B of 32 tokens x 4 heads = 128 rows, the M of one tcgen05.mma each (a job of up to 32
 // has A alone).  The pages that any of its queries sees (leading ones, then from the
 // first query's window on) are counted through and go in key tiles of 128 (8 pages), so a
-// job costs its window and its own length, not its context.  One CTA per SM runs its
-// share of the jobs one after another without a barrier between them: rings, phases and
-// buffers are indexed by running counts.
+// job costs its window and its own length, not its context.  The jobs' key tiles are
+// laid end to end and cut into one equal share per SM (a job counts kJobCost tiles more,
+// for its start and end), so that no SM waits for the others with whole jobs still to
+// run.  A CTA runs its share without a barrier between jobs: rings, phases and buffers are
+// indexed by running counts.  A job that is cut leaves a part per CTA in the workspace,
+// which merge_window_kernel puts together.  Where whole jobs end about as soon, they are
+// dealt out whole (an instantiation of its own: the other's code costs the loops 2 %).
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory lane =
 // row).  8 and 9: issue the products of A and of B (8 also copies Q by TMA and owns the
@@ -46,18 +50,21 @@ constexpr int kTok = kPrefillQTile;  // query tokens of a tile
 constexpr int kRows = kTok * kGroup;
 constexpr int kKeys = kTcKeyTile;
 constexpr int kPagesPerTile = kKeys / kPage;
-constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kSub = 64;          // keys of a score product and of a stage
+constexpr int kPagesPerSub = kSub / kPage;
+constexpr int kHalf = 128 * 128;  // a query tile: 128 rows x 64 bf16
 constexpr int kTileBytes = 2 * kHalf;
+constexpr int kSubHalf = kSub * 128;  // 64 keys x 64 bf16
+constexpr int kSubBytes = 2 * kSubHalf;
 constexpr int kPageHalfBytes = kPage * 128;
-constexpr int kStages = 2;  // of K and of V
+constexpr int kStages = 4;  // of K and of V
+constexpr int kBad = 16;      // entries of the flags below: more than stages and sub-tiles on their way
 constexpr int kMmaWarp = 8, kKWarp = 10, kVWarp = 11, kClearWarp = 12;  // (kMmaWarp + 1: tile B)
 constexpr int kThreads = 13 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for tile B
 constexpr float kMaxSum = 1024.f;           // of 32 weights, before their row's reference is raised
 constexpr int kOutTok = kQ4OutTok;          // query tokens of a softmax warp
-constexpr int kSub = 64;                    // keys of a score product
-constexpr int kPagesPerSub = kSub / kPage;
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
 static_assert(kRows == 128 && kKeys == 128 && kWindowTileTokens == 2 * kTok, "tile shape");
@@ -65,8 +72,8 @@ static_assert(kOutTok * kGroup == 32 && 4 * kOutTok == kTok, "a softmax warp's 3
 
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];
-  uint8_t k[kStages][kTileBytes];
-  uint8_t v[kStages][kTileBytes];
+  uint8_t k[kStages][kSubBytes];
+  uint8_t v[kStages][kSubBytes];
   uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 dims at a time
   uint64_t q_full, q_free;   // a job's Q has landed; its last scores are done
   uint64_t o_free[2];        // the softmax warps have read a job's output
@@ -74,7 +81,7 @@ struct __align__(1024) Smem {
   uint64_t v_full[kStages], v_ready[kStages], v_empty[kStages];  // landed; cleared; read
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per query tile and buffer: phase i / 2 for sub-tile i
   uint64_t drained[2];  // every product issued by a query tile's warp has completed
-  uint8_t bad_k[8][kPagesPerTile], bad_v[8][kPagesPerTile];  // of key tile j mod 8: pages outside the pool
+  uint8_t bad_k[kBad][kPagesPerSub], bad_v[kBad][kPagesPerSub];  // pages outside the pool, of a sub-tile
   uint32_t tmem;
   int abort;
 };
@@ -97,34 +104,64 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, i
   }
 }
 
+// The same for a warp that has time: it sleeps between looks, off the schedulers' back.
+__device__ __forceinline__ bool wait_idle(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      record_error(err, PA_ERR_DEVICE_TIMEOUT);
+      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+      return false;
+    }
+    __nanosleep(500);
+  }
+  return true;
+}
+
 struct Job {
   int32_t tok0;  // first query token of the job
   int32_t nq;    // its query tokens (1 .. 64)
   int32_t kvh;
   int32_t pos0;  // position of the first
   const int32_t* table;
-  Seen seen;               // pages that any of its queries sees
-  int32_t n_pages;         // how many
+  // this CTA's part of the pages that any of its queries sees: page v of them is page v + (v
+  // < lead ? lo : hi) of the row
+  int32_t lead, lo, hi;
+  int32_t n_pages;         // to the job's end
   int32_t n_tiles, n_sub;  // key tiles; sub-tiles of 64 keys (for both query tiles)
   int32_t n_x;             // query tiles
+  int32_t u;               // (kCut) the job
+  __device__ __forceinline__ int page(int v) const { return v + (v < lead ? lo : hi); }
 };
 
-// The CTA's jobs: job b of every round of gridDim.x jobs, in reverse order on odd rounds
-// (the items come longest first).
+// The CTA's jobs.  kCut: its share of all key tiles, from start[b] to start[b + 1], whose
+// first and last job may be cut.  Else job b of every round of gridDim.x whole jobs, in reverse order on odd
+// rounds (the items come longest first).
+template <bool kCut>
 struct Jobs {
   const WindowParams& p;
   const WindowItems& items;
-  int base, odd;
-  __device__ __forceinline__ Jobs(const WindowParams& p_, const WindowItems& items_) : p(p_), items(items_), base(0), odd(0) {}
+  int k, odd;  // kCut: the share's jobs given; else the jobs of the rounds before
+  __device__ __forceinline__ Jobs(const WindowParams& p_, const WindowItems& items_) : p(p_), items(items_), k(0), odd(0) {}
   __device__ __forceinline__ bool next(Job& job) {
-    const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
-    const int u = base + (odd ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    if (u >= n) {  // (a last round that has no job for this CTA)
-      base = n;
-      return false;
+    const int b = (int)blockIdx.x;
+    int u;
+    if constexpr (kCut) {
+      const int2 s0 = items.start[b], s1 = items.start[b + 1];
+      const int n = s1.x - s0.x + (s1.y > 0 ? 1 : 0);
+      if (k >= n) return false;
+      u = s0.x + k++;
+    } else {
+      const int n = items.count * p.num_kv_heads, G = (int)gridDim.x;
+      u = k + (odd ? G - 1 - b : b);
+      if (u >= n) {  // (a last round that has no job for this CTA)
+        k = n;
+        return false;
+      }
+      k += G;
+      odd ^= 1;
     }
-    base += G;
-    odd ^= 1;
     const int it = u / p.num_kv_heads;
     const int4 item = items.item[it];  // request, first query token, its position, queries
     job.tok0 = item.y;
@@ -132,13 +169,40 @@ struct Jobs {
     job.kvh = u - it * p.num_kv_heads;
     job.pos0 = item.z;
     job.table = p.block_tables + (size_t)item.x * p.max_blocks_per_req;
-    job.seen = seen_pages(item.z + item.w, item.w, p.window, p.sink_tokens);
-    job.n_pages = job.seen.count();
+    const Seen seen = seen_pages(item.z + item.w, item.w, p.window, p.sink_tokens);
+    job.n_pages = seen.count();
+    job.n_x = job.nq > kTok ? 2 : 1;
+    job.lead = seen.lead;
+    job.lo = 0;
+    job.hi = seen.first - seen.lead;
     job.n_tiles = (job.n_pages + kPagesPerTile - 1) / kPagesPerTile;
     job.n_sub = (job.n_pages + kPagesPerSub - 1) / kPagesPerSub;
-    job.n_x = job.nq > kTok ? 2 : 1;
+    if constexpr (kCut) {
+      const int2 s0 = items.start[b], s1 = items.start[b + 1];
+      job.u = u;
+      if (u == s1.x) {
+        job.n_tiles = s1.y;
+        job.n_sub = min(job.n_sub, 2 * s1.y);
+      }
+      if (u == s0.x) {  // from key tile s0.y on
+        const int v = s0.y * kPagesPerTile;
+        job.n_pages -= v;
+        job.lead -= v;
+        job.lo += v;
+        job.hi += v;
+        job.n_tiles -= s0.y;
+        job.n_sub -= 2 * s0.y;
+      }
+    }
     return true;
   }
+  // Whether the job given last is cut.
+  __device__ __forceinline__ bool cut(const Job& job) const {
+    const int2 s0 = items.start[blockIdx.x], s1 = items.start[blockIdx.x + 1];
+    return (job.u == s0.x && s0.y > 0) || (job.u == s1.x && s1.y > 0);
+  }
+  // Where its part goes: with the CTA's first job or its last.
+  __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (k > 1 ? 1 : 0); }
 };
 
 // Bits n .. 31 (n clamped to 0 .. 32).
@@ -150,56 +214,70 @@ __device__ __forceinline__ uint32_t page_seen(int t0, int pos, int window, int s
 }
 
 // Whether every query from position a to b sees every key of the pages v0 .. v1.
-__device__ __forceinline__ bool all_seen(const Seen& seen, int v0, int v1, int a, int b, int window, int sinks) {
-  const int first = seen.page(v0) * kPage, last = seen.page(v1) * kPage + kPage - 1;
+__device__ __forceinline__ bool all_seen(const Job& job, int v0, int v1, int a, int b, int window, int sinks) {
+  const int first = job.page(v0) * kPage, last = job.page(v1) * kPage + kPage - 1;
   return last <= a && (first > b - window || last < sinks);
 }
 
-// Copies of K (is_k) or V: key tile by key tile, 8 lanes a page each.  J0: the CTA's key
-// tiles before the job's.  False after a timeout.
-__device__ __forceinline__ bool copy_tiles(Smem& sm, const Job& job, bool is_k, const CUtensorMap* map, int J0,
-                                           int& last_issued, int num_kv_heads, int64_t num_blocks, int* err) {
-  const int lane = threadIdx.x & 31;
-  // pool rows four tiles at a time, one group ahead: lane l holds page l % 8 of tile 4 g +
-  // l / 8; pages past the end repeat the last one (hidden, and V's cleared)
-  auto load_group = [&](int g) -> int {
-    const int t = 4 * g + (lane >> 3);
-    if (t >= job.n_tiles) return 0;
-    const int b = job.table[job.seen.page(min(t * kPagesPerTile + (lane & 7), job.n_pages - 1))];
-    if (b < 0 || b >= num_blocks) {
-      record_error(err, PA_ERR_DEVICE_INDEX);
-      return -1;
-    }
-    return (b * num_kv_heads + job.kvh) * kPage;
-  };
-  int cur = load_group(0), next = load_group(1);
-  uint64_t* full = is_k ? sm.k_full : sm.v_full;
-  uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-  for (int j = 0; j < job.n_tiles; ++j) {
-    const int J = J0 + j, s = J % kStages;
-    if (j > 0 && (j & 3) == 0) {
-      cur = next;
-      next = load_group((j >> 2) + 1);
-    }
-    const int row = __shfl_sync(0xffffffffu, cur, ((j & 3) << 3) + (lane & 7));
-    if (J >= kStages && !__all_sync(0xffffffffu, wait(sm, &empty[s], ((J / kStages) - 1) & 1, err))) return false;
-    if (lane < kPagesPerTile) (is_k ? sm.bad_k : sm.bad_v)[J & 7][lane] = row < 0;
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], kTileBytes);
-    __syncwarp();
-    uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
-    if (lane < kPagesPerTile) {
-      const int off = lane * kPageHalfBytes;
-      tma_load_2d(dst + off, map, 0, max(row, 0), &full[s]);
-      tma_load_2d(dst + kHalf + off, map, 64, max(row, 0), &full[s]);
-    }
-    last_issued = J;
+// Pool rows of 32 of a job's pages, one per lane (eight sub-tiles); pages past the end
+// repeat the last one (hidden, and V's cleared); -1: outside the pool.
+__device__ __forceinline__ int load_group(const Job& job, int g, int num_kv_heads, int64_t num_blocks, int* err) {
+  const int v = 32 * g + (int)(threadIdx.x & 31);
+  if (v >= job.n_sub * kPagesPerSub) return 0;
+  const int b = job.table[job.page(min(v, job.n_pages - 1))];
+  if (b < 0 || b >= num_blocks) {
+    record_error(err, PA_ERR_DEVICE_INDEX);
+    return -1;
   }
-  return true;
+  return (b * num_kv_heads + job.kvh) * kPage;
 }
 
+// Copies of K (is_k) or V, a sub-tile per stage, two lanes a page; block ids one group or
+// job ahead.
+template <bool kCut>
+__device__ __forceinline__ void copy_tiles(Smem& sm, const WindowParams& p, const WindowItems& items, bool is_k,
+                                           const CUtensorMap* map) {
+  const int lane = threadIdx.x & 31;
+  uint64_t* full = is_k ? sm.k_full : sm.v_full;
+  uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+  Jobs<kCut> jobs(p, items);
+  Job job, after;
+  bool more = jobs.next(job), ok = true;
+  int R = 0;  // sub-tiles so far
+  int cur = more ? load_group(job, 0, p.num_kv_heads, p.num_blocks, p.err) : 0;
+  while (more && ok) {
+    int next = load_group(job, 1, p.num_kv_heads, p.num_blocks, p.err), first = 0;
+    for (int i = 0; i < job.n_sub; ++i, ++R) {
+      const int s = R % kStages;
+      if (i > 0 && (i & 7) == 0) {
+        cur = next;
+        next = load_group(job, (i >> 3) + 1, p.num_kv_heads, p.num_blocks, p.err);
+      }
+      if (i == job.n_sub - 1) {
+        more = jobs.next(after);
+        if (more) first = load_group(after, 0, p.num_kv_heads, p.num_blocks, p.err);
+      }
+      const int row = __shfl_sync(0xffffffffu, cur, ((i & 7) << 2) + ((lane >> 1) & 3));
+      ok = R < kStages || __all_sync(0xffffffffu, wait(sm, &empty[s], ((R / kStages) - 1) & 1, p.err));
+      if (!ok) break;
+      if (lane < 2 * kPagesPerSub && !(lane & 1)) (is_k ? sm.bad_k : sm.bad_v)[R % kBad][lane >> 1] = row < 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], kSubBytes);
+      __syncwarp();
+      uint8_t* dst = is_k ? sm.k[s] : sm.v[s];
+      if (lane < 2 * kPagesPerSub)
+        tma_load_2d(dst + (lane & 1) * kSubHalf + (lane >> 1) * kPageHalfBytes, map, 64 * (lane & 1), max(row, 0), &full[s]);
+    }
+    job = after;
+    cur = first;
+  }
+  if (!ok)  // gave up: the copies in flight land before the CTA leaves (bounded)
+    for (int r = max(0, R - kStages); r < R; ++r) mbar_wait_bounded(&full[r % kStages], (r / kStages) & 1);
+}
+
+template <bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_window_kernel(const WindowParams p, const __grid_constant__ WindowItems items,
+    prefill_window_kernel(const __grid_constant__ WindowParams p, const __grid_constant__ WindowItems items,
                           const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap out_map,
                           const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ uint8_t smem_raw[];
@@ -241,41 +319,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp == kKWarp || warp == kVWarp) {
-    const bool is_k = warp == kKWarp;
-    const CUtensorMap* map = is_k ? &k_map : &v_map;
+    const CUtensorMap* map = warp == kKWarp ? &k_map : &v_map;
     if (lane == 0) prefetch_tensormap(map);
-    Jobs jobs(p, items);
-    Job job;
-    int J0 = 0, last = -1;
-    bool ok = true;
-    while (jobs.next(job) && (ok = copy_tiles(sm, job, is_k, map, J0, last, p.num_kv_heads, p.num_blocks, p.err)))
-      J0 += job.n_tiles;
-    if (!ok)  // gave up: the copies in flight land before the CTA leaves (bounded)
-      for (int J = max(0, last - kStages + 1); J <= last; ++J)
-        mbar_wait_bounded(&(is_k ? sm.k_full : sm.v_full)[J % kStages], (J / kStages) & 1);
+    copy_tiles<kCut>(sm, p, items, warp == kKWarp, map);
   } else if (warp == kClearWarp) {
     // ------------------------------------------- V's rows that no query sees
-    Jobs jobs(p, items);
+    Jobs<kCut> jobs(p, items);
     Job job;
-    int J0 = 0;
+    int R = 0;
     bool ok = true;
     while (ok && jobs.next(job)) {
       const int keys = job.pos0 + job.nq, low = max(job.pos0 - p.window + 1, 0);
-      for (int j = 0; j < job.n_tiles; ++j) {
-        const int J = J0 + j, s = J % kStages;
-        ok = __all_sync(0xffffffffu, wait(sm, &sm.v_full[s], (J / kStages) & 1, p.err));
+      for (int i = 0; i < job.n_sub; ++i, ++R) {
+        const int s = R % kStages;
+        ok = __all_sync(0xffffffffu, wait(sm, &sm.v_full[s], (R / kStages) & 1, p.err));
         if (!ok) break;
         bool cleared = false;
 #pragma unroll 1
-        for (int y = 0; y < kKeys / 32; ++y) {
-          const int row = 32 * y + lane, v = j * kPagesPerTile + row / kPage;
-          const int t = job.seen.page(v) * kPage + row % kPage;
+        for (int y = 0; y < kSub / 32; ++y) {
+          const int row = 32 * y + lane, v = i * kPagesPerSub + row / kPage;
+          const int t = job.page(v) * kPage + row % kPage;
           const bool hide = v >= job.n_pages || t >= keys || (t >= p.sink_tokens && t < low) ||
-                            reinterpret_cast<volatile uint8_t*>(sm.bad_v[J & 7])[row / kPage];
+                            reinterpret_cast<volatile uint8_t*>(sm.bad_v[R % kBad])[row / kPage];
           if (hide) {
             uint4* d = reinterpret_cast<uint4*>(sm.v[s] + row * 128);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) d[c] = d[c + kHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c) d[c] = d[c + kSubHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
             cleared = true;
           }
         }
@@ -283,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_ready[s]);
       }
-      J0 += job.n_tiles;
     }
   } else if (warp >= kMmaWarp) {
     // --------------------------------------------------------- MMA issuers
@@ -292,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp - kMmaWarp;
     const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
     const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
-    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kHalf, 1024);
+    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kSubHalf, 1024);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t t_s = tm + kColS + x * kKeys, t_o = tm + kColO + x * kHeadDim;
     auto arrived = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
     };
-    // running counts: key tiles, jobs, this query tile's sub-tiles and jobs, Qs loaded
-    int J0 = 0, n_job = 0, I0 = 0, n_own = 0, n_q = 0;
+    // running counts: sub-tiles, jobs, this query tile's sub-tiles and jobs, Qs loaded
+    int R0 = 0, n_job = 0, I0 = 0, n_own = 0, n_q = 0;
     // Q of a job: after the last scores of the job before
     auto load_q = [&](const Job& job) {
       n_q += 1;
@@ -312,45 +380,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    Jobs jobs(p, items);
+    Jobs<kCut> jobs(p, items);
     Job job, next;
     bool more = jobs.next(job), ok = true;
     if (x == 0 && more) load_q(job);
     while (more && ok) {
       if (x < job.n_x) {
         const int n_sub = job.n_sub;
-        // scores of sub-tile i: 64 keys, half i & 1 of the job's key tile i / 2
+        // scores of sub-tile i
         auto issue_s = [&](int i) {
-          const int J = J0 + (i >> 1), b = (I0 + i) & 1;
-          const uint64_t kd = k_desc + (uint32_t)(J % kStages) * (kTileBytes >> 4) + (uint32_t)(i & 1) * (kSub * 128 >> 4);
+          const int s = (R0 + i) % kStages, b = (I0 + i) & 1;
+          const uint64_t kd = k_desc + (uint32_t)s * (kSubBytes >> 4);
           const uint32_t on = elect_one();
           fence_after_sync();
 #pragma unroll
           for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;  // 64-dim half, 16-dim step in it
-            mma_ss_if(on, t_s + b * kSub, q_desc + off, kd + off, kIdescS, ks > 0);
+            // 64-dim half, 16-dim step in it
+            mma_ss_if(on, t_s + b * kSub, q_desc + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                      kd + (((ks >> 2) * kSubHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0);
           }
           commit_if(on, &sm.s_full[x][b]);
-          if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.k_empty[J % kStages]);  // the tile's last use here
+          commit_if(on, &sm.k_empty[s]);
           if (i == n_sub - 1) commit_if(on, &sm.q_free);
         };
         auto issue_pv = [&](int i) {
-          const int J = J0 + (i >> 1), b = (I0 + i) & 1;
-          const uint64_t vd = v_desc + (uint32_t)(J % kStages) * (kTileBytes >> 4);
+          const int s = (R0 + i) % kStages, b = (I0 + i) & 1;
+          const uint64_t vd = v_desc + (uint32_t)s * (kSubBytes >> 4);
           const uint32_t on = elect_one();
           fence_after_sync();
 #pragma unroll
           for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
-            mma_ts_if(on, t_o, t_s + b * kSub + 8 * ks, vd + (uint32_t)((i & 1) * (kSub / 16) + ks) * (2 * 1024 >> 4),
+            mma_ts_if(on, t_o, t_s + b * kSub + 8 * ks, vd + (uint32_t)ks * (2 * 1024 >> 4),
                       kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
           commit_if(on, &sm.pv_done[x][b]);
-          if ((i & 1) || i == n_sub - 1) commit_if(on, &sm.v_empty[J % kStages]);
+          commit_if(on, &sm.v_empty[s]);
         };
         // before the scores of sub-tile i: its key tile, and the PV product of the
         // sub-tile whose weights lie where they go
         auto may_score = [&](int i) {
-          const int J = J0 + (i >> 1), I = I0 + i;
-          return ((i & 1) || arrived(&sm.k_full[J % kStages], J / kStages)) &&
+          const int R = R0 + i, I = I0 + i;
+          return arrived(&sm.k_full[R % kStages], R / kStages) &&
                  (I < 2 || arrived(&sm.pv_done[x][I & 1], (I >> 1) - 1));
         };
         ok = ok && arrived(&sm.q_full, n_job);
@@ -360,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the first PV product overwrites the output of this tile's job before
         ok = ok && (n_own == 0 || arrived(&sm.o_free[x], n_own - 1));
         for (int i = 0; ok && i < n_sub; ++i) {
-          const int J = J0 + (i >> 1), I = I0 + i;
+          const int R = R0 + i, I = I0 + i;
           if (x == 0 && more && i == n_sub - 1) {  // the next job's Q, while the softmax has the last scores
             ok = arrived(&sm.q_free, n_job);
             if (!ok) break;
             load_q(next);
           }
-          ok = ((i & 1) || arrived(&sm.v_ready[J % kStages], J / kStages)) && arrived(&sm.p_full[x][I & 1], I >> 1);
+          ok = arrived(&sm.v_ready[R % kStages], R / kStages) && arrived(&sm.p_full[x][I & 1], I >> 1);
           if (!ok) break;
           issue_pv(i);
           if (i + 2 < n_sub && (ok = may_score(i + 2))) issue_s(i + 2);
@@ -383,14 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         };
         pass(&sm.q_full, &sm.q_free, n_job);
-        for (int j = 0; j < job.n_tiles; ++j) {
-          const int J = J0 + j;
-          pass(&sm.k_full[J % kStages], &sm.k_empty[J % kStages], J / kStages);
-          pass(&sm.v_ready[J % kStages], &sm.v_empty[J % kStages], J / kStages);
+        for (int R = R0; R < R0 + job.n_sub; ++R) {
+          pass(&sm.k_full[R % kStages], &sm.k_empty[R % kStages], R / kStages);
+          pass(&sm.v_ready[R % kStages], &sm.v_empty[R % kStages], R / kStages);
         }
         more = jobs.next(next);
       }
-      J0 += job.n_tiles;
+      R0 += job.n_sub;
       n_job += 1;
       job = next;
     }
@@ -407,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
-    int J0 = 0, I0 = 0;  // running counts: key tiles, this query tile's sub-tiles
-    Jobs jobs(p, items);
+    int R0 = 0, I0 = 0;  // running counts: sub-tiles, this query tile's
+    Jobs<kCut> jobs(p, items);
     Job job;
     bool more = jobs.next(job), ok = true;
     while (more) {
       if (x >= job.n_x) {
-        J0 += job.n_tiles;
+        R0 += job.n_sub;
         more = jobs.next(job);
         continue;
       }
@@ -427,11 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         // bytes of its 4 pages
-        const uint32_t bad =
-            reinterpret_cast<volatile uint32_t*>(sm.bad_k[(J0 + (i >> 1)) & 7])[i & 1];
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(sm.bad_k[(R0 + i) % kBad]);
         const int v0 = i * kPagesPerSub;
         const bool masked = v0 + kPagesPerSub > job.n_pages || bad != 0u ||
-                            !all_seen(job.seen, v0, v0 + kPagesPerSub - 1, a, b, p.window, p.sink_tokens);
+                            !all_seen(job, v0, v0 + kPagesPerSub - 1, a, b, p.window, p.sink_tokens);
         const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
         // One pass over the scores, 32 keys at a time, the next ones' load in flight.
         // The weights are taken against the row's reference m_run first; only when
@@ -452,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int v = v0 + 2 * h + e;
               if (v < job.n_pages && ((bad >> (8 * (2 * h + e))) & 0xffu) == 0u)
-                see |= page_seen(job.seen.page(v) * kPage, pos, p.window, p.sink_tokens) << (16 * e);
+                see |= page_seen(job.page(v) * kPage, pos, p.window, p.sink_tokens) << (16 * e);
             }
 #pragma unroll
             for (int y = 0; y < 32; ++y)
@@ -488,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               fence_after_sync();
             }
-            rescale(t_o, t_s, h, i > 0, corr);
+            if (i > 0 || h > 0) rescale(t_o, t_s, h, i > 0, corr);
           }
           ls = __fadd2_rn(ls, sum);
           store16(t_s + 16 * h, w);  // weights over scores already read
@@ -504,54 +571,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
       fence_after_sync();
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-      // The output, 64 dims at a time, through shared memory (128-byte swizzle) and out
-      // by TMA, the warp's 8 tokens x 4 heads x 64 dims.
+      float lse = lse_log2(m_run, l_run);
       const int tok = x * kTok + (row >> 2);
       const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
-      uint8_t* stg = sm.out[warp];
-      uint32_t o[2][32];
-      tmem_ld32_async(t_o, o[0]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (lane == 0) bulk_wait_read();  // what was staged before has been read
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          wait_ld(o[c]);
-          if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
-          uint32_t w[16];
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+      if (kCut && jobs.cut(job)) {
+        // the row's part, 4 dims of 32 rows at a time
+        const size_t at = ((size_t)jobs.slot() * 2 + x) * kRows;
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + row;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim / 16; ++c) {
+          uint32_t o[16];
+          load16(t_o + 16 * c, o);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
-                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+            dst[(4 * c + y) * kRows] =
+                make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
+                            __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
         }
-        if (h == 1) {
-          fence_before_sync();  // the tensor-memory reads above precede the arrive
-          mbar_arrive(&sm.o_free[x]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (tok_w + kOutTok <= job.nq) {
-          if (lane == 0) {
-            tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
-            bulk_commit();
+        fence_before_sync();  // the tensor-memory reads above precede the arrive
+        mbar_arrive(&sm.o_free[x]);
+        p.part_lse[at + row] = lse;
+      } else {
+        // The output, 64 dims at a time, through shared memory (128-byte swizzle) and out
+        // by TMA, the warp's 8 tokens x 4 heads x 64 dims.
+        uint8_t* stg = sm.out[warp];
+        uint32_t o[2][32];
+        tmem_ld32_async(t_o, o[0]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) bulk_wait_read();  // what was staged before has been read
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            wait_ld(o[c]);
+            if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+            uint32_t w[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
           }
-        } else {  // the row's last tokens
+          if (h == 1) {
+            fence_before_sync();  // the tensor-memory reads above precede the arrive
+            mbar_arrive(&sm.o_free[x]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (tok_w + kOutTok <= job.nq) {
+            if (lane == 0) {
+              tma_store_3d(&out_map, stg, 64 * h, job.kvh * kGroup, job.tok0 + tok_w);
+              bulk_commit();
+            }
+          } else {  // the row's last tokens
 #pragma unroll 1
-          for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
-            const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
-            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
-                *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+            for (int i = lane >> 3; i < kGroup * (job.nq - tok_w); i += 4) {
+              const size_t at = (size_t)(job.tok0 + tok_w + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3);
+              *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 64 * h + 8 * (lane & 7)) =
+                  *reinterpret_cast<const uint4*>(stg + 128 * i + (((lane ^ i) & 7) << 4));
+            }
+            __syncwarp();  // (read before the next 64 dims go there)
           }
-          __syncwarp();  // (read before the next 64 dims go there)
         }
+        if (p.lse && tok < job.nq)
+          p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] = lse * kLn2;
       }
-      if (p.lse && tok < job.nq)
-        p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] = lse_log2(m_run, l_run) * kLn2;
-      J0 += job.n_tiles;
+      R0 += job.n_sub;
       I0 += job.n_sub;
       more = jobs.next(job);
     }
@@ -564,22 +651,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-std::atomic<bool> g_attr_set[kMaxDevices];
+// The outputs of cut jobs: the log-sum-exp merge of their parts, in order.  A CTA takes 32
+// dims of a query tile's 128 rows, a thread 16 dims of a row.  The parts lie as 4 dims of
+// neighbouring rows, so a warp reads 512 bytes at once.
+__global__ void __launch_bounds__(256) merge_window_kernel(const __grid_constant__ WindowParams p,
+                                                           const __grid_constant__ WindowCuts cuts) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const WindowCut cut = cuts.cut[blockIdx.x];
+  const int x = blockIdx.y, row = threadIdx.x & 127, tok = x * kTok + (row >> 2);
+  if (x * kTok >= cut.nq) return;
+  // rows of part i: with CTA b0's last job, unless that is its first; the others with their
+  // CTAs' first
+  auto at = [&](int i) { return ((size_t)(i == 0 ? cut.slot0 : 2 * (cut.b0 + i)) * 2 + x) * kRows; };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < cut.parts; ++i) m = max_nan(m, load_cg(p.part_lse + at(i) + row));
+  const float ref = m == -INFINITY ? 0.f : m;
+  const int c = blockIdx.z * 8 + 4 * (threadIdx.x >> 7);  // dims 4 c .. 4 c + 15
+  float l = 0.f;
+  float4 o[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < cut.parts; ++i) {
+    const float w = fast_exp2(load_cg(p.part_lse + at(i) + row) - ref);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + at(i) * kHeadDim) + c * kRows + row;
+    l += w;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const float4 a = load_cg(src + y * kRows);
+      o[y] = make_float4(fmaf(w, a.x, o[y].x), fmaf(w, a.y, o[y].y), fmaf(w, a.z, o[y].z), fmaf(w, a.w, o[y].w));
+    }
+  }
+  if (tok >= cut.nq) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t orow = (size_t)(cut.tok0 + tok) * p.num_q_heads + cut.kvh * kGroup + (row & 3);
+#pragma unroll
+  for (int y = 0; y < 4; y += 2)
+    *reinterpret_cast<uint4*>(p.out + orow * kHeadDim + 4 * (c + y)) =
+        make_uint4(pack_bf16x2(o[y].x * inv, o[y].y * inv), pack_bf16x2(o[y].z * inv, o[y].w * inv),
+                   pack_bf16x2(o[y + 1].x * inv, o[y + 1].y * inv), pack_bf16x2(o[y + 1].z * inv, o[y + 1].w * inv));
+  if (p.lse && c == 0) p.lse[orow] = lse_log2(ref, l) * kLn2;
+}
+
+std::atomic<bool> g_attr_set[2][kMaxDevices];
+
+template <bool kCut>
+cudaError_t launch(const WindowParams& p, const WindowItems& items, const TcMaps& maps, const CUtensorMap& out_map, int ctas,
+                   cudaStream_t stream) {
+  const cudaError_t e = set_smem_limit_once((const void*)prefill_window_kernel<kCut>, (int)kSmemBytes, g_attr_set[kCut]);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_window_kernel<kCut>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, items, maps.q,
+                    out_map, maps.k, maps.v);
+}
 
 }  // namespace
 
-cudaError_t launch_prefill_window(const WindowParams& p, const WindowItems& items, const TcMaps& maps,
+cudaError_t launch_prefill_window(const WindowParams& p, const WindowItems& items, bool cut, const TcMaps& maps,
                                   const CUtensorMap& out_map, int ctas, cudaStream_t stream) {
-  if (items.count <= 0) return cudaSuccess;
   // a zero scale (every score 0) as 2^-100, so that a hidden score scales to -inf:
   // scores of q and k whose products stay below 2^40 are below 2^-60 then and weigh 1
   // as before
   WindowParams pp = p;
   if (pp.scale_log2 == 0.f) pp.scale_log2 = 7.888609e-31f;
-  const cudaError_t e = set_smem_limit_once((const void*)prefill_window_kernel, (int)kSmemBytes, g_attr_set);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_window_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, pp, items, maps.q,
-                    out_map, maps.k, maps.v);
+  return cut ? launch<true>(pp, items, maps, out_map, ctas, stream) : launch<false>(pp, items, maps, out_map, ctas, stream);
+}
+
+cudaError_t launch_merge_window(const WindowParams& p, const WindowCuts& cuts, int n, cudaStream_t stream) {
+  return launch_pdl(merge_window_kernel, dim3((unsigned)n, 2, 4), dim3(256), 0, stream, p, cuts);
 }
 
 }  // namespace pa
