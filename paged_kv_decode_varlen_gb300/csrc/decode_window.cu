@@ -26,8 +26,17 @@
 //   Maxima are looked at only when a score exceeds its column's reference by 2^8
 // (one vote a page), so sums stay far inside binary32.
 //   At a row's end each consumer warp leaves its partial sums in shared memory and goes
-// on with the next row; two merging warps put them together behind it.  A row cut between CTAs leaves one partial per CTA in the workspace; the last CTA
-// to arrive at the row's count merges them in order: results do not depend on timing.
+// on with the next row; two merging warps put them together behind it.  A row cut between
+// CTAs leaves one partial per CTA in the workspace; the last CTA to arrive at the row's
+// count merges them in order: results do not depend on timing.  Both merges work out
+// what each part counts for all columns at once, a lane a column, and then add up several
+// columns' sums at a time: a column after another, each with its own reductions and
+// loads, a row of 5 queries kept a CTA for 6 us (80 rows of 5 queries, 1024 keys: 76.3 us;
+// 69.1 with the first, 61.5 with both and a row's q fetched by copies all in flight).
+//
+// Measured (GB300, in a graph, bytes of the pages seen over time): 64 rows of 1 query,
+// 1028 keys 47.9 us; 80 rows of 1, 2, 4, 5, 8 queries, 4096 keys 6.7, 6.7, 6.6, 6.4, 5.2 TB/s; from
+// seven queries on it is the products and not the memory that take the time.
 #include <math.h>
 #include <stddef.h>
 
@@ -44,14 +53,17 @@ constexpr int kOStride = kHeadDim + 4;  // floats between columns of a partial: 
 constexpr int kQStride = kHeadDim + 8;  // bf16 between rows of q: matrix loads meet no bank twice
 
 // NT: tiles of 8 columns (2 queries).  Consumer warps, pages in flight of each, and
-// partial buffers fill the shared memory; with the merging warps and the one that
-// fetches q, 12 warps leave 168 registers to a thread.
+// partial buffers fill the shared memory; up to 8 warps in all a thread has 255 registers,
+// which three and four tiles need, up to 12 it has 168.  Measured, 80 rows, 1024 keys, us:
+// 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4 67.8, 4 x 3 68.9,
+// 5 x 3 70.9, 5 x 2 71.9; 4 tiles, 4 x 3 82.1, 4 x 2 82.7, 5 x 2 82.2.  Two warps that share
+// a ring's pages and split the columns load each page's fragments twice: 111 for 85.6 then.
 template <int NT>
 struct Cfg {
   static constexpr int kQueries = NT == 1 ? 1 : 2 * NT;
   static constexpr int kCols = kQueries * kGroup;
-  static constexpr int kWarps = NT <= 2 ? 8 : NT == 3 ? 4 : 5;
-  static constexpr int kStages = NT == 3 ? 3 : 2;
+  static constexpr int kWarps = NT <= 2 ? 8 : 4;
+  static constexpr int kStages = NT <= 2 ? 2 : NT == 3 ? 4 : 3;
   static constexpr int kBufs = NT == 1 ? 2 : 1;
   static constexpr bool kQRegs = NT <= 2;  // q's fragments kept in registers
   static constexpr int kThreads = (kWarps + kMergeWarps + 1) * 32;
@@ -310,12 +322,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int b = n_item & 1;
       if (n_item >= 2 && !__all_sync(0xffffffffu, wait(sm, &sm.q_free[b], ((n_item >> 1) - 1) & 1, p.err))) return;
-#pragma unroll 4
-      for (int i = lane; i < it.n * kGroup * (kHeadDim / 8); i += 32) {
+      for (int i = lane; i < it.n * kGroup * (kHeadDim / 8); i += 32) {  // all in flight at once
         const int col = i / (kHeadDim / 8), ch = i % (kHeadDim / 8);
         const uint16_t* src = p.q + ((size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup) * kHeadDim;
-        *reinterpret_cast<uint4*>(&sm.q[b][col][8 * ch]) = load_cs(reinterpret_cast<const uint4*>(src) + ch);
+        cp_async16(&sm.q[b][col][8 * ch], src + 8 * ch);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[b]);
     }
@@ -587,43 +600,61 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     cp_async_wait<0>();  // (none is left but after a wait that gave up)
   } else {
     // -------------------------------------------------------------- merging
-    const int h0 = warp - C::kWarps;  // heads h0 and h0 + 2 of the group
+    // The warp has every second column, h0 + 2 j.  What a column's parts count is worked
+    // out by lane j; their sums are then added up kAt columns at a time.
+    constexpr int kAt = NT == 1 ? 2 : 4;
+    const int h0 = warp - C::kWarps;
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int buf = n_item % C::kBufs;
       if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[buf], (n_item / C::kBufs) & 1, p.err))) return;
       const size_t mine = ((size_t)blockIdx.x * 2 + it.slot) * p.piece_cols;
-      for (int col = h0; col < kGroup * it.n; col += kMergeWarps) {
-        const float mw = lane < C::kWarps ? sm.m[buf][lane][col] : -INFINITY;
-        const float lw = lane < C::kWarps ? sm.l[buf][lane][col] : 0.f;
-        float M = mw;
+      const int n_col = kGroup / kMergeWarps * it.n;  // columns of the warp
+      const int own = h0 + kMergeWarps * min(lane, n_col - 1);  // the lane's column
+      auto out_row = [&](int col) {
+        return (size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup;
+      };
+      float f[C::kWarps], M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 1; w < 8; w <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-        M = __shfl_sync(0xffffffffu, M, 0);  // (of lanes 0 .. 7)
-        const float f = fast_exp2(mw - (M == -INFINITY ? 0.f : M));  // mw = -inf -> 0
-        float L = f * lw;  // (0 x NaN: a NaN of a part without a maximum shows)
+      for (int w = 0; w < C::kWarps; ++w) {
+        f[w] = sm.m[buf][w][own];
+        M = fmaxf(M, f[w]);
+      }
 #pragma unroll
-        for (int w = 1; w < 8; w <<= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-        L = __shfl_sync(0xffffffffu, L, 0);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < C::kWarps; ++w) {
+        f[w] = fast_exp2(f[w] - (M == -INFINITY ? 0.f : M));  // -inf -> 0
+        L = fmaf(f[w], sm.l[buf][w][own], L);                 // (0 x NaN: a NaN of a part without a maximum shows)
+      }
+      const float inv = L == 0.f ? 0.f : (L != L ? L : 1.f / L);
 #pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) {
-          const float fw = __shfl_sync(0xffffffffu, f, w);
-          if (fw != 0.f) {
-            const float4 x = *reinterpret_cast<const float4*>(&sm.o[buf][w][col][4 * lane]);
-            a = make_float4(fmaf(fw, x.x, a.x), fmaf(fw, x.y, a.y), fmaf(fw, x.z, a.z), fmaf(fw, x.w, a.w));
+      for (int w = 0; w < C::kWarps; ++w) f[w] *= inv;
+      const float lse = lse_log2(M == -INFINITY ? 0.f : M, L);
+      if (lane < n_col) {
+        if (it.pieces > 1) p.piece_lse[mine + own] = lse;
+        else if (p.lse) p.lse[out_row(own)] = lse * kLn2;
+      }
+      for (int j0 = 0; j0 < n_col; j0 += kAt) {
+        float4 a[kAt];
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) {
+          const int j = min(j0 + u, n_col - 1);
+          a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < C::kWarps; ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f[w], j);
+            const float4 x = *reinterpret_cast<const float4*>(&sm.o[buf][w][h0 + kMergeWarps * j][4 * lane]);
+            if (fw != 0.f)  // (a part that had no page left nothing there)
+              a[u] = make_float4(fmaf(fw, x.x, a[u].x), fmaf(fw, x.y, a[u].y), fmaf(fw, x.z, a[u].z), fmaf(fw, x.w, a[u].w));
           }
         }
-        const float inv = L == 0.f ? 0.f : (L != L ? L : 1.f / L);
-        a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        const float lse = lse_log2(M == -INFINITY ? 0.f : M, L);
-        if (it.pieces == 1) {
-          const size_t row = (size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup;
-          *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
-              make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-          if (p.lse && lane == 0) p.lse[row] = lse * kLn2;
-        } else {
-          *reinterpret_cast<float4*>(p.piece_o + (mine + col) * kHeadDim + 4 * lane) = a;
-          if (lane == 0) p.piece_lse[mine + col] = lse;
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) {
+          if (j0 + u >= n_col) break;
+          const int col = h0 + kMergeWarps * (j0 + u);
+          if (it.pieces == 1)
+            *reinterpret_cast<uint2*>(p.out + out_row(col) * kHeadDim + 4 * lane) =
+                make_uint2(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w));
+          else
+            *reinterpret_cast<float4*>(p.piece_o + (mine + col) * kHeadDim + 4 * lane) = a[u];
         }
       }
       __syncwarp();
@@ -638,48 +669,67 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       }
       __syncwarp();  // lane 0's acquire orders the reads below
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-      for (int col = h0; col < kGroup * it.n; col += kMergeWarps) {
-        // piece x lies with segment s0 + x, as its CTA's first row but for a row
-        // that begins inside the segment
-        auto slot = [&](int x) {
-          const int b = (it.s0 + x) * Hkv + kvh;
-          const int which = x == 0 && !per_row && sm.start[it.r - p.row0] != it.s0 * seg ? 1 : 0;
-          return ((size_t)b * 2 + which) * p.piece_cols + col;
-        };
-        float M = -INFINITY, sum = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x0 = 0; x0 < it.pieces; x0 += 4) {
-          const int nx = min(4, it.pieces - x0);
-          float e[4];
-          float4 y[4];
+      // piece x lies with segment s0 + x, as its CTA's first row but for a row that
+      // begins inside the segment
+      const int first = !per_row && sm.start[it.r - p.row0] != it.s0 * seg ? 1 : 0;
+      auto slot = [&](int x) {
+        return ((size_t)((it.s0 + x) * Hkv + kvh) * 2 + (x == 0 ? first : 0)) * p.piece_cols;
+      };
+      constexpr int kMany = NT == 1 ? 2 : NT == 2 ? 4 : 8;  // columns at a time, of two pieces each
+      float e[kMany][2];
+      float4 y[kMany][2];
+      auto fetch = [&](int j0, int x0) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            e[u] = -INFINITY;
-            y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (u < nx) {
-              const size_t at = slot(x0 + u);
-              e[u] = load_cg(p.piece_lse + at);
-              y[u] = load_cg(reinterpret_cast<const float4*>(p.piece_o + at * kHeadDim + 4 * lane));
+        for (int u = 0; u < kMany; ++u)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            e[u][v] = -INFINITY;
+            y[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + v < it.pieces) {
+              const size_t at = slot(x0 + v) + h0 + kMergeWarps * min(j0 + u, n_col - 1);
+              e[u][v] = load_cg(p.piece_lse + at);
+              y[u][v] = load_cg(reinterpret_cast<const float4*>(p.piece_o + at * kHeadDim + 4 * lane));
             }
           }
-          const float mx = max_nan(max_nan(M, max_nan(e[0], e[1])), max_nan(e[2], e[3]));
-          if (mx == -INFINITY) continue;
-          const float fs = fast_exp2(M - mx);
-          sum *= fs;
-          a = make_float4(a.x * fs, a.y * fs, a.z * fs, a.w * fs);
+      };
+      fetch(0, 0);
+      float top = -INFINITY, sum = 0.f;  // of the lane's column
+      for (int x0 = 0; x0 < it.pieces; x0 += 4) {
+        float x[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float fu = fast_exp2(e[u] - mx);
-            sum += fu;
-            a = make_float4(fmaf(fu, y[u].x, a.x), fmaf(fu, y[u].y, a.y), fmaf(fu, y[u].z, a.z), fmaf(fu, y[u].w, a.w));
-          }
-          M = mx;
+        for (int u = 0; u < 4; ++u) x[u] = x0 + u < it.pieces ? load_cg(p.piece_lse + slot(x0 + u) + own) : -INFINITY;
+        const float mx = max_nan(max_nan(top, max_nan(x[0], x[1])), max_nan(x[2], x[3]));
+        if (mx == -INFINITY) continue;
+        sum *= fast_exp2(top - mx);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum += fast_exp2(x[u] - mx);
+        top = mx;
+      }
+      if (p.lse && lane < n_col) p.lse[out_row(own)] = lse_log2(top, sum) * kLn2;
+      const float over = sum == 0.f ? 0.f : 1.f / sum;
+      const float base = top == -INFINITY ? 0.f : top;
+      for (int j0 = 0; j0 < n_col; j0 += kMany) {
+        float4 a[kMany];
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = 0; x0 < it.pieces; x0 += 2) {
+          if (j0 > 0 || x0 > 0) fetch(j0, x0);
+#pragma unroll
+          for (int u = 0; u < kMany; ++u)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int j = min(j0 + u, n_col - 1);
+              const float fu = fast_exp2(e[u][v] - __shfl_sync(0xffffffffu, base, j)) * __shfl_sync(0xffffffffu, over, j);
+              const float4& x = y[u][v];
+              a[u] = make_float4(fmaf(fu, x.x, a[u].x), fmaf(fu, x.y, a[u].y), fmaf(fu, x.z, a[u].z), fmaf(fu, x.w, a[u].w));
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const size_t row = (size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup;
-        *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (p.lse && lane == 0) p.lse[row] = lse_log2(M, sum) * kLn2;
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) {
+          if (j0 + u >= n_col) break;
+          *reinterpret_cast<uint2*>(p.out + out_row(h0 + kMergeWarps * (j0 + u)) * kHeadDim + 4 * lane) =
+              make_uint2(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w));
+        }
       }
     }
   }
@@ -690,7 +740,6 @@ std::atomic<bool> g_attr_set[4][kMaxDevices];
 template <int NT>
 cudaError_t launch(const WindowParams& p, int grid, cudaStream_t stream) {
   constexpr size_t kBytes = sizeof(Smem<NT>) + 1024;  // + slack to align the base
-  static_assert(Cfg<NT>::kWarps <= 8, "merged by 8 lanes");
   static_assert(kBytes <= 232448, "shared memory per CTA");
   const cudaError_t e = set_smem_limit_once((const void*)decode_window_kernel<NT>, (int)kBytes, g_attr_set[NT - 1]);
   if (e != cudaSuccess) return e;
