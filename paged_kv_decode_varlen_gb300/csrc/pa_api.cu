@@ -1280,8 +1280,11 @@ int window_item_tiles(const pa::WindowParams& p, const int4& it) {
 // What a job costs beside its key tiles, in tiles.
 constexpr int kWindowJobCost = 3;
 // What cutting jobs costs beside: a share's ends are jobs of their own, their parts are
-// written and merged.
-constexpr int kWindowCutCost = 14;
+// written and merged.  Measured (152 SMs), whole against cut, and how many tiles the
+// longest CTA of whole jobs is above the even share: 4 x 512 queries over 4608 keys 119.0
+// and 117.4 us (11 tiles), 8 x 512 229 and 212 (23), 3 x 400 queries, 3 heads 58.6 and 38.6
+// (25); 16 x 100 queries over 612 keys 29.4 and 36.6 (4), 8000 queries, 1024 keys 116 and 133 (2).
+constexpr int kWindowCutCost = 12;
 
 // The tile launches of the rows of more than kWindowDecodeQueries queries: the jobs' key
 // tiles as one stream, cut into equal shares.

@@ -17,10 +17,11 @@
 // dealt out whole (an instantiation of its own: the other's code costs the loops 2 %).
 //
 // Warps.  0-3 and 4-7: softmax of A and B, one thread per row (tensor-memory lane =
-// row).  8 and 9: issue the products of A and of B (8 also copies Q by TMA and owns the
-// tensor memory).  10 and 11: copy K and V by tiled TMA, a page's half of 64 dims per
-// box.  12: clears V's rows that no query of the job sees, whose weight is 0 but which may
-// hold infinities or NaN (only key tiles at the ends have any).
+// row).  8 and 9: issue the score products of A and of B (8 also copies Q by TMA and owns
+// the tensor memory), 10 and 11 the PV products, so that the waits of one kind do not hold
+// up the other.  12 and 13: copy K and V by tiled TMA, a page's half of 64 dims per box.
+// 14: clears V's rows that no query of the job sees, whose weight is 0 but which may hold
+// infinities or NaN (only key tiles at the ends have any).
 //
 // Tensor memory: per query tile two score buffers of 64 keys and the output, 128
 // columns; that is all 512.  Scores are made 64 keys at a time (a sub-tile) and a
@@ -31,10 +32,23 @@
 // Weights are rounded to bf16, as the tensor cores take them; their sum is kept in
 // binary32 from the unrounded ones, as are scores, maxima and outputs.
 //
+// Bound and measured (GB300).  Per sub-tile of both query tiles the tensor pipe is busy for
+// 1281 cycles: 2 x 256 of PV, 2 x 384 of scores (64 keys at a time a product reads Q's 4 KB
+// and K's 2 KB from shared memory, 48 cycles at 128 B, for 32 cycles of arithmetic; 128
+// keys at a time would take 256, but then one buffer has to do, and 1089 busy cycles became
+// 2500 in all).  A sub-tile takes 1360 cycles in the middle of a job; a job costs about 3 us
+// beside (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
+// (152 CTAs fetch their first 30 MB at once).  Softmax of a row by two threads of 32 columns
+// each was slower (1120 ns a sub-tile for 870), as were scores, weights and PV from one warp
+// (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 63.6 now) and a masked
+// path in line with the plain one.
+//
 // Every wait is bounded; on a timeout the CTA records the error, lets its copies and
 // products finish (bounded), frees its tensor memory and returns.
 #include <math.h>
 #include <stddef.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "q4.cuh"  // lse_log2
@@ -59,11 +73,11 @@ constexpr int kSubBytes = 2 * kSubHalf;
 constexpr int kPageHalfBytes = kPage * 128;
 constexpr int kStages = 4;  // of K and of V
 constexpr int kBad = 16;      // entries of the flags below: more than stages and sub-tiles on their way
-constexpr int kMmaWarp = 8, kKWarp = 10, kVWarp = 11, kClearWarp = 12;  // (kMmaWarp + 1: tile B)
-constexpr int kThreads = 13 * 32;
+constexpr int kScoreWarp = 8, kPvWarp = 10, kKWarp = 12, kVWarp = 13, kClearWarp = 14;  // (+ 1: tile B)
+constexpr int kThreads = 15 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for tile B
-constexpr float kMaxSum = 1024.f;           // of 32 weights, before their row's reference is raised
+constexpr float kMaxSum = 1024.f;           // of 64 weights, before their row's reference is raised
 constexpr int kOutTok = kQ4OutTok;          // query tokens of a softmax warp
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
@@ -80,7 +94,7 @@ struct __align__(1024) Smem {
   uint64_t k_full[kStages], k_empty[kStages];
   uint64_t v_full[kStages], v_ready[kStages], v_empty[kStages];  // landed; cleared; read
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per query tile and buffer: phase i / 2 for sub-tile i
-  uint64_t drained[2];  // every product issued by a query tile's warp has completed
+  uint64_t drained[4];  // every product issued by a warp has completed
   uint8_t bad_k[kBad][kPagesPerSub], bad_v[kBad][kPagesPerSub];  // pages outside the pool, of a sub-tile
   uint32_t tmem;
   int abort;
@@ -102,21 +116,6 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, i
       }
     }
   }
-}
-
-// The same for a warp that has time: it sleeps between looks, off the schedulers' back.
-__device__ __forceinline__ bool wait_idle(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
-  const unsigned long long t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      record_error(err, PA_ERR_DEVICE_TIMEOUT);
-      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-      return false;
-    }
-    __nanosleep(500);
-  }
-  return true;
 }
 
 struct Job {
@@ -213,10 +212,14 @@ __device__ __forceinline__ uint32_t page_seen(int t0, int pos, int window, int s
   return ~bits_from(pos - t0 + 1) & (bits_from(pos - window + 1 - t0) | ~bits_from(sinks - t0)) & 0xffffu;
 }
 
-// Whether every query from position a to b sees every key of the pages v0 .. v1.
-__device__ __forceinline__ bool all_seen(const Job& job, int v0, int v1, int a, int b, int window, int sinks) {
-  const int first = job.page(v0) * kPage, last = job.page(v1) * kPage + kPage - 1;
-  return last <= a && (first > b - window || last < sinks);
+// The job's sub-tiles of the window of whose keys every query from position a to b sees all:
+// x .. y - 1.
+__device__ __forceinline__ int2 whole_subs(const Job& job, int a, int b, int window) {
+  // first and last page (of the job's count) of which they do
+  const int lo = max(job.lead, ((b - window) >> 4) + 1 - job.hi);  // its first key > b - window
+  const int hi = min(job.n_pages, ((a + 1) >> 4) - job.hi) - 1;    // its last key <= a
+  static_assert(kPage == 16, "positions to pages");
+  return make_int2((max(lo, 0) + kPagesPerSub - 1) / kPagesPerSub, (hi + 1) / kPagesPerSub);
 }
 
 // Pool rows of 32 of a job's pages, one per lane (eight sub-tiles); pages past the end
@@ -230,6 +233,18 @@ __device__ __forceinline__ int load_group(const Job& job, int g, int num_kv_head
     return -1;
   }
   return (b * num_kv_heads + job.kvh) * kPage;
+}
+
+// The weights of 32 scores against a reference -nm, in pairs of bf16, and their sums.
+__device__ __forceinline__ void weigh(const uint32_t (&c)[32], uint32_t (&w)[16], float2 (&s2)[2], float scale, float nm) {
+  const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+#pragma unroll
+  for (int y = 0; y < 16; ++y) {
+    const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
+    const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+    s2[y & 1] = __fadd2_rn(s2[y & 1], e);
+    w[y] = pack_bf16x2(e.x, e.y);
+  }
 }
 
 // Copies of K (is_k) or V, a sub-tile per stage, two lanes a page; block ids one group or
@@ -258,7 +273,8 @@ __device__ __forceinline__ void copy_tiles(Smem& sm, const WindowParams& p, cons
         if (more) first = load_group(after, 0, p.num_kv_heads, p.num_blocks, p.err);
       }
       const int row = __shfl_sync(0xffffffffu, cur, ((i & 7) << 2) + ((lane >> 1) & 3));
-      ok = R < kStages || __all_sync(0xffffffffu, wait(sm, &empty[s], ((R / kStages) - 1) & 1, p.err));
+      ok = R < kStages ? is_k || R > 0 || __all_sync(0xffffffffu, wait(sm, &sm.k_full[0], 0, p.err))
+                       : __all_sync(0xffffffffu, wait(sm, &empty[s], ((R / kStages) - 1) & 1, p.err));
       if (!ok) break;
       if (lane < 2 * kPagesPerSub && !(lane & 1)) (is_k ? sm.bad_k : sm.bad_v)[R % kBad][lane >> 1] = row < 0;
       __syncwarp();
@@ -283,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == kMmaWarp && lane == 0) {
+  if (warp == kScoreWarp && lane == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_free, 2);
     for (int s = 0; s < kStages; ++s) {
@@ -300,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.pv_done[x][b], 1);
       }
       mbar_init(&sm.o_free[x], kRows);
-      mbar_init(&sm.drained[x], 1);
     }
+    for (int w = 0; w < 4; ++w) mbar_init(&sm.drained[w], 1);
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     __syncwarp();
     tmem_alloc(&sm.tmem, kTmemCols);
   }
@@ -353,120 +369,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.v_ready[s]);
       }
     }
-  } else if (warp >= kMmaWarp) {
+  } else if (warp >= kScoreWarp) {
     // --------------------------------------------------------- MMA issuers
     // The whole warp runs this (so that descriptors and addresses are warp-uniform
-    // values) and one elected lane issues.
-    const int x = warp - kMmaWarp;
-    const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
-    const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
-    const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kSubHalf, 1024);
+    // values) and one elected lane issues.  Scores and PV products of a query tile come
+    // from two warps, so that neither's waits delay the other's products.
+    const int x = (warp - kScoreWarp) & 1;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t t_s = tm + kColS + x * kKeys, t_o = tm + kColO + x * kHeadDim;
     auto arrived = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, wait(sm, bar, (uint32_t)phase & 1u, p.err)) != 0;
     };
-    // running counts: sub-tiles, jobs, this query tile's sub-tiles and jobs, Qs loaded
-    int R0 = 0, n_job = 0, I0 = 0, n_own = 0, n_q = 0;
-    // Q of a job: after the last scores of the job before
-    auto load_q = [&](const Job& job) {
-      n_q += 1;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&sm.q_full, job.n_x * kTileBytes);
-        for (int y = 0; y < job.n_x; ++y) {
-          tma_load_3d(sm.q[y], &q_map, 0, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
-          tma_load_3d(sm.q[y] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
-        }
-      }
+    // two barriers, looked at together
+    auto both = [&](uint64_t* bar0, int phase0, uint64_t* bar1, int phase1) {
+      const bool a = mbar_try_wait(bar0, (uint32_t)phase0 & 1u), b = mbar_try_wait(bar1, (uint32_t)phase1 & 1u);
+      if (__all_sync(0xffffffffu, a && b)) return true;
+      return arrived(bar0, phase0) && arrived(bar1, phase1);
+    };
+    // a job without this tile: every phase is waited for in turn all the same (a wait by
+    // parity tells a phase only from its neighbours), and every stage given back
+    auto pass = [&](uint64_t* full, uint64_t* empty, int phase) {
+      const bool there = arrived(full, phase);
+      if (there && lane == 0) mbar_arrive(empty);
       __syncwarp();
+      return there;
     };
     Jobs<kCut> jobs(p, items);
-    Job job, next;
+    Job job;
     bool more = jobs.next(job), ok = true;
-    if (x == 0 && more) load_q(job);
-    while (more && ok) {
-      if (x < job.n_x) {
-        const int n_sub = job.n_sub;
-        // scores of sub-tile i
-        auto issue_s = [&](int i) {
-          const int s = (R0 + i) % kStages, b = (I0 + i) & 1;
-          const uint64_t kd = k_desc + (uint32_t)s * (kSubBytes >> 4);
-          const uint32_t on = elect_one();
-          fence_after_sync();
-#pragma unroll
-          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-            // 64-dim half, 16-dim step in it
-            mma_ss_if(on, t_s + b * kSub, q_desc + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
-                      kd + (((ks >> 2) * kSubHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0);
+    int R0 = 0, I0 = 0;  // running counts: sub-tiles, this query tile's
+    if (warp < kPvWarp) {
+      const uint64_t q_desc = desc_sw128(smem_addr(sm.q[0]), 16, 1024) + (uint32_t)x * (kTileBytes >> 4);
+      const uint64_t k_desc = desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+      auto load_q = [&](const Job& job) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.q_full, job.n_x * kTileBytes);
+          for (int y = 0; y < job.n_x; ++y) {
+            tma_load_3d(sm.q[y], &q_map, 0, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
+            tma_load_3d(sm.q[y] + kHalf, &q_map, 64, job.kvh * kGroup, job.tok0 + y * kTok, &sm.q_full);
           }
-          commit_if(on, &sm.s_full[x][b]);
-          commit_if(on, &sm.k_empty[s]);
-          if (i == n_sub - 1) commit_if(on, &sm.q_free);
-        };
-        auto issue_pv = [&](int i) {
-          const int s = (R0 + i) % kStages, b = (I0 + i) & 1;
-          const uint64_t vd = v_desc + (uint32_t)s * (kSubBytes >> 4);
-          const uint32_t on = elect_one();
-          fence_after_sync();
-#pragma unroll
-          for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
-            mma_ts_if(on, t_o, t_s + b * kSub + 8 * ks, vd + (uint32_t)ks * (2 * 1024 >> 4),
-                      kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
-          commit_if(on, &sm.pv_done[x][b]);
-          commit_if(on, &sm.v_empty[s]);
-        };
-        // before the scores of sub-tile i: its key tile, and the PV product of the
-        // sub-tile whose weights lie where they go
-        auto may_score = [&](int i) {
-          const int R = R0 + i, I = I0 + i;
-          return arrived(&sm.k_full[R % kStages], R / kStages) &&
-                 (I < 2 || arrived(&sm.pv_done[x][I & 1], (I >> 1) - 1));
-        };
-        ok = ok && arrived(&sm.q_full, n_job);
-        for (int i = 0; ok && i < min(n_sub, 2); ++i)
-          if ((ok = may_score(i))) issue_s(i);
-        more = jobs.next(next);
-        // the first PV product overwrites the output of this tile's job before
-        ok = ok && (n_own == 0 || arrived(&sm.o_free[x], n_own - 1));
-        for (int i = 0; ok && i < n_sub; ++i) {
-          const int R = R0 + i, I = I0 + i;
-          if (x == 0 && more && i == n_sub - 1) {  // the next job's Q, while the softmax has the last scores
-            ok = arrived(&sm.q_free, n_job);
-            if (!ok) break;
-            load_q(next);
-          }
-          ok = arrived(&sm.v_ready[R % kStages], R / kStages) && arrived(&sm.p_full[x][I & 1], I >> 1);
+        }
+        __syncwarp();
+      };
+      int n_job = 0, n_q = 0;
+      while (more && ok) {
+        if (x == 0) {  // Q, after the last scores of the job before
+          ok = n_job == 0 || arrived(&sm.q_free, n_job - 1);
           if (!ok) break;
-          issue_pv(i);
-          if (i + 2 < n_sub && (ok = may_score(i + 2))) issue_s(i + 2);
+          load_q(job);
+          n_q += 1;
         }
-        I0 += n_sub;
-        n_own += 1;
-      } else {
-        // a job without this tile: every phase is waited for in turn all the same (a
-        // wait by parity tells a phase only from its neighbours), and every stage
-        // given back
-        auto pass = [&](uint64_t* full, uint64_t* empty, int phase) {
-          ok = ok && arrived(full, phase);
-          if (ok && lane == 0) mbar_arrive(empty);
-          __syncwarp();
-        };
-        pass(&sm.q_full, &sm.q_free, n_job);
-        for (int R = R0; R < R0 + job.n_sub; ++R) {
-          pass(&sm.k_full[R % kStages], &sm.k_empty[R % kStages], R / kStages);
-          pass(&sm.v_ready[R % kStages], &sm.v_empty[R % kStages], R / kStages);
+        if (x < job.n_x) {
+          ok = arrived(&sm.q_full, n_job);
+          for (int i = 0; ok && i < job.n_sub; ++i) {
+            // scores of sub-tile i: its keys are there, and the PV product of the sub-tile
+            // whose weights lie where they go is done
+            const int R = R0 + i, s = R % kStages, I = I0 + i, b = I & 1;
+            ok = I < 2 ? arrived(&sm.k_full[s], R / kStages)
+                       : both(&sm.k_full[s], R / kStages, &sm.pv_done[x][b], (I >> 1) - 1);
+            if (!ok) break;
+            const uint64_t kd = k_desc + (uint32_t)s * (kSubBytes >> 4);
+            const uint32_t on = elect_one();
+            fence_after_sync();
+#pragma unroll
+            for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+              // 64-dim half, 16-dim step in it
+              mma_ss_if(on, t_s + b * kSub, q_desc + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                        kd + (((ks >> 2) * kSubHalf + (ks & 3) * 32) >> 4), kIdescS, ks > 0);
+            }
+            commit_if(on, &sm.s_full[x][b]);
+            commit_if(on, &sm.k_empty[s]);
+            if (i == job.n_sub - 1) commit_if(on, &sm.q_free);
+          }
+          I0 += job.n_sub;
+        } else {
+          ok = pass(&sm.q_full, &sm.q_free, n_job);
+          for (int R = R0; ok && R < R0 + job.n_sub; ++R) ok = pass(&sm.k_full[R % kStages], &sm.k_empty[R % kStages], R / kStages);
         }
-        more = jobs.next(next);
+        R0 += job.n_sub;
+        n_job += 1;
+        more = jobs.next(job);
       }
-      R0 += job.n_sub;
-      n_job += 1;
-      job = next;
+      if (n_q > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(n_q - 1) & 1u);  // Q has landed before the CTA leaves
+    } else {
+      const uint64_t v_desc = desc_sw128(smem_addr(sm.v[0]), kSubHalf, 1024);
+      int n_own = 0;
+      while (more && ok) {
+        if (x < job.n_x) {
+          // the first product overwrites the output of this tile's job before
+          ok = n_own == 0 || arrived(&sm.o_free[x], n_own - 1);
+          for (int i = 0; ok && i < job.n_sub; ++i) {
+            const int R = R0 + i, s = R % kStages, I = I0 + i, b = I & 1;
+            ok = both(&sm.v_ready[s], R / kStages, &sm.p_full[x][b], I >> 1);
+            if (!ok) break;
+            const uint64_t vd = v_desc + (uint32_t)s * (kSubBytes >> 4);
+            const uint32_t on = elect_one();
+            fence_after_sync();
+#pragma unroll
+            for (int ks = 0; ks < kSub / 16; ++ks)  // 16 keys: two 8-row groups of V, 8 columns of weight pairs
+              mma_ts_if(on, t_o, t_s + b * kSub + 8 * ks, vd + (uint32_t)ks * (2 * 1024 >> 4), kIdescO,
+                        (i > 0 || ks > 0) ? 1u : 0u);
+            commit_if(on, &sm.pv_done[x][b]);
+            commit_if(on, &sm.v_empty[s]);
+          }
+          I0 += job.n_sub;
+          n_own += 1;
+        } else {
+          for (int R = R0; ok && R < R0 + job.n_sub; ++R) ok = pass(&sm.v_ready[R % kStages], &sm.v_empty[R % kStages], R / kStages);
+        }
+        R0 += job.n_sub;
+        more = jobs.next(job);
+      }
     }
     // every product issued has completed before the tensor memory is freed (a commit
-    // tracks all of them), and Q has landed before the CTA leaves
-    commit_if(elect_one(), &sm.drained[x]);
-    mbar_wait_bounded(&sm.drained[x], 0);
-    if (n_q > 0) mbar_wait_bounded(&sm.q_full, (uint32_t)(n_q - 1) & 1u);
+    // tracks all of the warp's)
+    commit_if(elect_one(), &sm.drained[warp - kScoreWarp]);
+    mbar_wait_bounded(&sm.drained[warp - kScoreWarp], 0);
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
@@ -475,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_o = lane_base + kColO + x * kHeadDim;
     const float scale = p.scale_log2;  // not 0 (see the launch)
+    const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
     int R0 = 0, I0 = 0;  // running counts: sub-tiles, this query tile's
     Jobs<kCut> jobs(p, items);
     Job job;
@@ -487,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int a = job.pos0 + x * kTok, b = min(a + kTok, job.pos0 + job.nq) - 1;  // the tile's positions
       const int pos = a + (row >> 2);
+      const int2 whole = whole_subs(job, a, b, p.window);
       float m_run = -INFINITY, l_run = 0.f;
       for (int i = 0; i < job.n_sub; ++i) {
         const int I = I0 + i;
@@ -496,72 +516,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         // bytes of its 4 pages
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(sm.bad_k[(R0 + i) % kBad]);
-        const int v0 = i * kPagesPerSub;
-        const bool masked = v0 + kPagesPerSub > job.n_pages || bad != 0u ||
-                            !all_seen(job, v0, v0 + kPagesPerSub - 1, a, b, p.window, p.sink_tokens);
-        const uint32_t hide = scale >= 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
-        // One pass over the scores, 32 keys at a time, the next ones' load in flight.
-        // The weights are taken against the row's reference m_run first; only when
-        // their sum shows that it lies too low (or there is none yet) the maximum is
-        // looked for, m_run re-based to it, and the output and the weights stored so
-        // far rescaled.  After a row's first keys that is rare.
-        float2 ls = make_float2(0.f, 0.f);
-        uint32_t buf[2][32];
-        tmem_ld32_async(t_s, buf[0]);
+        // The weights are taken against the row's reference m_run.  Only when their sum
+        // shows that it lies too low are the scores read again for their maximum, m_run
+        // re-based to it and the output rescaled: rare after a row's first keys.
+        uint32_t c[2][32], w[2][16];
+        float sum = 0.f;
+        // what the row does not see hidden
+        auto hide_some = [&](int h) {
+          uint32_t see = 0u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t(&c)[32] = buf[h & 1];
-          wait_ld(c);
-          if (h < 1) tmem_ld32_async(t_s + 32 * (h + 1), buf[(h + 1) & 1]);
-          if (masked) {
-            uint32_t see = 0u;
+          for (int e = 0; e < 2; ++e) {
+            const int v = i * kPagesPerSub + 2 * h + e;
+            if (v < job.n_pages && ((bad >> (8 * (2 * h + e))) & 0xffu) == 0u)
+              see |= page_seen(job.page(v) * kPage, pos, p.window, p.sink_tokens) << (16 * e);
+          }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int v = v0 + 2 * h + e;
-              if (v < job.n_pages && ((bad >> (8 * (2 * h + e))) & 0xffu) == 0u)
-                see |= page_seen(job.page(v) * kPage, pos, p.window, p.sink_tokens) << (16 * e);
-            }
+          for (int y = 0; y < 32; ++y)
+            if (!((see >> y) & 1u)) c[h][y] = hide;
+        };
+        auto weights = [&](auto some) {
+          const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          tmem_ld32_async(t_s, c[0]);
+          wait_ld(c[0]);
+          tmem_ld32_async(t_s + 32, c[1]);
+          if (decltype(some)::value) hide_some(0);
+          weigh(c[0], w[0], s2, scale, nm);
+          wait_ld(c[1]);
+          if (decltype(some)::value) hide_some(1);
+          weigh(c[1], w[1], s2, scale, nm);
+          s2[0] = __fadd2_rn(s2[0], s2[1]);
+          sum = s2[0].x + s2[0].y;
+        };
+        const bool some = i < whole.x || i >= whole.y || bad != 0u;
+        bool low = true;
+        if (i > 0) {
+          if (some) weights(std::true_type{});
+          else weights(std::false_type{});
+          low = sum > kMaxSum || m_run == -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, low)) {
+          float mt = __uint_as_float(hide);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32_async(t_s + 32 * h, c[h]);
+            wait_ld(c[h]);
+            hide_some(h);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (!((see >> y) & 1u)) c[y] = hide;
+              mt = scale >= 0.f ? fmaxf(mt, __uint_as_float(c[h][y])) : fminf(mt, __uint_as_float(c[h][y]));
           }
-          uint32_t w[16];
-          float2 sum;
-          for (bool again = false;; again = true) {
-            const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
-            const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const float2 d = __ffma2_rn(make_float2(__uint_as_float(c[2 * y]), __uint_as_float(c[2 * y + 1])), sc2, nm2);
-              const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-              s2[y & 1] = __fadd2_rn(s2[y & 1], e);
-              w[y] = pack_bf16x2(e.x, e.y);
-            }
-            sum = __fadd2_rn(s2[0], s2[1]);
-            const bool low = sum.x + sum.y > kMaxSum || m_run == -INFINITY;
-            if (again || !__any_sync(0xffffffffu, low)) break;
-            if (h < 1) wait_ld(buf[(h + 1) & 1]);  // nothing in flight across the call
-            float mt = -INFINITY;
-#pragma unroll
-            for (int y = 0; y < 32; ++y) mt = fmaxf(mt, __uint_as_float(c[y]) * scale);
-            const bool grow = low && mt > m_run;
-            const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
-            if (grow) m_run = mt;
-            l_run *= corr;
-            ls = __fmul2_rn(ls, make_float2(corr, corr));
-            if (i > 0) {  // O is stable once PV of the sub-tile before is done
-              ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(I - 1) & 1], ((I - 1) >> 1) & 1, p.err));
-              if (!ok) break;
-              fence_after_sync();
-            }
-            if (i > 0 || h > 0) rescale(t_o, t_s, h, i > 0, corr);
+          mt *= scale;
+          const bool grow = low && mt > m_run;
+          const float corr = grow ? fast_exp2(m_run - mt) : 1.f;  // m_run = -inf -> 0
+          if (grow) m_run = mt;
+          l_run *= corr;
+          if (i > 0) {  // O is stable once PV of the sub-tile before is done
+            ok = __all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][(I - 1) & 1], ((I - 1) >> 1) & 1, p.err));
+            if (!ok) break;
+            fence_after_sync();
+            rescale(t_o, t_s, 0, true, corr);
           }
-          ls = __fadd2_rn(ls, sum);
-          store16(t_s + 16 * h, w);  // weights over scores already read
+          const float nm = (m_run == -INFINITY) ? 0.f : -m_run;
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          weigh(c[0], w[0], s2, scale, nm);
+          weigh(c[1], w[1], s2, scale, nm);
+          s2[0] = __fadd2_rn(s2[0], s2[1]);
+          sum = s2[0].x + s2[0].y;
         }
-        if (!ok) break;
-        l_run += ls.x + ls.y;
+        store16(t_s, w[0]);  // weights over scores already read
+        store16(t_s + 16, w[1]);
+        l_run += sum;
         wait_st();
         fence_before_sync();  // the tensor-memory accesses above precede the arrive
         mbar_arrive(&sm.p_full[x][I & 1]);
@@ -648,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // The outputs of cut jobs: the log-sum-exp merge of their parts, in order.  A CTA takes 32
