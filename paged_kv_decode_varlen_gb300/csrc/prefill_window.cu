@@ -36,12 +36,13 @@
 // 1281 cycles: 2 x 256 of PV, 2 x 384 of scores (64 keys at a time a product reads Q's 4 KB
 // and K's 2 KB from shared memory, 48 cycles at 128 B, for 32 cycles of arithmetic; 128
 // keys at a time would take 256, but then one buffer has to do, and 1089 busy cycles became
-// 2500 in all).  A sub-tile takes 1360 cycles in the middle of a job; a job costs about 3 us
-// beside (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
+// 2500 in all).  A sub-tile takes 1360 cycles in the middle of a job; a job costs about 3 us beside
+// (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
 // (152 CTAs fetch their first 30 MB at once).  Softmax of a row by two threads of 32 columns
 // each was slower (1120 ns a sub-tile for 870), as were scores, weights and PV from one warp
-// (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 63.6 now) and a masked
-// path in line with the plain one.
+// (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 62.5 now).  Most of
+// what a job costs beside is code that runs once in it and is not in the instruction
+// caches: every path laid out a second time shows.
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its copies and
 // products finish (bounded), frees its tensor memory and returns.
@@ -77,7 +78,10 @@ constexpr int kScoreWarp = 8, kPvWarp = 10, kKWarp = 12, kVWarp = 13, kClearWarp
 constexpr int kThreads = 15 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for tile B
-constexpr float kMaxSum = 1024.f;           // of 64 weights, before their row's reference is raised
+// The sum of 64 weights above which their row's reference is raised: binary32 and bf16 hold
+// larger ones as exactly, so it only keeps far from their ends; at 2^10 a row whose first
+// sub-tile shows it few keys re-bases more often.
+constexpr float kMaxSum = 65536.f;
 constexpr int kOutTok = kQ4OutTok;          // query tokens of a softmax warp
 constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kSub, false);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, true);
@@ -102,8 +106,9 @@ struct __align__(1024) Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
-__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+// (The loop is a function of its own: at every wait's place it would be more code than the
+// instruction caches take along: 8 prompts behind a window of 512 took 118.7 us for 107.1.)
+__device__ __noinline__ bool wait_on(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -116,6 +121,11 @@ __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, i
       }
     }
   }
+}
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_on(sm, bar, parity, err);
 }
 
 struct Job {
