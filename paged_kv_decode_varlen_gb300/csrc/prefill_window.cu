@@ -40,7 +40,7 @@
 // (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
 // (152 CTAs fetch their first 30 MB at once).  Softmax of a row by two threads of 32 columns
 // each was slower (1120 ns a sub-tile for 870), as were scores, weights and PV from one warp
-// (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 62.5 now).  Most of
+// (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 61.4 now).  Most of
 // what a job costs beside is code that runs once in it and is not in the instruction
 // caches: every path laid out a second time shows.
 //
@@ -107,7 +107,7 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 // (The loop is a function of its own: at every wait's place it would be more code than the
-// instruction caches take along: 8 prompts behind a window of 512 took 118.7 us for 107.1.)
+// instruction caches take along: 8 prompts behind a window of 512 took 118.7 us for 107.1, and the output by a rolled-up loop 103.)
 __device__ __noinline__ bool wait_on(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
@@ -123,7 +123,6 @@ __device__ __noinline__ bool wait_on(Smem& sm, uint64_t* bar, uint32_t parity, i
   }
 }
 __device__ __forceinline__ bool wait(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
   if (mbar_try_wait(bar, parity)) return true;
   return wait_on(sm, bar, parity, err);
 }
@@ -630,20 +629,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The output, 64 dims at a time, through shared memory (128-byte swizzle) and out
         // by TMA, the warp's 8 tokens x 4 heads x 64 dims.
         uint8_t* stg = sm.out[warp];
-        uint32_t o[2][32];
-        tmem_ld32_async(t_o, o[0]);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if (lane == 0) bulk_wait_read();  // what was staged before has been read
           __syncwarp();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
-            wait_ld(o[c]);
-            if (h == 0 || c == 0) tmem_ld32_async(t_o + 64 * h + 32 * (c + 1), o[c ^ 1]);
+            uint32_t o[32];
+            tmem_ld32_async(t_o + 64 * h + 32 * c, o);
+            wait_ld(o);
             uint32_t w[16];
 #pragma unroll
             for (int y = 0; y < 16; ++y)
-              w[y] = pack_bf16x2(__uint_as_float(o[c][2 * y]) * inv, __uint_as_float(o[c][2 * y + 1]) * inv);
+              w[y] = pack_bf16x2(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
