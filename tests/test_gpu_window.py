@@ -289,3 +289,91 @@ def test_on_a_stream_that_is_not_the_current_one():
     out, lse = c.run(stream=side)
     side.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("qo", [1, 2, 5, 8, 40, 130])
+@pytest.mark.parametrize("scale", [0.5, -2.0])
+def test_scores_that_climb_along_the_keys(qo, scale):
+    """Keys that grow along the row, so that every row's reference is raised over and
+    over, between tiles without a hidden key too, and by far more than a float's range."""
+    c = Case([1800, 700], [qo, qo], 1500, 4, 2, seed=qo, scale=scale)
+    x = oracle.bf16_to_f64(c.k)
+    for r in range(2):
+        for j, b in enumerate(c.tables[r]):
+            if b >= 0:
+                x[b] *= (1 + j % 40) / 8 * (1 if r else 1 + j / 16)
+    k = torch.from_numpy(x).to(torch.bfloat16)
+    c.d["k"], c.k = k.to(DEV), bf16_host(k)
+    c.check(*c.run())
+
+
+def test_more_items_than_one_launch_takes():
+    R = 1600
+    c = Case(rand(20, R, 9, 40), [9] * R, 12, 1, 1, seed=21)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("seq,qo,window", [([6000], [100], 5000), ([3000] * 3, [200] * 3, 2500), ([900] * 40, [5] * 40, 700)])
+def test_rows_cut_between_processors_give_the_same_bits_again(seq, qo, window):
+    c = Case(seq, qo, window, 4, 3, seed=22)
+    ws = c.workspace()
+    out, lse = c.run(workspace=ws)
+    c.check(out, lse)
+    for _ in range(8):
+        o, l = c.run(workspace=ws)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_threads_with_streams_and_workspaces_of_their_own():
+    import threading
+    cases = [Case([900, 300, 40], [100, 1, 5], 200, 4, 2, seed=23), Case([2000] * 4, [1, 70, 9, 3], 500, 0, 4, seed=24),
+             Case([40] * 30, [1] * 30, 20, 4, 1, seed=25)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            side, ws = torch.cuda.Stream(), cases[i].workspace()
+            side.wait_stream(torch.cuda.default_stream())
+            for _ in range(30):
+                out, lse = cases[i].run(stream=side, workspace=ws)
+                side.synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                    wrong.append(i)
+        except Exception as e:  # noqa: BLE001 (shown by the assertion)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i % 3,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_a_pool_whose_offsets_pass_32_bits():
+    """Blocks at the far end of a pool of more than 2^31 values, written by the append
+    and read by each kernel."""
+    Hkv, nb = 8, 140_000
+    small = Case([600, 350, 90, 33], [70, 1, 5, 1], 200, 4, Hkv, seed=26)
+    far = nb - small.k.shape[0]
+    k, v = (torch.empty(nb, Hkv, 16, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[far:], v[far:] = small.d["k"], small.d["v"]
+    tables = torch.where(small.d["tables"] >= 0, small.d["tables"] + far, small.d["tables"])
+    want, want_lse = small.run()
+    out, lse = B.pa_attention_varlen_window(small.d["q"], k, v, tables, small.d["seq"], small.d["ind"], small.scale,
+                                            small.window, small.sinks, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    # the last slot of the pool
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, kn, vn = (torch.randn(1, h, 128, generator=g, device=DEV).to(torch.bfloat16) for h in (4 * Hkv, Hkv, Hkv))
+    ws = small.workspace()
+    slot = torch.tensor([16 * nb - 1], device=DEV)
+    turns = B.pa_rope_turns([1.0 / 10000 ** (i / 64) for i in range(64)]).to(DEV)
+    before = k[-1, :, :15].clone()
+    B.pa_qk_norm_rope_append(q, kn, vn, torch.zeros(1, dtype=torch.int32, device=DEV), slot, turns, k, v, workspace=ws)
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
+    assert torch.equal(k[-1, :, 15], kn[0]) and torch.equal(v[-1, :, 15], vn[0]) and torch.equal(
+        k[-1, :, :15].view(torch.int16), before.view(torch.int16))
