@@ -193,6 +193,10 @@ __device__ __forceinline__ RowInfo row_info(const WindowParams& p, int d, bool f
   }
   x.L = p.seq_lens[r];
   if (x.n < 1 || x.n > kWindowDecodeQueries) return x;  // no row of this kernel
+  if (x.tok < 0 || x.tok > p.total_q - x.n) {  // (not what the host copy says)
+    if (first_cta) record_error(p.err, PA_ERR_DEVICE_INDEX);
+    return x;
+  }
   if (x.L < x.n || x.L > PA_MAX_SEQ_LEN || (x.L + kPage - 1) / kPage > p.max_blocks_per_req || x.n > Cfg<NT>::kQueries) {
     if (x.L != 0 && first_cta) record_error(p.err, PA_ERR_DEVICE_INDEX);
     x.L = -1;  // padding

@@ -377,3 +377,23 @@ def test_a_pool_whose_offsets_pass_32_bits():
     assert B.pa_get_device_error(ws) == 0
     assert torch.equal(k[-1, :, 15], kn[0]) and torch.equal(v[-1, :, 15], vn[0]) and torch.equal(
         k[-1, :, :15].view(torch.int16), before.view(torch.int16))
+
+
+@pytest.mark.parametrize("shift", [-3, 1000, (1 << 31) - 40])
+def test_a_row_whose_queries_lie_outside_is_recorded_and_left(shift):
+    """A device copy of qo_indptr that is not the host's."""
+    c = Case([300, 64, 40], [1, 4, 2], 64, 4, 2, seed=31)
+    want, want_lse = c.run()
+    ws = c.workspace()
+    out, lse = torch.full_like(want, 5.0), torch.full_like(want_lse, 5.0)
+    wrong = torch.from_numpy(c.ind).clone()
+    wrong[2:] += shift                       # (row 1 has another number of queries, row 2 others)
+    c.d["ind"].copy_(wrong)
+    d = c.d
+    B.pa_attention_varlen_window(d["q"], d["k"], d["v"], d["tables"], d["seq"], d["ind"], c.scale, c.window, c.sinks,
+                                 seq_lens_host=torch.from_numpy(c.seq), qo_indptr_host=torch.from_numpy(c.ind), out=out,
+                                 lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:1], want[:1]) and torch.equal(lse[:1], want_lse[:1])
+    if shift > 0:
+        assert B.pa_get_device_error(ws) == B.PA_ERR_DEVICE_INDEX and bool((out[1:] == 5.0).all())
