@@ -1,4 +1,4 @@
-// Decode with a sliding window: rows of 1 to 8 queries over the pages they see.
+// Decode with a sliding window: rows of 1 to 6 queries over the pages they see.
 //
 // What is computed: the query at position p sees keys t <= p with t < sinks or t > p -
 // window; softmax attention over these.  Scores, maxima, sums and outputs in
@@ -18,7 +18,7 @@
 // M = 16 keys, N = 8 columns (a column is a query and one of the 4 heads of the group),
 // O^T += V^T P^T has M = 16 dims, so K and V are the A operands as they lie in shared
 // memory, and a page costs 16 products per 8 columns.  tcgen05 would want 64 or 128 keys
-// or rows at once: with 4 to 32 rows it would wait for 8 pages and idle on 75 % of its
+// or rows at once: with 4 to 24 rows it would wait for 8 pages and idle on 80 % of its
 // M.
 //   The weights of one query fill half of N = 8, those of two queries one of two
 // column tiles; the other half takes what their rounding to bf16 left (16 bits in all).
@@ -35,8 +35,8 @@
 // 69.1 with the first, 61.5 with both and a row's q fetched by copies all in flight).
 //
 // Measured (GB300, in a graph, bytes of the pages seen over time): 64 rows of 1 query,
-// 1028 keys 47.9 us; 80 rows of 1, 2, 4, 5, 8 queries, 4096 keys 6.7, 6.7, 6.6, 6.4, 5.2 TB/s; from
-// seven queries on it is the products and not the memory that take the time.
+// 1028 keys 47.9 us; 80 rows of 1, 2, 4, 5 queries, 4096 keys 6.8, 6.8, 6.7, 6.45 TB/s.
+// Of seven and more queries the products would take the time (5.3 TB/s): the tile kernel's.
 #include <math.h>
 #include <stddef.h>
 
@@ -54,16 +54,16 @@ constexpr int kQStride = kHeadDim + 8;  // bf16 between rows of q: matrix loads 
 
 // NT: tiles of 8 columns (2 queries).  Consumer warps, pages in flight of each, and
 // partial buffers fill the shared memory; up to 8 warps in all a thread has 255 registers,
-// which three and four tiles need, up to 12 it has 168.  Measured, 80 rows, 1024 keys, us:
+// which three tiles need, up to 12 it has 168.  Measured, 80 rows, 1024 keys, us:
 // 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4 67.8, 4 x 3 68.9,
-// 5 x 3 70.9, 5 x 2 71.9; 4 tiles, 4 x 3 82.1, 4 x 2 82.7, 5 x 2 82.2.  Two warps that share
+// 5 x 3 70.9, 5 x 2 71.9.  Two warps that share
 // a ring's pages and split the columns load each page's fragments twice: 111 for 85.6 then.
 template <int NT>
 struct Cfg {
   static constexpr int kQueries = NT == 1 ? 1 : 2 * NT;
   static constexpr int kCols = kQueries * kGroup;
   static constexpr int kWarps = NT <= 2 ? 8 : 4;
-  static constexpr int kStages = NT <= 2 ? 2 : NT == 3 ? 4 : 3;
+  static constexpr int kStages = NT <= 2 ? 2 : 4;
   static constexpr int kBufs = NT == 1 ? 2 : 1;
   static constexpr bool kQRegs = NT <= 2;  // q's fragments kept in registers
   static constexpr int kThreads = (kWarps + kMergeWarps + 1) * 32;
@@ -85,21 +85,25 @@ struct __align__(1024) Smem {
   int abort;
 };
 
-template <class S>
-__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+// (The loop is a function of its own: code at every wait's place that the instruction
+// caches need not take along.)
+__device__ __noinline__ bool wait_on(int* abort, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
-      if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+      if (*reinterpret_cast<volatile int*>(abort)) return false;
       if (globaltimer() - t0 > kWaitLimitNs) {
         record_error(err, PA_ERR_DEVICE_TIMEOUT);
-        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+        *reinterpret_cast<volatile int*>(abort) = 1;
         return false;
       }
     }
   }
+}
+template <class S>
+__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, int* err) {
+  return mbar_try_wait(bar, parity) || wait_on(&sm.abort, bar, parity, err);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -739,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
   }
 }
 
-std::atomic<bool> g_attr_set[4][kMaxDevices];
+std::atomic<bool> g_attr_set[3][kMaxDevices];
 
 template <int NT>
 cudaError_t launch(const WindowParams& p, int grid, cudaStream_t stream) {
@@ -753,12 +757,8 @@ cudaError_t launch(const WindowParams& p, int grid, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream) {
-  switch ((queries + 1) / 2) {
-    case 1: return queries == 1 ? launch<1>(p, grid, stream) : launch<2>(p, grid, stream);
-    case 2: return launch<2>(p, grid, stream);
-    case 3: return launch<3>(p, grid, stream);
-    default: return launch<4>(p, grid, stream);
-  }
+  if (queries == 1) return launch<1>(p, grid, stream);
+  return queries <= 4 ? launch<2>(p, grid, stream) : launch<3>(p, grid, stream);
 }
 
 }  // namespace pa

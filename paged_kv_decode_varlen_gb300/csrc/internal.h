@@ -262,8 +262,10 @@ struct WindowParams {
   float* part_lse;  // log2 domain
   int* err;
 };
-// Rows of up to this many queries run the decode kernel with a window.
-constexpr int kWindowDecodeQueries = 8;
+// Rows of up to this many queries run the decode kernel with a window, others the tiles.
+// Decode and tiles, us, 8 kv heads, rows x keys: 3 queries 80 x 256 27.5 and 30.5, 40 x 4096
+// 107 and 114; 5 queries 31.0 and 31.5, 112 and 115; 8 queries 37.2 and 29.2, 130 and 115.
+constexpr int kWindowDecodeQueries = 6;
 // The items of a tile launch: request, first query token, its position, queries (up to
 // kWindowTileTokens).
 constexpr int kWindowTileTokens = 64;

@@ -1,4 +1,4 @@
-// Tensor-core tiles of attention with a sliding window: rows with more than eight
+// Tensor-core tiles of attention with a sliding window: rows with more than six
 // queries (prompt chunks).
 //
 // What is computed: the query at position p sees keys t <= p with t < sinks or t > p -
