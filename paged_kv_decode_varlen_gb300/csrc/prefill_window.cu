@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v < job.n_pages && ((bad >> (8 * (2 * h + e))) & 0xffu) == 0u)
               see |= page_seen(job.page(v) * kPage, pos, p.window, p.sink_tokens) << (16 * e);
           }
+          if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;  // (half of the time)
 #pragma unroll
           for (int y = 0; y < 32; ++y)
             if (!((see >> y) & 1u)) c[h][y] = hide;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             tmem_ld32_async(t_s + 32 * h, c[h]);
             wait_ld(c[h]);
-            hide_some(h);
+            if (some) hide_some(h);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
               mt = scale >= 0.f ? fmaxf(mt, __uint_as_float(c[h][y])) : fminf(mt, __uint_as_float(c[h][y]));
@@ -602,15 +603,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const int I1 = I0 + job.n_sub - 1;
+      const bool is_cut = kCut && jobs.cut(job);
+      const int slot = kCut ? jobs.slot() : 0;
+      Job after;  // (the next one, while the last product runs)
+      more = jobs.next(after);
       if (!__all_sync(0xffffffffu, wait(sm, &sm.pv_done[x][I1 & 1], (I1 >> 1) & 1, p.err))) break;
       fence_after_sync();
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       float lse = lse_log2(m_run, l_run);
       const int tok = x * kTok + (row >> 2);
       const int tok_w = x * kTok + kOutTok * (warp & 3);  // the warp's first token
-      if (kCut && jobs.cut(job)) {
+      if (is_cut) {
         // the row's part, 4 dims of 32 rows at a time
-        const size_t at = ((size_t)jobs.slot() * 2 + x) * kRows;
+        const size_t at = ((size_t)slot * 2 + x) * kRows;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + row;
 #pragma unroll 1
         for (int c = 0; c < kHeadDim / 16; ++c) {
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       R0 += job.n_sub;
       I0 += job.n_sub;
-      more = jobs.next(job);
+      job = after;
     }
     if (lane == 0) bulk_wait_all();  // the stores have been written
     __syncwarp();
