@@ -26,16 +26,17 @@
 //   Maxima are looked at only when a score exceeds its column's reference by 2^8
 // (one vote a page), so sums stay far inside binary32.
 //   At a row's end each consumer warp leaves its partial sums in shared memory and goes
-// on with the next row; two merging warps put them together behind it.  A row cut between
+// on with the next row; two or three merging warps put them together behind it.  A row cut between
 // CTAs leaves one partial per CTA in the workspace; the last CTA to arrive at the row's
 // count merges them in order: results do not depend on timing.  Both merges work out
 // what each part counts for all columns at once, a lane a column, and then add up several
 // columns' sums at a time: a column after another, each with its own reductions and
 // loads, a row of 5 queries kept a CTA for 6 us (80 rows of 5 queries, 1024 keys: 76.3 us;
-// 69.1 with the first, 61.5 with both and a row's q fetched by copies all in flight).
+// 69.1 with the first, 61.5 with both and a row's q fetched by copies all in flight, 59.1
+// with three merging warps for two).
 //
 // Measured (GB300, in a graph, bytes of the pages seen over time): 64 rows of 1 query,
-// 1028 keys 47.9 us; 80 rows of 1, 2, 4, 5 queries, 4096 keys 6.8, 6.8, 6.7, 6.45 TB/s.
+// 1028 keys 47.5 us; 80 rows of 1, 2, 4, 5 queries, 4096 keys 6.8, 6.8, 6.6, 6.5 TB/s.
 // Of seven and more queries the products would take the time (5.3 TB/s): the tile kernel's.
 #include <math.h>
 #include <stddef.h>
@@ -47,14 +48,13 @@
 namespace pa {
 namespace {
 
-constexpr int kMergeWarps = 2;  // two heads of the group each
 constexpr float kSlack = 8.f;        // log2 of the largest weight against a column's reference
 constexpr int kOStride = kHeadDim + 4;  // floats between columns of a partial: stores meet no bank twice
 constexpr int kQStride = kHeadDim + 8;  // bf16 between rows of q: matrix loads meet no bank twice
 
 // NT: tiles of 8 columns (2 queries).  Consumer warps, pages in flight of each, and
 // partial buffers fill the shared memory; up to 8 warps in all a thread has 255 registers,
-// which three tiles need, up to 12 it has 168.  Measured, 80 rows, 1024 keys, us:
+// which three tiles need, up to 12 it has 168.  Measured (with two merging warps), 80 rows, 1024 keys, us:
 // 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4 67.8, 4 x 3 68.9,
 // 5 x 3 70.9, 5 x 2 71.9.  Two warps that share
 // a ring's pages and split the columns load each page's fragments twice: 111 for 85.6 then.
@@ -66,7 +66,9 @@ struct Cfg {
   static constexpr int kStages = NT <= 2 ? 2 : 4;
   static constexpr int kBufs = NT == 1 ? 2 : 1;
   static constexpr bool kQRegs = NT <= 2;  // q's fragments kept in registers
+  static constexpr int kMergeWarps = NT == 1 ? 2 : 3;  // every second or third column each
   static constexpr int kThreads = (kWarps + kMergeWarps + 1) * 32;
+  static_assert(kMergeWarps <= kWindowMergeWarps, "counts");
 };
 
 template <int NT>
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&sm.part_full[b], C::kWarps);
-      mbar_init(&sm.part_free[b], kMergeWarps);
+      mbar_init(&sm.part_free[b], C::kMergeWarps);
     }
     sm.abort = 0;
     fence_mbar_init();
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
   Rows<NT> rows(p, sm, S, E, seg, d0, per_row, sidx);
   Item it;
 
-  if (warp == C::kWarps + kMergeWarps) {
+  if (warp == C::kWarps + C::kMergeWarps) {
     // --------------------------------------------------- each row's queries
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int b = n_item & 1;
@@ -608,15 +610,15 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     cp_async_wait<0>();  // (none is left but after a wait that gave up)
   } else {
     // -------------------------------------------------------------- merging
-    // The warp has every second column, h0 + 2 j.  What a column's parts count is worked
+    // The warp has every second or third column, h0 + kMergeWarps j.  What a column's parts count is worked
     // out by lane j; their sums are then added up kAt columns at a time.
-    constexpr int kAt = NT == 1 ? 2 : 4;
+    constexpr int kMergeWarps = C::kMergeWarps, kAt = NT == 1 ? 2 : 4;
     const int h0 = warp - C::kWarps;
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int buf = n_item % C::kBufs;
       if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[buf], (n_item / C::kBufs) & 1, p.err))) return;
       const size_t mine = ((size_t)blockIdx.x * 2 + it.slot) * p.piece_cols;
-      const int n_col = kGroup / kMergeWarps * it.n;  // columns of the warp
+      const int n_col = (kGroup * it.n - h0 + kMergeWarps - 1) / kMergeWarps;  // columns of the warp
       const int own = h0 + kMergeWarps * min(lane, n_col - 1);  // the lane's column
       auto out_row = [&](int col) {
         return (size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup;
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       // the row is cut between CTAs: the last of them to get here merges its pieces
       int last = 0;
       if (lane == 0) {
-        int* cnt = p.counters + ((size_t)it.r * Hkv + kvh) * kMergeWarps + h0;
+        int* cnt = p.counters + ((size_t)it.r * Hkv + kvh) * kWindowMergeWarps + h0;
         last = atom_add_acq_rel_gpu(cnt, 1) == it.pieces - 1;
         if (last) *cnt = 0;  // ready for the next call
       }

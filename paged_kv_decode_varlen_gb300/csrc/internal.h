@@ -232,6 +232,7 @@ constexpr int kQ4MaxRanges = 32;
 
 // Attention with a window: a query at position p sees keys t <= p with t <
 // sink_tokens or t > p - window.
+constexpr int kWindowMergeWarps = 3;  // at most; each counts a row's pieces for itself
 struct WindowParams {
   const uint16_t* q;
   const uint16_t* k_cache;
@@ -256,7 +257,7 @@ struct WindowParams {
   float* piece_o;      // fp32 [2 x CTAs, piece_cols, D] of rows cut between CTAs
   float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
   int32_t piece_cols;  // (query, head) columns of a piece
-  int* counters;       // [num_reqs, Hkv, 2] pieces that have arrived; zero between calls
+  int* counters;       // [num_reqs, Hkv, kWindowMergeWarps] pieces that have arrived; zero between calls
   // the tile kernel's parts of jobs cut between CTAs: [2 x CTAs][2 query tiles][128 rows]
   float* part_o;    // ... x D fp32, 4 dims of neighbouring rows side by side
   float* part_lse;  // log2 domain
