@@ -54,10 +54,10 @@ constexpr int kQStride = kHeadDim + 8;  // bf16 between rows of q: matrix loads 
 
 // NT: tiles of 8 columns (2 queries).  Consumer warps, pages in flight of each, and
 // partial buffers fill the shared memory; up to 8 warps in all a thread has 255 registers,
-// which three tiles need, up to 12 it has 168.  Measured (with two merging warps), 80 rows, 1024 keys, us:
-// 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4 67.8, 4 x 3 68.9,
-// 5 x 3 70.9, 5 x 2 71.9.  Two warps that share
-// a ring's pages and split the columns load each page's fragments twice: 111 for 85.6 then.
+// which three tiles need, up to 12 it has 168.  Measured (with two merging warps), 80 rows,
+// 1024 keys, us: 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4
+// 67.8, 4 x 3 68.9, 5 x 3 70.9, 5 x 2 71.9.  Two warps that share a ring's pages and split
+// the columns load each page's fragments twice: 111 for 85.6 then.
 template <int NT>
 struct Cfg {
   static constexpr int kQueries = NT == 1 ? 1 : 2 * NT;
@@ -610,8 +610,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     cp_async_wait<0>();  // (none is left but after a wait that gave up)
   } else {
     // -------------------------------------------------------------- merging
-    // The warp has every second or third column, h0 + kMergeWarps j.  What a column's parts count is worked
-    // out by lane j; their sums are then added up kAt columns at a time.
+    // The warp has every second or third column, h0 + kMergeWarps j.  What a column's
+    // parts count is worked out by lane j; their sums are then added up kAt columns at a
+    // time.
     constexpr int kMergeWarps = C::kMergeWarps, kAt = NT == 1 ? 2 : 4;
     const int h0 = warp - C::kWarps;
     for (int n_item = 0; rows.next(it); ++n_item) {

@@ -9,8 +9,8 @@
 // has A alone).  The pages that any of its queries sees (leading ones, then from the
 // first query's window on) are counted through and go in key tiles of 128 (8 pages), so a
 // job costs its window and its own length, not its context.  The jobs' key tiles are
-// laid end to end and cut into one equal share per SM (a job counts kJobCost tiles more,
-// for its start and end), so that no SM waits for the others with whole jobs still to
+// laid end to end and cut into one equal share per SM (a job counts some tiles more, for
+// its start and end), so that no SM waits for the others with whole jobs still to
 // run.  A CTA runs its share without a barrier between jobs: rings, phases and buffers are
 // indexed by running counts.  A job that is cut leaves a part per CTA in the workspace,
 // which merge_window_kernel puts together.  Where whole jobs end about as soon, they are
@@ -36,13 +36,15 @@
 // 1281 cycles: 2 x 256 of PV, 2 x 384 of scores (64 keys at a time a product reads Q's 4 KB
 // and K's 2 KB from shared memory, 48 cycles at 128 B, for 32 cycles of arithmetic; 128
 // keys at a time would take 256, but then one buffer has to do, and 1089 busy cycles became
-// 2500 in all).  A sub-tile takes 1360 cycles in the middle of a job; a job costs about 3 us beside
-// (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
+// 2500 in all).  A sub-tile takes 1360 cycles in the middle of a job; a job costs about 3 us
+// beside (its first sub-tile's maximum, masks at both ends, the output), a launch 10 us
 // (152 CTAs fetch their first 30 MB at once).  Softmax of a row by two threads of 32 columns
 // each was slower (1120 ns a sub-tile for 870), as were scores, weights and PV from one warp
 // (67.2 us for 65.7, 19 jobs of 64 queries x 8 heads over 4160 keys; 61.4 now).  Most of
 // what a job costs beside is code that runs once in it and is not in the instruction
-// caches: every path laid out a second time shows.
+// caches: every path laid out a second time shows.  A second buffer for Q, three stages of K
+// and V for four and the output staged in the Q that is done with was slower too (109.7 us
+// for 100.4 on those prompts): the softmax warps are what a job's ends wait for.
 //
 // Every wait is bounded; on a timeout the CTA records the error, lets its copies and
 // products finish (bounded), frees its tensor memory and returns.
@@ -107,7 +109,8 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 // (The loop is a function of its own: at every wait's place it would be more code than the
-// instruction caches take along: 8 prompts behind a window of 512 took 118.7 us for 107.1, and the output by a rolled-up loop 103.)
+// instruction caches take along.  8 prompts behind a window of 512 took 118.7 us for
+// 107.1; the output by a rolled-up loop made that 103.)
 __device__ __noinline__ bool wait_on(Smem& sm, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
