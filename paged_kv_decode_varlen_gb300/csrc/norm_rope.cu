@@ -7,9 +7,9 @@
 //
 // Angles.  A speed comes as the fraction of a turn per position in units of 2^-64
 // (pa_rope_turns); position times that in 64-bit integers, whose overflow drops whole
-// turns, is the angle to 2^-64 of a turn times the position.  Its upper 32 bits, as
-// a signed fraction of half a turn, go to sincospif: no range reduction, and as exact
-// at position 2^20 as at 1.
+// turns, is the angle to 2^-64 of a turn times the position.  Its upper 32 bits, less the
+// nearest quarter turn, go to sincospif as a signed fraction of half a turn: no range
+// reduction, and as exact at position 2^20 as at 1.
 //
 // Work.  A unit is a token and up to kHeads of its kv heads, with the 4 query heads of
 // each.  A warp takes units in turn: its lane 0 keeps the rows of the next kStages units
@@ -60,8 +60,15 @@ __device__ __forceinline__ float2 shfl2(float2 v, int from) {
 __device__ __forceinline__ float2 angle(const RopeParams& p, int pos, int j, int half) {
   float2 r = make_float2(1.f, 0.f);
   if (j >= 0 && j < half) {
-    const uint64_t a = (uint64_t)(int64_t)pos * p.turns[j];
-    sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &r.y, &r.x);  // 2^-31: of half a turn
+    const uint32_t a = (uint32_t)(((uint64_t)(int64_t)pos * p.turns[j]) >> 32);
+    // what is left of it to the nearest quarter turn: 30 bits, of which a float keeps 24
+    const uint32_t quarter = (a + (1u << 29)) >> 30;
+    float c, s;
+    sincospif((float)(int32_t)(a - (quarter << 30)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: of half a turn
+    r.x = (quarter & 1u) ? s : c;
+    r.y = (quarter & 1u) ? c : s;
+    if ((quarter + 1u) & 2u) r.x = -r.x;  // cos of the second and third quarter
+    if (quarter & 2u) r.y = -r.y;
   }
   return r;
 }
@@ -169,7 +176,12 @@ __device__ __forceinline__ void row16(uint4& lo, uint4& hi, const float2 (&w)[8]
     float ss = s2.x + s2.y;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float q = rsqrtf(fmaf(ss, 1.f / kHeadDim, eps));
+    // (a Newton step: without it, and with angles to 2^-24 of half a turn, twice as many of
+    // the results were rounded to the other neighbour as the formula's)
+    const float v = fmaf(ss, 1.f / kHeadDim, eps);
+    float q = rsqrtf(v);
+    const float r = fmaf(-v * q, q, 1.f);
+    if (fabsf(r) < 1.f) q = fmaf(0.5f * q, r, q);  // (not of a zero or an infinity)
     const float2 q2 = make_float2(q, q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], w[i]), q2);
