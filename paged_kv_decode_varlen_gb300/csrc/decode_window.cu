@@ -5,13 +5,14 @@
 // binary32; log2 domain.
 //
 // Work.  A row's visible pages (leading ones, then the window's) are counted through,
-// and for each kv head all rows' pages form one stream that is cut into one equal
-// segment per CTA; with few rows each row is cut into pieces of its own instead, so
-// that no CTA needs the other rows' lengths.  The plan is made on the device from the
+// and for each kv head all rows' pages form one stream that is cut into equal segments,
+// one for each gang of a CTA's warps (two gangs, one for rows of five and six queries);
+// with few rows each row is cut into pieces of its own instead, so that no CTA needs the
+// other rows' lengths.  The plan is made on the device from the
 // lengths (one load per row and a scan), so the launch depends on scalars alone.
 //
-// Bound: HBM (2 FMA per byte of K and V and query).  A CTA's pages go to its consumer
-// warps in turn; each warp keeps its next ones in flight in a ring of its own, by
+// Bound: HBM (2 FMA per byte of K and V and query).  A segment's pages go to the gang's
+// consumer warps in turn; each warp keeps its next ones in flight in a ring of its own, by
 // asynchronous 16-byte copies that place the 16-byte chunks of a row of 64 dims at c ^
 // (row mod 8), so that matrix loads meet no bank twice.
 //   Products: mma.sync m16n8k16 with keys as M.  A page is 16 keys: S^T = K Q^T has
@@ -58,7 +59,7 @@ constexpr int kQStride = kHeadDim + 8;  // bf16 between rows of q: matrix loads 
 // 1024 keys, us: 2 tiles, 8 warps x 2 pages 63.8, 7 x 2 63.9, 5 x 4 65.3; 3 tiles, 4 x 4
 // 67.8, 4 x 3 68.9, 5 x 3 70.9, 5 x 2 71.9.  Two warps that share a ring's pages and split
 // the columns load each page's fragments twice: 111 for 85.6 then.
-template <int NT>
+template <int NT, int kGangs>
 struct Cfg {
   static constexpr int kQueries = NT == 1 ? 1 : 2 * NT;
   static constexpr int kCols = kQueries * kGroup;
@@ -66,20 +67,22 @@ struct Cfg {
   static constexpr int kStages = NT <= 2 ? 2 : 4;
   static constexpr int kBufs = NT == 1 ? 2 : 1;
   static constexpr bool kQRegs = NT <= 2;  // q's fragments kept in registers
-  static constexpr int kMergeWarps = NT == 1 ? 2 : 3;  // every second or third column each
-  static constexpr int kThreads = (kWarps + kMergeWarps + 1) * 32;
-  static_assert(kMergeWarps <= kWindowMergeWarps, "counts");
+  // the CTA's warps as kGangs gangs, each with a segment, merging warps and a q of its own
+  static constexpr int kGang = kWarps / kGangs;                          // consumer warps of a gang
+  static constexpr int kMergeWarps = kGangs == 2 ? 1 : NT == 1 ? 2 : 3;  // every so many-th column each
+  static constexpr int kThreads = (kWarps + kGangs * (kMergeWarps + 1)) * 32;
+  static_assert(kMergeWarps <= kWindowMergeWarps && kGangs <= kWindowGangs, "counts, pieces");
 };
 
-template <int NT>
+template <int NT, int kGangs>
 struct __align__(1024) Smem {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, kGangs>;
   uint8_t page[C::kWarps][C::kStages][4][kPage * 128];  // K dims 0-63, 64-127, V dims 0-63, 64-127
-  uint16_t q[2][8 * NT][kQStride];                       // a row's q by column (columns without a query: anything)
+  uint16_t q[kGangs][2][8 * NT][kQStride];  // a row's q by column (columns without a query: anything)
   float o[C::kBufs][C::kWarps][C::kCols][kOStride];
   float m[C::kBufs][C::kWarps][C::kCols], l[C::kBufs][C::kWarps][C::kCols];
-  uint64_t q_full[2], q_free[2];
-  uint64_t part_full[C::kBufs], part_free[C::kBufs];
+  uint64_t q_full[kGangs][2], q_free[kGangs][2];
+  uint64_t part_full[kGangs][C::kBufs], part_free[kGangs][C::kBufs];
   int start[kPlanMaxRows + 1];  // pages of the rows before
   int len[kPlanMaxRows], tok[kPlanMaxRows];
   uint8_t n_q[kPlanMaxRows];
@@ -144,12 +147,12 @@ struct Item {
 
 // The rows of a CTA's segment, one after another.  pieces > 0: each row is cut into
 // that many segments of its own (at most; of 8 pages at least).
-template <int NT>
+template <int NT, int kGangs>
 struct Rows {
   const WindowParams& p;
-  const Smem<NT>& sm;
+  const Smem<NT, kGangs>& sm;
   int S, E, seg, d, per_row, sidx;
-  __device__ __forceinline__ Rows(const WindowParams& p_, const Smem<NT>& sm_, int S_, int E_, int seg_, int d_, int per,
+  __device__ __forceinline__ Rows(const WindowParams& p_, const Smem<NT, kGangs>& sm_, int S_, int E_, int seg_, int d_, int per,
                                   int sidx_)
       : p(p_), sm(sm_), S(S_), E(E_), seg(seg_), d(d_), per_row(per), sidx(sidx_) {}
   __device__ __forceinline__ bool next(Item& it) {
@@ -189,7 +192,7 @@ struct Rows {
 struct RowInfo {
   int pages, L, n, tok;
 };
-template <int NT>
+template <int NT, int kGangs>
 __device__ __forceinline__ RowInfo row_info(const WindowParams& p, int d, bool first_cta) {
   const int r = p.row0 + d;
   RowInfo x{0, 0, 1, r};
@@ -203,7 +206,7 @@ __device__ __forceinline__ RowInfo row_info(const WindowParams& p, int d, bool f
     if (first_cta) record_error(p.err, PA_ERR_DEVICE_INDEX);
     return x;
   }
-  if (x.L < x.n || x.L > PA_MAX_SEQ_LEN || (x.L + kPage - 1) / kPage > p.max_blocks_per_req || x.n > Cfg<NT>::kQueries) {
+  if (x.L < x.n || x.L > PA_MAX_SEQ_LEN || (x.L + kPage - 1) / kPage > p.max_blocks_per_req || x.n > Cfg<NT, kGangs>::kQueries) {
     if (x.L != 0 && first_cta) record_error(p.err, PA_ERR_DEVICE_INDEX);
     x.L = -1;  // padding
     return x;
@@ -212,23 +215,29 @@ __device__ __forceinline__ RowInfo row_info(const WindowParams& p, int d, bool f
   return x;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
+template <int NT, int kGangs>
+__global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
     decode_window_kernel(const WindowParams p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, kGangs>;
   extern __shared__ uint8_t smem_raw[];
-  Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem<NT, kGangs>& sm = *reinterpret_cast<Smem<NT, kGangs>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int Hkv = p.num_kv_heads, kvh = (int)blockIdx.x % Hkv, sidx = (int)blockIdx.x / Hkv;
-  const int nseg = (int)gridDim.x / Hkv;
+  // the warp's gang: consumers, then merging warps, then the warps that fetch q
+  const int gang = warp < C::kWarps ? warp / C::kGang
+                                    : warp < C::kWarps + kGangs * C::kMergeWarps ? (warp - C::kWarps) / C::kMergeWarps
+                                                                                   : warp - C::kWarps - kGangs * C::kMergeWarps;
+  const int Hkv = p.num_kv_heads, kvh = (int)blockIdx.x % Hkv, sidx = (int)blockIdx.x / Hkv * kGangs + gang;
+  const int nseg = (int)gridDim.x / Hkv * kGangs;
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.q_full[b], 1);
-      mbar_init(&sm.q_free[b], C::kWarps);
-    }
-    for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(&sm.part_full[b], C::kWarps);
-      mbar_init(&sm.part_free[b], C::kMergeWarps);
+    for (int x = 0; x < kGangs; ++x) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sm.q_full[x][b], 1);
+        mbar_init(&sm.q_free[x][b], C::kGang);
+      }
+      for (int b = 0; b < C::kBufs; ++b) {
+        mbar_init(&sm.part_full[x][b], C::kGang);
+        mbar_init(&sm.part_free[x][b], C::kMergeWarps);
+      }
     }
     sm.abort = 0;
     fence_mbar_init();
@@ -237,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
   pdl_wait();
 
   // ---- the plan: every row's pages, laid end to end
-  const int per_row = p.per_row;
+  const int per_row = kGangs == 1 ? p.per_row : 0;
   int total = 0, S, E, seg, d0 = 0;
   constexpr int kPer = (kPlanMaxRows + C::kThreads - 1) / C::kThreads;
   if (per_row > 0) {
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     const int d = sidx / per_row;
     if (d >= p.rows) return;
     if (tid == 0) {
-      const RowInfo x = row_info<NT>(p, d, kvh == 0 && sidx == d * per_row);
+      const RowInfo x = row_info<NT, kGangs>(p, d, kvh == 0 && sidx == d * per_row);
       sm.start[d] = 0;
       sm.start[d + 1] = x.pages;
       sm.len[d] = x.L;
@@ -274,12 +283,12 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       const int d = tid * kPer + i;
       pages[i] = 0;
       if (d < p.rows) {
-        const RowInfo x = row_info<NT>(p, d, blockIdx.x == 0);
+        const RowInfo x = row_info<NT, kGangs>(p, d, blockIdx.x == 0);
         pages[i] = x.pages;
         sm.len[d] = x.L;
         sm.tok[d] = x.tok;
         sm.n_q[d] = (uint8_t)x.n;
-        if (x.pages == 0 && x.L <= 0 && !p.qo_indptr && sidx == d % nseg) {  // padding: defined outputs
+        if (x.pages == 0 && x.L <= 0 && !p.qo_indptr && (int)blockIdx.x / Hkv == d % (nseg / kGangs)) {  // padding: defined outputs
           const size_t row = (size_t)x.tok * p.num_q_heads + kvh * kGroup;
           uint4* o = reinterpret_cast<uint4*>(p.out + row * kHeadDim);
           for (int j = 0; j < kGroup * kHeadDim * 2 / 16; ++j) o[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -324,31 +333,32 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     d0 = lo;
   }
   const int n_pages = E - S;
-  Rows<NT> rows(p, sm, S, E, seg, d0, per_row, sidx);
+  Rows<NT, kGangs> rows(p, sm, S, E, seg, d0, per_row, sidx);
   Item it;
 
-  if (warp == C::kWarps + C::kMergeWarps) {
+  if (warp >= C::kWarps + kGangs * C::kMergeWarps) {
     // --------------------------------------------------- each row's queries
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int b = n_item & 1;
-      if (n_item >= 2 && !__all_sync(0xffffffffu, wait(sm, &sm.q_free[b], ((n_item >> 1) - 1) & 1, p.err))) return;
+      if (n_item >= 2 && !__all_sync(0xffffffffu, wait(sm, &sm.q_free[gang][b], ((n_item >> 1) - 1) & 1, p.err))) return;
       for (int i = lane; i < it.n * kGroup * (kHeadDim / 8); i += 32) {  // all in flight at once
         const int col = i / (kHeadDim / 8), ch = i % (kHeadDim / 8);
         const uint16_t* src = p.q + ((size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup) * kHeadDim;
-        cp_async16(&sm.q[b][col][8 * ch], src + 8 * ch);
+        cp_async16(&sm.q[gang][b][col][8 * ch], src + 8 * ch);
       }
       cp_async_commit();
       cp_async_wait<0>();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full[b]);
+      if (lane == 0) mbar_arrive(&sm.q_full[gang][b]);
     }
   } else if (warp < C::kWarps) {
     // ----------------------------------------------------------- consumers
-    // The warp's pages are i = warp + kWarps k, k = 0 .. n_own - 1.  Slabs of 32 of
-    // them by lane, a batch ahead: which (block, kv head); -1: outside the pool
-    const int n_own = (n_pages - warp + C::kWarps - 1) / C::kWarps;
+    // The warp's pages are i = gw + kGang k, k = 0 .. n_own - 1.  Slabs of 32 of them by
+    // lane, a batch ahead: which (block, kv head); -1: outside the pool
+    const int gw = warp % C::kGang;
+    const int n_own = (n_pages - gw + C::kGang - 1) / C::kGang;
     auto load_ids = [&](int k0) -> int {
-      const int i = warp + C::kWarps * (k0 + lane);
+      const int i = gw + C::kGang * (k0 + lane);
       if (i >= n_pages) return 0;
       int lo = d0, hi = per_row ? d0 : p.rows - 1;
       while (lo < hi) {
@@ -400,13 +410,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     const int v_row = (lane & 7) + (lane >> 4) * 8, v_ch = (lane >> 3) & 1;
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int qb = n_item & 1;
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.q_full[qb], (n_item >> 1) & 1, p.err))) break;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.q_full[gang][qb], (n_item >> 1) & 1, p.err))) break;
       // q as the B operand, columns 8 t .. 8 t + 7 (matrix loads: column lane mod 8, dims
       // 32 y + 8 (lane / 8) on).  One query: columns 4 .. 7 again (for what rounding
       // leaves); two: tile 1 is tile 0
       auto q_at = [&](int t, int y) {
         const int col = it.n == 1 ? lane & 3 : it.n == 2 && t == 1 ? lane & 7 : 8 * t + (lane & 7);
-        return smem_addr(&sm.q[qb][col][32 * y + 8 * (lane >> 3)]);
+        return smem_addr(&sm.q[gang][qb][col][32 * y + 8 * (lane >> 3)]);
       };
       uint32_t qf[C::kQRegs ? NT : 1][4][4];
       if constexpr (C::kQRegs) {
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) ldsm4(qf[t][y], q_at(t, y));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_free[qb]);
+        if (lane == 0) mbar_arrive(&sm.q_free[gang][qb]);
       }
       const Seen seen = seen_pages(it.L, it.n, p.window, p.sink_tokens);
       const int p0 = it.L - it.n;  // position of the first query
@@ -431,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
           for (int y = 0; y < 4; ++y) o[mt][t][y] = 0.f;
       }
       const int k_first = k;
-      for (int i; (i = warp + C::kWarps * k) < it.i1; ++k) {
+      for (int i; (i = gw + C::kGang * k) < it.i1; ++k) {
         cp_async_wait<C::kStages - 1>();
         __syncwarp();  // every lane's copies have landed
         if ((bad >> (k & 31)) & 1u) {
@@ -559,12 +569,12 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       }
       if constexpr (!C::kQRegs) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_free[qb]);
+        if (lane == 0) mbar_arrive(&sm.q_free[gang][qb]);
       }
       // ---- the warp's part of the row
       const int buf = n_item % C::kBufs;
       if (n_item >= C::kBufs &&
-          !__all_sync(0xffffffffu, wait(sm, &sm.part_free[buf], ((n_item / C::kBufs) - 1) & 1, p.err)))
+          !__all_sync(0xffffffffu, wait(sm, &sm.part_free[gang][buf], ((n_item / C::kBufs) - 1) & 1, p.err)))
         break;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
           }
         }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.part_full[buf]);
+      if (lane == 0) mbar_arrive(&sm.part_full[gang][buf]);
     }
     cp_async_wait<0>();  // (none is left but after a wait that gave up)
   } else {
@@ -613,31 +623,31 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     // The warp has every second or third column, h0 + kMergeWarps j.  What a column's
     // parts count is worked out by lane j; their sums are then added up kAt columns at a
     // time.
-    constexpr int kMergeWarps = C::kMergeWarps, kAt = NT == 1 ? 2 : 4;
-    const int h0 = warp - C::kWarps;
+    constexpr int kMergeWarps = C::kMergeWarps, kAt = NT == 1 && kMergeWarps == 2 ? 2 : 4;
+    const int h0 = (warp - C::kWarps) % C::kMergeWarps, w0 = gang * C::kGang;
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int buf = n_item % C::kBufs;
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[buf], (n_item / C::kBufs) & 1, p.err))) return;
-      const size_t mine = ((size_t)blockIdx.x * 2 + it.slot) * p.piece_cols;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[gang][buf], (n_item / C::kBufs) & 1, p.err))) return;
+      const size_t mine = ((size_t)(sidx * Hkv + kvh) * 2 + it.slot) * p.piece_cols;
       const int n_col = (kGroup * it.n - h0 + kMergeWarps - 1) / kMergeWarps;  // columns of the warp
       const int own = h0 + kMergeWarps * min(lane, n_col - 1);  // the lane's column
       auto out_row = [&](int col) {
         return (size_t)(it.tok + col / kGroup) * p.num_q_heads + kvh * kGroup + col % kGroup;
       };
-      float f[C::kWarps], M = -INFINITY, L = 0.f;
+      float f[C::kGang], M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        f[w] = sm.m[buf][w][own];
+      for (int w = 0; w < C::kGang; ++w) {
+        f[w] = sm.m[buf][w0 + w][own];
         M = fmaxf(M, f[w]);
       }
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
+      for (int w = 0; w < C::kGang; ++w) {
         f[w] = fast_exp2(f[w] - (M == -INFINITY ? 0.f : M));  // -inf -> 0
-        L = fmaf(f[w], sm.l[buf][w][own], L);                 // (0 x NaN: a NaN of a part without a maximum shows)
+        L = fmaf(f[w], sm.l[buf][w0 + w][own], L);                 // (0 x NaN: a NaN of a part without a maximum shows)
       }
       const float inv = L == 0.f ? 0.f : (L != L ? L : 1.f / L);
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) f[w] *= inv;
+      for (int w = 0; w < C::kGang; ++w) f[w] *= inv;
       const float lse = lse_log2(M == -INFINITY ? 0.f : M, L);
       if (lane < n_col) {
         if (it.pieces > 1) p.piece_lse[mine + own] = lse;
@@ -650,9 +660,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
           const int j = min(j0 + u, n_col - 1);
           a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < C::kWarps; ++w) {
+          for (int w = 0; w < C::kGang; ++w) {
             const float fw = __shfl_sync(0xffffffffu, f[w], j);
-            const float4 x = *reinterpret_cast<const float4*>(&sm.o[buf][w][h0 + kMergeWarps * j][4 * lane]);
+            const float4 x = *reinterpret_cast<const float4*>(&sm.o[buf][w0 + w][h0 + kMergeWarps * j][4 * lane]);
             if (fw != 0.f)  // (a part that had no page left nothing there)
               a[u] = make_float4(fmaf(fw, x.x, a[u].x), fmaf(fw, x.y, a[u].y), fmaf(fw, x.z, a[u].z), fmaf(fw, x.w, a[u].w));
           }
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.part_free[buf]);
+      if (lane == 0) mbar_arrive(&sm.part_free[gang][buf]);
       if (it.pieces == 1) continue;
       // the row is cut between CTAs: the last of them to get here merges its pieces
       int last = 0;
@@ -686,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       auto slot = [&](int x) {
         return ((size_t)((it.s0 + x) * Hkv + kvh) * 2 + (x == 0 ? first : 0)) * p.piece_cols;
       };
-      constexpr int kMany = NT == 1 ? 2 : NT == 2 ? 4 : 8;  // columns at a time, of two pieces each
+      constexpr int kMany = NT == 1 ? kAt : NT == 2 ? 4 : 8;  // columns at a time, of two pieces each
       float e[kMany][2];
       float4 y[kMany][2];
       auto fetch = [&](int j0, int x0) {
@@ -746,22 +756,29 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
   }
 }
 
-std::atomic<bool> g_attr_set[3][kMaxDevices];
+std::atomic<bool> g_attr_set[3][2][kMaxDevices];
 
-template <int NT>
+template <int NT, int kGangs>
 cudaError_t launch(const WindowParams& p, int grid, cudaStream_t stream) {
-  constexpr size_t kBytes = sizeof(Smem<NT>) + 1024;  // + slack to align the base
+  constexpr size_t kBytes = sizeof(Smem<NT, kGangs>) + 1024;  // + slack to align the base
   static_assert(kBytes <= 232448, "shared memory per CTA");
-  const cudaError_t e = set_smem_limit_once((const void*)decode_window_kernel<NT>, (int)kBytes, g_attr_set[NT - 1]);
+  const cudaError_t e = set_smem_limit_once((const void*)decode_window_kernel<NT, kGangs>, (int)kBytes, g_attr_set[NT - 1][kGangs - 1]);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_window_kernel<NT>, dim3((unsigned)grid), dim3(Cfg<NT>::kThreads), kBytes, stream, p);
+  return launch_pdl(decode_window_kernel<NT, kGangs>, dim3((unsigned)grid), dim3(Cfg<NT, kGangs>::kThreads), kBytes, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream) {
-  if (queries == 1) return launch<1>(p, grid, stream);
-  return queries <= 4 ? launch<2>(p, grid, stream) : launch<3>(p, grid, stream);
+  // Two gangs a CTA where rows outnumber the segments: a row's start and end take a gang
+  // 1.3 us, and two do them side by side.  Measured, us, one gang and two: 1000 rows of 100
+  // keys 95.9 and 85.4, 143 of 100 20.8 and 17.4, 300 of 512 101.0 and 100.8; with rows cut into
+  // segments of their own the pieces are twice as many: one row of 80,000 keys 57.8 and 65.4.
+  // Rows of five and six queries leave no registers for another gang's warps.
+  const bool two = p.per_row == 0;
+  if (queries == 1) return two ? launch<1, 2>(p, grid, stream) : launch<1, 1>(p, grid, stream);
+  if (queries <= 4) return two ? launch<2, 2>(p, grid, stream) : launch<2, 1>(p, grid, stream);
+  return launch<3, 1>(p, grid, stream);
 }
 
 }  // namespace pa

@@ -232,6 +232,7 @@ constexpr int kQ4MaxRanges = 32;
 
 // Attention with a window: a query at position p sees keys t <= p with t <
 // sink_tokens or t > p - window.
+constexpr int kWindowGangs = 2;       // groups of warps of a decode CTA, at most; each has a segment
 constexpr int kWindowMergeWarps = 3;  // at most; each counts a row's pieces for itself
 struct WindowParams {
   const uint16_t* q;
@@ -254,8 +255,8 @@ struct WindowParams {
   // rows of a decode launch (at most kPlanMaxRows), and the segments that each is cut
   // into (0: all rows' pages as one stream)
   int32_t row0, rows, per_row;
-  float* piece_o;      // fp32 [2 x CTAs, piece_cols, D] of rows cut between CTAs
-  float* piece_lse;    // fp32 [2 x CTAs, piece_cols], log2 domain
+  float* piece_o;      // fp32 [2 x segments, piece_cols, D] of rows cut between segments
+  float* piece_lse;    // fp32 [2 x segments, piece_cols], log2 domain
   int32_t piece_cols;  // (query, head) columns of a piece
   int* counters;       // [num_reqs, Hkv, kWindowMergeWarps] pieces that have arrived; zero between calls
   // the tile kernel's parts of jobs cut between CTAs: [2 x CTAs][2 query tiles][128 rows]

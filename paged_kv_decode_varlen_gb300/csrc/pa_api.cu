@@ -1249,7 +1249,7 @@ pa_status norm_rope(pa::RopeParams& p, bool append, int32_t interleaved, int32_t
 }
 
 // Workspace of the attention with a window: [error word | counts (num_reqs x Hkv x
-// 3 int32) | pieces of rows cut between CTAs, two per CTA (columns x D fp32) | their lse |
+// 3 int32) | pieces of rows cut between segments, two per gang of a CTA (columns x D fp32) | their lse |
 // and for the tile kernel, parts of jobs cut between CTAs, two per CTA (2 x 128 rows x D
 // fp32) | their lse].
 struct WindowLayout {
@@ -1260,7 +1260,7 @@ WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_head
   const int32_t hkv = std::max(num_q_heads / PA_GQA_GROUP, 1);
   WindowLayout w;
   w.cols = PA_GQA_GROUP * std::min(std::max(total_q, 1), pa::kWindowDecodeQueries);
-  const size_t slots = (size_t)2 * std::max(pa::kWindowMaxSms, hkv) * w.cols;
+  const size_t slots = (size_t)2 * pa::kWindowGangs * std::max(pa::kWindowMaxSms, hkv) * w.cols;
   w.counters = PA_ERROR_WORD_BYTES;
   w.piece_o = w.counters + align256((size_t)num_reqs * hkv * pa::kWindowMergeWarps * 4);
   w.piece_lse = w.piece_o + slots * pa::kHeadDim * 4;
