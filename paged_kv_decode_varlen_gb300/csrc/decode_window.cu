@@ -6,7 +6,7 @@
 //
 // Work.  A row's visible pages (leading ones, then the window's) are counted through,
 // and for each kv head all rows' pages form one stream that is cut into equal segments,
-// one for each gang of a CTA's warps (two gangs, one for rows of five and six queries);
+// one for each gang of a CTA's warps (one gang, or two where rows are many and short);
 // with few rows each row is cut into pieces of its own instead, so that no CTA needs the
 // other rows' lengths.  The plan is made on the device from the
 // lengths (one load per row and a scan), so the launch depends on scalars alone.
@@ -41,6 +41,8 @@
 // Of seven and more queries the products would take the time (5.3 TB/s): the tile kernel's.
 #include <math.h>
 #include <stddef.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "q4.cuh"  // load_cg, max_nan, lse_log2
@@ -223,9 +225,8 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
   Smem<NT, kGangs>& sm = *reinterpret_cast<Smem<NT, kGangs>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // the warp's gang: consumers, then merging warps, then the warps that fetch q
-  const int gang = warp < C::kWarps ? warp / C::kGang
-                                    : warp < C::kWarps + kGangs * C::kMergeWarps ? (warp - C::kWarps) / C::kMergeWarps
-                                                                                   : warp - C::kWarps - kGangs * C::kMergeWarps;
+  const int past = warp - C::kWarps, fetch = past - kGangs * C::kMergeWarps;
+  const int gang = past < 0 ? warp / C::kGang : fetch < 0 ? past / C::kMergeWarps : fetch;
   const int Hkv = p.num_kv_heads, kvh = (int)blockIdx.x % Hkv, sidx = (int)blockIdx.x / Hkv * kGangs + gang;
   const int nseg = (int)gridDim.x / Hkv * kGangs;
   if (tid == 0) {
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
   Rows<NT, kGangs> rows(p, sm, S, E, seg, d0, per_row, sidx);
   Item it;
 
-  if (warp >= C::kWarps + kGangs * C::kMergeWarps) {
+  if (fetch >= 0) {
     // --------------------------------------------------- each row's queries
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int b = n_item & 1;
@@ -770,12 +771,14 @@ cudaError_t launch(const WindowParams& p, int grid, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_window(const WindowParams& p, int queries, int grid, cudaStream_t stream) {
-  // Two gangs a CTA where rows outnumber the segments: a row's start and end take a gang
-  // 1.3 us, and two do them side by side.  Measured, us, one gang and two: 1000 rows of 100
-  // keys 95.9 and 85.4, 143 of 100 20.8 and 17.4, 300 of 512 101.0 and 100.8; with rows cut into
-  // segments of their own the pieces are twice as many: one row of 80,000 keys 57.8 and 65.4.
-  // Rows of five and six queries leave no registers for another gang's warps.
-  const bool two = p.per_row == 0;
+  // Two gangs a CTA where rows are many and short: a row's start and end take a gang 1.3 us,
+  // and two do them side by side.  Measured, us, one gang and two.  Rows of one query, more
+  // than three a segment: 1000 of 100 keys 95.9 and 85.4, 143 of 100 20.8 and 17.4, 100 of 64
+  // 14.4 and 13.1, 58 of 300 15.0 and 14.6, 58 of 1024 44.5 and 44.7; fewer (20 of 300) 10.1 and
+  // 14.2.  Rows of three and four: 179 of 149 23.8 and 20.9, 100 of 64 22.5 and 19.8, 100 of 300
+  // 30.2 and 31.5.  Rows of five and six would have two warps a gang: 80 of 1024 65.9 and 69.2.
+  const int64_t pages = std::min<int64_t>(p.max_blocks_per_req, (int64_t)p.window / kPage + p.sink_tokens / kPage + 3);
+  const bool two = p.per_row == 0 && p.rows > 3 * (grid / p.num_kv_heads) && pages <= (queries == 1 ? 32 : 14);
   if (queries == 1) return two ? launch<1, 2>(p, grid, stream) : launch<1, 1>(p, grid, stream);
   if (queries <= 4) return two ? launch<2, 2>(p, grid, stream) : launch<2, 1>(p, grid, stream);
   return launch<3, 1>(p, grid, stream);

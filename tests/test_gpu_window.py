@@ -397,3 +397,31 @@ def test_a_row_whose_queries_lie_outside_is_recorded_and_left(shift):
     assert torch.equal(out[:1], want[:1]) and torch.equal(lse[:1], want_lse[:1])
     if shift > 0:
         assert B.pa_get_device_error(ws) == B.PA_ERR_DEVICE_INDEX and bool((out[1:] == 5.0).all())
+
+
+@pytest.mark.parametrize("most,Hkv,window,sinks", [(1, 3, 100, 4), (1, 8, 300, 17), (1, 2, 1, 1), (2, 2, 150, 0), (3, 8, 20, 0),
+                                                   (4, 3, 100, 4)])
+def test_many_short_rows(most, Hkv, window, sinks):
+    """More rows than segments several times over, some of them empty."""
+    R = 500
+    rng = np.random.default_rng(most + Hkv)
+    seq = rng.integers(1, 141, R)
+    qo = np.minimum(rng.integers(0, most + 1, R) if most > 1 else np.ones(R, int), seq)
+    qo[7] = min(most, int(seq[7]))
+    c = Case(seq.tolist(), qo.tolist(), window, sinks, Hkv, seed=most)
+    ws = c.workspace()
+    out, lse = c.run(workspace=ws)
+    c.check(out, lse)
+    again = c.run(workspace=ws) if most > 1 else c.decode(workspace=ws)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    if most == 1:                                # padding rows between (and so other cuts)
+        live = np.arange(R) % 3 != 0
+        c.d["seq"][torch.from_numpy(~live).to(DEV)] = 0
+        out, lse = c.decode(workspace=ws)
+        at = torch.from_numpy(live).to(DEV)
+        assert not bool(out[~at].any()) and bool(torch.isneginf(lse[~at]).all())
+        c.seq, c.qo, c.q = np.where(live, c.seq, 0).astype(np.int32), live.astype(np.int32), c.q[live]
+        c.ind = np.concatenate([[0], np.cumsum(c.qo)]).astype(np.int32)
+        c.check(out[at], lse[at])
+    torch.cuda.synchronize()
+    assert B.pa_get_device_error(ws) == 0
