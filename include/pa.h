@@ -652,8 +652,12 @@ size_t pa_window_workspace_size(int32_t num_reqs, int32_t total_q, int32_t num_q
  * sink_tokens    >= 0.
  * workspace      >= pa_window_workspace_size(num_reqs, total_q, num_q_heads,
  *                head_dim, window, sink_tokens) bytes, 256-byte aligned, zero-filled
- *                before its first use, left reusable by every call; as
- *                pa_attention_varlen otherwise.
+ *                before its first use; as pa_attention_varlen otherwise.  Calls and
+ *                graphs of any sizes may share one that is large enough for each:
+ *                beside the error word nothing depends on what it held.  It may be
+ *                pa_attention_varlen's for the same num_reqs and heads, whose counters
+ *                stay as they are; for other batches the partial results that a call
+ *                leaves are no zeros for that call's counters.
  * Errors: as pa_attention_varlen; PA_ERR_INVALID_ARG for window < 1 or
  *   sink_tokens < 0.
  */

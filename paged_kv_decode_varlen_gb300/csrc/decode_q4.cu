@@ -141,13 +141,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// As atom_add_acq_rel_gpu of common.cuh, on 64 bits (here, since that file is
-// part of the bf16 decode kernel's measured source).
-__device__ __forceinline__ unsigned long long atom_add64_acq_rel_gpu(unsigned long long* addr, unsigned long long v) {
-  unsigned long long old;
-  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
-  return old;
-}
 __device__ __forceinline__ uint32_t at(const uint4& v, int g) { return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w; }
 
 // An output row (head of this lane, 16 dims per lane as described at the
@@ -742,19 +735,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
 std::atomic<bool> g_attr_set[6][kMaxDevices];
 
-// A tag that no earlier launch of this process has had, and that other data
-// are as good as never: 47 bits of a scrambled count (the finalizer of the
-// splitmix64 generator), never 0.
-uint64_t next_tag() {
-  static std::atomic<uint64_t> count{
-      (uint64_t)std::chrono::system_clock::now().time_since_epoch().count()};
-  uint64_t z = count.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;
-  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
-  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
-  z ^= z >> 31;
-  return z >> 17 | uint64_t(1) << 47;
-}
-
 template <int kTiles, class Plan>
 cudaError_t launch(const DecodeParams& p, const Plan& plan, int grid, bool overlap, std::atomic<bool>* done,
                    cudaStream_t stream) {
@@ -792,6 +772,19 @@ cudaError_t launch_tiles(const DecodeParams& p, const DecodePlan& plan, const in
 }
 
 }  // namespace
+
+// A tag that no earlier launch of this process has had, and that other data
+// are as good as never: 47 bits of a scrambled count (the finalizer of the
+// splitmix64 generator), never 0.
+uint64_t next_tag() {
+  static std::atomic<uint64_t> count{
+      (uint64_t)std::chrono::system_clock::now().time_since_epoch().count()};
+  uint64_t z = count.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  z ^= z >> 31;
+  return z >> 17 | uint64_t(1) << 47;
+}
 
 cudaError_t launch_decode_q4(const DecodeParams& p, const DecodePlan& plan, const int32_t* n_q, int tiles, int grid,
                              bool by_row, bool overlap, cudaStream_t stream) {

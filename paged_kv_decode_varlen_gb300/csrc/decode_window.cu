@@ -29,7 +29,10 @@
 //   At a row's end each consumer warp leaves its partial sums in shared memory and goes
 // on with the next row; two or three merging warps put them together behind it.  A row cut between
 // CTAs leaves one partial per CTA in the workspace; the last CTA to arrive at the row's
-// count merges them in order: results do not depend on timing.  Both merges work out
+// count merges them in order: results do not depend on timing.  The counts carry a tag of the
+// launch, which every CTA of the row makes sure of before it adds to one, so that what the
+// workspace held before does not matter: the pieces of batches of other sizes lie where the
+// counts of this one do.  Both merges work out
 // what each part counts for all columns at once, a lane a column, and then add up several
 // columns' sums at a time: a column after another, each with its own reductions and
 // loads, a row of 5 queries kept a CTA for 6 us (80 rows of 5 queries, 1024 keys: 76.3 us;
@@ -628,7 +631,12 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
     const int h0 = (warp - C::kWarps) % C::kMergeWarps, w0 = gang * C::kGang;
     for (int n_item = 0; rows.next(it); ++n_item) {
       const int buf = n_item % C::kBufs;
+      // (a row cut between CTAs: no other is cut at the end of its first segment)
+      unsigned long long* word = p.words + ((size_t)it.s0 * Hkv + kvh) * kWindowMergeWarps + h0;
+      unsigned long long was = 0;  // (fetched while the row's pages are on their way)
+      if (it.pieces > 1 && lane == 0) was = *reinterpret_cast<volatile unsigned long long*>(word);
       if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[gang][buf], (n_item / C::kBufs) & 1, p.err))) return;
+      if (it.pieces > 1 && lane == 0 && was >> 16 != p.tag) atomicCAS(word, was, (unsigned long long)p.tag << 16);
       const size_t mine = ((size_t)(sidx * Hkv + kvh) * 2 + it.slot) * p.piece_cols;
       const int n_col = (kGroup * it.n - h0 + kMergeWarps - 1) / kMergeWarps;  // columns of the warp
       const int own = h0 + kMergeWarps * min(lane, n_col - 1);  // the lane's column
@@ -685,9 +693,8 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
       // the row is cut between CTAs: the last of them to get here merges its pieces
       int last = 0;
       if (lane == 0) {
-        int* cnt = p.counters + ((size_t)it.r * Hkv + kvh) * kWindowMergeWarps + h0;
-        last = atom_add_acq_rel_gpu(cnt, 1) == it.pieces - 1;
-        if (last) *cnt = 0;  // ready for the next call
+        last = (int)(atom_add64_acq_rel_gpu(word, 1ull) & 0xffffu) == it.pieces - 1;
+        if (last) *word = 0;  // ready for the next replay with this tag
       }
       __syncwarp();  // lane 0's acquire orders the reads below
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;

@@ -109,7 +109,7 @@ template <int R, int C>
 struct Q4Plan {
   int32_t n_rows, seg, total;
   int32_t by_row;  // a segment holds pages of its first row only
-  uint64_t tag;    // marks this launch's words in the workspace (48 bits)
+  uint64_t tag;    // marks this launch's words in the workspace (next_tag)
   int4 row[R];    // request, seq_len, first query token, queries
   int2 start[C];  // a segment's first row and that row's first page
 };
@@ -258,7 +258,10 @@ struct WindowParams {
   float* piece_o;      // fp32 [2 x segments, piece_cols, D] of rows cut between segments
   float* piece_lse;    // fp32 [2 x segments, piece_cols], log2 domain
   int32_t piece_cols;  // (query, head) columns of a piece
-  int* counters;       // [num_reqs, Hkv, kWindowMergeWarps] pieces that have arrived; zero between calls
+  // pieces that have arrived, of the row that is cut at segment s's end: [s, Hkv,
+  // kWindowMergeWarps], tag << 16 | count
+  unsigned long long* words;
+  uint64_t tag;  // marks this launch's words (next_tag)
   // the tile kernel's parts of jobs cut between CTAs: [2 x CTAs][2 query tiles][128 rows]
   float* part_o;    // ... x D fp32, 4 dims of neighbouring rows side by side
   float* part_lse;  // log2 domain
@@ -451,6 +454,9 @@ cudaError_t launch_prefill(const PrefillParams& p, const PrefillItems& items, co
 cudaError_t launch_prefix(const PrefixParams& p, int n_chunks, const TcMaps& maps, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixParams& p, int n_chunks, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
+// A mark for the words that a launch counts in (48 bits), another one for every launch.
+uint64_t next_tag();
+
 cudaError_t launch_step_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const RopeParams& p, bool append, bool interleaved, cudaStream_t stream);
 // rows of up to `queries` queries on grid CTAs, a multiple of the kv heads

@@ -1248,21 +1248,24 @@ pa_status norm_rope(pa::RopeParams& p, bool append, int32_t interleaved, int32_t
   return s == PA_OK ? ok() : s;
 }
 
-// Workspace of the attention with a window: [error word | counts (num_reqs x Hkv x
-// 3 int32) | pieces of rows cut between segments, two per gang of a CTA (columns x D fp32) | their lse |
+// Workspace of the attention with a window: [error word | a gap, where pa_attention_varlen
+// has its counts for the batch: they stay zero | words that count the pieces of rows cut
+// between segments (segments x Hkv x 3) | these pieces, two per gang of a CTA (columns x D fp32) | their lse |
 // and for the tile kernel, parts of jobs cut between CTAs, two per CTA (2 x 128 rows x D
-// fp32) | their lse].
+// fp32) | their lse].  The words carry a tag of the launch: nothing depends on what the
+// workspace held before, such as the pieces of a batch of another size.
 struct WindowLayout {
-  size_t counters, piece_o, piece_lse, part_o, part_lse, total;
+  size_t words, piece_o, piece_lse, part_o, part_lse, total;
   int32_t cols;
 };
 WindowLayout window_layout(int32_t num_reqs, int32_t total_q, int32_t num_q_heads) {
   const int32_t hkv = std::max(num_q_heads / PA_GQA_GROUP, 1);
   WindowLayout w;
   w.cols = PA_GQA_GROUP * std::min(std::max(total_q, 1), pa::kWindowDecodeQueries);
-  const size_t slots = (size_t)2 * pa::kWindowGangs * std::max(pa::kWindowMaxSms, hkv) * w.cols;
-  w.counters = PA_ERROR_WORD_BYTES;
-  w.piece_o = w.counters + align256((size_t)num_reqs * hkv * pa::kWindowMergeWarps * 4);
+  const size_t segs = (size_t)pa::kWindowGangs * std::max(pa::kWindowMaxSms, hkv);  // x kv heads
+  const size_t slots = 2 * segs * w.cols;
+  w.words = PA_ERROR_WORD_BYTES + align256((size_t)num_reqs * hkv * 4);
+  w.piece_o = w.words + align256(segs * pa::kWindowMergeWarps * 8);
   w.piece_lse = w.piece_o + slots * pa::kHeadDim * 4;
   // jobs of rows for the tile kernel: two parts a CTA
   const size_t parts = total_q > pa::kWindowDecodeQueries ? (size_t)2 * std::min(sm_count(), pa::kWindowMaxSms) : 0;
@@ -1383,6 +1386,7 @@ pa_status window_decode(pa::WindowParams& p, int queries, cudaStream_t stream) {
   for (p.row0 = 0; p.row0 < p.num_reqs; p.row0 += pa::kPlanMaxRows) {
     p.rows = std::min(p.num_reqs - p.row0, pa::kPlanMaxRows);
     p.per_row = p.rows <= nseg ? nseg / p.rows : 0;
+    p.tag = pa::next_tag();
     const pa_status s = run_launch(PA_KERNEL_DECODE, "decode_window", stream, [&] {
       return pa::launch_decode_window(p, queries, nseg * p.num_kv_heads, stream);
     });
@@ -1593,7 +1597,7 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.err = static_cast<int*>(workspace);
-  p.counters = reinterpret_cast<int*>(ws + wl.counters);
+  p.words = reinterpret_cast<unsigned long long*>(ws + wl.words);
   p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
   p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
   p.piece_cols = wl.cols;
@@ -1645,7 +1649,7 @@ pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cac
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.err = static_cast<int*>(workspace);
-  p.counters = reinterpret_cast<int*>(ws + wl.counters);
+  p.words = reinterpret_cast<unsigned long long*>(ws + wl.words);
   p.piece_o = reinterpret_cast<float*>(ws + wl.piece_o);
   p.piece_lse = reinterpret_cast<float*>(ws + wl.piece_lse);
   p.piece_cols = wl.cols;

@@ -78,6 +78,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // NaN where a score was.
 __device__ __forceinline__ float lse_log2(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
+// As atom_add_acq_rel_gpu of common.cuh, on 64 bits (here, since that file is
+// part of the bf16 decode kernel's measured source).
+__device__ __forceinline__ unsigned long long atom_add64_acq_rel_gpu(unsigned long long* addr, unsigned long long v) {
+  unsigned long long old;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
+  return old;
+}
+
 // Byte of token t's 16 code bytes of group g, and of its (D, Z) pair.
 __device__ __forceinline__ int q4_code_at(int t, int g) { return t * kQ4Row + ((g ^ ((t >> 1) & 3)) << 4); }
 __device__ __forceinline__ int q4_scale_at(int t, int g) { return kQ4Codes + (t * kQ4Groups + g) * 4; }
