@@ -633,10 +633,11 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
       const int buf = n_item % C::kBufs;
       // (a row cut between CTAs: no other is cut at the end of its first segment)
       unsigned long long* word = p.words + ((size_t)it.s0 * Hkv + kvh) * kWindowMergeWarps + h0;
-      unsigned long long was = 0;  // (fetched while the row's pages are on their way)
-      if (it.pieces > 1 && lane == 0) was = *reinterpret_cast<volatile unsigned long long*>(word);
+      if (it.pieces > 1 && lane == 0) {  // (while the row's pages are on their way)
+        const unsigned long long was = *reinterpret_cast<volatile unsigned long long*>(word);
+        if (was >> 16 != p.tag) atomicCAS(word, was, (unsigned long long)p.tag << 16);
+      }
       if (!__all_sync(0xffffffffu, wait(sm, &sm.part_full[gang][buf], (n_item / C::kBufs) & 1, p.err))) return;
-      if (it.pieces > 1 && lane == 0 && was >> 16 != p.tag) atomicCAS(word, was, (unsigned long long)p.tag << 16);
       const size_t mine = ((size_t)(sidx * Hkv + kvh) * 2 + it.slot) * p.piece_cols;
       const int n_col = (kGroup * it.n - h0 + kMergeWarps - 1) / kMergeWarps;  // columns of the warp
       const int own = h0 + kMergeWarps * min(lane, n_col - 1);  // the lane's column
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
       int last = 0;
       if (lane == 0) {
         last = (int)(atom_add64_acq_rel_gpu(word, 1ull) & 0xffffu) == it.pieces - 1;
-        if (last) *word = 0;  // ready for the next replay with this tag
+        if (last) *word = (unsigned long long)p.tag << 16;  // ready for the next replay with this tag
       }
       __syncwarp();  // lane 0's acquire orders the reads below
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
