@@ -504,7 +504,8 @@ pa_status pa_attention_varlen_noalloc(const void* q, const void* k_cache, const 
  *   the total to n_tokens are padding: slot -1, position 0.
  *   Pages given back go to the ring's tail, in the order of requests and pages,
  *   and are not granted before the next call.  Their table entries stay as they
- *   are.  Of a request that has ended: all that it holds, except its first
+ *   are.  A page whose entry is outside the pool has no block, and nothing is given
+ *   back for it.  Of a request that has ended: all that it holds, except its first
  *   shared_pages.  With window > 0, of a request with n > 0: pages j >= keep with
  *   16 (j + 1) <= c - window + 1, which no query of this or a later step of
  *   pa_attention_varlen_window sees, where keep = max(ceil(sink_tokens / 16),
@@ -517,7 +518,7 @@ pa_status pa_attention_varlen_noalloc(const void* q, const void* k_cache, const 
  * block_tables    [num_reqs, max_blocks_per_req] int32, device, modified in place:
  *                 only the entries of granted pages are written.
  * free_ring       [num_blocks] int32, device, modified in place: the ids of the
- *                 pool's free blocks, in a ring.
+ *                 pool's free blocks, in a ring (places behind them: anything).
  * free_state      [2] int32, device: the ring's head (0 .. num_blocks - 1) and the
  *                 number of ids in it.
  * window, sink_tokens, shared_pages  >= 0.  window = 0: nothing is given back
@@ -545,7 +546,10 @@ pa_status pa_attention_varlen_noalloc(const void* q, const void* k_cache, const 
  *   wait, and no page is granted or given back.  An id in the ring outside the
  *   pool is granted as -1.
  *   PA_ERR_DEVICE_NO_BLOCKS: the ring has fewer ids than pages are needed: the
- *   pages it could not grant get the table entry -1, their tokens the slot -1.
+ *   pages it could not grant get the table entry -1, their tokens the slot -1, in
+ *   later steps too (each records it again).  What these tokens would have written
+ *   is lost to their request: end it (the blocks that it has come back) and begin it
+ *   anew.  No other request is touched.
  * Errors: PA_ERR_INVALID_ARG (num_reqs outside [0, 65535], n_tokens < 0,
  *   num_blocks outside [1, 2^31 - 1], a negative window, sink_tokens or
  *   shared_pages, max_blocks_per_req < 1, null or misaligned pointers),

@@ -45,10 +45,9 @@ def step_tables(new, cached, first, tables, ring, state, window, sinks, shared, 
             return [j for j in range(had) if j >= keep and j >= f and PAGE * (j + 1) <= c - window + 1]
         return []
 
-    need = sum(-(-(c + n) // PAGE) - -(-c // PAGE) for c, n, _, _ in rows)
-    back = sum(len(returned(*row)) for row in rows)
+    back = sum(0 <= tables[r, j] < cap for r, row in enumerate(rows) for j in returned(*row))
     bad = not (0 <= head < cap and 0 <= count <= cap)
-    if bad or sum(n for _, n, _, _ in rows) > n_tokens or max(count - need, 0) + back > cap:
+    if bad or sum(n for _, n, _, _ in rows) > n_tokens or count + back > cap:
         errors.add(DEVICE_INDEX)
         rows = [[c, 0, False, f] for c, _, _, f in rows]
     seq, indptr, slots, pos, first_out, given_back = [], [0], [], [], [], []
@@ -68,9 +67,11 @@ def step_tables(new, cached, first, tables, ring, state, window, sinks, shared, 
         for t in range(c, c + n):
             pos.append(t)
             block = int(tables[r, t // PAGE])
+            if block < 0 and t // PAGE < -(-c // PAGE):   # a page that an earlier step could not grant
+                errors.add(NO_BLOCKS)
             slots.append(block * PAGE + t % PAGE if block >= 0 else -1)
         out = returned(c, n, ended, f)
-        given_back += [int(tables[r, j]) for j in out]
+        given_back += [int(tables[r, j]) for j in out if 0 <= tables[r, j] < cap]
         seq.append(0 if ended else c + n)
         indptr.append(indptr[-1] + n)
         first_out.append(0 if ended else out[-1] + 1 if out else f)
