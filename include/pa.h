@@ -513,6 +513,13 @@ pa_status pa_attention_varlen_noalloc(const void* q, const void* k_cache, const 
  *   still holds (first_page[r] where nothing was given back, 0 for a request
  *   that has ended).
  * new_tokens, cached_lens  [num_reqs] int32, device.
+ *                 Lengths grow: cached_lens[r] is what seq_lens[r] was after the
+ *                 call before (0 for a new request).  Where it is less (drafts that
+ *                 were refused) the call knows nothing of the pages behind it: if
+ *                 ceil(cached_lens[r] / 16) is less too, the caller first puts the
+ *                 blocks of the pages from there to ceil(seq_lens[r] / 16) - 1 back,
+ *                 each id to place (head + count) modulo num_blocks of free_ring,
+ *                 and adds one to count; else they are lost to the pool.
  * first_page      [num_reqs] int32, device, or NULL for zeros: what the call
  *                 before left in first_page_out (0 for a new request).
  * block_tables    [num_reqs, max_blocks_per_req] int32, device, modified in place:

@@ -34,6 +34,15 @@ class Loop:
             out += [int(b) for b in self.tables[r, at] if b >= 0]
         return out
 
+    def roll_back(self, r, c):
+        """Request r keeps c tokens: the blocks of the pages behind them go back."""
+        pages = -(-c // 16), -(-int(self.cached[r]) // 16)
+        self.cached, self.ring, self.state = self.cached.copy(), self.ring.copy(), self.state.copy()
+        for b in self.tables[r, pages[0]:pages[1]]:
+            self.ring[self.state.sum() % self.cap] = b
+            self.state[1] += 1
+        self.cached[r] = c
+
     def step(self, new):
         """One step; the recorded errors.  Every block has to be somewhere, once."""
         new = np.asarray(new, np.int32)
@@ -101,8 +110,22 @@ def pages_without_blocks_slide_behind_a_window(make):
     assert a.step([-1, -1]) == set() and sorted(a.free()) == list(range(5))
 
 
+def drafts_are_refused(make):
+    """Verify steps of five tokens of which some are kept, across page borders."""
+    a = Loop(3, 40, 20, window=50, sinks=2, make=make)
+    rng = np.random.default_rng(1)
+    a.step([30, 1, 44])
+    for _ in range(40):
+        before = a.cached.copy()
+        assert a.step([5, 5, 5]) == set()
+        for r in range(3):
+            a.roll_back(r, int(before[r] + rng.integers(1, 6)))
+    a.step([-1, -1, -1])
+    assert a.state[1] == 40
+
+
 SEQUENCES = [two_that_do_not_fit, a_prompt_larger_than_the_pool, ends_beside_starts, tokens_of_a_page_without_a_block,
-             pages_without_blocks_slide_behind_a_window]
+             pages_without_blocks_slide_behind_a_window, drafts_are_refused]
 
 
 @pytest.mark.parametrize("sequence", SEQUENCES, ids=lambda f: f.__name__)
