@@ -695,7 +695,8 @@ pa_status pa_attention_varlen_window(const void* q, const void* k_cache, const v
  * q, out         [num_reqs, num_q_heads, head_dim] bf16; lse [num_reqs,
  *                num_q_heads] float32 or NULL.
  * workspace      >= pa_window_workspace_size(num_reqs, num_reqs, ...).
- * Errors: as pa_attention_varlen_window; PA_ERR_UNSUPPORTED for num_reqs > 65535.
+ * Errors: as pa_attention_varlen_window; num_reqs is 0 .. 65535 (PA_ERR_INVALID_ARG
+ *   otherwise).
  */
 pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, int64_t num_blocks,
                            const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* seq_lens,

@@ -250,12 +250,12 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
   pdl_wait();
 
   // ---- the plan: every row's pages, laid end to end
-  const int per_row = kGangs == 1 ? p.per_row : 0;
+  const int per_row = kGangs == 1 ? p.per_row : 0, per = kGangs == 1 ? per_row : 1;  // (per: > 0 where it divides)
   int total = 0, S, E, seg, d0 = 0;
   constexpr int kPer = (kPlanMaxRows + C::kThreads - 1) / C::kThreads;
   if (per_row > 0) {
     // rows cut into per_row segments: this CTA has one row
-    const int d = sidx / per_row;
+    const int d = sidx / per;
     if (d >= p.rows) return;
     if (tid == 0) {
       const RowInfo x = row_info<NT, kGangs>(p, d, kvh == 0 && sidx == d * per_row);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
     }
     __syncthreads();
     total = sm.start[d + 1];
-    seg = max(8, (total + per_row - 1) / per_row);
+    seg = max(8, (total + per - 1) / per);
     S = (sidx - d * per_row) * seg;
     E = min(S + seg, total);
     d0 = d;
