@@ -39,7 +39,7 @@ constexpr int kStages = 2;  // units in flight per warp
 constexpr int kHeads = 8;   // kv heads of a unit
 
 // How dims pair up.  kFull: dim i with 64 + i.  kPairs: 2 i with 2 i + 1.  kPart: i with i
-// + half, for i < half < 64.
+// + half, for i < half < 64 (half 0: nothing is rotated).
 enum class Mode { kFull, kPairs, kPart };
 
 // Lane c of a row's 8 holds dims [8 c, 8 c + 8) and [64 + 8 c, 64 + 8 c + 8): in pairs f[0
@@ -119,6 +119,9 @@ __device__ __forceinline__ void make_angles(const RopeParams& p, int pos, Angles
   }
 }
 
+// Dims from 2 half on stay as they are: a product with cos 0 and sin 0 would make NaN of an
+// infinity.  (half is a multiple of 8, so a lane's chunk of 8 dims is rotated or not as a
+// whole.)
 template <Mode kMode>
 __device__ __forceinline__ void rotate(float2 (&f)[8], const Angles<kMode>& t, int half) {
   auto neg = [](float2 v) { return make_float2(-v.x, -v.y); };
@@ -130,11 +133,13 @@ __device__ __forceinline__ void rotate(float2 (&f)[8], const Angles<kMode>& t, i
       f[4 + u] = __ffma2_rn(b, t.c[u], __fmul2_rn(a, t.s[u]));
     }
   } else if constexpr (kMode == Mode::kPairs) {
+    const int first = 4 * (threadIdx.x & 7);  // pair of f[0]; f[4]'s is 32 further
+    const bool turned[2] = {first < half, 32 + first < half};
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float c = u < 4 ? t.c[u & 3].x : t.c[u & 3].y, s = u < 4 ? t.s[u & 3].x : t.s[u & 3].y;
       const float a = f[u].x, b = f[u].y;
-      f[u] = make_float2(fmaf(a, c, -b * s), fmaf(b, c, a * s));
+      if (turned[u >> 2]) f[u] = make_float2(fmaf(a, c, -b * s), fmaf(b, c, a * s));
     }
   } else {
     const int lane = threadIdx.x & 31, c = lane & 7, far = half / 8;
@@ -151,7 +156,8 @@ __device__ __forceinline__ void rotate(float2 (&f)[8], const Angles<kMode>& t, i
       }
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) f[u] = __ffma2_rn(f[u], t.c[u], __fmul2_rn(other[u], t.s[u]));
+    for (int u = 0; u < 8; ++u)
+      if (8 * (u >> 2) + c < 2 * far) f[u] = __ffma2_rn(f[u], t.c[u], __fmul2_rn(other[u], t.s[u]));
   }
 }
 
@@ -324,7 +330,7 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 template <bool kAppend>
 cudaError_t launch_mode(const RopeParams& p, bool interleaved, cudaStream_t stream) {
   if (interleaved) return launch<kAppend, Mode::kPairs>(p, stream);
-  if (p.rotary_dim == kHeadDim || p.rotary_dim == 0) return launch<kAppend, Mode::kFull>(p, stream);
+  if (p.rotary_dim == kHeadDim) return launch<kAppend, Mode::kFull>(p, stream);
   return launch<kAppend, Mode::kPart>(p, stream);
 }
 
