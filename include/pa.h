@@ -572,9 +572,11 @@ pa_status pa_step_tables(const int32_t* new_tokens, const int32_t* cached_lens, 
 /*
  * pa_rope_turns -- the rotation speeds of pa_qk_norm_rope, computed on the host:
  * turns[i] = the fraction of a turn that pair i advances per position, inv_freq[i]
- * / (2 pi) modulo 1, in units of 2^-64.  A position times this, modulo 2^64, is the
- * pair's angle whatever the position: nothing is lost far into a context, where a
- * binary32 angle would be off by whole radians.
+ * / (2 pi) modulo 1, in units of 2^-64, off by 2^-52 of the speed (a quotient in
+ * binary64) or 2^-54 of a turn, whichever is more.  A position times this, modulo
+ * 2^64, is the pair's angle, off by as much times the position: 2^-34 of a turn at
+ * position 2^20 for a speed of one radian, where an angle in binary32 would be off
+ * by up to a sixteenth of a radian.
  * inv_freq, turns  [n] host arrays.  Errors: PA_ERR_INVALID_ARG (n outside
  * [0, 64], null pointers, a speed that is not finite).
  */

@@ -7,9 +7,11 @@
 //
 // Angles.  A speed comes as the fraction of a turn per position in units of 2^-64
 // (pa_rope_turns); position times that in 64-bit integers, whose overflow drops whole
-// turns, is the angle to 2^-64 of a turn times the position.  Its upper 32 bits, less the
-// nearest quarter turn, go to sincospif as a signed fraction of half a turn: no range
-// reduction, and as exact at position 2^20 as at 1.
+// turns, is off by what the speed is (2^-52 of it, from binary64) times the position, and
+// by nothing else: 2^-34 of a turn at position 2^20 for a speed of one radian.  Its upper 32
+// bits, less the nearest quarter turn, go to sincospif as a signed fraction of half a turn,
+// without a range reduction: what binary32 leaves of it, 2^-25 of a turn, is the larger error
+// at every position.
 //
 // Work.  A unit is a token and up to kHeads of its kv heads, with the 4 query heads of
 // each.  A warp takes units in turn: its lane 0 keeps the rows of the next kStages units
