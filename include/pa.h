@@ -656,8 +656,8 @@ size_t pa_window_workspace_size(int32_t num_reqs, int32_t total_q, int32_t num_q
  *   sees are never read: with pa_step_tables they are given back.  Keys and
  *   values that no query of the request sees (slots behind its last token, tokens
  *   behind its window) may hold anything, infinities and NaN included.  Infinities
- *   and NaN in values that one query of a request sees may reach other queries
- *   of the same request.
+ *   and NaN in values that some queries of a request see reach these and no others
+ *   (outputs that are not finite are computed a second time, which takes long).
  *   Weights are rounded to bf16 before they meet V in rows of more than two
  *   queries; in rows of one or two they carry 16 bits.  A (query, head) with a NaN
  *   among its scores has NaN in its out row and its lse, and changes no other.

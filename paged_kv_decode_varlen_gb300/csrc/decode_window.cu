@@ -50,6 +50,7 @@
 #include "internal.h"
 #include "q4.cuh"  // load_cg, max_nan, lse_log2
 #include "window.cuh"
+#include "window_mend.cuh"
 
 namespace pa {
 namespace {
@@ -222,7 +223,7 @@ __device__ __forceinline__ RowInfo row_info(const WindowParams& p, int d, bool f
 
 template <int NT, int kGangs>
 __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
-    decode_window_kernel(const WindowParams p) {
+    decode_window_kernel(const __grid_constant__ WindowParams p) {
   using C = Cfg<NT, kGangs>;
   extern __shared__ uint8_t smem_raw[];
   Smem<NT, kGangs>& sm = *reinterpret_cast<Smem<NT, kGangs>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -663,6 +664,23 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
         if (it.pieces > 1) p.piece_lse[mine + own] = lse;
         else if (p.lse) p.lse[out_row(own)] = lse * kLn2;
       }
+      // columns whose output is not finite: see window_mend.cuh
+      uint32_t odd = 0;
+      auto look = [&](int j, const float4& v) {
+        const float z = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
+        if (z != 0.f) odd |= 1u << j;
+      };
+      auto mend = [&]() {
+        uint32_t todo = __reduce_or_sync(0xffffffffu, odd);
+        if (todo == 0u) return;
+        const Seen seen = seen_pages(it.L, it.n, p.window, p.sink_tokens);
+        for (; todo != 0u; todo &= todo - 1u) {
+          const int col = h0 + kMergeWarps * (__ffs((int)todo) - 1);
+          mend_out(p, p.out + out_row(col) * kHeadDim, p.q + out_row(col) * kHeadDim,
+                   p.block_tables + (size_t)it.r * p.max_blocks_per_req, kvh, seen.lead, 0, seen.first - seen.lead, seen.count(),
+                   it.L - it.n + col / kGroup);
+        }
+      };
       for (int j0 = 0; j0 < n_col; j0 += kAt) {
         float4 a[kAt];
 #pragma unroll
@@ -681,6 +699,7 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
         for (int u = 0; u < kAt; ++u) {
           if (j0 + u >= n_col) break;
           const int col = h0 + kMergeWarps * (j0 + u);
+          if (it.pieces == 1) look(j0 + u, a[u]);
           if (it.pieces == 1)
             *reinterpret_cast<uint2*>(p.out + out_row(col) * kHeadDim + 4 * lane) =
                 make_uint2(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w));
@@ -690,7 +709,10 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.part_free[gang][buf]);
-      if (it.pieces == 1) continue;
+      if (it.pieces == 1) {
+        mend();
+        continue;
+      }
       // the row is cut between CTAs: the last of them to get here merges its pieces
       int last = 0;
       if (lane == 0) {
@@ -757,10 +779,12 @@ __global__ void __launch_bounds__(Cfg<NT, kGangs>::kThreads, 1)
 #pragma unroll
         for (int u = 0; u < kMany; ++u) {
           if (j0 + u >= n_col) break;
+          look(j0 + u, a[u]);
           *reinterpret_cast<uint2*>(p.out + out_row(h0 + kMergeWarps * (j0 + u)) * kHeadDim + 4 * lane) =
               make_uint2(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w));
         }
       }
+      mend();
     }
   }
 }

@@ -10,7 +10,7 @@
 // turns, is off by what the speed is (2^-52 of it, from binary64) times the position, and
 // by nothing else: 2^-34 of a turn at position 2^20 for a speed of one radian.  Its upper 32
 // bits, less the nearest quarter turn, go to sincospif as a signed fraction of half a turn,
-// without a range reduction: what binary32 leaves of it, 2^-25 of a turn, is the larger error
+// without a range reduction: what binary32 leaves of it, 2^-28 of a turn, is the larger error
 // at every position.
 //
 // Work.  A unit is a token and up to kHeads of its kv heads, with the 4 query heads of

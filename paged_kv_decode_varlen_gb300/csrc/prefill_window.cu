@@ -54,9 +54,10 @@
 #include <type_traits>
 
 #include "internal.h"
-#include "q4.cuh"  // lse_log2
+#include "q4.cuh"  // lse_log2, load_cg, bf16x2_fma
 #include "tc.cuh"
 #include "window.cuh"
+#include "window_mend.cuh"
 
 namespace pa {
 namespace {
@@ -104,6 +105,7 @@ struct __align__(1024) Smem {
   uint8_t bad_k[kBad][kPagesPerSub], bad_v[kBad][kPagesPerSub];  // pages outside the pool, of a sub-tile
   uint32_t tmem;
   int abort;
+  int odd;  // some output is not finite
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + slack to align the base
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -303,6 +305,32 @@ __device__ __forceinline__ void copy_tiles(Smem& sm, const WindowParams& p, cons
     for (int r = max(0, R - kStages); r < R; ++r) mbar_wait_bounded(&full[r % kStages], (r / kStages) & 1);
 }
 
+// The outputs (or parts) of the CTA's jobs that are not finite, again (see window_mend.cuh), a row
+// at a time and warp.  Out of line: few registers are alive where it is called.
+template <bool kCut>
+__device__ __noinline__ void mend_jobs(const WindowParams& p, const WindowItems& items) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Jobs<kCut> jobs(p, items);
+  Job job;
+  while (jobs.next(job)) {
+    const int n = min(job.n_pages, job.n_sub * kPagesPerSub);
+    const bool is_cut = kCut && jobs.cut(job);
+    const size_t part = kCut ? (size_t)jobs.slot() * 2 * kRows : 0;
+    for (int i = warp; i < kGroup * job.nq; i += kThreads / 32) {
+      const int pos = job.pos0 + (i >> 2);
+      const size_t at = ((size_t)(job.tok0 + (i >> 2)) * p.num_q_heads + job.kvh * kGroup + (i & 3)) * kHeadDim;
+      if (is_cut) {  // (tile B's rows lie behind tile A's)
+        float4* o = reinterpret_cast<float4*>(p.part_o + (part + (i & ~(kRows - 1))) * kHeadDim) + lane * kRows + (i & (kRows - 1));
+        const float4 y = load_cg(o);
+        if (__any_sync(0xffffffffu, fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, y.w * 0.f))) != 0.f))
+          *o = mend_row(p, y, p.q + at, job.table, job.kvh, job.lead, job.lo, job.hi, n, pos);
+      } else {
+        mend_out(p, p.out + at, p.q + at, job.table, job.kvh, job.lead, job.lo, job.hi, n, pos);
+      }
+    }
+  }
+}
+
 template <bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ WindowParams p, const __grid_constant__ WindowItems items,
@@ -331,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = 0; w < 4; ++w) mbar_init(&sm.drained[w], 1);
     sm.abort = 0;
+    sm.odd = 0;
     fence_mbar_init();
   }
   if (warp == kScoreWarp) {
@@ -620,10 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the row's part, 4 dims of 32 rows at a time
         const size_t at = ((size_t)slot * 2 + x) * kRows;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + row;
+        float zero = 0.f;  // 0 times every value: NaN where one is not finite
 #pragma unroll 1
         for (int c = 0; c < kHeadDim / 16; ++c) {
           uint32_t o[16];
           load16(t_o + 16 * c, o);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) zero = fmaf(__uint_as_float(o[y]), 0.f, zero);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             dst[(4 * c + y) * kRows] =
@@ -633,10 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before_sync();  // the tensor-memory reads above precede the arrive
         mbar_arrive(&sm.o_free[x]);
         p.part_lse[at + row] = lse;
+        if (zero != 0.f && tok < job.nq) *reinterpret_cast<volatile int*>(&sm.odd) = 1;
       } else {
         // The output, 64 dims at a time, through shared memory (128-byte swizzle) and out
         // by TMA, the warp's 8 tokens x 4 heads x 64 dims.
         uint8_t* stg = sm.out[warp];
+        uint32_t zero = 0u;  // 0 times every value, in pairs: 0 or NaN
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if (lane == 0) bulk_wait_read();  // what was staged before has been read
@@ -650,6 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 16; ++y)
               w[y] = pack_bf16x2(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) zero = bf16x2_fma(w[y], 0u, zero);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * c + y) ^ (lane & 7)) << 4)) =
@@ -676,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();  // (read before the next 64 dims go there)
           }
         }
+        if ((zero & 0x7fff7fffu) != 0u && tok < job.nq) *reinterpret_cast<volatile int*>(&sm.odd) = 1;
         if (p.lse && tok < job.nq)
           p.lse[(size_t)(job.tok0 + tok) * p.num_q_heads + job.kvh * kGroup + (row & 3)] = lse * kLn2;
       }
@@ -690,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
+  if (sm.odd && !sm.abort) mend_jobs<kCut>(p, items);  // (rare)
 }
 
 // The outputs of cut jobs: the log-sum-exp merge of their parts, in order.  A CTA takes 32
