@@ -1283,10 +1283,13 @@ int window_item_tiles(const pa::WindowParams& p, const int4& it) {
 // What a job costs beside its key tiles, in tiles.
 constexpr int kWindowJobCost = 3;
 // What cutting jobs costs beside: a share's ends are jobs of their own, their parts are
-// written and merged.  Measured (152 SMs), whole against cut, and how many tiles the
-// longest CTA of whole jobs is above the even share: 4 x 512 queries over 4608 keys 119.0
-// and 117.4 us (11 tiles), 8 x 512 229 and 212 (23), 3 x 400 queries, 3 heads 58.6 and 38.6
-// (25); 16 x 100 queries over 612 keys 29.4 and 36.6 (4), 8000 queries, 1024 keys 116 and 133 (2).
+// written and merged.  Measured (152 SMs, 8 kv heads), us, whole against cut, by how many
+// tiles the longest CTA of whole jobs is above the even share.  3 tiles: 8000 queries, window
+// of 1024, 104 and 127; 6: 2 x 512 queries over 4600 keys 56 and 65; 12: 4 x 512 106 and 113; 13
+// (4 heads): 2000 queries, window of 8000, 97.8 and 99.5; 14: 20 x 100 over 1600 71.7 and 67.0;
+// 18: 6 x 512 157 and 161; 20: 5 x 300 over 3300 84 and 75, 10 x 200 over 2700 87 and 95; 22 (3
+// heads): 3 x 400 54 and 41; 27: 3 x 512 103 and 89; 33: 5 x 512 153 and 136.  Between 13 and 23
+// either wins, by as much; below and above, one.
 constexpr int kWindowCutCost = 12;
 
 // The tile launches of the rows of more than kWindowDecodeQueries queries: the jobs' key
