@@ -318,8 +318,11 @@ size_t pa_attention_workspace_size(int32_t num_reqs, int32_t total_q, int32_t nu
  *                holds the error word, per-(request, kv head) counters of
  *                finished key ranges and the partial results of key ranges
  *                cut between CTAs; every call leaves the counters at zero,
- *                so a workspace is reused without clearing.  Calls sharing a workspace must not run
- *                concurrently.  After a PA_ERR_DEVICE_* error, zero it again.
+ *                so a workspace is reused without clearing by calls with the same
+ *                num_reqs and num_kv_heads; where these change, the counters of one
+ *                batch lie where another kept its partial results: zero it between
+ *                them, or keep a workspace for each.  Calls sharing a workspace must
+ *                not run concurrently.  After a PA_ERR_DEVICE_* error, zero it again.
  *                The error word is not cleared by this call (see
  *                pa_clear_device_error).
  */
