@@ -77,3 +77,31 @@ def test_a_long_request_without_many_of_its_blocks_ends(pad):
     assert loop.step([-1] * 30 + [1] * 36 + [-1, 50, 0, 20]) == {step.NO_BLOCKS}
     assert loop.step([0] * 30 + [-1] * 36 + [0, -1, 0, -1]) == set()
     assert loop.state[1] == 3000
+
+
+@pytest.mark.parametrize("in_place,pad", FORMS)
+@pytest.mark.parametrize("R", [1, 7, 60, 300, 1300])
+def test_tables_and_rings_that_hold_anything(R, in_place, pad):
+    """Entries and ids inside the pool and outside, lengths of all kinds, few places
+    and many: the oracle's step, whatever it is."""
+    make = caller(in_place, B.new_workspace(256, DEV), pad)
+    rng = np.random.default_rng(R)
+    done = short = 0
+    for i in range(24):
+        cap = int(rng.integers(1, [8, 4 * R, 40 * R][i % 3] + 2))
+        cached = rng.integers(0, 150, R)
+        new = np.where(rng.random(R) < 0.3, -1, rng.integers(0, 40, R) * (rng.random(R) < 0.5))
+        tables = rng.integers(0, cap, (R, 12))
+        tables[rng.random(tables.shape) < [0, 0.3, 0.9, 1][i % 4]] = -1
+        tables[rng.random(tables.shape) < 0.02] = cap + 5
+        ring = rng.integers(0, cap, cap)
+        ring[rng.random(cap) < 0.02] = -3
+        state = [int(rng.integers(cap)), int(rng.integers(0, cap + 1))]
+        window, sinks = int(rng.choice([0, 20, 64])), int(rng.choice([0, 3, 40]))
+        first = rng.integers(0, 4, R) if window else np.zeros(R)
+        n = int(np.maximum(np.where(cached + new > 192, 0, new), 0).sum())
+        i32 = [np.asarray(x, np.int32) for x in (new, cached, first, tables, ring, state)]
+        got, errors = make(*i32, window, sinks, int(rng.choice([0, 0, 2])), n)
+        short += step.NO_BLOCKS in errors
+        done += got["qo_indptr"][-1] > 0 or not errors
+    assert done > 2 and (R < 5 or short > 2)
